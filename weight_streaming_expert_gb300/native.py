@@ -1,5 +1,5 @@
-"""ctypes binding of include/moe.h and include/lm_head.h (same names; argument
-marshalling only).
+"""ctypes binding of include/moe.h, lm_head.h, attention.h and sampling.h (same
+names; argument marshalling only).
 
 Every step of the layer runs in the CUDA library ``_build/libwse.so``.  There
 is no Python or CPU fallback: if the library is missing or fails to load,
@@ -33,6 +33,9 @@ MOE_FWD_TRACE = 0x4
 MOE_FWD_OUT_F32 = 0x8
 MOE_FWD_TEST_SKIP_ARRIVAL = 0x40000000
 TRACE_SLOTS = 32
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_FP16 = 1
+MOE_COPY_ROWS_MAX = 64
 
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_CUDA",
                 4: "MOE_ERR_OOM", 5: "MOE_ERR_DEVICE_TIMEOUT"}
@@ -54,6 +57,29 @@ class moe_info_t(ctypes.Structure):
 class moe_layer_opts_t(ctypes.Structure):
     _fields_ = [("w_shared_gate_up", ctypes.c_void_p), ("w_shared_down", ctypes.c_void_p),
                 ("routed_scale", ctypes.c_float), ("bias_selection_only", ctypes.c_int)]
+
+
+_i, _l, _p, _f = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
+
+
+class moe_qk_norm_rope_args_t(ctypes.Structure):
+    _fields_ = [("dtype", _i), ("n_tokens", _i), ("n_heads", _i), ("n_kv_heads", _i), ("head_dim", _i),
+                ("rotary_dim", _i), ("interleaved", _i), ("eps", _f), ("q", _p), ("k", _p), ("v", _p),
+                ("q_token_stride", _l), ("q_head_stride", _l), ("k_token_stride", _l), ("k_head_stride", _l),
+                ("v_token_stride", _l), ("v_head_stride", _l), ("q_weight", _p), ("k_weight", _p), ("turns", _p),
+                ("positions", _p), ("slots", _p), ("q_out", _p), ("q_out_token_stride", _l),
+                ("q_out_head_stride", _l), ("k_cache", _p), ("v_cache", _p), ("k_page_stride", _l),
+                ("k_row_stride", _l), ("v_page_stride", _l), ("v_row_stride", _l), ("n_pages", _i),
+                ("page_size", _i)]
+
+
+class moe_attn_args_t(ctypes.Structure):
+    _fields_ = [("dtype", _i), ("batch", _i), ("n_tokens", _i), ("max_q_len", _i), ("scale", _f), ("q", _p),
+                ("q_token_stride", _l), ("q_head_stride", _l), ("k_cache", _p), ("v_cache", _p),
+                ("k_page_stride", _l), ("k_row_stride", _l), ("v_page_stride", _l), ("v_row_stride", _l),
+                ("n_pages", _i), ("page_size", _i), ("block_table", _p), ("table_stride", _i), ("q_starts", _p),
+                ("kv_lens", _p), ("tree_mask", _p), ("out", _p), ("out_token_stride", _l), ("out_head_stride", _l),
+                ("lse", _p)]
 
 
 class MoEError(RuntimeError):
@@ -130,6 +156,23 @@ def lib(build_if_missing: bool = True):
         L.moe_gemv.restype = ci
         L.moe_gemv_get_status.argtypes = []
         L.moe_gemv_get_status.restype = ci
+        i64 = ctypes.c_int64
+        L.moe_qk_norm_rope.argtypes = [ctypes.POINTER(moe_qk_norm_rope_args_t), vp]
+        L.moe_qk_norm_rope.restype = ci
+        L.moe_attn_create.argtypes = [ci, ci, ci]
+        L.moe_attn_create.restype = vp
+        L.moe_attn_forward.argtypes = [vp, ctypes.POINTER(moe_attn_args_t), vp]
+        L.moe_attn_forward.restype = ci
+        L.moe_attn_get_status.argtypes = [vp]
+        L.moe_attn_get_status.restype = ci
+        L.moe_attn_destroy.argtypes = [vp]
+        L.moe_attn_destroy.restype = None
+        L.moe_copy_pages.argtypes = [vp, vp, ci, i64, i64, i64, i64, ci, i64, vp, vp, ci, vp]
+        L.moe_copy_pages.restype = ci
+        L.moe_copy_rows.argtypes = [vp, vp, ci, i64, i64, i64, i64, ci, ci, i64, vp, vp, ci, vp]
+        L.moe_copy_rows.restype = ci
+        L.moe_sample.argtypes = [vp, i64, ci, ci, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.moe_sample.restype = ci
         L.moe_last_error.argtypes = []
         L.moe_last_error.restype = ctypes.c_char_p
         _lib = L
