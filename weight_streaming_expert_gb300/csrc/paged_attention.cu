@@ -1,29 +1,58 @@
 // paged_attention.cu -- attention of a chunk of new tokens over a paged cache
-// (include/attention.h).
+// (include/attention.h), on the fifth-generation tensor cores.
 //
-// One warp per (token, query head) walks the positions it sees with a running
-// maximum and sum.
+// For a query row q (one token, one head) over the positions it sees:
+//   s_j = q.k_j,  m = max_j s_j,  p_j = 2^(c (s_j - m)) with c = scale log2 e,
+//   out = sum_j p_j v_j / sum_j p_j,
+// in one pass over the positions with a running m: when m grows, what was
+// summed so far is multiplied by 2^(c (m_old - m_new)).  Any m gives the same
+// quotient, so the sums are only rescaled when m has grown by a factor of more
+// than 2^8 in p (p then stays below 2^8: exact enough in fp32 sums, and in
+// range for 16-bit probabilities); most rows rescale once or twice in all.
+//
+// A tile is 128 query rows: the chunk's tokens times the heads that share a
+// key/value head, so that a page is read once for all of them.  Per 128
+// positions one warp issues S = Q K^T into TMEM (128 x 128 fp32), four warps
+// turn S into probabilities, one row a thread with no exchange between
+// threads, and write them over S as the 16-bit A operand of O += P V, which
+// stays in TMEM.  Two such chains run in turn, so that one's products cover
+// the other's exponentials:
+//   pair   two tiles of rows over the same positions (chunks of many rows);
+//   split  one tile, the even 128 positions in one chain and the odd ones in
+//          the other, merged at the end (chunks of up to 128 rows, which are
+//          bound by reading the cache).
+// One warp copies the pages with TMA into a ring of 128-position tiles.
+//
+// The work is a list of (sequence, key/value head, tile of rows, 128
+// positions) in that order.  Every CTA takes an equal contiguous share of it,
+// computed on the device from the lengths that the call finds there: one long
+// sequence spreads over all SMs, many short ones share an SM, and a captured
+// graph adapts to lengths that change.  A tile that a boundary cuts leaves
+// unnormalised sums with their m; a second, small kernel joins them in a fixed
+// order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "attention.h"
 #include "host_util.cuh"
+#include "tcgen05.cuh"
 
 namespace wse {
 namespace {
 
 enum : int { kAttnBadPage = 1, kAttnBadLength = 2, kAttnTimeout = 4 };
 
-template <typename T>
-__device__ __forceinline__ float2 unpack(uint32_t v);
-template <>
-__device__ __forceinline__ float2 unpack<__nv_bfloat16>(uint32_t v) {
-  return make_float2(bf16lo(v), bf16hi(v));
-}
-template <>
-__device__ __forceinline__ float2 unpack<__half>(uint32_t v) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&v));
-}
+constexpr int kTile = 128;                 // query rows of a tile, and positions
+constexpr int kAttnThreads = 320;          // two softmax warpgroups, the MMA warp, the copy warp
+constexpr int kMmaWarp = 8, kCopyWarp = 9;
+constexpr int kMaxBatch = 4096;
+constexpr int kMaxStages = 10;
+constexpr uint32_t kHeadBytes = 2048;      // barriers, plan and the exchange area before the tiles
+constexpr float kRescaleLog2 = 8.f;
+constexpr int kJoinThreads = 128, kJoinSplit = 16;
+
 template <typename T>
 __device__ __forceinline__ uint32_t pack(float x, float y);
 template <>
@@ -36,71 +65,683 @@ __device__ __forceinline__ uint32_t pack<__half>(float x, float y) {
   const __half2 v = __floats2half2_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A tile that was cut at the end of CTA c's share: joined from its partial
+// sums in CTAs c, c + 1, .., c + parts - 1 (0: no such tile).
+struct Cut {
+  int parts, b, h, tile;
+};
 
 struct AttnParams {
   moe_attn_args_t a;
-  int n_heads, n_kv_heads;
+  int n_kv_heads, group;
   int* status;
+  float* part_o;    // [CTAs][2][D / 4][rows of an item] float4: unnormalised sums
+  float2* part_ml;  // [CTAs][2][rows of an item]: (m, sum of p)
+  Cut* cuts;        // [CTAs]
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p) {
-  constexpr int kWords = D / 64;  // 32-bit words of a lane
+// One sequence as the kernel takes it: lengths that do not fit are cut.
+struct Seq {
+  int q0, n, kv, base, rows;  // first new token, their count, positions, those before the chunk, query rows
+  bool bad;
+};
+__device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
   const moe_attn_args_t& a = p.a;
-  const int lane = threadIdx.x & 31;
+  Seq s;
+  const int q0 = a.q_starts[b], q1 = a.q_starts[b + 1], kv = a.kv_lens[b];
+  const long long room = (long long)a.table_stride * a.page_size;
+  s.q0 = max(0, min(q0, a.n_tokens));
+  s.n = max(0, min(min(q1, a.n_tokens) - s.q0, a.max_q_len));
+  s.kv = (int)max(0ll, min((long long)kv, room));
+  s.bad = s.q0 != q0 || (long long)s.n != (long long)q1 - q0 || s.kv != kv;
+  // the chunk's place goes by the lengths as given; what was cut is hidden
+  const long long base = (long long)kv - ((long long)q1 - q0);
+  s.base = (int)max(-(1ll << 30), min(base, 1ll << 30));
+  s.rows = s.n * p.group;
+  return s;
+}
+// 128-position tiles that row tile i of a sequence visits (at least one, which
+// writes the zeros of rows that see nothing).
+template <int kRows>
+__device__ __forceinline__ int units_of(const AttnParams& p, const Seq& s, int i) {
+  const int last = (min(s.rows, (i + 1) * kRows) - 1) / p.group;
+  const int end = p.a.tree_mask ? s.kv : min(s.kv, max(0, s.base + last + 1));
+  return max(1, (end + kTile - 1) / kTile);
+}
+
+// A CTA's next piece of work.
+struct Item {
+  int b, h, tile, u0, u1, units;
+  Seq s;
+};
+
+struct Plan {
+  long long total, start, todo;  // of the whole list; where this CTA's share begins, and its length
+  int parts;                     // CTAs with a share (each at least one unit)
+  int b, h, tile, u0;
+};
+
+template <int kRows>
+struct Walk {
+  const AttnParams& p;
+  int b, h, tile, u0;
+  long long todo;
+  Seq s;
+  int loaded;
+  __device__ Walk(const AttnParams& p_, const Plan& plan)
+      : p(p_), b(plan.b), h(plan.h), tile(plan.tile), u0(plan.u0), todo(plan.todo), loaded(-1) {}
+  __device__ bool next(Item& it) {
+    if (todo <= 0) return false;
+    for (;;) {
+      if (loaded != b) {
+        s = load_seq(p, b);
+        loaded = b;
+      }
+      if (tile * kRows < s.rows) break;
+      tile = 0;
+      if (s.rows > 0 && ++h < p.n_kv_heads) continue;
+      h = 0;
+      ++b;
+    }
+    it.b = b, it.h = h, it.tile = tile, it.s = s;
+    it.units = units_of<kRows>(p, s, tile);
+    it.u0 = u0;
+    it.u1 = (int)min((long long)it.units, u0 + todo);
+    todo -= it.u1 - it.u0;
+    u0 = 0;
+    ++tile;
+    return true;
+  }
+};
+
+// Waits with a limit.  The first that runs out sets the CTA's flag, after
+// which no wait of the CTA waits any more: every role walks to its end (its
+// addresses never depend on data that a wait guards, only on the plan).
+struct Waiter {
+  volatile int* gone;
+  int* status;
+  __device__ void operator()(uint32_t bar, uint32_t parity) const {
+    if (mbar_try_wait(bar, parity)) return;
+    if (*gone) return;
+    unsigned long long waited;
+    // in slices, so that a wait ends soon after another one has given up
+    for (int i = 0; i < 200; ++i) {
+      if (mbar_wait(bar, parity, &waited, kWaitTimeoutNs / 200)) return;
+      if (*gone) return;
+    }
+    *gone = 1;
+    atomicOr(status, kAttnTimeout);
+  }
+};
+
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+template <int D, bool kPair>
+struct Layout {
+  static constexpr uint32_t kTileBytes = kTile * D * 2;          // one tile of Q, K or V
+  static constexpr int kQTiles = kPair ? 2 : 1;
+  static constexpr int kRows = kQTiles * kTile;                   // query rows of an item
+  static constexpr int kFit = (int)((232448 - 1024 - kHeadBytes) / kTileBytes) - kQTiles;
+  static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
+  static constexpr uint32_t kSmem = 1024 + kHeadBytes + (kQTiles + kStages) * kTileBytes;
+};
+
+template <typename T, int D, bool kPair>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    paged_attention_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap k_map,
+                           const __grid_constant__ CUtensorMap v_map) {
+  using L = Layout<D, kPair>;
+  constexpr int kRows = L::kRows, kStages = L::kStages;
+  constexpr uint32_t kTileBytes = L::kTileBytes, kPanel = kTile * 128;
+  extern __shared__ uint8_t raw_smem[];
+  uint8_t* smem = raw_smem + (1024 - (smem_u32(raw_smem) & 1023)) % 1024;
+  const uint32_t sb = smem_u32(smem);
+  auto full = [&](int s) { return sb + 8u * s; };
+  auto empty = [&](int s) { return sb + 80u + 8u * s; };
+  auto q_full = [&](int t) { return sb + 160u + 8u * t; };
+  auto s_full = [&](int t) { return sb + 176u + 8u * t; };
+  auto p_full = [&](int t) { return sb + 192u + 8u * t; };
+  auto o_full = [&](int t) { return sb + 208u + 8u * t; };
+  const uint32_t drained = sb + 224u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + 232);
+  int* gone = reinterpret_cast<int*>(smem + 236);
+  Plan& plan = *reinterpret_cast<Plan*>(smem + 256);
+  float2* exchange = reinterpret_cast<float2*>(smem + 1024);        // [128]: the odd chain's (m, sum)
+  const uint32_t q_at = sb + kHeadBytes, ring = q_at + L::kQTiles * kTileBytes;
+  uint8_t* q_smem = smem + kHeadBytes;
+  uint8_t* ring_smem = q_smem + L::kQTiles * kTileBytes;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const moe_attn_args_t& a = p.a;
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(q_full(t), kPair ? 4 : 8);
+      mbar_init(s_full(t), 1);
+      mbar_init(p_full(t), 4);
+      mbar_init(o_full(t), 1);
+    }
+    mbar_init(drained, 1);
+    fence_mbar_init();
+    *gone = 0;
+  }
+  if (warp == kMmaWarp) tmem_alloc(smem_u32(tmem_slot), 512);
+  if (warp == kCopyWarp && lane == 0) {
+    tma_prefetch_map(&k_map);
+    tma_prefetch_map(&v_map);
+  }
   pdl_wait();
   pdl_launch_dependents();
-  const long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (unit >= (long long)a.n_tokens * p.n_heads) return;
-  const int t = (int)(unit / p.n_heads), h = (int)(unit % p.n_heads), kvh = h / (p.n_heads / p.n_kv_heads);
-  int b = 0;
-  while (b < a.batch && a.q_starts[b + 1] <= t) ++b;
-  if (b == a.batch || t < a.q_starts[0]) return;
-  const int n = a.q_starts[b + 1] - a.q_starts[b], i = t - a.q_starts[b];
-  int kv = a.kv_lens[b];
-  const long long room = (long long)a.table_stride * a.page_size;
-  if (kv < 0 || kv > room) {
-    if (lane == 0) atomicOr(p.status, kAttnBadLength);
-    kv = kv < 0 ? 0 : (int)room;
-  }
-  const int base = kv - n;
-  const long long bits = a.tree_mask ? a.tree_mask[t] : 0;
-  const int end = a.tree_mask ? kv : min(kv, base + i + 1);
-  const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.q) + t * a.q_token_stride +
-                                                        h * a.q_head_stride) + lane * kWords;
-  float2 qv[kWords], acc[kWords];
-  for (int w = 0; w < kWords; ++w) qv[w] = unpack<T>(q[w]), acc[w] = make_float2(0.f, 0.f);
-  float m = -INFINITY, l = 0.f;
-  for (int j = 0; j < end; ++j) {
-    if (a.tree_mask && j >= base && !((bits >> min(63, j - base)) & 1)) continue;
-    const int page = a.block_table[(long long)b * a.table_stride + j / a.page_size];
-    const bool bad = (unsigned)page >= (unsigned)a.n_pages;
-    if (bad && lane == 0) atomicOr(p.status, kAttnBadPage);
-    const long long off = j % a.page_size;
-    const uint32_t* kp = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.k_cache) + page * a.k_page_stride +
-                                                           off * a.k_row_stride + kvh * D) + lane * kWords;
-    const uint32_t* vp = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.v_cache) + page * a.v_page_stride +
-                                                           off * a.v_row_stride + kvh * D) + lane * kWords;
-    float s = 0.f;
-    float2 v[kWords];
-    for (int w = 0; w < kWords; ++w) {
-      const float2 kx = unpack<T>(bad ? 0u : kp[w]);
-      v[w] = unpack<T>(bad ? 0u : vp[w]);
-      s = fmaf(qv[w].x, kx.x, fmaf(qv[w].y, kx.y, s));
+
+  // ---- the plan: cost of each sequence (of one key/value head), their prefix
+  // sums, and where this CTA's share begins
+  long long* cost = reinterpret_cast<long long*>(ring_smem);  // the ring is not in use yet
+  {
+    // sequences of few row tiles: one thread each; of many: one warp each
+    const bool wide = (a.max_q_len * p.group + kRows - 1) / kRows > 4;
+    const int step = wide ? kAttnThreads / 32 : kAttnThreads;
+    for (int b = wide ? warp : tid; b < a.batch; b += step) {
+      const Seq s = load_seq(p, b);
+      if (s.bad && (!wide || lane == 0) && blockIdx.x == 0) atomicOr(p.status, kAttnBadLength);
+      long long sum = 0;
+      const int tiles = (s.rows + kRows - 1) / kRows;
+      for (int i = wide ? lane : 0; i < tiles; i += wide ? 32 : 1) sum += units_of<kRows>(p, s, i);
+      if (wide) {
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+      }
+      if (!wide || lane == 0) cost[b] = sum;
     }
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    s *= a.scale;
-    const float top = fmaxf(m, s);
-    const float was = m == -INFINITY ? 0.f : __expf(m - top), e = s == -INFINITY ? 0.f : __expf(s - top);
-    l = l * was + e;
-    for (int w = 0; w < kWords; ++w) acc[w].x = acc[w].x * was + e * v[w].x, acc[w].y = acc[w].y * was + e * v[w].y;
-    m = top;
+    __syncthreads();
+    if (warp == 0) {
+      // lane l: sequences [l * per, (l + 1) * per)
+      const int per = (a.batch + 31) / 32;
+      const int b0 = min(a.batch, lane * per), b1 = min(a.batch, b0 + per);
+      long long sum = 0;
+      for (int b = b0; b < b1; ++b) sum += cost[b];
+      long long upto = sum;
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, upto, m);
+        if (lane >= m) upto += o;
+      }
+      const long long total = __shfl_sync(0xffffffffu, upto, 31) * p.n_kv_heads;
+      const int parts = (int)min((long long)gridDim.x, total), c = min((int)blockIdx.x, parts);
+      const long long start = parts ? total * c / parts : 0;
+      const long long end = c < parts ? total * (c + 1) / parts : start;
+      if (lane == 0) {
+        plan.total = total;
+        plan.start = start;
+        plan.todo = end - start;
+        plan.parts = parts;
+      }
+      long long at = (upto - sum) * p.n_kv_heads;
+      if (end > start && start >= at && start < upto * p.n_kv_heads) {  // one lane
+        int b = b0;
+        while (start >= at + cost[b] * p.n_kv_heads) at += cost[b++] * p.n_kv_heads;
+        const Seq s = load_seq(p, b);
+        long long rest = (start - at) % cost[b];
+        int tile = 0;
+        for (int u; rest >= (u = units_of<kRows>(p, s, tile)); ++tile) rest -= u;
+        plan.b = b;
+        plan.h = (int)((start - at) / cost[b]);
+        plan.tile = tile;
+        plan.u0 = (int)rest;
+      }
+    }
+    fence_proxy_async_smem();  // the plan's scratch becomes the ring
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
   }
-  uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + t * a.out_token_stride + h * a.out_head_stride) +
-                lane * kWords;
-  const float r = l > 0.f ? 1.f / l : 0.f;
-  for (int w = 0; w < kWords; ++w) o[w] = pack<T>(acc[w].x * r, acc[w].y * r);
-  if (a.lse && lane == 0) a.lse[unit] = l > 0.f ? m + logf(l) : -INFINITY;
+  const uint32_t tmem = *tmem_slot;
+  const Waiter wait{gone, p.status};
+  if (tid == 0) p.cuts[blockIdx.x].parts = 0;
+  Walk<kRows> walk(p, plan);
+  Item it{};
+
+  if (warp == kCopyWarp) {
+    // ---- copies: per 128 positions one box per page and 64 columns, a lane each
+    constexpr int kHalves = D / 64;
+    const int box_rows = min(a.page_size, kTile), per_tile = kTile / box_rows;
+    const int box = lane / kHalves, half = lane % kHalves;
+    int filled = 0;
+    auto load = [&](const CUtensorMap* map, int u) {
+      const int stage = filled % kStages, round = filled / kStages;
+      const int pos = u * kTile + box * box_rows;
+      const bool mine = box < per_tile && pos < it.s.kv;
+      int page = 0;
+      if (mine) page = a.block_table[(long long)it.b * a.table_stride + pos / a.page_size];
+      if (mine && (unsigned)page >= (unsigned)a.n_pages) {
+        atomicOr(p.status, kAttnBadPage);
+        page = a.n_pages;  // outside the tensor: reads as zeros
+      }
+      if (round > 0) wait(empty(stage), (round - 1) & 1);
+      const unsigned boxes = __popc(__ballot_sync(0xffffffffu, mine));
+      if (lane == 0) mbar_arrive_expect_tx(full(stage), boxes * box_rows * 128u);
+      __syncwarp();
+      if (mine)
+        tma_load_3d(ring + stage * kTileBytes + half * kPanel + box * box_rows * 128, map, it.h * D + half * 64,
+                    pos % a.page_size, page, full(stage));
+      ++filled;
+    };
+    while (walk.next(it)) {
+      const int n = it.u1 - it.u0;
+      if (kPair) {
+        for (int j = 0; j < n; ++j) {
+          load(&k_map, it.u0 + j);
+          load(&v_map, it.u0 + j);
+        }
+      } else {
+        load(&k_map, it.u0);
+        if (n > 1) load(&k_map, it.u0 + 1);
+        for (int j = 0; j < n; ++j) {
+          load(&v_map, it.u0 + j);
+          if (j + 2 < n) load(&k_map, it.u0 + j + 2);
+        }
+      }
+    }
+    // no copy is in flight when the CTA ends, also after a wait has given up
+    for (int f = max(0, filled - kStages); f < filled; ++f) {
+      unsigned long long waited;
+      mbar_wait(full(f % kStages), (f / kStages) & 1, &waited);
+    }
+  } else if (warp == kMmaWarp) {
+    // ---- products, issued by lane 0
+    constexpr uint32_t kDescS = mma_desc(std::is_same<T, __nv_bfloat16>::value, false, kTile, kTile);
+    constexpr uint32_t kDescO = mma_desc(std::is_same<T, __nv_bfloat16>::value, true, kTile, D);
+    int taken = 0, q_round = 0, p_round[2] = {0, 0};
+    auto next_stage = [&]() {
+      const int stage = taken % kStages;
+      wait(full(stage), (taken / kStages) & 1);
+      ++taken;
+      return stage;
+    };
+    auto scores = [&](int chain, int q_tile, int stage) {
+      if (lane == 0) {
+        const uint32_t qa = q_at + q_tile * kTileBytes, ka = ring + stage * kTileBytes;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k / 4) * kPanel + (k % 4) * 32;
+          mma_ss(tmem + chain * kTile, smem_desc(qa + off, 16, 1024), smem_desc(ka + off, 16, 1024), kDescS, k > 0);
+        }
+        mma_commit(s_full(chain));
+      }
+    };
+    auto products = [&](int chain, int stage, bool add) {
+      wait(p_full(chain), p_round[chain]++ & 1);
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t va = ring + stage * kTileBytes;
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          mma_ts(tmem + 2 * kTile + chain * D, tmem + chain * kTile + k * 8, smem_desc(va + k * 2048, kPanel, 1024),
+                 kDescO, add || k > 0);
+        mma_commit(o_full(chain));
+      }
+    };
+    auto release = [&](int stage) {
+      if (lane == 0) mma_commit(empty(stage));
+    };
+    // Rows of the cache past the sequence's end hold anything, and 0 * NaN is
+    // NaN: they become zeros.
+    auto value_stage = [&](int u) {
+      const int stage = next_stage(), valid = max(0, it.s.kv - u * kTile);
+      if (valid < kTile) {
+        uint8_t* v = ring_smem + stage * kTileBytes;
+        for (int i = lane; i < (kTile - valid) * (D / 8); i += 32) {
+          const int row = valid + i / (D / 8), c = i % (D / 8);
+          *reinterpret_cast<uint4*>(v + (c / 8) * kPanel + row * 128 + (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      return stage;
+    };
+    while (walk.next(it)) {
+      const int n = it.u1 - it.u0;
+      wait(q_full(0), q_round & 1);
+      if (kPair) {
+        int ks = next_stage();
+        tc_fence_after();
+        scores(0, 0, ks);
+        wait(q_full(1), q_round & 1);
+        scores(1, 1, ks);
+        release(ks);
+        for (int j = 0; j < n; ++j) {
+          const int vs = value_stage(it.u0 + j);
+          products(0, vs, j > 0);
+          if (j + 1 < n) {
+            ks = next_stage();
+            scores(0, 0, ks);
+          }
+          products(1, vs, j > 0);
+          release(vs);
+          if (j + 1 < n) {
+            scores(1, 1, ks);
+            release(ks);
+          }
+        }
+      } else {
+        for (int j = 0; j < min(n, 2); ++j) {
+          const int ks = next_stage();
+          tc_fence_after();
+          scores(j, 0, ks);
+          release(ks);
+        }
+        for (int j = 0; j < n; ++j) {
+          const int vs = value_stage(it.u0 + j);
+          products(j & 1, vs, j > 1);
+          release(vs);
+          if (j + 2 < n) {
+            const int ks = next_stage();
+            scores(j & 1, 0, ks);
+            release(ks);
+          }
+        }
+      }
+      ++q_round;
+    }
+    if (lane == 0) mma_commit(drained);
+    unsigned long long waited;
+    mbar_wait(drained, 0, &waited);
+    __syncwarp();
+  } else {
+    // ---- softmax: chain 0 in warps 0-3, chain 1 in warps 4-7, a row per thread
+    const int chain = warp >> 2, r = tid & 127;
+    const int q_tile = kPair ? chain : 0;
+    const uint32_t lane_at = (uint32_t)(warp & 3) << 21;  // TMEM lane 32 * (warp % 4)
+    const uint32_t s_at = tmem + lane_at + chain * kTile, o_at = tmem + lane_at + 2 * kTile + chain * D;
+    const float c = a.scale * 1.4426950408889634f;  // exponents in base 2
+    const float rescale = kRescaleLog2 / c;
+    int s_round = 0, o_round[2] = {0, 0};  // products finished or under way, of both chains
+    while (walk.next(it)) {
+      const int row0 = it.tile * kRows + q_tile * kTile;
+      // queries into shared memory, each 16-byte chunk a thread; rows past the
+      // last become zeros
+      {
+        constexpr int kChunks = D / 8;
+        constexpr int kLoaders = kPair ? 128 : 256;
+        const int loader = kPair ? r : tid;
+        const int cc = loader % kChunks;
+        uint8_t* dst = q_smem + q_tile * kTileBytes + (cc / 8) * kPanel;
+#pragma unroll 8
+        for (int row = loader / kChunks; row < kTile; row += kLoaders / kChunks) {
+          const int g = row0 + row;
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (g < it.s.rows) {
+            const int token = g / p.group, head = it.h * p.group + g % p.group;
+            v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
+                                                (long long)(it.s.q0 + token) * a.q_token_stride +
+                                                head * a.q_head_stride + cc * 8);
+          }
+          *reinterpret_cast<uint4*>(dst + row * 128 + ((cc % 8) ^ (row % 8)) * 16) = v;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full(kPair ? chain : 0));
+      }
+      const int g = row0 + r;
+      const bool valid = g < it.s.rows;
+      const bool warp_valid = row0 + (r & ~31) < it.s.rows;
+      const int token = valid ? g / p.group : 0;
+      // positions below `plain` are seen, from `end` on hidden, between them
+      // the tree's bits decide
+      const unsigned long long bits = a.tree_mask && valid ? (unsigned long long)a.tree_mask[it.s.q0 + token] : 0ull;
+      const int end = !valid ? 0 : a.tree_mask ? it.s.kv : min(it.s.kv, max(0, it.s.base + token + 1));
+      const int plain = a.tree_mask ? max(0, min(it.s.base, end)) : end;
+      float m = -INFINITY, l = 0.f;
+      const int first = kPair ? it.u0 : it.u0 + chain, step = kPair ? 1 : 2;
+      int done = 0;
+      for (int u = first; u < it.u1; u += step) {
+        wait(s_full(chain), s_round++ & 1);
+        tc_fence_after();
+        if (warp_valid) {
+          uint32_t s[kTile];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, s + 32 * i);
+          tmem_wait_ld();
+          const int left = plain - u * kTile;  // columns below it are seen
+          if (__any_sync(0xffffffffu, left < kTile)) {
+            if (a.tree_mask) {
+              const int cut = end - u * kTile;
+#pragma unroll
+              for (int i = 0; i < kTile; ++i) {
+                const int bit = i - (it.s.base - u * kTile);
+                const bool seen = i < left || (i < cut && bit >= 0 && ((bits >> (bit & 63)) & 1));
+                if (!seen) s[i] = 0xff800000u;
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < kTile; ++i)
+                if (i >= left) s[i] = 0xff800000u;
+            }
+          }
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < kTile; ++i) top[i & 3] = fmaxf(top[i & 3], __uint_as_float(s[i]));
+          const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+          float shrink = 1.f;
+          if (high > m + rescale || m == -INFINITY) {
+            if (m != -INFINITY) shrink = exp2_approx((m - high) * c);
+            m = high;
+          }
+          if (done > 0 && __any_sync(0xffffffffu, shrink != 1.f)) {
+            // the products so far have to be in before their sums shrink
+            wait(o_full(chain), (o_round[chain] + done - 1) & 1);
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+              uint32_t o[32];
+              tmem_ld32(o_at + 32 * i, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * shrink);
+              tmem_st32(o_at + 32 * i, o);
+            }
+            l *= shrink;
+          }
+          const float off = m == -INFINITY ? 0.f : m * c;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t packed[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float x = exp2_approx(fmaf(__uint_as_float(s[32 * i + 2 * k]), c, -off));
+              const float y = exp2_approx(fmaf(__uint_as_float(s[32 * i + 2 * k + 1]), c, -off));
+              sum[(2 * k) & 3] += x;
+              sum[(2 * k + 1) & 3] += y;
+              packed[k] = pack<T>(x, y);
+            }
+            tmem_st16(s_at + 16 * i, packed);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_wait_st();
+        }
+        ++done;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(chain));
+      }
+      // ---- the end of the item
+      const int n = it.u1 - it.u0;
+      int count[2];
+      count[0] = kPair ? n : (n + 1) / 2;
+      count[1] = kPair ? n : n / 2;
+      const bool cut = n < it.units;
+      const int slot = 2 * blockIdx.x + (it.u0 == 0 ? 1 : 0);
+      const int local = kPair ? chain * kTile + r : r;  // row of the item
+      float f0 = 1.f, f1 = 0.f;
+      if (!kPair) {
+        // both chains' (m, l): the odd one's through shared memory, the even
+        // one's back; then each chain's warps write half of the columns
+        if (chain == 1) exchange[r] = make_float2(m, l);
+        named_sync(1, 256);
+        const float2 odd = exchange[r];
+        named_sync(1, 256);
+        if (chain == 0) exchange[r] = make_float2(m, l);
+        named_sync(1, 256);
+        const float2 even = exchange[r];
+        m = fmaxf(even.x, odd.x);
+        f0 = even.x == -INFINITY ? 0.f : exp2_approx((even.x - m) * c);
+        f1 = odd.x == -INFINITY ? 0.f : exp2_approx((odd.x - m) * c);
+        l = even.y * f0 + odd.y * f1;
+      }
+      for (int t = 0; t < 2; ++t)
+        if ((!kPair || t == chain) && count[t] > 0) wait(o_full(t), (o_round[t] + count[t] - 1) & 1);
+      o_round[0] += count[0];
+      o_round[1] += count[1];
+      tc_fence_after();
+      if (warp_valid) {
+        const float norm = cut ? 1.f : (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
+        constexpr int kBlocks = kPair ? D / 32 : D / 64;  // 32-column blocks of this warp
+        const int block0 = kPair ? 0 : chain * kBlocks;
+        const uint32_t even_at = tmem + lane_at + 2 * kTile + (kPair ? chain * D : 0);
+        T* out = static_cast<T*>(a.out) + (long long)(it.s.q0 + token) * a.out_token_stride +
+                 (it.h * p.group + (valid ? g % p.group : 0)) * a.out_head_stride;
+        float4* part = reinterpret_cast<float4*>(p.part_o) + (long long)slot * (D / 4) * kRows + local;
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) {
+          uint32_t o[32];
+          tmem_ld32(even_at + 32 * (block0 + i), o);
+          tmem_wait_ld();
+          if (!kPair && count[1] > 0) {
+            uint32_t o1[32];
+            tmem_ld32(even_at + D + 32 * (block0 + i), o1);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              o[k] = __float_as_uint((f0 != 0.f ? __uint_as_float(o[k]) * f0 : 0.f) +
+                                     (f1 != 0.f ? __uint_as_float(o1[k]) * f1 : 0.f));
+          }
+          if (!valid) continue;
+          if (cut) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              part[(long long)(8 * (block0 + i) + k) * kRows] =
+                  make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]), __uint_as_float(o[4 * k + 2]),
+                              __uint_as_float(o[4 * k + 3]));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint4 v;
+              uint32_t* w = &v.x;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                w[j] = pack<T>(__uint_as_float(o[8 * k + 2 * j]) * norm, __uint_as_float(o[8 * k + 2 * j + 1]) * norm);
+              *reinterpret_cast<uint4*>(out + 32 * (block0 + i) + 8 * k) = v;
+            }
+          }
+        }
+        if (valid && (kPair || chain == 0)) {
+          if (cut)
+            p.part_ml[(long long)slot * kRows + local] = make_float2(m, l);
+          else if (a.lse)
+            a.lse[(long long)(it.s.q0 + token) * (p.group * p.n_kv_heads) + it.h * p.group + g % p.group] =
+                l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f;
+        }
+      }
+      if (cut && it.u0 == 0 && tid == 0) {
+        // this share ends inside the tile: which CTA's share holds its last unit
+        const long long last = plan.start + (plan.todo - walk.todo) - n + it.units;  // the tile's end in the list
+        const long long e = (last * plan.parts + plan.total - 1) / plan.total - 1;
+        p.cuts[blockIdx.x] = Cut{(int)(e - blockIdx.x) + 1, it.b, it.h, it.tile};
+      }
+      if (!kPair) named_sync(1, 256);  // both chains' sums are read before the next item's
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_free(tmem, 512);
+}
+
+// Joins the tiles that shares have cut: out = sum_i O_i 2^(c (m_i - m)) / sum_i
+// l_i 2^(c (m_i - m)) in the order of the shares.  Block (c, y): the tile that
+// was cut at the end of share c, 32 rows by 16 columns at a time.
+template <typename T, int D, int kRows>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnParams p) {
+  const moe_attn_args_t& a = p.a;
+  pdl_wait();
+  pdl_launch_dependents();
+  const Cut cut = p.cuts[blockIdx.x];
+  if (cut.parts == 0) return;
+  const Seq s = load_seq(p, cut.b);
+  const int rows = min(kRows, s.rows - cut.tile * kRows);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float c = a.scale * 1.4426950408889634f;
+  auto slot = [&](int i) { return 2ll * (blockIdx.x + i) + (i == 0 ? 1 : 0); };
+  for (int w = blockIdx.y; w < (rows + 31) / 32 * (D / 16); w += gridDim.y) {
+    const int row = w / (D / 16) * 32 + lane, d4 = w % (D / 16) * 4 + warp;
+    if (row >= rows) continue;
+    float m = -INFINITY;
+#pragma unroll 4
+    for (int i = 0; i < cut.parts; ++i) m = fmaxf(m, p.part_ml[slot(i) * kRows + row].x);
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int i = 0; i < cut.parts; ++i) {
+      const float2 ml = p.part_ml[slot(i) * kRows + row];
+      const float4 v = reinterpret_cast<const float4*>(p.part_o)[(slot(i) * (D / 4) + d4) * kRows + row];
+      const float f = ml.x == -INFINITY ? 0.f : exp2_approx((ml.x - m) * c);
+      l += ml.y * f;
+      o.x += v.x * f;
+      o.y += v.y * f;
+      o.z += v.z * f;
+      o.w += v.w * f;
+    }
+    const float norm = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    const int g = cut.tile * kRows + row, token = g / p.group, head = cut.h * p.group + g % p.group;
+    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (long long)(s.q0 + token) * a.out_token_stride +
+                              head * a.out_head_stride + d4 * 4) =
+        make_uint2(pack<T>(o.x * norm, o.y * norm), pack<T>(o.z * norm, o.w * norm));
+    if (a.lse && d4 == 0)
+      a.lse[(long long)(s.q0 + token) * (p.group * p.n_kv_heads) + head] =
+          l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
+using MapEncode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+MapEncode map_encode() {
+  static const MapEncode fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess)
+      f = nullptr;
+    return reinterpret_cast<MapEncode>(f);
+  }();
+  return fn;
+}
+
+// The cache of one layer as (columns of all heads, rows of a page, pages);
+// a box: 64 columns of one page's rows (128 of a longer page).
+int encode_cache(CUtensorMap* map, const moe_attn_args_t& a, const void* base, int64_t row_stride,
+                 int64_t page_stride, int columns) {
+  const MapEncode encode = map_encode();
+  if (!encode) return fail(MOE_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
+  const cuuint64_t dims[3] = {(cuuint64_t)columns, (cuuint64_t)a.page_size, (cuuint64_t)a.n_pages};
+  const cuuint64_t strides[2] = {(cuuint64_t)row_stride * 2, (cuuint64_t)page_stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)(a.page_size < kTile ? a.page_size : kTile), 1};
+  const cuuint32_t steps[3] = {1, 1, 1};
+  const CUresult r = encode(
+      map, a.dtype == MOE_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+      const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MOE_OK : fail(MOE_ERR_INVALID_ARG, "no tensor map for this cache (driver error %d)", (int)r);
 }
 
 }  // namespace
@@ -109,9 +750,53 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const AttnParams p
 using namespace wse;
 
 struct moe_attn {
-  int n_heads, n_kv_heads, head_dim;
-  int* status;
+  int n_heads = 0, n_kv_heads = 0, head_dim = 0, n_sms = 0;
+  int* status = nullptr;
+  float* part_o = nullptr;
+  float2* part_ml = nullptr;
+  Cut* cuts = nullptr;
 };
+
+namespace {
+
+void free_attn(moe_attn* h) {
+  cudaFree(h->status);
+  cudaFree(h->part_o);
+  cudaFree(h->part_ml);
+  cudaFree(h->cuts);
+  delete h;
+}
+
+template <typename T, int D, bool kPair>
+cudaError_t allow_smem() {
+  return cudaFuncSetAttribute(paged_attention_kernel<T, D, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)Layout<D, kPair>::kSmem);
+}
+template <typename T, int D>
+cudaError_t allow_smem_both() {
+  const cudaError_t e = allow_smem<T, D, true>();
+  return e != cudaSuccess ? e : allow_smem<T, D, false>();
+}
+
+template <typename T, int D, bool kPair>
+int launch_attn(const moe_attn* h, const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v,
+                moe_stream_t stream) {
+  using L = Layout<D, kPair>;
+  const int rc = launch_pdl(paged_attention_kernel<T, D, kPair>, dim3(h->n_sms), dim3(kAttnThreads), L::kSmem, stream,
+                            1, p, k, v);
+  if (rc != MOE_OK) return rc;
+  return launch_pdl(join_kernel<T, D, L::kRows>, dim3(h->n_sms, kJoinSplit), dim3(kJoinThreads), 0, stream, 1, p);
+}
+
+template <typename T, int D>
+int launch_attn(const moe_attn* h, const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v,
+                moe_stream_t stream) {
+  // one tile of rows per sequence and key/value head: the split form
+  return (long long)p.a.max_q_len * p.group > kTile ? launch_attn<T, D, true>(h, p, k, v, stream)
+                                                    : launch_attn<T, D, false>(h, p, k, v, stream);
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -125,13 +810,26 @@ moe_attn_t* moe_attn_create(int n_heads, int n_kv_heads, int head_dim) {
     return nullptr;
   }
   if (check_device() != MOE_OK) return nullptr;
-  auto* h = new moe_attn{n_heads, n_kv_heads, head_dim, nullptr};
-  cudaError_t e = cudaMalloc(&h->status, sizeof(int));
+  auto* h = new moe_attn;
+  h->n_heads = n_heads;
+  h->n_kv_heads = n_kv_heads;
+  h->head_dim = head_dim;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->n_sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess)
+    e = head_dim == 64 ? allow_smem_both<__nv_bfloat16, 64>() : allow_smem_both<__nv_bfloat16, 128>();
+  if (e == cudaSuccess) e = head_dim == 64 ? allow_smem_both<__half, 64>() : allow_smem_both<__half, 128>();
+  const size_t rows = (size_t)h->n_sms * 2 * (2 * kTile);  // two partial tiles per CTA, of a pair's rows
+  if (e == cudaSuccess) e = cudaMalloc(&h->status, sizeof(int));
+  if (e == cudaSuccess) e = cudaMalloc(&h->part_o, rows * head_dim * sizeof(float));
+  if (e == cudaSuccess) e = cudaMalloc(&h->part_ml, rows * sizeof(float2));
+  if (e == cudaSuccess) e = cudaMalloc(&h->cuts, h->n_sms * sizeof(Cut));
   if (e == cudaSuccess) e = cudaMemset(h->status, 0, sizeof(int));
   if (e != cudaSuccess) {
-    fail_cuda(e, "attention workspace");
-    cudaFree(h->status);
-    delete h;
+    fail(e == cudaErrorMemoryAllocation ? MOE_ERR_OOM : MOE_ERR_CUDA, "attention workspace: %s", cudaGetErrorString(e));
+    cudaGetLastError();
+    free_attn(h);
     return nullptr;
   }
   return h;
@@ -159,13 +857,20 @@ int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t strea
   if ((a->q_token_stride | a->q_head_stride | a->out_token_stride | a->out_head_stride | a->k_page_stride |
        a->k_row_stride | a->v_page_stride | a->v_row_stride) & 7)
     return fail(MOE_ERR_INVALID_ARG, "every stride must be a multiple of 8 elements (16 bytes)");
-  const AttnParams p{*a, h->n_heads, h->n_kv_heads, h->status};
-  const long long units = (long long)a->n_tokens * h->n_heads;
-  void (*kernel)(const AttnParams) =
-      a->dtype == MOE_DTYPE_BF16
-          ? (h->head_dim == 64 ? paged_attention_kernel<__nv_bfloat16, 64> : paged_attention_kernel<__nv_bfloat16, 128>)
-          : (h->head_dim == 64 ? paged_attention_kernel<__half, 64> : paged_attention_kernel<__half, 128>);
-  return launch_pdl(kernel, dim3((unsigned)((units + 3) / 4)), dim3(128), 0, stream, 1, p);
+  if ((long long)a->n_tokens * (h->n_heads / h->n_kv_heads) > (1 << 30))
+    return fail(MOE_ERR_UNSUPPORTED, "n_tokens = %d is too many", a->n_tokens);
+  if (a->batch > kMaxBatch) return fail(MOE_ERR_UNSUPPORTED, "batch = %d exceeds %d", a->batch, kMaxBatch);
+  CUtensorMap k_map, v_map;
+  int rc = encode_cache(&k_map, *a, a->k_cache, a->k_row_stride, a->k_page_stride, h->n_kv_heads * h->head_dim);
+  if (rc == MOE_OK)
+    rc = encode_cache(&v_map, *a, a->v_cache, a->v_row_stride, a->v_page_stride, h->n_kv_heads * h->head_dim);
+  if (rc != MOE_OK) return rc;
+  const AttnParams p{*a, h->n_kv_heads, h->n_heads / h->n_kv_heads, h->status, h->part_o, h->part_ml, h->cuts};
+  if (a->dtype == MOE_DTYPE_BF16)
+    return h->head_dim == 64 ? launch_attn<__nv_bfloat16, 64>(h, p, k_map, v_map, stream)
+                             : launch_attn<__nv_bfloat16, 128>(h, p, k_map, v_map, stream);
+  return h->head_dim == 64 ? launch_attn<__half, 64>(h, p, k_map, v_map, stream)
+                           : launch_attn<__half, 128>(h, p, k_map, v_map, stream);
 }
 
 int moe_attn_get_status(moe_attn_t* h) {
@@ -186,8 +891,7 @@ int moe_attn_get_status(moe_attn_t* h) {
 void moe_attn_destroy(moe_attn_t* h) {
   if (!h) return;
   cudaDeviceSynchronize();
-  cudaFree(h->status);
-  delete h;
+  free_attn(h);
 }
 
 }  // extern "C"
