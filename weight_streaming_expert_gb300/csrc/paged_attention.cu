@@ -45,7 +45,8 @@ namespace {
 enum : int { kAttnBadPage = 1, kAttnBadLength = 2, kAttnTimeout = 4 };
 
 constexpr int kTile = 128;                 // query rows of a tile, and positions
-constexpr int kAttnThreads = 320;          // two softmax warpgroups, the MMA warp, the copy warp
+constexpr int kAttnThreads = 384;          // two softmax warpgroups; the MMA warp, the copy warp and two idle ones
+constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;  // 2 x 128 x 224 + 128 x 56 = 384 x 168, the launch's total
 constexpr int kMmaWarp = 8, kCopyWarp = 9;
 constexpr int kMaxBatch = 4096;
 constexpr int kMaxStages = 10;
@@ -69,6 +70,31 @@ __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Two fp32 values in one instruction.
+__device__ __forceinline__ uint64_t pair_of(uint32_t x, uint32_t y) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(x), "r"(y));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair_of(float x, float y) {
+  return pair_of(__float_as_uint(x), __float_as_uint(y));
+}
+__device__ __forceinline__ float low_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float high_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  return d;
+}
+__device__ __forceinline__ void max3(float& top, uint32_t x, uint32_t y) {
+  asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(__uint_as_float(x)), "f"(__uint_as_float(y)));
 }
 
 // A tile that was cut at the end of CTA c's share: joined from its partial
@@ -159,6 +185,9 @@ struct Walk {
     return true;
   }
 };
+
+// The n lowest bits of a word (none below 0, all from 32 on).
+__device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
 
 // Waits with a limit.  The first that runs out sets the CTA's flag, after
 // which no wait of the CTA waits any more: every role walks to its end (its
@@ -308,156 +337,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const Waiter wait{gone, p.status};
   if (tid == 0) p.cuts[blockIdx.x].parts = 0;
-  Walk<kRows> walk(p, plan);
-  Item it{};
 
-  if (warp == kCopyWarp) {
-    // ---- copies: per 128 positions one box per page and 64 columns, a lane each
-    constexpr int kHalves = D / 64;
-    const int box_rows = min(a.page_size, kTile), per_tile = kTile / box_rows;
-    const int box = lane / kHalves, half = lane % kHalves;
-    int filled = 0;
-    auto load = [&](const CUtensorMap* map, int u) {
-      const int stage = filled % kStages, round = filled / kStages;
-      const int pos = u * kTile + box * box_rows;
-      const bool mine = box < per_tile && pos < it.s.kv;
-      int page = 0;
-      if (mine) page = a.block_table[(long long)it.b * a.table_stride + pos / a.page_size];
-      if (mine && (unsigned)page >= (unsigned)a.n_pages) {
-        atomicOr(p.status, kAttnBadPage);
-        page = a.n_pages;  // outside the tensor: reads as zeros
-      }
-      if (round > 0) wait(empty(stage), (round - 1) & 1);
-      const unsigned boxes = __popc(__ballot_sync(0xffffffffu, mine));
-      if (lane == 0) mbar_arrive_expect_tx(full(stage), boxes * box_rows * 128u);
-      __syncwarp();
-      if (mine)
-        tma_load_3d(ring + stage * kTileBytes + half * kPanel + box * box_rows * 128, map, it.h * D + half * 64,
-                    pos % a.page_size, page, full(stage));
-      ++filled;
-    };
-    while (walk.next(it)) {
-      const int n = it.u1 - it.u0;
-      if (kPair) {
-        for (int j = 0; j < n; ++j) {
-          load(&k_map, it.u0 + j);
-          load(&v_map, it.u0 + j);
-        }
-      } else {
-        load(&k_map, it.u0);
-        if (n > 1) load(&k_map, it.u0 + 1);
-        for (int j = 0; j < n; ++j) {
-          load(&v_map, it.u0 + j);
-          if (j + 2 < n) load(&k_map, it.u0 + j + 2);
-        }
-      }
-    }
-    // no copy is in flight when the CTA ends, also after a wait has given up
-    for (int f = max(0, filled - kStages); f < filled; ++f) {
-      unsigned long long waited;
-      mbar_wait(full(f % kStages), (f / kStages) & 1, &waited);
-    }
-  } else if (warp == kMmaWarp) {
-    // ---- products, issued by lane 0
-    constexpr uint32_t kDescS = mma_desc(std::is_same<T, __nv_bfloat16>::value, false, kTile, kTile);
-    constexpr uint32_t kDescO = mma_desc(std::is_same<T, __nv_bfloat16>::value, true, kTile, D);
-    int taken = 0, q_round = 0, p_round[2] = {0, 0};
-    auto next_stage = [&]() {
-      const int stage = taken % kStages;
-      wait(full(stage), (taken / kStages) & 1);
-      ++taken;
-      return stage;
-    };
-    auto scores = [&](int chain, int q_tile, int stage) {
-      if (lane == 0) {
-        const uint32_t qa = q_at + q_tile * kTileBytes, ka = ring + stage * kTileBytes;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k / 4) * kPanel + (k % 4) * 32;
-          mma_ss(tmem + chain * kTile, smem_desc(qa + off, 16, 1024), smem_desc(ka + off, 16, 1024), kDescS, k > 0);
-        }
-        mma_commit(s_full(chain));
-      }
-    };
-    auto products = [&](int chain, int stage, bool add) {
-      wait(p_full(chain), p_round[chain]++ & 1);
-      tc_fence_after();
-      if (lane == 0) {
-        const uint32_t va = ring + stage * kTileBytes;
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          mma_ts(tmem + 2 * kTile + chain * D, tmem + chain * kTile + k * 8, smem_desc(va + k * 2048, kPanel, 1024),
-                 kDescO, add || k > 0);
-        mma_commit(o_full(chain));
-      }
-    };
-    auto release = [&](int stage) {
-      if (lane == 0) mma_commit(empty(stage));
-    };
-    // Rows of the cache past the sequence's end hold anything, and 0 * NaN is
-    // NaN: they become zeros.
-    auto value_stage = [&](int u) {
-      const int stage = next_stage(), valid = max(0, it.s.kv - u * kTile);
-      if (valid < kTile) {
-        uint8_t* v = ring_smem + stage * kTileBytes;
-        for (int i = lane; i < (kTile - valid) * (D / 8); i += 32) {
-          const int row = valid + i / (D / 8), c = i % (D / 8);
-          *reinterpret_cast<uint4*>(v + (c / 8) * kPanel + row * 128 + (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      return stage;
-    };
-    while (walk.next(it)) {
-      const int n = it.u1 - it.u0;
-      wait(q_full(0), q_round & 1);
-      if (kPair) {
-        int ks = next_stage();
-        tc_fence_after();
-        scores(0, 0, ks);
-        wait(q_full(1), q_round & 1);
-        scores(1, 1, ks);
-        release(ks);
-        for (int j = 0; j < n; ++j) {
-          const int vs = value_stage(it.u0 + j);
-          products(0, vs, j > 0);
-          if (j + 1 < n) {
-            ks = next_stage();
-            scores(0, 0, ks);
-          }
-          products(1, vs, j > 0);
-          release(vs);
-          if (j + 1 < n) {
-            scores(1, 1, ks);
-            release(ks);
-          }
-        }
-      } else {
-        for (int j = 0; j < min(n, 2); ++j) {
-          const int ks = next_stage();
-          tc_fence_after();
-          scores(j, 0, ks);
-          release(ks);
-        }
-        for (int j = 0; j < n; ++j) {
-          const int vs = value_stage(it.u0 + j);
-          products(j & 1, vs, j > 1);
-          release(vs);
-          if (j + 2 < n) {
-            const int ks = next_stage();
-            scores(j & 1, 0, ks);
-            release(ks);
-          }
-        }
-      }
-      ++q_round;
-    }
-    if (lane == 0) mma_commit(drained);
-    unsigned long long waited;
-    mbar_wait(drained, 0, &waited);
-    __syncwarp();
-  } else {
+  if (warp < kMmaWarp) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    Walk<kRows> walk(p, plan);
+    Item it{};
     // ---- softmax: chain 0 in warps 0-3, chain 1 in warps 4-7, a row per thread
     const int chain = warp >> 2, r = tid & 127;
     const int q_tile = kPair ? chain : 0;
@@ -504,33 +388,31 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       float m = -INFINITY, l = 0.f;
       const int first = kPair ? it.u0 : it.u0 + chain, step = kPair ? 1 : 2;
       int done = 0;
-      for (int u = first; u < it.u1; u += step) {
-        wait(s_full(chain), s_round++ & 1);
-        tc_fence_after();
-        if (warp_valid) {
+      auto softmax_tile = [&](int u, int left, auto masked_type) {
+          constexpr bool masked = decltype(masked_type)::value;
           uint32_t s[kTile];
 #pragma unroll
           for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, s + 32 * i);
           tmem_wait_ld();
-          const int left = plain - u * kTile;  // columns below it are seen
-          if (__any_sync(0xffffffffu, left < kTile)) {
-            if (a.tree_mask) {
-              const int cut = end - u * kTile;
+          if (masked) {
+            // a bit for each column: those below `left`, and a tree's
+            const int sh = it.s.base - u * kTile;
 #pragma unroll
-              for (int i = 0; i < kTile; ++i) {
-                const int bit = i - (it.s.base - u * kTile);
-                const bool seen = i < left || (i < cut && bit >= 0 && ((bits >> (bit & 63)) & 1));
-                if (!seen) s[i] = 0xff800000u;
+            for (int w = 0; w < 4; ++w) {
+              uint32_t seen = below(left - 32 * w);
+              if (a.tree_mask) {
+                const int k = 32 * w - sh;
+                const unsigned long long part = k >= 64 || k <= -32 ? 0ull : k >= 0 ? bits >> k : bits << -k;
+                seen |= (uint32_t)part & below(end - u * kTile - 32 * w);
               }
-            } else {
 #pragma unroll
-              for (int i = 0; i < kTile; ++i)
-                if (i >= left) s[i] = 0xff800000u;
+              for (int i = 0; i < 32; ++i)
+                if (!((seen >> i) & 1)) s[32 * w + i] = 0xff800000u;
             }
           }
           float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < kTile; ++i) top[i & 3] = fmaxf(top[i & 3], __uint_as_float(s[i]));
+          for (int i = 0; i < kTile; i += 2) max3(top[(i / 2) & 3], s[i], s[i + 1]);
           const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
           float shrink = 1.f;
           if (high > m + rescale || m == -INFINITY) {
@@ -553,22 +435,35 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             l *= shrink;
           }
           const float off = m == -INFINITY ? 0.f : m * c;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t c2 = pair_of(c, c), off2 = pair_of(-off, -off);
+          uint64_t sum[2] = {0ull, 0ull};  // two pairs of fp32 zeros
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t packed[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              const float x = exp2_approx(fmaf(__uint_as_float(s[32 * i + 2 * k]), c, -off));
-              const float y = exp2_approx(fmaf(__uint_as_float(s[32 * i + 2 * k + 1]), c, -off));
-              sum[(2 * k) & 3] += x;
-              sum[(2 * k + 1) & 3] += y;
+              const uint64_t z = fma2(pair_of(s[32 * i + 2 * k], s[32 * i + 2 * k + 1]), c2, off2);
+              const float x = exp2_approx(low_of(z)), y = exp2_approx(high_of(z));
+              sum[k & 1] = add2(sum[k & 1], pair_of(x, y));
               packed[k] = pack<T>(x, y);
             }
             tmem_st16(s_at + 16 * i, packed);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          sum[0] = add2(sum[0], sum[1]);
+          l += low_of(sum[0]) + high_of(sum[0]);
           tmem_wait_st();
+      };
+      for (int u = first; u < it.u1; u += step) {
+        wait(s_full(chain), s_round++ & 1);
+        tc_fence_after();
+        const int left = plain - u * kTile;  // columns below it are seen
+        if (warp_valid) {
+          // straight through in either form: a branch around the masking alone
+          // would hold the scores twice
+          if (__any_sync(0xffffffffu, left < kTile))
+            softmax_tile(u, left, std::true_type{});
+          else
+            softmax_tile(u, left, std::false_type{});
         }
         ++done;
         tc_fence_before();
@@ -660,6 +555,159 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         p.cuts[blockIdx.x] = Cut{(int)(e - blockIdx.x) + 1, it.b, it.h, it.tile};
       }
       if (!kPair) named_sync(1, 256);  // both chains' sums are read before the next item's
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kCopyWarp) {
+    Walk<kRows> walk(p, plan);
+    Item it{};
+    // ---- copies: per 128 positions one box per page and 64 columns, a lane each
+    constexpr int kHalves = D / 64;
+    const int box_rows = min(a.page_size, kTile), per_tile = kTile / box_rows;
+    const int box = lane / kHalves, half = lane % kHalves;
+    int filled = 0;
+    auto load = [&](const CUtensorMap* map, int u) {
+      const int stage = filled % kStages, round = filled / kStages;
+      const int pos = u * kTile + box * box_rows;
+      const bool mine = box < per_tile && pos < it.s.kv;
+      int page = 0;
+      if (mine) page = a.block_table[(long long)it.b * a.table_stride + pos / a.page_size];
+      if (mine && (unsigned)page >= (unsigned)a.n_pages) {
+        atomicOr(p.status, kAttnBadPage);
+        page = a.n_pages;  // outside the tensor: reads as zeros
+      }
+      if (round > 0) wait(empty(stage), (round - 1) & 1);
+      const unsigned boxes = __popc(__ballot_sync(0xffffffffu, mine));
+      if (lane == 0) mbar_arrive_expect_tx(full(stage), boxes * box_rows * 128u);
+      __syncwarp();
+      if (mine)
+        tma_load_3d(ring + stage * kTileBytes + half * kPanel + box * box_rows * 128, map, it.h * D + half * 64,
+                    pos % a.page_size, page, full(stage));
+      ++filled;
+    };
+    while (walk.next(it)) {
+      const int n = it.u1 - it.u0;
+      if (kPair) {
+        for (int j = 0; j < n; ++j) {
+          load(&k_map, it.u0 + j);
+          load(&v_map, it.u0 + j);
+        }
+      } else {
+        load(&k_map, it.u0);
+        if (n > 1) load(&k_map, it.u0 + 1);
+        for (int j = 0; j < n; ++j) {
+          load(&v_map, it.u0 + j);
+          if (j + 2 < n) load(&k_map, it.u0 + j + 2);
+        }
+      }
+    }
+    // no copy is in flight when the CTA ends, also after a wait has given up
+    for (int f = max(0, filled - kStages); f < filled; ++f) {
+      unsigned long long waited;
+      mbar_wait(full(f % kStages), (f / kStages) & 1, &waited);
+    }
+    } else if (warp == kMmaWarp) {
+    Walk<kRows> walk(p, plan);
+    Item it{};
+    // ---- products, issued by lane 0
+    constexpr uint32_t kDescS = mma_desc(std::is_same<T, __nv_bfloat16>::value, false, kTile, kTile);
+    constexpr uint32_t kDescO = mma_desc(std::is_same<T, __nv_bfloat16>::value, true, kTile, D);
+    int taken = 0, q_round = 0, p_round[2] = {0, 0};
+    auto next_stage = [&]() {
+      const int stage = taken % kStages;
+      wait(full(stage), (taken / kStages) & 1);
+      ++taken;
+      return stage;
+    };
+    auto scores = [&](int chain, int q_tile, int stage) {
+      if (lane == 0) {
+        const uint64_t qd = smem_desc(q_at + q_tile * kTileBytes, 16, 1024), kd = smem_desc(ring + stage * kTileBytes, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k / 4) * kPanel + (k % 4) * 32;
+          mma_ss(tmem + chain * kTile, qd + off / 16, kd + off / 16, kDescS, k > 0);
+        }
+        mma_commit(s_full(chain));
+      }
+    };
+    auto products = [&](int chain, int stage, bool add) {
+      wait(p_full(chain), p_round[chain]++ & 1);
+      tc_fence_after();
+      if (lane == 0) {
+        const uint64_t vd = smem_desc(ring + stage * kTileBytes, kPanel, 1024);
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          mma_ts(tmem + 2 * kTile + chain * D, tmem + chain * kTile + k * 8, vd + k * 128,
+                 kDescO, add || k > 0);
+        mma_commit(o_full(chain));
+      }
+    };
+    auto release = [&](int stage) {
+      if (lane == 0) mma_commit(empty(stage));
+    };
+    // Rows of the cache past the sequence's end hold anything, and 0 * NaN is
+    // NaN: they become zeros.
+    auto value_stage = [&](int u) {
+      const int stage = next_stage(), valid = max(0, it.s.kv - u * kTile);
+      if (valid < kTile) {
+        uint8_t* v = ring_smem + stage * kTileBytes;
+        for (int i = lane; i < (kTile - valid) * (D / 8); i += 32) {
+          const int row = valid + i / (D / 8), c = i % (D / 8);
+          *reinterpret_cast<uint4*>(v + (c / 8) * kPanel + row * 128 + (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      return stage;
+    };
+    while (walk.next(it)) {
+      const int n = it.u1 - it.u0;
+      wait(q_full(0), q_round & 1);
+      if (kPair) {
+        int ks = next_stage();
+        tc_fence_after();
+        scores(0, 0, ks);
+        wait(q_full(1), q_round & 1);
+        scores(1, 1, ks);
+        release(ks);
+        for (int j = 0; j < n; ++j) {
+          const int vs = value_stage(it.u0 + j);
+          products(0, vs, j > 0);
+          if (j + 1 < n) {
+            ks = next_stage();
+            scores(0, 0, ks);
+          }
+          products(1, vs, j > 0);
+          release(vs);
+          if (j + 1 < n) {
+            scores(1, 1, ks);
+            release(ks);
+          }
+        }
+      } else {
+        for (int j = 0; j < min(n, 2); ++j) {
+          const int ks = next_stage();
+          tc_fence_after();
+          scores(j, 0, ks);
+          release(ks);
+        }
+        for (int j = 0; j < n; ++j) {
+          const int vs = value_stage(it.u0 + j);
+          products(j & 1, vs, j > 1);
+          release(vs);
+          if (j + 2 < n) {
+            const int ks = next_stage();
+            scores(j & 1, 0, ks);
+            release(ks);
+          }
+        }
+      }
+      ++q_round;
+    }
+    if (lane == 0) mma_commit(drained);
+    unsigned long long waited;
+    mbar_wait(drained, 0, &waited);
+    __syncwarp();
     }
   }
   tc_fence_before();
