@@ -28,7 +28,7 @@
 extern "C" {
 #endif
 
-#define MOE_SAMPLE_MAX_VOCAB 16777216
+#define MOE_SAMPLE_MAX_VOCAB 8388608
 
 /*
  * moe_sample -- asynchronous on `stream`, allocates nothing.

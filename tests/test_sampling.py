@@ -126,6 +126,7 @@ def test_model_vocabulary(M):
 @pytest.mark.gpu
 def test_larger_vocabularies_and_many_rows():
     check(logits(2, 1_000_003, 1), SETTINGS[:2], torch.tensor([0.3, 0.8]), real=False)
+    check(logits(1, 1 << 23, 4, spread=4.0), SETTINGS[3:4], torch.tensor([0.7]), real=False)
     rows = [SETTINGS[i % len(SETTINGS)] for i in range(700)]
     check(logits(700, 300, 2), rows, torch.rand(700, generator=torch.Generator().manual_seed(3)), real=False)
 
@@ -241,7 +242,7 @@ def test_refusals():
         v = lambda x: None if x is None else ctypes.c_void_p(x)
         return L.moe_sample(v(logits), stride, rows, vocab, v(u), v(t), v(k), v(p), v(m), v(tokens), v(probs), None)
 
-    for bad in (dict(rows=-1), dict(rows=65536), dict(vocab=0), dict(vocab=(1 << 24) + 1), dict(logits=None),
+    for bad in (dict(rows=-1), dict(rows=65536), dict(vocab=0), dict(vocab=(1 << 23) + 1), dict(logits=None),
                 dict(u=None), dict(tokens=None), dict(logits=2), dict(t=1), dict(k=2), dict(p=3), dict(m=6),
                 dict(probs=2), dict(stride=99)):
         assert call(**bad) == N.MOE_ERR_INVALID_ARG, bad

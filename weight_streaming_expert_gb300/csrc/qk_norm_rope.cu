@@ -10,10 +10,13 @@
 // wraps modulo a whole turn by itself, so the angle has an error of
 // position * 2^-65 turns and the 32 leading bits go to sincospif.
 //
-// Bound by memory: 2 bytes in and 2 out per value.  One CTA per token: the
-// rot/2 sine/cosine pairs are computed once per token (one per thread) while
-// the heads' 16-byte loads are in flight, and D/8 lanes share a head, so that
-// the sum of squares and the pairs' partners are shuffles inside a warp.
+// Bound by memory: 2 bytes in and 2 out per value.  A warp handles a token, or
+// a share of its heads where there are few tokens; D/8 lanes share a head.  A
+// lane holds four values of a head's first half and their four partners of the
+// second (or four adjacent pairs), so a pair turns inside a thread and only
+// the sum of squares crosses lanes.  The sines and cosines of a token are
+// computed once by the warp, two or so per lane, while its first heads are on
+// their way, and no warp waits for another.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -23,8 +26,8 @@
 namespace wse {
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeLoads = 4;  // heads a thread has in flight
+constexpr int kRopeThreads = 256, kRopeWarps = kRopeThreads / 32;
+constexpr int kRopeLoads = 4;  // heads a lane has in flight
 
 template <typename T>
 __device__ __forceinline__ float to_f32(T v);
@@ -48,111 +51,135 @@ __device__ __forceinline__ __half from_f32<__half>(float v) {
 }
 
 template <typename T, int D, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const moe_qk_norm_rope_args_t a) {
-  constexpr int kLanes = D / 8;                       // lanes of a head
-  constexpr int kPerPass = kRopeThreads / kLanes;     // heads of a pass
-  __shared__ float2 turn[D / 2];                      // (cos, sin) of this token's angles
-  const int tid = threadIdx.x, part = tid % kLanes, row = tid / kLanes;
-  const long long t = blockIdx.x;
+__global__ void __launch_bounds__(kRopeThreads, D == 256 ? 3 : 4) qk_norm_rope_kernel(const __grid_constant__ moe_qk_norm_rope_args_t a,
+                                                                     int warps_per_token) {
+  constexpr int kLanes = D / 8;               // lanes of a head
+  constexpr int kHeads = 32 / kLanes;         // heads of a warp at a time
+  __shared__ float2 turn[kRopeWarps][D / 2];  // (cos, sin) of the warp's token
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = lane % kLanes;
+  const long long t = (long long)blockIdx.x * (kRopeWarps / warps_per_token) + warp / warps_per_token;
   const int n_qk = a.n_heads + a.n_kv_heads, n_all = n_qk + a.n_kv_heads;
-  const int rot = a.rotary_dim;
+  const int pairs = a.rotary_dim / 2;
   pdl_wait();
   pdl_launch_dependents();
+  if (t >= a.n_tokens) return;
 
+  // where this lane's first and second four values of a head lie; lanes past
+  // the rotated pairs share out the rest in the same way
+  const bool turns = part * 4 < pairs;
+  int lo = part * 8, hi = part * 8 + 4;
+  if (!kInterleaved) {
+    lo = turns ? part * 4 : part * 4 + pairs;
+    hi = turns ? part * 4 + pairs : part * 4 + D / 2;
+  }
   const long long slot = a.n_kv_heads > 0 ? a.slots[t] : -1;
   const bool keep = slot >= 0 && slot < (long long)a.n_pages * a.page_size;
-  const long long page = keep ? slot / a.page_size : 0, off = keep ? slot % a.page_size : 0;
+  const long long page = keep ? slot / a.page_size : 0, row = keep ? slot % a.page_size : 0;
+  const T* q = static_cast<const T*>(a.q) + t * a.q_token_stride;
+  const T* k = static_cast<const T*>(a.k) + t * a.k_token_stride;
+  const T* v = static_cast<const T*>(a.v) + t * a.v_token_stride;
+  T* q_out = static_cast<T*>(a.q_out) + t * a.q_out_token_stride;
+  T* k_out = static_cast<T*>(a.k_cache) + page * a.k_page_stride + row * a.k_row_stride;
+  T* v_out = static_cast<T*>(a.v_cache) + page * a.v_page_stride + row * a.v_row_stride;
   const T* qw = static_cast<const T*>(a.q_weight);
   const T* kw = static_cast<const T*>(a.k_weight);
-  float c[8], s[8];
+
+  const int step = warps_per_token * kHeads;
+  const int h0 = (warp % warps_per_token) * kHeads + lane / kLanes;
+  float2 cs[4];
   bool first = true;
-  for (int base = 0; base < n_all; base += kRopeLoads * kPerPass) {
-    uint4 raw[kRopeLoads];
+  for (int base = h0 - lane / kLanes; base < n_all; base += kRopeLoads * step) {
+    uint2 x0[kRopeLoads], x1[kRopeLoads];
 #pragma unroll
     for (int i = 0; i < kRopeLoads; ++i) {
-      const int h = base + i * kPerPass + row;
-      raw[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (h < a.n_heads)
-        raw[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + t * a.q_token_stride +
-                                                 h * a.q_head_stride + part * 8);
-      else if (h < n_qk)
-        raw[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.k) + t * a.k_token_stride +
-                                                 (h - a.n_heads) * a.k_head_stride + part * 8);
-      else if (h < n_all)
-        raw[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) + t * a.v_token_stride +
-                                                 (h - n_qk) * a.v_head_stride + part * 8);
+      const int h = base + i * step + lane / kLanes;
+      if (h >= n_all) continue;
+      const T* p = h < a.n_heads ? q + h * a.q_head_stride
+                   : h < n_qk    ? k + (h - a.n_heads) * a.k_head_stride
+                                 : v + (h - n_qk) * a.v_head_stride;
+      x0[i] = *reinterpret_cast<const uint2*>(p + lo);
+      x1[i] = *reinterpret_cast<const uint2*>(p + hi);
     }
     if (first) {
       first = false;
-      if (tid < rot / 2) {
-        const unsigned long long at = (unsigned long long)(long long)a.positions[t] * a.turns[tid];
-        float sn, cs;
-        sincospif((float)(int)(at >> 32) * 0x1p-31f, &sn, &cs);  // 2 * turns half-turns, turns in [-1/2, 1/2)
-        turn[tid] = make_float2(cs, sn);
+      for (int i = lane; i < pairs; i += 32) {
+        const unsigned long long at = (unsigned long long)(long long)a.positions[t] * a.turns[i];
+        float sn, c;
+        sincospif((float)(int)(at >> 32) * 0x1p-31f, &sn, &c);  // in half turns, turns in [-1/2, 1/2)
+        turn[warp][i] = make_float2(c, sn);
       }
-      __syncthreads();
+      __syncwarp();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int e = part * 8 + j;
-        const int pair = kInterleaved ? e / 2 : (e < rot / 2 ? e : e - rot / 2);
-        const float2 v = e < rot ? turn[pair] : make_float2(1.f, 0.f);
-        c[j] = v.x;
-        // the first of a pair takes -sin of its partner, the second +sin
-        s[j] = (kInterleaved ? (e & 1) == 0 : e < rot / 2) ? -v.y : v.y;
-      }
+      for (int j = 0; j < 4; ++j) cs[j] = turns ? turn[warp][part * 4 + j] : make_float2(1.f, 0.f);
     }
-    // the lane of this head that holds the partners of this lane's values
-    const int half = rot / 16, lane = tid & 31;
-    const int partner = part < half ? lane + half : (part < 2 * half ? lane - half : lane);
 #pragma unroll
     for (int i = 0; i < kRopeLoads; ++i) {
-      const int h = base + i * kPerPass + row;
-      const T* e = reinterpret_cast<const T*>(&raw[i]);
+      if (base + i * step >= n_all) break;  // the whole warp
+      const int h = base + i * step + lane / kLanes;
+      const T* e0 = reinterpret_cast<const T*>(&x0[i]);
+      const T* e1 = reinterpret_cast<const T*>(&x1[i]);
       float x[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = to_f32<T>(e[j]);
-      const T* w = h < a.n_heads ? qw : kw;
+      for (int j = 0; j < 4; ++j) x[j] = to_f32<T>(e0[j]), x[4 + j] = to_f32<T>(e1[j]);
       float sq = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) sq = fmaf(x[j], x[j], sq);
 #pragma unroll
       for (int m = kLanes / 2; m > 0; m >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, m);
-      if (w && h < n_qk) {
+      if (h >= n_all) continue;
+      if (h >= n_qk) {
+        if (keep) {
+          *reinterpret_cast<uint2*>(v_out + (h - n_qk) * D + lo) = x0[i];
+          *reinterpret_cast<uint2*>(v_out + (h - n_qk) * D + hi) = x1[i];
+        }
+        continue;
+      }
+      const T* w = h < a.n_heads ? qw : kw;
+      if (w) {
         const float r = rsqrtf(sq * (1.f / D) + a.eps);
-        const uint4 wraw = *reinterpret_cast<const uint4*>(w + part * 8);
-        const T* we = reinterpret_cast<const T*>(&wraw);
+        const uint2 w0 = *reinterpret_cast<const uint2*>(w + lo), w1 = *reinterpret_cast<const uint2*>(w + hi);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] *= r * to_f32<T>(we[j]);
+        for (int j = 0; j < 4; ++j) {
+          x[j] *= r * to_f32<T>(reinterpret_cast<const T*>(&w0)[j]);
+          x[4 + j] *= r * to_f32<T>(reinterpret_cast<const T*>(&w1)[j]);
+        }
       }
-      uint4 packed;
-      T* o = reinterpret_cast<T*>(&packed);
+      if (turns) {  // others stay as they are: 0 * inf must not reach them
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float other = kInterleaved ? x[j ^ 1] : __shfl_sync(0xffffffffu, x[j], partner);
-        // values outside the rotated part stay as they are (0 * inf must not reach them)
-        o[j] = from_f32<T>(part * 8 + j < rot ? fmaf(other, s[j], x[j] * c[j]) : x[j]);
+        for (int j = 0; j < 4; ++j) {
+          float& x_a = x[kInterleaved ? 2 * j : j];
+          float& x_b = x[kInterleaved ? 2 * j + 1 : 4 + j];
+          const float y_a = fmaf(-x_b, cs[j].y, x_a * cs[j].x), y_b = fmaf(x_a, cs[j].y, x_b * cs[j].x);
+          x_a = y_a;
+          x_b = y_b;
+        }
       }
-      if (h < a.n_heads)
-        *reinterpret_cast<uint4*>(static_cast<T*>(a.q_out) + t * a.q_out_token_stride + h * a.q_out_head_stride +
-                                  part * 8) = packed;
-      else if (h < n_qk && keep)
-        *reinterpret_cast<uint4*>(static_cast<T*>(a.k_cache) + page * a.k_page_stride + off * a.k_row_stride +
-                                  (long long)(h - a.n_heads) * D + part * 8) = packed;
-      else if (h < n_all && h >= n_qk && keep)
-        *reinterpret_cast<uint4*>(static_cast<T*>(a.v_cache) + page * a.v_page_stride + off * a.v_row_stride +
-                                  (long long)(h - n_qk) * D + part * 8) = raw[i];
+      uint2 o0, o1;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        reinterpret_cast<T*>(&o0)[j] = from_f32<T>(x[j]);
+        reinterpret_cast<T*>(&o1)[j] = from_f32<T>(x[4 + j]);
+      }
+      T* o = h < a.n_heads ? q_out + h * a.q_out_head_stride : k_out + (h - a.n_heads) * D;
+      if (h < a.n_heads || keep) {
+        *reinterpret_cast<uint2*>(o + lo) = o0;
+        *reinterpret_cast<uint2*>(o + hi) = o1;
+      }
     }
   }
 }
 
 template <typename T>
 int launch_rope(const moe_qk_norm_rope_args_t& a, moe_stream_t stream) {
-  void (*kernel)(const moe_qk_norm_rope_args_t) = nullptr;
+  void (*kernel)(const moe_qk_norm_rope_args_t, int) = nullptr;
   const bool il = a.interleaved != 0;
   if (a.head_dim == 64) kernel = il ? qk_norm_rope_kernel<T, 64, true> : qk_norm_rope_kernel<T, 64, false>;
   else if (a.head_dim == 128) kernel = il ? qk_norm_rope_kernel<T, 128, true> : qk_norm_rope_kernel<T, 128, false>;
   else kernel = il ? qk_norm_rope_kernel<T, 256, true> : qk_norm_rope_kernel<T, 256, false>;
-  return launch_pdl(kernel, dim3((unsigned)a.n_tokens), dim3(kRopeThreads), 0, stream, 1, a);
+  // few tokens: all warps of a CTA on one token, for the latency; many: a warp each
+  const int warps = a.n_tokens <= 512 ? kRopeWarps : 1, tokens = kRopeWarps / warps;
+  return launch_pdl(kernel, dim3((unsigned)((a.n_tokens + tokens - 1) / tokens)), dim3(kRopeThreads), 0, stream, 1, a,
+                    warps);
 }
 
 }  // namespace

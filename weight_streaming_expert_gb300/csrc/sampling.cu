@@ -12,8 +12,13 @@
 // A row belongs to one thread-block cluster: its CTAs take contiguous slices
 // of the vocabulary, hold them in shared memory, and exchange maxima, bins and
 // sums through distributed shared memory.  The row is read from memory once;
-// what remains is the latency of about a dozen cluster-wide exchanges.
+// what remains is the latency of the exchanges (one takes 1-3 us).  So where a
+// filter cuts among the 2048 largest logits, as it mostly does, one pass of
+// bins finds those, the CTAs hand them to the first one in the order of their
+// ids, and it goes on alone with the same code.
 #include <cooperative_groups.h>
+
+#include <cstddef>
 
 #include "host_util.cuh"
 #include "sampling.h"
@@ -25,13 +30,17 @@ namespace {
 
 constexpr int kSampleThreads = 512;
 constexpr int kSampleWarps = kSampleThreads / 32;
-constexpr int kBins = kSampleThreads;    // of a pass, over the whole cluster
-constexpr int kBinBits = 9;
-constexpr int kFirstShift = 15;          // the first pass resolves 2^24 keys below the largest: two to three octaves
+constexpr int kBinBits = 12, kBins = 1 << kBinBits;  // of a pass, over the whole cluster
+constexpr int kBarBits = 10;             // of the pass that finds the kList largest logits
+constexpr int kWindowBits = 24;          // the first pass looks at the 2^24 keys from the largest: two to three octaves
 constexpr int kMaxCluster = 16;
 constexpr float kOne = 274877906944.f;   // 2^38
-constexpr int kMaxCached = 49152;        // logits of a slice that fit in shared memory
+constexpr int kMaxCached = 36864;        // logits of a slice that fit in shared memory
 constexpr uint32_t kKeyNegInf = 0x007fffffu;
+constexpr int kList = 2048;              // largest logits that one CTA can go on with
+constexpr int kAllTies = 0x7fffffff;
+constexpr int kLimbBits = 13;            // of a weight (39 bits) in a bin's three words
+constexpr int kMaxSlice = 1 << (32 - kLimbBits);  // a slice's sums of 13-bit parts fit a word
 
 using u64 = unsigned long long;
 
@@ -39,7 +48,6 @@ struct SampleArgs {
   const float* logits;
   int64_t row_stride;
   int vocab, slice;  // logits of a CTA's slice
-  bool cached;       // the slice is held in shared memory
   const float* u;
   const float* temperature;
   const int32_t* top_k;
@@ -60,11 +68,15 @@ __device__ __forceinline__ float logit_of(uint32_t key) {
 }
 
 struct Shared {
-  u64 hist[kBins];
-  u64 sums[kSampleWarps];
-  u64 scan[2];   // read by the other CTAs: the CTA's value of a scan, alternating
-  u64 found[3];  // read by the other CTAs: a pass's bin + 1 (0: none), the measure before it, its own
-  unsigned best;
+  uint32_t hist[3][kBins];   // counts, or the sums of the weights' 13-bit parts, then 64-bit sums over the first two
+  uint32_t list_key[kList];  // of the first CTA: the largest logits, by id
+  int list_id[kList];
+  u64 sums[kSampleWarps];    // of this CTA's warps
+  u64 scan[2][3];            // read by the other CTAs: the CTA's values of an exchange, alternating
+  u64 result[6];             // of an exchange, for this CTA's threads
+  u64 found[3];              // written by the CTA that found it: a pass's bin, the measure before it, its own
+  u64 shared[2];             // of this CTA: what one thread computes for the others
+  int tie_end;               // written by the CTA that found it
 };
 
 __device__ __forceinline__ u64 warp_sum(u64 v) {
@@ -72,253 +84,536 @@ __device__ __forceinline__ u64 warp_sum(u64 v) {
   for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
   return v;
 }
+__device__ __forceinline__ u64 warp_max(u64 v) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, m));
+  return v;
+}
 
-struct Cta {
+// The CTAs that work on a row, and this one's part of it: n keys, of which each
+// thread has `run` in a row (an odd number: consecutive threads then read
+// different banks).
+template <bool kCached>
+struct Team {
   Shared& s;
   cg::cluster_group cluster;
-  int rank, size;
-  const float* data;  // this CTA's slice, in shared or global memory
-  int seg0, seg1;     // this warp's contiguous part of it
+  int rank, size;   // 0 and 1 once the first CTA goes on alone
+  bool alone;       // it does, with the list: its keys and their ids
+  const float* row; // before that, the slice's logits, whose ids are begin, begin + 1, ..
+  int begin;
   int warp, lane;
   unsigned phase;
+  int i0, i1;            // this thread's keys
 
-  // Sum of `v` over the CTA (v: one value per warp, uniform in it).
-  __device__ u64 cta_sum(u64 v) {
-    __syncthreads();
-    if (lane == 0) s.sums[warp] = v;
-    __syncthreads();
-    u64 total = 0;
-    for (int w = 0; w < kSampleWarps; ++w) total += s.sums[w];
-    return total;
+  __device__ void split(int n) {
+    const int run = ((n + kSampleThreads - 1) / kSampleThreads) | 1;
+    i0 = min(n, (int)threadIdx.x * run);
+    i1 = min(n, i0 + run);
   }
-  // Over the cluster: the sum of the CTAs' values before this one, and of all.
-  // Two slots in turn: a slot is written again only after another exchange,
-  // which every CTA enters after it has read this one.
-  __device__ void cluster_scan(u64 mine, u64& below, u64& total) {
-    phase ^= 1;
-    if (threadIdx.x == 0) s.scan[phase] = mine;
-    cluster.sync();
-    below = total = 0;
-    for (int r = 0; r < size; ++r) {
-      const u64 v = *cluster.map_shared_rank(&s.scan[phase], r);
-      if (r < rank) below += v;
-      total += v;
+  // Keys in shared memory: of the slice after the struct, or the list's.
+  __device__ __forceinline__ uint32_t cached(int i) const {
+    return reinterpret_cast<const uint32_t*>(&s)[(alone ? (int)offsetof(Shared, list_key) : (int)sizeof(Shared)) / 4 + i];
+  }
+  __device__ __forceinline__ uint32_t key(int i) const { return kCached || alone ? cached(i) : key_of(row[i]); }
+  // f(i, keys i .. i + 3) for this thread's keys, four at a time so that their
+  // latencies overlap; keys past the end are 0, below every key of a logit and
+  // of no weight
+  template <typename F>
+  __device__ __forceinline__ void each4(F f) const {
+    uint32_t k[4];
+    for (int i = i0; i < i1; i += 4) {
+      if (kCached || alone) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) k[j] = i + j < i1 ? cached(i + j) : 0u;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) k[j] = i + j < i1 ? key_of(row[i + j]) : 0u;
+      }
+      f(i, k);
     }
   }
-  __device__ u64 cluster_max(u64 mine) {
+  __device__ __forceinline__ int id(int i) const { return alone ? s.list_id[i] : begin + i; }
+  __device__ __forceinline__ void sync() {
+    if (size > 1)
+      cluster.sync();
+    else
+      __syncthreads();
+  }
+  template <typename X>
+  __device__ __forceinline__ X* peer(X* mine, int r) const {
+    return size > 1 ? cluster.map_shared_rank(mine, r) : mine;
+  }
+
+  // Sum of the values of the threads before this one, and of all of the CTA.
+  __device__ u64 cta_scan(u64 v, u64& total) {
+    u64 upto = v;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const u64 o = __shfl_up_sync(0xffffffffu, upto, m);
+      if (lane >= m) upto += o;
+    }
+    __syncthreads();
+    if (lane == 31) s.sums[warp] = upto;
+    __syncthreads();
+    u64 before = upto - v;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kSampleWarps; ++w) {
+      const u64 x = s.sums[w];
+      if (w < warp) before += x;
+      total += x;
+    }
+    return before;
+  }
+  // The same over the team.
+  __device__ u64 team_scan(u64 v, u64& total) {
+    u64 mine, below;
+    const u64 before = cta_scan(v, mine);
+    exchange(mine, below, total);
+    return below + before;
+  }
+  // Over the team: the sums of the CTAs' values before this one, and of all.
+  // One warp reads the others' memory (a read there is slow, and its
+  // bandwidth too small for every warp to do it).  Two slots in turn: a slot
+  // is written again only after another exchange, which every CTA enters
+  // after it has read this one.
+  template <int kValues>
+  __device__ void exchange(const u64 (&mine)[kValues], u64 (&below)[kValues], u64 (&total)[kValues]) {
+    if (size == 1) {
+      for (int q = 0; q < kValues; ++q) below[q] = 0, total[q] = mine[q];
+      return;
+    }
     phase ^= 1;
-    if (threadIdx.x == 0) s.scan[phase] = mine;
+    if (threadIdx.x == 0)
+      for (int q = 0; q < kValues; ++q) s.scan[phase][q] = mine[q];
     cluster.sync();
-    u64 top = 0;
-    for (int r = 0; r < size; ++r) top = max(top, *cluster.map_shared_rank(&s.scan[phase], r));
-    return top;
+    if (warp == 0) {
+#pragma unroll
+      for (int q = 0; q < kValues; ++q) {
+        const u64 v = lane < size ? *cluster.map_shared_rank(&s.scan[phase][q], lane) : 0;
+        const u64 b = warp_sum(lane < rank ? v : 0), t = warp_sum(v);
+        if (lane == 0) s.result[q] = b, s.result[3 + q] = t;
+      }
+    }
+    __syncthreads();
+    for (int q = 0; q < kValues; ++q) below[q] = s.result[q], total[q] = s.result[3 + q];
+  }
+  __device__ void exchange(u64 mine, u64& below, u64& total) {
+    u64 b[1], t[1];
+    exchange<1>({mine}, b, t);
+    below = b[0];
+    total = t[0];
+  }
+  __device__ u64 team_max(u64 mine) {
+    if (size == 1) return mine;
+    phase ^= 1;
+    if (threadIdx.x == 0) s.scan[phase][0] = mine;
+    cluster.sync();
+    if (warp == 0) {
+      const u64 v = warp_max(lane < size ? *cluster.map_shared_rank(&s.scan[phase][0], lane) : 0);
+      if (lane == 0) s.result[0] = v;
+    }
+    __syncthreads();
+    return s.result[0];
   }
 
   // The smallest key K in [lo, hi] of the row (of non-zero measure) with
   // measure(keys in (K, hi]) < target; `above` is that measure and `at` the
-  // measure of K itself.  target > 0 and hi is in the row.
-  template <typename Measure>
-  __device__ void select(uint32_t lo, uint32_t hi, double target, Measure measure, uint32_t& key, u64& above,
-                         u64& at) {
+  // measure of K itself.  0 < target <= measure of the whole range, and hi is
+  // in the row.  With kOnce only as far as the first bin that holds it: `found`
+  // is that bin's largest possible key, `above` the measure above the bin.
+  // kParts: words of a bin, 1 for counts and 3 for weights (a 64-bit add in
+  // shared memory is a loop of compare-and-swap, three 32-bit adds are not).
+  template <int kParts, int kBits, bool kOnce, typename Measure>
+  __device__ void select(uint32_t lo, uint32_t hi, u64 target, Measure measure, uint32_t& found, u64& above, u64& at) {
+    constexpr int kWide = kParts == 1 ? 4 : 2;  // bins of a 16-byte read
+    constexpr int kUsed = 1 << kBits;           // bins of a pass
+    static_assert(kUsed <= kBins && kUsed / kMaxCluster >= kWide);
     above = 0;
-    for (bool first = true;; first = false) {
-      const uint32_t range = hi - lo;  // keys - 1
-      const int fit = max(0, 32 - __clz((int)range) - kBinBits);
-      const int shift = first ? min(kFirstShift, fit) : fit;
-      s.hist[threadIdx.x] = 0;
-      if (threadIdx.x == 0) s.best = 0;
-      __syncthreads();
-      for (int i = seg0 + lane; i < seg1; i += 32) {
-        const uint32_t k = key_of(data[i]);
-        if (k < lo || k > hi) continue;
-        const u64 m = measure(k);
-        if (m) atomicAdd(&s.hist[min((hi - k) >> shift, (uint32_t)kBins - 1)], m);
-      }
-      cluster.sync();
-      // each CTA sums its share of the bins over the cluster, one per thread
-      const int per = kBins / size;
-      const bool mine = (int)threadIdx.x < per;
-      u64 bin = 0;
-      if (mine)
-        for (int r = 0; r < size; ++r) bin += cluster.map_shared_rank(s.hist, r)[rank * per + threadIdx.x];
-      u64 upto = bin;  // inclusive scan over the share
+    // The first pass looks only near the top, where the filters usually cut:
+    // most of the row then touches no bin.  Where the cut lies below, the next
+    // pass covers all the rest.
+    uint32_t from = hi - lo >= (1u << kWindowBits) ? hi - (1u << kWindowBits) + 1 : lo;
+    for (;;) {
+      const int shift = max(0, 32 - __clz((int)(hi - from)) - kBits);
 #pragma unroll
-      for (int m = 1; m < 32; m <<= 1) {
-        const u64 o = __shfl_up_sync(0xffffffffu, upto, m);
-        if (lane >= m) upto += o;
-      }
-      const u64 share = cta_sum(__shfl_sync(0xffffffffu, upto, 31));
-      for (int w = 0; w < warp; ++w) upto += s.sums[w];
-      u64 below, total;
-      cluster_scan(share, below, total);
-      const u64 before = above + below + upto - bin;
-      const bool good = bin > 0 && (double)before < target;
-      if (good) atomicMax(&s.best, threadIdx.x + 1);
+      for (int q = 0; q < kParts; ++q)
+#pragma unroll
+        for (int b = threadIdx.x; b < kUsed / 4; b += kSampleThreads)
+          reinterpret_cast<uint4*>(s.hist[q])[b] = make_uint4(0u, 0u, 0u, 0u);
       __syncthreads();
-      if (s.best == 0 && threadIdx.x == 0) s.found[0] = 0;
-      if (good && s.best == threadIdx.x + 1) {
-        s.found[0] = rank * per + threadIdx.x + 1;
-        s.found[1] = before;
-        s.found[2] = bin;
+      each4([&](int, const uint32_t (&k)[4]) {
+        bool in[4], any = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) any |= in[j] = k[j] >= max(from, 1u) && k[j] <= hi;
+        if (!any) return;
+        u64 w[4];
+        measure(k, w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t bin = (hi - k[j]) >> shift;
+          if (!in[j]) continue;
+          if (kParts == 1) {
+            atomicAdd(&s.hist[0][bin], (uint32_t)w[j]);
+          } else if (w[j]) {
+            atomicAdd(&s.hist[0][bin], (uint32_t)w[j] & ((1u << kLimbBits) - 1));
+            atomicAdd(&s.hist[1][bin], (uint32_t)(w[j] >> kLimbBits) & ((1u << kLimbBits) - 1));
+            atomicAdd(&s.hist[2][bin], (uint32_t)(w[j] >> (2 * kLimbBits)));
+          }
+        }
+      });
+      u64* wide = reinterpret_cast<u64*>(s.hist[0]);
+      if (kParts > 1 && size > 1) {
+        __syncthreads();
+        static_assert(kParts == 1 || kUsed % kSampleThreads == 0);
+        u64 sum[kUsed / kSampleThreads];
+#pragma unroll
+        for (int b = 0; b < kUsed / kSampleThreads; ++b) {
+          const int at_b = threadIdx.x + b * kSampleThreads;
+          sum[b] = s.hist[0][at_b] + ((u64)s.hist[1][at_b] << kLimbBits) + ((u64)s.hist[2][at_b] << (2 * kLimbBits));
+        }
+        __syncthreads();
+#pragma unroll
+        for (int b = 0; b < kUsed / kSampleThreads; ++b) wide[threadIdx.x + b * kSampleThreads] = sum[b];
       }
-      cluster.sync();
-      u64 b = 1;
-      for (int r = size - 1; r >= 0; --r) {
-        const u64* f = cluster.map_shared_rank(s.found, r);
-        if (f[0]) {
-          b = f[0];
-          above = f[1];
-          at = f[2];
-          break;
+      sync();
+      // each CTA sums its share of the bins over the team, a thread a few bins
+      // in a row
+      const int share = kUsed / size, own_bins = max(kWide, share / kSampleThreads);
+      const int first = rank * share + threadIdx.x * own_bins;
+      const bool mine = (int)threadIdx.x * own_bins < share;
+      auto bins_of = [&](int b, u64 (&sum)[kWide]) {
+        const uint4* bins = reinterpret_cast<const uint4*>(kParts == 1 ? (const void*)(s.hist[0] + b) : wide + b);
+        auto add = [&](uint4 v) {
+          if (kParts == 1) {
+            sum[0] += v.x, sum[1] += v.y, sum[kWide - 2] += v.z, sum[kWide - 1] += v.w;
+          } else {
+            sum[0] += (u64)v.x | (u64)v.y << 32;
+            sum[1] += (u64)v.z | (u64)v.w << 32;
+          }
+        };
+        for (int e = 0; e < kWide; ++e) sum[e] = 0;
+        if (size == 1) {  // alone: the words as they are
+#pragma unroll
+          for (int q = 0; q < kParts; ++q)
+#pragma unroll
+            for (int e = 0; e < kWide; ++e) sum[e] += (u64)s.hist[q][b + e] << (q * kLimbBits);
+          return;
+        }
+        uint4 v[kMaxCluster];  // all reads under way at once: each takes about half a microsecond
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          v[r] = r < size ? *cluster.map_shared_rank(bins, r) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) add(v[r]);
+      };
+      u64 own = 0, part[kWide];
+      if (mine)
+        for (int e = 0; e < own_bins; e += kWide) {
+          bins_of(first + e, part);
+          for (int i = 0; i < kWide; ++i) own += part[i];
+        }
+      u64 total;
+      u64 before = team_scan(own, total);
+      if (from > lo && above + total < target) {
+        above += total;
+        hi = from - 1;
+        from = lo;
+        sync();  // the sums are read before the next pass writes them
+        continue;
+      }
+      before += above;
+      // the bin that the target falls into is one thread's, whose warp tells all
+      const bool here = mine && before < target && before + own >= target;
+      const unsigned vote = __ballot_sync(0xffffffffu, here);
+      if (vote) {
+        int b = first;
+        u64 bin = 0;
+        if (here)
+          for (bool done = false; !done; b += kWide) {
+            bins_of(b, part);
+            for (int i = 0; i < kWide && !done; ++i) {
+              bin = part[i];
+              done = before + bin >= target;
+              if (done)
+                b += i - kWide;
+              else
+                before += bin;
+            }
+          }
+        const int src = __ffs(vote) - 1;
+        b = __shfl_sync(0xffffffffu, b, src);
+        before = __shfl_sync(0xffffffffu, before, src);
+        bin = __shfl_sync(0xffffffffu, bin, src);
+        if (lane < size) {
+          u64* f = peer(s.found, lane);
+          f[0] = b;
+          f[1] = before;
+          f[2] = bin;
         }
       }
-      const uint32_t top = hi - ((uint32_t)(b - 1) << shift);
-      if (b < (u64)kBins && top - lo >= (1u << shift)) lo = top - (1u << shift) + 1;
-      hi = top;
-      if (lo == hi) break;
+      sync();
+      above = s.found[1];
+      at = s.found[2];
+      hi -= (uint32_t)s.found[0] << shift;
+      if (hi - from >= (1u << shift)) from = hi - (1u << shift) + 1;
+      lo = from;
+      if (from == hi || kOnce) break;
     }
-    key = hi;
+    found = hi;
   }
 };
 
-__global__ void __launch_bounds__(kSampleThreads) sample_kernel(const SampleArgs a) {
-  extern __shared__ float cache[];
-  __shared__ Shared s;
+// The lowest whole number that is not below x as a double: n < whole_of(x) is
+// the same as (double)n < x, which rounds above 2^53.
+__device__ u64 whole_of(double x) {
+  u64 n = (u64)ceil(x);
+  if (x < 0x1p53) return n;
+  for (u64 d = 1024; d > 0; d >>= 1)
+    while (n >= d && (double)(n - d) >= x) n -= d;
+  return n;
+}
+
+struct Ones {
+  __device__ void operator()(const uint32_t (&)[4], u64 (&w)[4]) const { w[0] = w[1] = w[2] = w[3] = 1; }
+};
+
+// x / y to about one unit in the last place: each as the sum of two fp32
+// numbers, the quotient of the larger ones corrected once by its remainder.
+__device__ float quotient(u64 x, u64 y) {
+  const float xh = (float)x, yh = (float)y;
+  const float xl = (float)(long long)(x - (u64)xh), yl = (float)(long long)(y - (u64)yh);
+  const float q = xh / yh;
+  return q + (fmaf(-q, yh, xh) + fmaf(-q, yl, xl)) / yh;
+}
+
+template <bool kCached>
+__global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  Shared& s = *reinterpret_cast<Shared*>(smem);
+  uint32_t* cache = reinterpret_cast<uint32_t*>(smem + sizeof(Shared));
   const int tid = threadIdx.x;
   cg::cluster_group cluster = cg::this_cluster();
   const int size = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const long long m = blockIdx.x / size;
   pdl_wait();
   pdl_launch_dependents();
-  const int begin = min(rank * a.slice, a.vocab);
-  const int n = min(a.slice, a.vocab - begin);
+  const float t = a.temperature ? a.temperature[m] : 1.f, p = a.top_p ? a.top_p[m] : 1.f;
+  const float min_p = a.min_p ? a.min_p[m] : 0.f, u = a.u[m];
+  const int k = a.top_k ? a.top_k[m] : 0;
+  const int begin = min(rank * a.slice, a.vocab), n = min(a.slice, a.vocab - begin);
   const float* row = a.logits + m * a.row_stride + begin;
-  const int seg = (n + kSampleThreads - 1) / kSampleThreads * 32;
-  Cta c{s, cluster, rank, size, a.cached ? cache : row, 0, 0, tid >> 5, tid & 31, 0};
-  c.seg0 = min(n, c.warp * seg);
-  c.seg1 = min(n, c.seg0 + seg);
+  Team<kCached> c{s, cluster, rank, size, false, row, begin, tid >> 5, tid & 31, 0, 0, 0};
+  c.split(n);
 
   // the row's largest logit, the lowest id first
   u64 best = 0;
 #pragma unroll 8
-  for (int i = c.seg0 + c.lane; i < c.seg1; i += 32) {
-    const float l = row[i];
-    if (a.cached) cache[i] = l;
-    best = max(best, (u64)key_of(l) << 32 | (uint32_t)~(begin + i));
+  for (int i = tid; i < n; i += kSampleThreads) {
+    const uint32_t key = key_of(row[i]);
+    if (kCached) cache[i] = key;
+    best = max(best, (u64)key << 32 | (uint32_t)~(begin + i));
   }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, d));
+  best = warp_max(best);
   if (c.lane == 0) s.sums[c.warp] = best;
   __syncthreads();
+#pragma unroll
   for (int w = 0; w < kSampleWarps; ++w) best = max(best, s.sums[w]);
-  best = c.cluster_max(best);
+  best = c.team_max(best);
   const uint32_t top_key = (uint32_t)(best >> 32);
   const float top = logit_of(top_key);
-  const float t = a.temperature ? a.temperature[m] : 1.f;
   if (top_key <= kKeyNegInf || !(t > 0.f)) {
     if (rank == 0 && tid == 0) {
       a.tokens[m] = top_key <= kKeyNegInf ? -1 : (int)~(uint32_t)best;
       if (a.probs) a.probs[m] = top_key <= kKeyNegInf ? 0.f : 1.f;
     }
-    cluster.sync();  // the others may still read this CTA's maximum
+    c.sync();  // the others may still read this CTA's maximum
     return;
   }
-  auto weight = [&](uint32_t key) -> u64 {
-    const float l = logit_of(key);
-    if (l == top) return (u64)kOne;  // an infinite one too
-    const float z = (l - top) / t;
-    return z == z ? (u64)(expf(z) * kOne) : 0;  // infinitely far below at an infinite temperature: 0
+  // d / t, correctly rounded like the operator: a quotient off by at most one
+  // unit in the last place, corrected by its exact remainder with a correctly
+  // rounded reciprocal, is (Markstein, IBM J. Res. Dev. 34, 1990), as long as
+  // nothing leaves the normal range on the way.  Where d is so small that it
+  // does, exp gives 1 either way; where d / t overflows the remainder is NaN,
+  // which counts as infinitely far below like an infinite d.
+  const float inverse = __frcp_rn(t);
+  const bool tame = t > 1e-4f && t < 1e4f;
+  // weights of four keys, without a branch between them
+  auto weights = [&](const uint32_t (&key)[4], u64 (&w)[4]) {
+    float d[4], z[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d[j] = logit_of(key[j]) - top;
+    if (tame) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float q = d[j] * inverse;
+        z[j] = fmaf(fmaf(-q, t, d[j]), inverse, q);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[j] = d[j] / t;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // infinitely far below (also at an infinite temperature): 0; the top,
+      // also an infinite one: 1
+      const float x = expf(z[j]);
+      const float e = key[j] == top_key ? 1.f : z[j] == z[j] ? x : 0.f;
+      // floor(2^38 e) in two parts: both steps are exact
+      const uint32_t high = (uint32_t)(e * 0x1p19f);
+      w[j] = ((u64)high << 19) + (uint32_t)fmaf(e, 0x1p38f, (float)high * -0x1p19f);
+    }
+  };
+  auto weight = [&](uint32_t key) {
+    const uint32_t k[4] = {key, 0u, 0u, 0u};
+    u64 w[4];
+    weights(k, w);
+    return w[0];
+  };
+  // weight of this thread's keys above `bar`
+  auto mass_above = [&](uint32_t bar) {
+    u64 sum = 0;
+    c.each4([&](int, const uint32_t (&key)[4]) {
+      if (max(max(key[0], key[1]), max(key[2], key[3])) <= bar) return;
+      u64 w[4];
+      weights(key, w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum += key[j] > bar ? w[j] : 0;
+    });
+    return sum;
   };
 
-  // the tokens that stay: keys above thr and the first `ties` of the `same`
-  // tokens whose key is thr
+  const bool by_count = k > 0 && k < a.vocab, by_mass = p < 1.f;
+  u64 above, at, total, row_mass = 0;
+  if (by_mass && !by_count) c.team_scan(mass_above(0), row_mass);  // top-p's share is of the whole row
+  if (size > 1 && (by_count || by_mass)) {
+    // the keys above `bar`: at most kList, those of this thread
+    uint32_t bar;
+    c.select<1, kBarBits, true>(0, top_key, (u64)min(kList + 1, a.vocab), Ones{}, bar, above, at);
+    u64 count = 0, in_list = ~0ull;
+    c.each4([&](int, const uint32_t (&key)[4]) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) count += key[j] > bar;
+    });
+    const int to = (int)c.team_scan(count, total);
+    if (by_mass && !by_count) c.team_scan(mass_above(bar), in_list);
+    if (tid == 0) s.shared[0] = by_mass && !by_count ? whole_of((double)p * (double)row_mass) : 0;
+    __syncthreads();
+    if (total > 0 && (by_count ? (u64)k <= total : s.shared[0] <= in_list)) {
+      // the cut lies among them
+      uint32_t* list_key = cluster.map_shared_rank(s.list_key, 0) + to;
+      int* list_id = cluster.map_shared_rank(s.list_id, 0) + to;
+      if (count)
+        c.each4([&](int i, const uint32_t (&key)[4]) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (key[j] > bar) {
+              *list_key++ = key[j];
+              *list_id++ = begin + i + j;
+            }
+        });
+      cluster.sync();
+      if (rank != 0) return;
+      c.size = 1;
+      c.alone = true;
+      c.split((int)total);
+    }
+  }
+
+  // the tokens that stay: keys above thr, and of the tokens whose key is thr
+  // those up to id tie_end
   uint32_t thr = 0;
-  u64 ties = ~0ull, same = 0;
-  const int k = a.top_k ? a.top_k[m] : 0;
-  const float p = a.top_p ? a.top_p[m] : 1.f;
-  u64 above, at, total;
-  if (k > 0 && k < a.vocab) {
-    c.select(0, top_key, (double)k, [](uint32_t) -> u64 { return 1; }, thr, above, at);
-    ties = min((u64)k - above, at);
+  int tie_end = kAllTies;
+  u64 ties = 0, same = 0;  // how many of the `same` tokens of key thr stay
+  if (by_count) {
+    c.select<1, kBinBits, false>(0, top_key, (u64)k, Ones{}, thr, above, at);
+    ties = (u64)k - above;  // at most `at`: k is reached there
     same = at;
   }
-  if (p < 1.f) {
-    u64 sum = 0, below;
-    for (int i = c.seg0 + c.lane; i < c.seg1; i += 32) {
-      const uint32_t key = key_of(c.data[i]);
-      if (key > thr) sum += weight(key);
+  if (by_mass) {
+    if (by_count) {
+      c.team_scan(mass_above(thr), row_mass);
+      row_mass += ties * weight(thr);
     }
-    c.cluster_scan(c.cta_sum(warp_sum(sum)), below, total);
-    const u64 at_thr = same ? weight(thr) : 0;
-    total += same ? ties * at_thr : 0;
-    double target = (double)p * (double)total;
-    if (!(target > 0.)) target = 0.5;  // the first token stays in any case
+    // 64-bit arithmetic is slow on this GPU: one thread does it for all
+    if (tid == 0) {
+      const double limit = (double)p * (double)row_mass;
+      s.shared[0] = limit > 0. ? whole_of(limit) : 1;  // 1: the first token stays in any case
+    }
+    __syncthreads();
+    const u64 target = s.shared[0];
     uint32_t key;
-    c.select(thr, top_key, target, weight, key, above, at);
-    const u64 w = weight(key), all = at / w;
-    u64 fit = (u64)fmax(1., ceil((target - (double)above) / (double)w));
-    // the last of them by the definition's own comparison
-    while (fit > 1 && !((double)(above + (fit - 1) * w) < target)) --fit;
-    while ((double)(above + fit * w) < target) ++fit;
-    ties = min(fit, key == thr && same ? ties : all);
-    same = all;
+    c.select<3, kBinBits, false>(thr, top_key, target, weights, key, above, at);
+    const u64 w = weight(key);
+    if (at == w) {
+      ties = same = 1;
+    } else {
+      if (tid == 0) {
+        const u64 every = at / w, fit = (target - above + w - 1) / w;
+        s.shared[0] = min(fit, key == thr && same ? ties : every);
+        s.shared[1] = every;
+      }
+      __syncthreads();
+      ties = s.shared[0];
+      same = s.shared[1];
+    }
     thr = key;
   }
-  const bool partial = same && ties < same;
-  const double least = a.min_p ? (double)fminf(a.min_p[m], 1.f) * (double)kOne : 0.;
-
-  // tokens of key thr before this warp's part, where only some of them stay
-  u64 tie0 = 0;
-  if (partial) {
-    u64 mine = 0, all;
-    for (int i = c.seg0 + c.lane; i < c.seg1; i += 32) mine += key_of(c.data[i]) == thr;
-    mine = c.cta_sum(warp_sum(mine));
-    c.cluster_scan(mine, tie0, all);
-    for (int w = 0; w < c.warp; ++w) tie0 += s.sums[w];
-  }
-  // weight of element i (0: it does not stay), all lanes of a warp in step
-  auto staying = [&](int i, u64& tie) -> u64 {
-    const uint32_t key = i < c.seg1 ? key_of(c.data[i]) : 0u;
-    bool stays = i < c.seg1 && (key > thr || !same || key == thr);
-    if (partial) {
-      const unsigned eq = __ballot_sync(0xffffffffu, i < c.seg1 && key == thr);
-      if (key == thr) stays = stays && tie + __popc(eq & ((1u << c.lane) - 1)) < ties;
-      tie += __popc(eq);
-    }
-    if (!stays || (same && key < thr)) return 0;
-    const u64 w = weight(key);
-    return (double)w >= least ? w : 0;
-  };
-  u64 sum = 0, tie = tie0, below;
-  for (int i = c.seg0; i < c.seg1; i += 32) sum += staying(i + c.lane, tie);
-  sum = warp_sum(sum);
-  const u64 mine = c.cta_sum(sum);
-  c.cluster_scan(mine, below, total);
-  const u64 wanted = min((u64)((double)a.u[m] * (double)total), total - 1);
-  for (int w = 0; w < c.warp; ++w) below += s.sums[w];
-  if (wanted >= below && wanted < below + sum) {  // the token lies in this warp's part
-    tie = tie0;
-    u64 base = below;
-    for (int i = c.seg0; i < c.seg1; i += 32) {
-      const u64 w = staying(i + c.lane, tie);
-      u64 upto = w;
+  if (same && ties < same) {
+    // the id of the last of them: the thread that holds it tells all
+    u64 count = 0;
+    c.each4([&](int, const uint32_t (&key)[4]) {
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const u64 o = __shfl_up_sync(0xffffffffu, upto, d);
-        if (c.lane >= d) upto += o;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, base + upto > wanted);
-      if (past) {
-        if (c.lane == __ffs(past) - 1) {
-          a.tokens[m] = begin + i + c.lane;
-          if (a.probs) a.probs[m] = (float)((double)w / (double)total);
-        }
-        break;
-      }
-      base += __shfl_sync(0xffffffffu, upto, 31);
+      for (int j = 0; j < 4; ++j) count += key[j] == thr;
+    });
+    u64 before = c.team_scan(count, total);
+    if (before < ties && ties <= before + count) {
+      int i = c.i0;
+      for (;; ++i)
+        if (c.key(i) == thr && ++before == ties) break;
+      for (int r = 0; r < c.size; ++r) *c.peer(&s.tie_end, r) = c.id(i);
     }
+    c.sync();
+    tie_end = s.tie_end;
   }
-  cluster.sync();  // no CTA leaves while another may read its sums
+  // ceil(2^38 min_p), exact in fp32: a power of two times it
+  const u64 least = min_p > 0.f ? (u64)ceilf(fminf(min_p, 1.f) * kOne) : 0;
+
+  // weights of keys i .. i + 3, 0 where the token does not stay
+  auto staying = [&](int i, const uint32_t (&key)[4], u64 (&w)[4]) {
+    weights(key, w);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (w[j] < least || key[j] < thr || (key[j] == thr && tie_end != kAllTies && c.id(i + j) > tie_end)) w[j] = 0;
+  };
+  u64 sum = 0;
+  c.each4([&](int i, const uint32_t (&key)[4]) {
+    if (max(max(key[0], key[1]), max(key[2], key[3])) < thr) return;
+    u64 w[4];
+    staying(i, key, w);
+    sum += (w[0] + w[1]) + (w[2] + w[3]);
+  });
+  u64 before = c.team_scan(sum, total);
+  if (tid == 0) s.shared[0] = min((u64)((double)u * (double)total), total - 1);
+  __syncthreads();
+  const u64 wanted = s.shared[0];
+  if (wanted >= before && wanted < before + sum) {  // the token is one of this thread's
+    bool found = false;
+    c.each4([&](int i, const uint32_t (&key)[4]) {
+      u64 w[4];
+      staying(i, key, w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        before += w[j];
+        if (!found && before > wanted) {
+          found = true;
+          a.tokens[m] = c.id(i + j);
+          if (a.probs) a.probs[m] = quotient(w[j], total);
+        }
+      }
+    });
+  }
+  c.sync();  // no CTA leaves while another may read its sums
 }
 
 }  // namespace
@@ -342,20 +637,25 @@ extern "C" int moe_sample(const float* logits, int64_t row_stride, int rows, int
   int rc = check_device();
   if (rc != MOE_OK) return rc;
   int cluster = kMaxCluster;
-  while (cluster > 1 && (rows * cluster > 1024 || (vocab + cluster - 1) / cluster < kSampleThreads)) cluster /= 2;
-  SampleArgs a{logits, row_stride, vocab, (vocab + cluster - 1) / cluster, false, u, temperature, top_k, top_p, min_p,
+  while (cluster > 1 && (rows * cluster > 1024 || (vocab + cluster - 1) / cluster < kSampleThreads) &&
+         (vocab + cluster / 2 - 1) / (cluster / 2) <= kMaxSlice)
+    cluster /= 2;
+  SampleArgs a{logits, row_stride, vocab, (vocab + cluster - 1) / cluster, u, temperature, top_k, top_p, min_p,
                tokens, probs};
-  a.cached = a.slice <= kMaxCached;
-  const size_t smem = a.cached ? (size_t)a.slice * 4 : 0;
+  const bool cached = a.slice <= kMaxCached;
+  const size_t smem = sizeof(Shared) + (cached ? (size_t)a.slice * 4 : 0);
   static thread_local int ready = -1;  // device whose kernel attributes this thread has set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && ready != dev) {
-    if ((e = cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxCached * 4)) ==
-        cudaSuccess)
-      e = cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    for (auto kernel : {sample_kernel<true>, sample_kernel<false>}) {
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)sizeof(Shared) + kMaxCached * 4);
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    }
     if (e == cudaSuccess) ready = dev;
   }
   if (e != cudaSuccess) return fail_cuda(e, "sampling set-up");
-  return launch_pdl(sample_kernel, dim3((unsigned)(rows * cluster)), dim3(kSampleThreads), smem, stream, cluster, a);
+  return launch_pdl(cached ? sample_kernel<true> : sample_kernel<false>, dim3((unsigned)(rows * cluster)), dim3(kSampleThreads), smem, stream, cluster, a);
 }
