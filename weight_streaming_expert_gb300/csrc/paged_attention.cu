@@ -33,6 +33,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "attention.h"
@@ -45,14 +46,15 @@ namespace {
 enum : int { kAttnBadPage = 1, kAttnBadLength = 2, kAttnTimeout = 4 };
 
 constexpr int kTile = 128;                 // query rows of a tile, and positions
-constexpr int kAttnThreads = 384;          // two softmax warpgroups; the MMA warp, the copy warp and two idle ones
-constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;  // 2 x 128 x 224 + 128 x 56 = 384 x 168, the launch's total
-constexpr int kMmaWarp = 8, kCopyWarp = 9;
+constexpr int kHalf = 64;                  // positions of a softmax step
+constexpr int kAttnThreads = 384;          // two softmax warpgroups, the MMA warp, the copy warp, two query warps
+constexpr int kMmaWarp = 8, kCopyWarp = 9, kQueryWarp = 10;  // and 11
 constexpr int kMaxBatch = 4096;
 constexpr int kMaxStages = 10;
 constexpr uint32_t kHeadBytes = 2048;      // barriers, plan and the exchange area before the tiles
 constexpr float kRescaleLog2 = 8.f;
-constexpr int kJoinThreads = 128, kJoinSplit = 16;
+constexpr int kJoinRows = 4, kJoinGroups = 4;  // rows of a joining CTA, and threads that share a row's parts
+constexpr int kMaxSpread = 8;              // key/value heads that neighbouring CTAs work on side by side
 
 template <typename T>
 __device__ __forceinline__ uint32_t pack(float x, float y);
@@ -102,12 +104,14 @@ __device__ __forceinline__ void max3(float& top, uint32_t x, uint32_t y) {
 struct Cut {
   int parts, b, h, tile;
 };
+constexpr int kMaxParts = 1024;            // CTAs, which is at least the shares of one tile
 
 struct AttnParams {
   moe_attn_args_t a;
   int n_kv_heads, group;
+  int spread;       // CTAs c, c + 1, .., c + spread - 1 do the same share of as many heads
   int* status;
-  float* part_o;    // [CTAs][2][D / 4][rows of an item] float4: unnormalised sums
+  float* part_o;    // [CTAs][2][rows of an item][D]: unnormalised sums
   float2* part_ml;  // [CTAs][2][rows of an item]: (m, sum of p)
   Cut* cuts;        // [CTAs]
 };
@@ -141,16 +145,25 @@ __device__ __forceinline__ int units_of(const AttnParams& p, const Seq& s, int i
   return max(1, (end + kTile - 1) / kTile);
 }
 
+// x / y, in 32 bits where they do: a 64-bit division takes some hundred
+// instructions on the way to the first copy.
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+  return (x | y) >> 32 ? x / y : (long long)((uint32_t)x / (uint32_t)y);
+}
+
 // A CTA's next piece of work.
 struct Item {
   int b, h, tile, u0, u1, units;
   Seq s;
 };
 
+// The list is split into equal shares, of which `spread` neighbouring CTAs do
+// the same one, each for a head of its own: what they read of a position lies
+// side by side in memory and is read at about the same time.
 struct Plan {
-  long long total, start, todo;  // of the whole list; where this CTA's share begins, and its length
-  int parts;                     // CTAs with a share (each at least one unit)
-  int b, h, tile, u0;
+  long long start, todo;  // where this CTA's share begins, and its length
+  long long share;        // of every CTA but the last
+  int b, h, tile, u0;     // h counts groups of `spread` heads
 };
 
 template <int kRows>
@@ -171,11 +184,11 @@ struct Walk {
       }
       if (tile * kRows < s.rows) break;
       tile = 0;
-      if (s.rows > 0 && ++h < p.n_kv_heads) continue;
+      if (s.rows > 0 && ++h < p.n_kv_heads / p.spread) continue;
       h = 0;
       ++b;
     }
-    it.b = b, it.h = h, it.tile = tile, it.s = s;
+    it.b = b, it.h = h * p.spread + (int)blockIdx.x % p.spread, it.tile = tile, it.s = s;
     it.units = units_of<kRows>(p, s, tile);
     it.u0 = u0;
     it.u1 = (int)min((long long)it.units, u0 + todo);
@@ -197,15 +210,15 @@ struct Waiter {
   int* status;
   __device__ void operator()(uint32_t bar, uint32_t parity) const {
     if (mbar_try_wait(bar, parity)) return;
-    if (*gone) return;
-    unsigned long long waited;
-    // in slices, so that a wait ends soon after another one has given up
-    for (int i = 0; i < 200; ++i) {
-      if (mbar_wait(bar, parity, &waited, kWaitTimeoutNs / 200)) return;
+    const unsigned long long t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity)) {
       if (*gone) return;
+      if (global_timer_ns() - t0 > kWaitTimeoutNs) {
+        *gone = 1;
+        atomicOr(status, kAttnTimeout);
+        return;
+      }
     }
-    *gone = 1;
-    atomicOr(status, kAttnTimeout);
   }
 };
 
@@ -236,13 +249,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   auto full = [&](int s) { return sb + 8u * s; };
   auto empty = [&](int s) { return sb + 80u + 8u * s; };
   auto q_full = [&](int t) { return sb + 160u + 8u * t; };
-  auto s_full = [&](int t) { return sb + 176u + 8u * t; };
-  auto p_full = [&](int t) { return sb + 192u + 8u * t; };
-  auto o_full = [&](int t) { return sb + 208u + 8u * t; };
-  const uint32_t drained = sb + 224u;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + 232);
-  int* gone = reinterpret_cast<int*>(smem + 236);
-  Plan& plan = *reinterpret_cast<Plan*>(smem + 256);
+  auto q_empty = [&](int t) { return sb + 176u + 8u * t; };
+  auto s_full = [&](int t) { return sb + 192u + 8u * t; };
+  auto p_full = [&](int t, int half) { return sb + 208u + 16u * t + 8u * half; };
+  auto o_done = [&](int t, int half) { return sb + 240u + 16u * t + 8u * half; };
+  const uint32_t drained = sb + 272u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + 280);
+  int* gone = reinterpret_cast<int*>(smem + 284);
+  Plan& plan = *reinterpret_cast<Plan*>(smem + 288);
   float2* exchange = reinterpret_cast<float2*>(smem + 1024);        // [128]: the odd chain's (m, sum)
   const uint32_t q_at = sb + kHeadBytes, ring = q_at + L::kQTiles * kTileBytes;
   uint8_t* q_smem = smem + kHeadBytes;
@@ -256,10 +270,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(empty(s), 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(q_full(t), kPair ? 4 : 8);
+      mbar_init(q_full(t), kPair ? 1 : 2);
+      mbar_init(q_empty(t), 1);
       mbar_init(s_full(t), 1);
-      mbar_init(p_full(t), 4);
-      mbar_init(o_full(t), 1);
+      for (int half = 0; half < 2; ++half) {
+        mbar_init(p_full(t, half), 4);
+        mbar_init(o_done(t, half), 1);
+      }
     }
     mbar_init(drained, 1);
     fence_mbar_init();
@@ -305,26 +322,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const long long o = __shfl_up_sync(0xffffffffu, upto, m);
         if (lane >= m) upto += o;
       }
-      const long long total = __shfl_sync(0xffffffffu, upto, 31) * p.n_kv_heads;
-      const int parts = (int)min((long long)gridDim.x, total), c = min((int)blockIdx.x, parts);
-      const long long start = parts ? total * c / parts : 0;
-      const long long end = c < parts ? total * (c + 1) / parts : start;
+      const int heads = p.n_kv_heads / p.spread, shares = gridDim.x / p.spread, c = blockIdx.x / p.spread;
+      const long long total = __shfl_sync(0xffffffffu, upto, 31) * heads;
+      // equal shares of whole units: fewer CTAs, and cuts, where there are few
+      const long long share = quotient(total + shares - 1, shares);
+      const long long start = share * c, end = min(total, start + share);
       if (lane == 0) {
-        plan.total = total;
         plan.start = start;
-        plan.todo = end - start;
-        plan.parts = parts;
+        plan.todo = max(0ll, end - start);
+        plan.share = share;
       }
-      long long at = (upto - sum) * p.n_kv_heads;
-      if (end > start && start >= at && start < upto * p.n_kv_heads) {  // one lane
+      long long at = (upto - sum) * heads;
+      if (end > start && start >= at && start < upto * heads) {  // one lane
         int b = b0;
-        while (start >= at + cost[b] * p.n_kv_heads) at += cost[b++] * p.n_kv_heads;
+        while (start >= at + cost[b] * heads) at += cost[b++] * heads;
         const Seq s = load_seq(p, b);
-        long long rest = (start - at) % cost[b];
+        const long long h = quotient(start - at, cost[b]);
+        long long rest = start - at - h * cost[b];
         int tile = 0;
         for (int u; rest >= (u = units_of<kRows>(p, s, tile)); ++tile) rest -= u;
         plan.b = b;
-        plan.h = (int)((start - at) / cost[b]);
+        plan.h = (int)h;
         plan.tile = tile;
         plan.u0 = (int)rest;
       }
@@ -339,7 +357,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   if (tid == 0) p.cuts[blockIdx.x].parts = 0;
 
   if (warp < kMmaWarp) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     Walk<kRows> walk(p, plan);
     Item it{};
     // ---- softmax: chain 0 in warps 0-3, chain 1 in warps 4-7, a row per thread
@@ -349,33 +366,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t s_at = tmem + lane_at + chain * kTile, o_at = tmem + lane_at + 2 * kTile + chain * D;
     const float c = a.scale * 1.4426950408889634f;  // exponents in base 2
     const float rescale = kRescaleLog2 / c;
-    int s_round = 0, o_round[2] = {0, 0};  // products finished or under way, of both chains
+    int tiles[2] = {0, 0};  // tiles of positions of the even and the odd chain before this item
     while (walk.next(it)) {
       const int row0 = it.tile * kRows + q_tile * kTile;
-      // queries into shared memory, each 16-byte chunk a thread; rows past the
-      // last become zeros
-      {
-        constexpr int kChunks = D / 8;
-        constexpr int kLoaders = kPair ? 128 : 256;
-        const int loader = kPair ? r : tid;
-        const int cc = loader % kChunks;
-        uint8_t* dst = q_smem + q_tile * kTileBytes + (cc / 8) * kPanel;
-#pragma unroll 8
-        for (int row = loader / kChunks; row < kTile; row += kLoaders / kChunks) {
-          const int g = row0 + row;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (g < it.s.rows) {
-            const int token = g / p.group, head = it.h * p.group + g % p.group;
-            v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
-                                                (long long)(it.s.q0 + token) * a.q_token_stride +
-                                                head * a.q_head_stride + cc * 8);
-          }
-          *reinterpret_cast<uint4*>(dst + row * 128 + ((cc % 8) ^ (row % 8)) * 16) = v;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full(kPair ? chain : 0));
-      }
       const int g = row0 + r;
       const bool valid = g < it.s.rows;
       const bool warp_valid = row0 + (r & ~31) < it.s.rows;
@@ -386,95 +379,97 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int end = !valid ? 0 : a.tree_mask ? it.s.kv : min(it.s.kv, max(0, it.s.base + token + 1));
       const int plain = a.tree_mask ? max(0, min(it.s.base, end)) : end;
       float m = -INFINITY, l = 0.f;
-      const int first = kPair ? it.u0 : it.u0 + chain, step = kPair ? 1 : 2;
-      int done = 0;
-      auto softmax_tile = [&](int u, int left, auto masked_type) {
-          constexpr bool masked = decltype(masked_type)::value;
-          uint32_t s[kTile];
+      int done = 0;  // tiles of this chain in this item
+      // One step: 64 positions, straight through with or without masking (a
+      // branch around the masking alone would hold the scores twice).
+      auto softmax_step = [&](int half, int first_pos, auto masked_type) {
+        constexpr bool masked = decltype(masked_type)::value;
+        uint32_t s[kHalf];
+        tmem_ld32(s_at + kHalf * half, s);
+        tmem_ld32(s_at + kHalf * half + 32, s + 32);
+        tmem_wait_ld();
+        if (masked) {
+          // a bit for each column: those below `plain`, and a tree's
+          const int left = plain - first_pos, sh = it.s.base - first_pos;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, s + 32 * i);
-          tmem_wait_ld();
-          if (masked) {
-            // a bit for each column: those below `left`, and a tree's
-            const int sh = it.s.base - u * kTile;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              uint32_t seen = below(left - 32 * w);
-              if (a.tree_mask) {
-                const int k = 32 * w - sh;
-                const unsigned long long part = k >= 64 || k <= -32 ? 0ull : k >= 0 ? bits >> k : bits << -k;
-                seen |= (uint32_t)part & below(end - u * kTile - 32 * w);
-              }
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((seen >> i) & 1)) s[32 * w + i] = 0xff800000u;
+          for (int w = 0; w < 2; ++w) {
+            uint32_t seen = below(left - 32 * w);
+            if (a.tree_mask) {
+              const int k = 32 * w - sh;
+              const unsigned long long part = k >= 64 || k <= -32 ? 0ull : k >= 0 ? bits >> k : bits << -k;
+              seen |= (uint32_t)part & below(end - first_pos - 32 * w);
             }
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((seen >> i) & 1)) s[32 * w + i] = 0xff800000u;
           }
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        }
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < kTile; i += 2) max3(top[(i / 2) & 3], s[i], s[i + 1]);
-          const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-          float shrink = 1.f;
-          if (high > m + rescale || m == -INFINITY) {
-            if (m != -INFINITY) shrink = exp2_approx((m - high) * c);
-            m = high;
+        for (int i = 0; i < kHalf; i += 2) max3(top[(i / 2) & 3], s[i], s[i + 1]);
+        const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        float shrink = 1.f;
+        if (high > m + rescale || m == -INFINITY) {
+          if (m != -INFINITY) shrink = exp2_approx((m - high) * c);
+          m = high;
+        }
+        if ((done > 0 || half > 0) && __any_sync(0xffffffffu, shrink != 1.f)) {
+          // the products so far have to be in before their sums shrink: those
+          // of the tiles before are, for this tile's scores came after them
+          if (half > 0) wait(o_done(chain, 0), (tiles[0] * (1 - chain) + tiles[1] * chain + done) & 1);
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t o[16];
+            tmem_ld16(o_at + 16 * i, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * shrink);
+            tmem_st16(o_at + 16 * i, o);
           }
-          if (done > 0 && __any_sync(0xffffffffu, shrink != 1.f)) {
-            // the products so far have to be in before their sums shrink
-            wait(o_full(chain), (o_round[chain] + done - 1) & 1);
-            tc_fence_after();
+          l *= shrink;
+        }
+        const float off = m == -INFINITY ? 0.f : m * c;
+        const uint64_t c2 = pair_of(c, c), off2 = pair_of(-off, -off);
+        uint64_t sum[2] = {0ull, 0ull};  // two pairs of fp32 zeros
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-              uint32_t o[32];
-              tmem_ld32(o_at + 32 * i, o);
-              tmem_wait_ld();
+        for (int i = 0; i < 2; ++i) {
+          uint32_t packed[16];
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * shrink);
-              tmem_st32(o_at + 32 * i, o);
-            }
-            l *= shrink;
+          for (int k = 0; k < 16; ++k) {
+            const uint64_t z = fma2(pair_of(s[32 * i + 2 * k], s[32 * i + 2 * k + 1]), c2, off2);
+            const float x = exp2_approx(low_of(z)), y = exp2_approx(high_of(z));
+            sum[k & 1] = add2(sum[k & 1], pair_of(x, y));
+            packed[k] = pack<T>(x, y);
           }
-          const float off = m == -INFINITY ? 0.f : m * c;
-          const uint64_t c2 = pair_of(c, c), off2 = pair_of(-off, -off);
-          uint64_t sum[2] = {0ull, 0ull};  // two pairs of fp32 zeros
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t packed[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const uint64_t z = fma2(pair_of(s[32 * i + 2 * k], s[32 * i + 2 * k + 1]), c2, off2);
-              const float x = exp2_approx(low_of(z)), y = exp2_approx(high_of(z));
-              sum[k & 1] = add2(sum[k & 1], pair_of(x, y));
-              packed[k] = pack<T>(x, y);
-            }
-            tmem_st16(s_at + 16 * i, packed);
-          }
-          sum[0] = add2(sum[0], sum[1]);
-          l += low_of(sum[0]) + high_of(sum[0]);
-          tmem_wait_st();
+          tmem_st16(s_at + kHalf / 2 * half + 16 * i, packed);
+        }
+        sum[0] = add2(sum[0], sum[1]);
+        l += low_of(sum[0]) + high_of(sum[0]);
+        tmem_wait_st();
       };
-      for (int u = first; u < it.u1; u += step) {
-        wait(s_full(chain), s_round++ & 1);
+      for (int u = kPair ? it.u0 : it.u0 + chain; u < it.u1; u += kPair ? 1 : 2) {
+        wait(s_full(chain), (tiles[0] * (1 - chain) + tiles[1] * chain + done) & 1);
         tc_fence_after();
-        const int left = plain - u * kTile;  // columns below it are seen
-        if (warp_valid) {
-          // straight through in either form: a branch around the masking alone
-          // would hold the scores twice
-          if (__any_sync(0xffffffffu, left < kTile))
-            softmax_tile(u, left, std::true_type{});
-          else
-            softmax_tile(u, left, std::false_type{});
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          const int first_pos = u * kTile + half * kHalf;
+          if (warp_valid) {
+            if (__any_sync(0xffffffffu, plain < first_pos + kHalf))
+              softmax_step(half, first_pos, std::true_type{});
+            else
+              softmax_step(half, first_pos, std::false_type{});
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(chain, half));
         }
         ++done;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(chain));
       }
       // ---- the end of the item
       const int n = it.u1 - it.u0;
-      int count[2];
-      count[0] = kPair ? n : (n + 1) / 2;
-      count[1] = kPair ? n : n / 2;
+      // both chains' tiles in this item
+      const int count0 = kPair ? n : (n + 1) / 2, count1 = kPair ? n : n / 2;
       const bool cut = n < it.units;
       const int slot = 2 * blockIdx.x + (it.u0 == 0 ? 1 : 0);
       const int local = kPair ? chain * kTile + r : r;  // row of the item
@@ -494,10 +489,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         f1 = odd.x == -INFINITY ? 0.f : exp2_approx((odd.x - m) * c);
         l = even.y * f0 + odd.y * f1;
       }
-      for (int t = 0; t < 2; ++t)
-        if ((!kPair || t == chain) && count[t] > 0) wait(o_full(t), (o_round[t] + count[t] - 1) & 1);
-      o_round[0] += count[0];
-      o_round[1] += count[1];
+      tiles[0] += count0;
+      tiles[1] += count1;
+      // the last tile's products (the one's before are in)
+      if (!kPair || chain == 0) wait(o_done(0, 1), (tiles[0] - 1) & 1);
+      if (kPair ? chain == 1 : count1 > 0) wait(o_done(1, 1), (tiles[1] - 1) & 1);
       tc_fence_after();
       if (warp_valid) {
         const float norm = cut ? 1.f : (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
@@ -506,13 +502,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const uint32_t even_at = tmem + lane_at + 2 * kTile + (kPair ? chain * D : 0);
         T* out = static_cast<T*>(a.out) + (long long)(it.s.q0 + token) * a.out_token_stride +
                  (it.h * p.group + (valid ? g % p.group : 0)) * a.out_head_stride;
-        float4* part = reinterpret_cast<float4*>(p.part_o) + (long long)slot * (D / 4) * kRows + local;
+        float4* part = reinterpret_cast<float4*>(p.part_o) + ((long long)slot * kRows + local) * (D / 4);
 #pragma unroll
         for (int i = 0; i < kBlocks; ++i) {
           uint32_t o[32];
           tmem_ld32(even_at + 32 * (block0 + i), o);
           tmem_wait_ld();
-          if (!kPair && count[1] > 0) {
+          if (!kPair && count1 > 0) {
             uint32_t o1[32];
             tmem_ld32(even_at + D + 32 * (block0 + i), o1);
             tmem_wait_ld();
@@ -525,7 +521,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (cut) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              part[(long long)(8 * (block0 + i) + k) * kRows] =
+              part[8 * (block0 + i) + k] =
                   make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]), __uint_as_float(o[4 * k + 2]),
                               __uint_as_float(o[4 * k + 3]));
           } else {
@@ -549,15 +545,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
       }
       if (cut && it.u0 == 0 && tid == 0) {
-        // this share ends inside the tile: which CTA's share holds its last unit
-        const long long last = plan.start + (plan.todo - walk.todo) - n + it.units;  // the tile's end in the list
-        const long long e = (last * plan.parts + plan.total - 1) / plan.total - 1;
-        p.cuts[blockIdx.x] = Cut{(int)(e - blockIdx.x) + 1, it.b, it.h, it.tile};
+        // this share ends inside the tile: which share holds its last unit
+        const long long last = plan.start + (plan.todo - walk.todo) - n + it.units - 1;
+        const int e = (int)quotient(last, plan.share);
+        p.cuts[blockIdx.x] = Cut{e - (int)blockIdx.x / p.spread + 1, it.b, it.h, it.tile};
       }
       if (!kPair) named_sync(1, 256);  // both chains' sums are read before the next item's
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kCopyWarp) {
     Walk<kRows> walk(p, plan);
     Item it{};
@@ -606,13 +601,37 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       unsigned long long waited;
       mbar_wait(full(f % kStages), (f / kStages) & 1, &waited);
     }
+    } else if (warp >= kQueryWarp) {
+      // ---- queries into shared memory with asynchronous 16-byte copies: a
+      // tile of the pair per warp, or half of the rows; rows past the last
+      // become zeros
+      Walk<kRows> walk(p, plan);
+      Item it{};
+      constexpr int kChunks = D / 8, kMine = kPair ? kTile : kTile / 2;
+      const int w = warp - kQueryWarp, t = kPair ? w : 0, from = kPair ? 0 : w * kMine;
+      const int cc = lane % kChunks;
+      const uint32_t dst = q_at + t * kTileBytes + (cc / 8) * kPanel;
+      for (int round = 0; walk.next(it); ++round) {
+        if (round > 0) wait(q_empty(t), (round - 1) & 1);
+#pragma unroll 4
+        for (int row = from + lane / kChunks; row < from + kMine; row += 32 / kChunks) {
+          const int g = it.tile * kRows + t * kTile + row, gc = min(g, it.s.rows - 1), token = gc / p.group;
+          const T* src = static_cast<const T*>(a.q) + (long long)(it.s.q0 + token) * a.q_token_stride +
+                         (it.h * p.group + gc - token * p.group) * a.q_head_stride + cc * 8;
+          copy16_async(dst + row * 128 + ((cc % 8) ^ (row % 8)) * 16, src, g < it.s.rows);
+        }
+        copies_done();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full(t));
+      }
     } else if (warp == kMmaWarp) {
     Walk<kRows> walk(p, plan);
     Item it{};
     // ---- products, issued by lane 0
     constexpr uint32_t kDescS = mma_desc(std::is_same<T, __nv_bfloat16>::value, false, kTile, kTile);
     constexpr uint32_t kDescO = mma_desc(std::is_same<T, __nv_bfloat16>::value, true, kTile, D);
-    int taken = 0, q_round = 0, p_round[2] = {0, 0};
+    int taken = 0, q_round = 0, p_round[2] = {0, 0};  // p_round: units of a chain
     auto next_stage = [&]() {
       const int stage = taken % kStages;
       wait(full(stage), (taken / kStages) & 1);
@@ -631,19 +650,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
     };
     auto products = [&](int chain, int stage, bool add) {
-      wait(p_full(chain), p_round[chain]++ & 1);
-      tc_fence_after();
-      if (lane == 0) {
-        const uint64_t vd = smem_desc(ring + stage * kTileBytes, kPanel, 1024);
+      const uint32_t parity = p_round[chain]++ & 1;
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          mma_ts(tmem + 2 * kTile + chain * D, tmem + chain * kTile + k * 8, vd + k * 128,
-                 kDescO, add || k > 0);
-        mma_commit(o_full(chain));
+      for (int half = 0; half < 2; ++half) {
+        wait(p_full(chain, half), parity);
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t vd = smem_desc(ring + stage * kTileBytes, kPanel, 1024);
+#pragma unroll
+          for (int k = half * (kHalf / 16); k < (half + 1) * (kHalf / 16); ++k)
+            mma_ts(tmem + 2 * kTile + chain * D, tmem + chain * kTile + k * 8, vd + k * 128, kDescO, add || k > 0);
+          mma_commit(o_done(chain, half));
+        }
       }
     };
     auto release = [&](int stage) {
       if (lane == 0) mma_commit(empty(stage));
+    };
+    // the item's scores are all issued: its queries make room for the next
+    auto release_queries = [&]() {
+      if (lane == 0) {
+        mma_commit(q_empty(0));
+        if (kPair) mma_commit(q_empty(1));
+      }
     };
     // Rows of the cache past the sequence's end hold anything, and 0 * NaN is
     // NaN: they become zeros.
@@ -670,6 +699,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         wait(q_full(1), q_round & 1);
         scores(1, 1, ks);
         release(ks);
+        if (n == 1) release_queries();
         for (int j = 0; j < n; ++j) {
           const int vs = value_stage(it.u0 + j);
           products(0, vs, j > 0);
@@ -682,6 +712,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (j + 1 < n) {
             scores(1, 1, ks);
             release(ks);
+            if (j + 2 == n) release_queries();
           }
         }
       } else {
@@ -690,6 +721,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           tc_fence_after();
           scores(j, 0, ks);
           release(ks);
+          if (j + 1 == n) release_queries();
         }
         for (int j = 0; j < n; ++j) {
           const int vs = value_stage(it.u0 + j);
@@ -699,6 +731,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int ks = next_stage();
             scores(j & 1, 0, ks);
             release(ks);
+            if (j + 3 == n) release_queries();
           }
         }
       }
@@ -716,47 +749,83 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 }
 
 // Joins the tiles that shares have cut: out = sum_i O_i 2^(c (m_i - m)) / sum_i
-// l_i 2^(c (m_i - m)) in the order of the shares.  Block (c, y): the tile that
-// was cut at the end of share c, 32 rows by 16 columns at a time.
+// l_i 2^(c (m_i - m)) in the order of the shares.  Block (c, y): of the tile
+// that was cut at the end of CTA c's share, 4 rows at a time.  What it costs is
+// the latency of its reads, so all of a row's statistics are read at once, by
+// the lanes of a warp, and then its parts by four threads per column, whose
+// sums are added in order.
 template <typename T, int D, int kRows>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4) join_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int kColumns = D / 4;
+  __shared__ float factor[kJoinRows][kMaxParts];
+  __shared__ float4 sums[kJoinGroups - 1][kJoinRows][kColumns];
+  __shared__ float2 total[kJoinRows];  // (1 / sum, log-sum)
   const moe_attn_args_t& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int column = tid % kColumns, row = tid / kColumns % kJoinRows, part = tid / (kColumns * kJoinRows);
   pdl_wait();
   pdl_launch_dependents();
   const Cut cut = p.cuts[blockIdx.x];
   if (cut.parts == 0) return;
   const Seq s = load_seq(p, cut.b);
   const int rows = min(kRows, s.rows - cut.tile * kRows);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float c = a.scale * 1.4426950408889634f;
-  auto slot = [&](int i) { return 2ll * (blockIdx.x + i) + (i == 0 ? 1 : 0); };
-  for (int w = blockIdx.y; w < (rows + 31) / 32 * (D / 16); w += gridDim.y) {
-    const int row = w / (D / 16) * 32 + lane, d4 = w % (D / 16) * 4 + warp;
-    if (row >= rows) continue;
-    float m = -INFINITY;
-#pragma unroll 4
-    for (int i = 0; i < cut.parts; ++i) m = fmaxf(m, p.part_ml[slot(i) * kRows + row].x);
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = 0; i < cut.parts; ++i) {
-      const float2 ml = p.part_ml[slot(i) * kRows + row];
-      const float4 v = reinterpret_cast<const float4*>(p.part_o)[(slot(i) * (D / 4) + d4) * kRows + row];
-      const float f = ml.x == -INFINITY ? 0.f : exp2_approx((ml.x - m) * c);
-      l += ml.y * f;
-      o.x += v.x * f;
-      o.y += v.y * f;
-      o.z += v.z * f;
-      o.w += v.w * f;
+  auto slot = [&](int i) { return 2ll * (blockIdx.x + i * p.spread) + (i == 0 ? 1 : 0); };
+  for (int r0 = blockIdx.y * kJoinRows; r0 < rows; r0 += gridDim.y * kJoinRows) {
+    if (warp < kJoinRows && r0 + warp < rows) {
+      float m = -INFINITY, l = 0.f;
+      for (int i = lane; i < cut.parts; i += 32) m = fmaxf(m, p.part_ml[slot(i) * kRows + r0 + warp].x);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      for (int i = lane; i < cut.parts; i += 32) {
+        const float2 ml = p.part_ml[slot(i) * kRows + r0 + warp];
+        const float f = ml.x == -INFINITY ? 0.f : exp2_approx((ml.x - m) * c);
+        factor[warp][i] = f;
+        l += ml.y * f;
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+      if (lane == 0)
+        total[warp] = make_float2(l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l),
+                                  l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f);
     }
-    const float norm = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-    const int g = cut.tile * kRows + row, token = g / p.group, head = cut.h * p.group + g % p.group;
-    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (long long)(s.q0 + token) * a.out_token_stride +
-                              head * a.out_head_stride + d4 * 4) =
-        make_uint2(pack<T>(o.x * norm, o.y * norm), pack<T>(o.z * norm, o.w * norm));
-    if (a.lse && d4 == 0)
-      a.lse[(long long)(s.q0 + token) * (p.group * p.n_kv_heads) + head] =
-          l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f;
+    __syncthreads();
+    const bool mine = r0 + row < rows;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (mine) {
+      const int per = (cut.parts + kJoinGroups - 1) / kJoinGroups;
+#pragma unroll 8
+      for (int i = part * per; i < min(cut.parts, (part + 1) * per); ++i) {
+        const float f = factor[row][i];
+        const float4 v = reinterpret_cast<const float4*>(p.part_o)[(slot(i) * kRows + r0 + row) * kColumns + column];
+        if (f != 0.f) {
+          o.x = fmaf(v.x, f, o.x);
+          o.y = fmaf(v.y, f, o.y);
+          o.z = fmaf(v.z, f, o.z);
+          o.w = fmaf(v.w, f, o.w);
+        }
+      }
+      if (part > 0) sums[part - 1][row][column] = o;
+    }
+    __syncthreads();
+    if (mine && part == 0) {
+#pragma unroll
+      for (int q = 0; q < kJoinGroups - 1; ++q) {
+        const float4 v = sums[q][row][column];
+        o.x += v.x;
+        o.y += v.y;
+        o.z += v.z;
+        o.w += v.w;
+      }
+      const float norm = total[row].x;
+      const int g = cut.tile * kRows + r0 + row, token = g / p.group, head = cut.h * p.group + g % p.group;
+      *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (long long)(s.q0 + token) * a.out_token_stride +
+                                head * a.out_head_stride + column * 4) =
+          make_uint2(pack<T>(o.x * norm, o.y * norm), pack<T>(o.z * norm, o.w * norm));
+      if (a.lse && column == 0)
+        a.lse[(long long)(s.q0 + token) * (p.group * p.n_kv_heads) + head] = total[row].y;
+    }
+    __syncthreads();
   }
 }
 
@@ -830,10 +899,13 @@ template <typename T, int D, bool kPair>
 int launch_attn(const moe_attn* h, const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v,
                 moe_stream_t stream) {
   using L = Layout<D, kPair>;
-  const int rc = launch_pdl(paged_attention_kernel<T, D, kPair>, dim3(h->n_sms), dim3(kAttnThreads), L::kSmem, stream,
+  const int grid = h->n_sms / p.spread * p.spread;
+  const int rc = launch_pdl(paged_attention_kernel<T, D, kPair>, dim3(grid), dim3(kAttnThreads), L::kSmem, stream,
                             1, p, k, v);
   if (rc != MOE_OK) return rc;
-  return launch_pdl(join_kernel<T, D, L::kRows>, dim3(h->n_sms, kJoinSplit), dim3(kJoinThreads), 0, stream, 1, p);
+  const int rows = (int)std::min<long long>(L::kRows, (long long)p.a.max_q_len * p.group);
+  return launch_pdl(join_kernel<T, D, L::kRows>, dim3(grid, (rows + kJoinRows - 1) / kJoinRows),
+                    dim3(kJoinRows * kJoinGroups * D / 4), 0, stream, 1, p);
 }
 
 template <typename T, int D>
@@ -865,6 +937,7 @@ moe_attn_t* moe_attn_create(int n_heads, int n_kv_heads, int head_dim) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->n_sms, cudaDevAttrMultiProcessorCount, dev);
+  h->n_sms = std::min(h->n_sms, kMaxParts);
   if (e == cudaSuccess)
     e = head_dim == 64 ? allow_smem_both<__nv_bfloat16, 64>() : allow_smem_both<__nv_bfloat16, 128>();
   if (e == cudaSuccess) e = head_dim == 64 ? allow_smem_both<__half, 64>() : allow_smem_both<__half, 128>();
@@ -913,7 +986,10 @@ int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t strea
   if (rc == MOE_OK)
     rc = encode_cache(&v_map, *a, a->v_cache, a->v_row_stride, a->v_page_stride, h->n_kv_heads * h->head_dim);
   if (rc != MOE_OK) return rc;
-  const AttnParams p{*a, h->n_kv_heads, h->n_heads / h->n_kv_heads, h->status, h->part_o, h->part_ml, h->cuts};
+  int spread = 1;
+  while (spread < kMaxSpread && h->n_kv_heads % (2 * spread) == 0) spread *= 2;
+  const AttnParams p{*a,        h->n_kv_heads, h->n_heads / h->n_kv_heads, spread, h->status,
+                     h->part_o, h->part_ml,    h->cuts};
   if (a->dtype == MOE_DTYPE_BF16)
     return h->head_dim == 64 ? launch_attn<__nv_bfloat16, 64>(h, p, k_map, v_map, stream)
                              : launch_attn<__nv_bfloat16, 128>(h, p, k_map, v_map, stream);

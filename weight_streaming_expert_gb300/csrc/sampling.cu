@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
   if (size > 1 && (by_count || by_mass)) {
     // the keys above `bar`: at most kList, those of this thread
     uint32_t bar;
-    c.select<1, kBarBits, true>(0, top_key, (u64)min(kList + 1, a.vocab), Ones{}, bar, above, at);
+    c.template select<1, kBarBits, true>(0, top_key, (u64)min(kList + 1, a.vocab), Ones{}, bar, above, at);
     u64 count = 0, in_list = ~0ull;
     c.each4([&](int, const uint32_t (&key)[4]) {
 #pragma unroll
@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
   int tie_end = kAllTies;
   u64 ties = 0, same = 0;  // how many of the `same` tokens of key thr stay
   if (by_count) {
-    c.select<1, kBinBits, false>(0, top_key, (u64)k, Ones{}, thr, above, at);
+    c.template select<1, kBinBits, false>(0, top_key, (u64)k, Ones{}, thr, above, at);
     ties = (u64)k - above;  // at most `at`: k is reached there
     same = at;
   }
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
     __syncthreads();
     const u64 target = s.shared[0];
     uint32_t key;
-    c.select<3, kBinBits, false>(thr, top_key, target, weights, key, above, at);
+    c.template select<3, kBinBits, false>(thr, top_key, target, weights, key, above, at);
     const u64 w = weight(key);
     if (at == w) {
       ties = same = 1;
