@@ -85,7 +85,7 @@ int moe_qk_norm_rope(const moe_qk_norm_rope_args_t* a, moe_stream_t stream);
  */
 typedef struct moe_attn moe_attn_t; /* opaque; holds the workspace of split sequences */
 
-/* n_heads a multiple of n_kv_heads, head_dim 64 or 128.  NULL on error. */
+/* n_heads a multiple of n_kv_heads (up to 128 times), head_dim 64 or 128.  NULL on error. */
 moe_attn_t* moe_attn_create(int n_heads, int n_kv_heads, int head_dim);
 
 typedef struct {

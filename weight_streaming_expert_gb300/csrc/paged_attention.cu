@@ -10,8 +10,9 @@
 // than 2^8 in p (p then stays below 2^8: exact enough in fp32 sums, and in
 // range for 16-bit probabilities); most rows rescale once or twice in all.
 //
-// A tile is 128 query rows: the chunk's tokens times the heads that share a
-// key/value head, so that a page is read once for all of them.  Per 128
+// A tile is up to 128 query rows: as many whole tokens of the chunk as fit,
+// each with the heads that share a key/value head, so that a page is read once
+// for all of them.  Per 128
 // positions one warp issues S = Q K^T into TMEM (128 x 128 fp32), four warps
 // turn S into probabilities, one row a thread with no exchange between
 // threads, and write them over S as the 16-bit A operand of O += P V, which
@@ -21,7 +22,8 @@
 //   split  one tile, the even 128 positions in one chain and the odd ones in
 //          the other, merged at the end (chunks of up to 128 rows, which are
 //          bound by reading the cache).
-// One warp copies the pages with TMA into a ring of 128-position tiles.
+// One warp copies the pages with TMA into a ring of 128-position tiles, another
+// the queries of the next tile.
 //
 // The work is a list of (sequence, key/value head, tile of rows, 128
 // positions) in that order.  Every CTA takes an equal contiguous share of it,
@@ -47,8 +49,8 @@ enum : int { kAttnBadPage = 1, kAttnBadLength = 2, kAttnTimeout = 4 };
 
 constexpr int kTile = 128;                 // query rows of a tile, and positions
 constexpr int kHalf = 64;                  // positions of a softmax step
-constexpr int kAttnThreads = 384;          // two softmax warpgroups, the MMA warp, the copy warp, two query warps
-constexpr int kMmaWarp = 8, kCopyWarp = 9, kQueryWarp = 10;  // and 11
+constexpr int kAttnThreads = 352;          // two softmax warpgroups, the MMA warp, the copy warp, the query warp
+constexpr int kMmaWarp = 8, kCopyWarp = 9, kQueryWarp = 10;
 constexpr int kMaxBatch = 4096;
 constexpr int kMaxStages = 10;
 constexpr uint32_t kHeadBytes = 2048;      // barriers, plan and the exchange area before the tiles
@@ -109,6 +111,7 @@ constexpr int kMaxParts = 1024;            // CTAs, which is at least the shares
 struct AttnParams {
   moe_attn_args_t a;
   int n_kv_heads, group;
+  int tokens;       // of a tile: 128 / group
   int spread;       // CTAs c, c + 1, .., c + spread - 1 do the same share of as many heads
   int* status;
   float* part_o;    // [CTAs][2][rows of an item][D]: unnormalised sums
@@ -118,7 +121,7 @@ struct AttnParams {
 
 // One sequence as the kernel takes it: lengths that do not fit are cut.
 struct Seq {
-  int q0, n, kv, base, rows;  // first new token, their count, positions, those before the chunk, query rows
+  int q0, n, kv, base;  // first new token, their count, positions, those before the chunk
   bool bad;
 };
 __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
@@ -133,14 +136,13 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
   // the chunk's place goes by the lengths as given; what was cut is hidden
   const long long base = (long long)kv - ((long long)q1 - q0);
   s.base = (int)max(-(1ll << 30), min(base, 1ll << 30));
-  s.rows = s.n * p.group;
   return s;
 }
-// 128-position tiles that row tile i of a sequence visits (at least one, which
-// writes the zeros of rows that see nothing).
-template <int kRows>
+// 128-position tiles that item i of a sequence visits (at least one, which
+// writes the zeros of rows that see nothing).  kTiles: query tiles of an item.
+template <int kTiles>
 __device__ __forceinline__ int units_of(const AttnParams& p, const Seq& s, int i) {
-  const int last = (min(s.rows, (i + 1) * kRows) - 1) / p.group;
+  const int last = min(s.n, (i + 1) * kTiles * p.tokens) - 1;
   const int end = p.a.tree_mask ? s.kv : min(s.kv, max(0, s.base + last + 1));
   return max(1, (end + kTile - 1) / kTile);
 }
@@ -166,7 +168,7 @@ struct Plan {
   int b, h, tile, u0;     // h counts groups of `spread` heads
 };
 
-template <int kRows>
+template <int kTiles>
 struct Walk {
   const AttnParams& p;
   int b, h, tile, u0;
@@ -182,14 +184,14 @@ struct Walk {
         s = load_seq(p, b);
         loaded = b;
       }
-      if (tile * kRows < s.rows) break;
+      if (tile * kTiles * p.tokens < s.n) break;
       tile = 0;
-      if (s.rows > 0 && ++h < p.n_kv_heads / p.spread) continue;
+      if (s.n > 0 && ++h < p.n_kv_heads / p.spread) continue;
       h = 0;
       ++b;
     }
     it.b = b, it.h = h * p.spread + (int)blockIdx.x % p.spread, it.tile = tile, it.s = s;
-    it.units = units_of<kRows>(p, s, tile);
+    it.units = units_of<kTiles>(p, s, tile);
     it.u0 = u0;
     it.u1 = (int)min((long long)it.units, u0 + todo);
     todo -= it.u1 - it.u0;
@@ -238,10 +240,10 @@ struct Layout {
 
 template <typename T, int D, bool kPair>
 __global__ void __launch_bounds__(kAttnThreads, 1)
-    paged_attention_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap k_map,
-                           const __grid_constant__ CUtensorMap v_map) {
+    paged_attention_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap q_map,
+                           const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   using L = Layout<D, kPair>;
-  constexpr int kRows = L::kRows, kStages = L::kStages;
+  constexpr int kTiles = L::kQTiles, kRows = L::kRows, kStages = L::kStages;
   constexpr uint32_t kTileBytes = L::kTileBytes, kPanel = kTile * 128;
   extern __shared__ uint8_t raw_smem[];
   uint8_t* smem = raw_smem + (1024 - (smem_u32(raw_smem) & 1023)) % 1024;
@@ -259,8 +261,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   Plan& plan = *reinterpret_cast<Plan*>(smem + 288);
   float2* exchange = reinterpret_cast<float2*>(smem + 1024);        // [128]: the odd chain's (m, sum)
   const uint32_t q_at = sb + kHeadBytes, ring = q_at + L::kQTiles * kTileBytes;
-  uint8_t* q_smem = smem + kHeadBytes;
-  uint8_t* ring_smem = q_smem + L::kQTiles * kTileBytes;
+  uint8_t* ring_smem = smem + kHeadBytes + L::kQTiles * kTileBytes;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const moe_attn_args_t& a = p.a;
 
@@ -270,7 +271,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(empty(s), 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(q_full(t), kPair ? 1 : 2);
+      mbar_init(q_full(t), 1);
       mbar_init(q_empty(t), 1);
       mbar_init(s_full(t), 1);
       for (int half = 0; half < 2; ++half) {
@@ -284,6 +285,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   }
   if (warp == kMmaWarp) tmem_alloc(smem_u32(tmem_slot), 512);
   if (warp == kCopyWarp && lane == 0) {
+    tma_prefetch_map(&q_map);
     tma_prefetch_map(&k_map);
     tma_prefetch_map(&v_map);
   }
@@ -295,14 +297,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   long long* cost = reinterpret_cast<long long*>(ring_smem);  // the ring is not in use yet
   {
     // sequences of few row tiles: one thread each; of many: one warp each
-    const bool wide = (a.max_q_len * p.group + kRows - 1) / kRows > 4;
+    const bool wide = a.max_q_len > 4 * kTiles * p.tokens;
     const int step = wide ? kAttnThreads / 32 : kAttnThreads;
     for (int b = wide ? warp : tid; b < a.batch; b += step) {
       const Seq s = load_seq(p, b);
       if (s.bad && (!wide || lane == 0) && blockIdx.x == 0) atomicOr(p.status, kAttnBadLength);
       long long sum = 0;
-      const int tiles = (s.rows + kRows - 1) / kRows;
-      for (int i = wide ? lane : 0; i < tiles; i += wide ? 32 : 1) sum += units_of<kRows>(p, s, i);
+      const int tiles = (s.n + kTiles * p.tokens - 1) / (kTiles * p.tokens);
+      for (int i = wide ? lane : 0; i < tiles; i += wide ? 32 : 1) sum += units_of<kTiles>(p, s, i);
       if (wide) {
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
@@ -340,7 +342,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const long long h = quotient(start - at, cost[b]);
         long long rest = start - at - h * cost[b];
         int tile = 0;
-        for (int u; rest >= (u = units_of<kRows>(p, s, tile)); ++tile) rest -= u;
+        for (int u; rest >= (u = units_of<kTiles>(p, s, tile)); ++tile) rest -= u;
         plan.b = b;
         plan.h = (int)h;
         plan.tile = tile;
@@ -357,7 +359,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   if (tid == 0) p.cuts[blockIdx.x].parts = 0;
 
   if (warp < kMmaWarp) {
-    Walk<kRows> walk(p, plan);
+    Walk<kTiles> walk(p, plan);
     Item it{};
     // ---- softmax: chain 0 in warps 0-3, chain 1 in warps 4-7, a row per thread
     const int chain = warp >> 2, r = tid & 127;
@@ -367,12 +369,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const float c = a.scale * 1.4426950408889634f;  // exponents in base 2
     const float rescale = kRescaleLog2 / c;
     int tiles[2] = {0, 0};  // tiles of positions of the even and the odd chain before this item
+    const int row_token = r / p.group, row_head = r - row_token * p.group;
     while (walk.next(it)) {
-      const int row0 = it.tile * kRows + q_tile * kTile;
-      const int g = row0 + r;
-      const bool valid = g < it.s.rows;
-      const bool warp_valid = row0 + (r & ~31) < it.s.rows;
-      const int token = valid ? g / p.group : 0;
+      const int token0 = (it.tile * kTiles + q_tile) * p.tokens;  // the tile's first, in the chunk
+      const int token = token0 + row_token, head = it.h * p.group + row_head;
+      const bool valid = row_token < p.tokens && token < it.s.n;
+      const bool warp_valid = __any_sync(0xffffffffu, valid);
       // positions below `plain` are seen, from `end` on hidden, between them
       // the tree's bits decide
       const unsigned long long bits = a.tree_mask && valid ? (unsigned long long)a.tree_mask[it.s.q0 + token] : 0ull;
@@ -501,7 +503,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int block0 = kPair ? 0 : chain * kBlocks;
         const uint32_t even_at = tmem + lane_at + 2 * kTile + (kPair ? chain * D : 0);
         T* out = static_cast<T*>(a.out) + (long long)(it.s.q0 + token) * a.out_token_stride +
-                 (it.h * p.group + (valid ? g % p.group : 0)) * a.out_head_stride;
+                 head * a.out_head_stride;
         float4* part = reinterpret_cast<float4*>(p.part_o) + ((long long)slot * kRows + local) * (D / 4);
 #pragma unroll
         for (int i = 0; i < kBlocks; ++i) {
@@ -540,7 +542,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (cut)
             p.part_ml[(long long)slot * kRows + local] = make_float2(m, l);
           else if (a.lse)
-            a.lse[(long long)(it.s.q0 + token) * (p.group * p.n_kv_heads) + it.h * p.group + g % p.group] =
+            a.lse[(long long)(it.s.q0 + token) * (p.group * p.n_kv_heads) + head] =
                 l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f;
         }
       }
@@ -554,7 +556,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
   } else {
     if (warp == kCopyWarp) {
-    Walk<kRows> walk(p, plan);
+    Walk<kTiles> walk(p, plan);
     Item it{};
     // ---- copies: per 128 positions one box per page and 64 columns, a lane each
     constexpr int kHalves = D / 64;
@@ -602,31 +604,32 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_wait(full(f % kStages), (f / kStages) & 1, &waited);
     }
     } else if (warp >= kQueryWarp) {
-      // ---- queries into shared memory with asynchronous 16-byte copies: a
-      // tile of the pair per warp, or half of the rows; rows past the last
-      // become zeros
-      Walk<kRows> walk(p, plan);
+      // ---- queries, of a tile as one box of its tokens, the heads of a group
+      // and 64 columns.  Past the sequence's last token it reads what follows,
+      // which no row that counts sees.
+      Walk<kTiles> walk(p, plan);
       Item it{};
-      constexpr int kChunks = D / 8, kMine = kPair ? kTile : kTile / 2;
-      const int w = warp - kQueryWarp, t = kPair ? w : 0, from = kPair ? 0 : w * kMine;
-      const int cc = lane % kChunks;
-      const uint32_t dst = q_at + t * kTileBytes + (cc / 8) * kPanel;
-      for (int round = 0; walk.next(it); ++round) {
-        if (round > 0) wait(q_empty(t), (round - 1) & 1);
-#pragma unroll 4
-        for (int row = from + lane / kChunks; row < from + kMine; row += 32 / kChunks) {
-          const int g = it.tile * kRows + t * kTile + row, gc = min(g, it.s.rows - 1), token = gc / p.group;
-          const T* src = static_cast<const T*>(a.q) + (long long)(it.s.q0 + token) * a.q_token_stride +
-                         (it.h * p.group + gc - token * p.group) * a.q_head_stride + cc * 8;
-          copy16_async(dst + row * 128 + ((cc % 8) ^ (row % 8)) * 16, src, g < it.s.rows);
+      int round = 0;
+      for (; walk.next(it); ++round) {
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          if (round > 0) wait(q_empty(t), (round - 1) & 1);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(q_full(t), p.tokens * p.group * D * 2);
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half)
+              tma_load_3d(q_at + t * kTileBytes + half * kPanel, &q_map, half * 64, it.h * p.group,
+                          it.s.q0 + (it.tile * kTiles + t) * p.tokens, q_full(t));
+          }
+          __syncwarp();
         }
-        copies_done();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full(t));
       }
+      // no copy is in flight when the CTA ends, also after a wait has given up
+      unsigned long long waited;
+      if (round > 0)
+        for (int t = 0; t < kTiles; ++t) mbar_wait(q_full(t), (round - 1) & 1, &waited);
     } else if (warp == kMmaWarp) {
-    Walk<kRows> walk(p, plan);
+    Walk<kTiles> walk(p, plan);
     Item it{};
     // ---- products, issued by lane 0
     constexpr uint32_t kDescS = mma_desc(std::is_same<T, __nv_bfloat16>::value, false, kTile, kTile);
@@ -768,11 +771,16 @@ __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4) join_kernel(c
   const Cut cut = p.cuts[blockIdx.x];
   if (cut.parts == 0) return;
   const Seq s = load_seq(p, cut.b);
-  const int rows = min(kRows, s.rows - cut.tile * kRows);
+  // rows of the item in use: of the pair's second tile from 128 on
+  auto token_of = [&](int row) {
+    const int in_tile = row % kTile / p.group;
+    return in_tile < p.tokens ? (cut.tile * (kRows / kTile) + row / kTile) * p.tokens + in_tile : s.n;
+  };
   const float c = a.scale * 1.4426950408889634f;
   auto slot = [&](int i) { return 2ll * (blockIdx.x + i * p.spread) + (i == 0 ? 1 : 0); };
-  for (int r0 = blockIdx.y * kJoinRows; r0 < rows; r0 += gridDim.y * kJoinRows) {
-    if (warp < kJoinRows && r0 + warp < rows) {
+  const int r0 = blockIdx.y * kJoinRows;
+  {
+    if (warp < kJoinRows && token_of(r0 + warp) < s.n) {
       float m = -INFINITY, l = 0.f;
       for (int i = lane; i < cut.parts; i += 32) m = fmaxf(m, p.part_ml[slot(i) * kRows + r0 + warp].x);
 #pragma unroll
@@ -790,7 +798,8 @@ __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4) join_kernel(c
                                   l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f);
     }
     __syncthreads();
-    const bool mine = r0 + row < rows;
+    const int token = token_of(r0 + row);
+    const bool mine = token < s.n;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (mine) {
       const int per = (cut.parts + kJoinGroups - 1) / kJoinGroups;
@@ -818,14 +827,13 @@ __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4) join_kernel(c
         o.w += v.w;
       }
       const float norm = total[row].x;
-      const int g = cut.tile * kRows + r0 + row, token = g / p.group, head = cut.h * p.group + g % p.group;
+      const int head = cut.h * p.group + (r0 + row) % kTile % p.group;
       *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (long long)(s.q0 + token) * a.out_token_stride +
                                 head * a.out_head_stride + column * 4) =
           make_uint2(pack<T>(o.x * norm, o.y * norm), pack<T>(o.z * norm, o.w * norm));
       if (a.lse && column == 0)
         a.lse[(long long)(s.q0 + token) * (p.group * p.n_kv_heads) + head] = total[row].y;
     }
-    __syncthreads();
   }
 }
 
@@ -844,22 +852,27 @@ MapEncode map_encode() {
   return fn;
 }
 
-// The cache of one layer as (columns of all heads, rows of a page, pages);
-// a box: 64 columns of one page's rows (128 of a longer page).
-int encode_cache(CUtensorMap* map, const moe_attn_args_t& a, const void* base, int64_t row_stride,
-                 int64_t page_stride, int columns) {
+// A three-dimensional map of 16-bit elements, innermost contiguous, whose boxes
+// are 64 columns of `rows` by `slabs`.
+int encode_map(CUtensorMap* map, int dtype, const void* base, int columns, int d1, int64_t stride1, int d2,
+               int64_t stride2, int rows, int slabs, const char* what) {
   const MapEncode encode = map_encode();
   if (!encode) return fail(MOE_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
-  const cuuint64_t dims[3] = {(cuuint64_t)columns, (cuuint64_t)a.page_size, (cuuint64_t)a.n_pages};
-  const cuuint64_t strides[2] = {(cuuint64_t)row_stride * 2, (cuuint64_t)page_stride * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)(a.page_size < kTile ? a.page_size : kTile), 1};
+  const cuuint64_t dims[3] = {(cuuint64_t)columns, (cuuint64_t)d1, (cuuint64_t)d2};
+  const cuuint64_t strides[2] = {(cuuint64_t)stride1 * 2, (cuuint64_t)stride2 * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)rows, (cuuint32_t)slabs};
   const cuuint32_t steps[3] = {1, 1, 1};
-  const CUresult r = encode(
-      map, a.dtype == MOE_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-      const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? MOE_OK : fail(MOE_ERR_INVALID_ARG, "no tensor map for this cache (driver error %d)", (int)r);
+  const CUresult r =
+      encode(map, dtype == MOE_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+             const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MOE_OK
+                           : fail(MOE_ERR_INVALID_ARG, "no tensor map for the strides of %s (driver error %d)", what, (int)r);
 }
+
+struct Maps {
+  CUtensorMap q, k, v;
+};
 
 }  // namespace
 }  // namespace wse
@@ -896,24 +909,22 @@ cudaError_t allow_smem_both() {
 }
 
 template <typename T, int D, bool kPair>
-int launch_attn(const moe_attn* h, const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v,
-                moe_stream_t stream) {
+int launch_attn(const moe_attn* h, const AttnParams& p, const Maps& maps, moe_stream_t stream) {
   using L = Layout<D, kPair>;
   const int grid = h->n_sms / p.spread * p.spread;
   const int rc = launch_pdl(paged_attention_kernel<T, D, kPair>, dim3(grid), dim3(kAttnThreads), L::kSmem, stream,
-                            1, p, k, v);
+                            1, p, maps.q, maps.k, maps.v);
   if (rc != MOE_OK) return rc;
-  const int rows = (int)std::min<long long>(L::kRows, (long long)p.a.max_q_len * p.group);
+  const int rows = kPair ? L::kRows : std::min(p.a.max_q_len, p.tokens) * p.group;
   return launch_pdl(join_kernel<T, D, L::kRows>, dim3(grid, (rows + kJoinRows - 1) / kJoinRows),
                     dim3(kJoinRows * kJoinGroups * D / 4), 0, stream, 1, p);
 }
 
 template <typename T, int D>
-int launch_attn(const moe_attn* h, const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v,
-                moe_stream_t stream) {
+int launch_attn(const moe_attn* h, const AttnParams& p, const Maps& maps, moe_stream_t stream) {
   // one tile of rows per sequence and key/value head: the split form
-  return (long long)p.a.max_q_len * p.group > kTile ? launch_attn<T, D, true>(h, p, k, v, stream)
-                                                    : launch_attn<T, D, false>(h, p, k, v, stream);
+  return p.a.max_q_len > p.tokens ? launch_attn<T, D, true>(h, p, maps, stream)
+                                  : launch_attn<T, D, false>(h, p, maps, stream);
 }
 
 }  // namespace
@@ -921,6 +932,10 @@ int launch_attn(const moe_attn* h, const AttnParams& p, const CUtensorMap& k, co
 extern "C" {
 
 moe_attn_t* moe_attn_create(int n_heads, int n_kv_heads, int head_dim) {
+  if (n_kv_heads >= 1 && n_heads / n_kv_heads > kTile) {
+    fail(MOE_ERR_UNSUPPORTED, "%d query heads share a key/value head: at most %d can", n_heads / n_kv_heads, kTile);
+    return nullptr;
+  }
   if (n_kv_heads < 1 || n_heads < 1 || n_heads % n_kv_heads || n_heads > 65536) {
     fail(MOE_ERR_INVALID_ARG, "n_heads = %d must be a multiple of n_kv_heads = %d", n_heads, n_kv_heads);
     return nullptr;
@@ -978,23 +993,28 @@ int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t strea
   if ((a->q_token_stride | a->q_head_stride | a->out_token_stride | a->out_head_stride | a->k_page_stride |
        a->k_row_stride | a->v_page_stride | a->v_row_stride) & 7)
     return fail(MOE_ERR_INVALID_ARG, "every stride must be a multiple of 8 elements (16 bytes)");
-  if ((long long)a->n_tokens * (h->n_heads / h->n_kv_heads) > (1 << 30))
-    return fail(MOE_ERR_UNSUPPORTED, "n_tokens = %d is too many", a->n_tokens);
+  if (a->n_tokens > (1 << 30)) return fail(MOE_ERR_UNSUPPORTED, "n_tokens = %d is too many", a->n_tokens);
   if (a->batch > kMaxBatch) return fail(MOE_ERR_UNSUPPORTED, "batch = %d exceeds %d", a->batch, kMaxBatch);
-  CUtensorMap k_map, v_map;
-  int rc = encode_cache(&k_map, *a, a->k_cache, a->k_row_stride, a->k_page_stride, h->n_kv_heads * h->head_dim);
+  const int group = h->n_heads / h->n_kv_heads, columns = h->n_kv_heads * h->head_dim;
+  const int tokens = kTile / group, box_rows = std::min(a->page_size, kTile);
+  Maps maps;
+  int rc = encode_map(&maps.q, a->dtype, a->q, h->head_dim, h->n_heads, a->q_head_stride, a->n_tokens,
+                      a->q_token_stride, group, tokens, "q");
   if (rc == MOE_OK)
-    rc = encode_cache(&v_map, *a, a->v_cache, a->v_row_stride, a->v_page_stride, h->n_kv_heads * h->head_dim);
+    rc = encode_map(&maps.k, a->dtype, a->k_cache, columns, a->page_size, a->k_row_stride, a->n_pages,
+                    a->k_page_stride, box_rows, 1, "k_cache");
+  if (rc == MOE_OK)
+    rc = encode_map(&maps.v, a->dtype, a->v_cache, columns, a->page_size, a->v_row_stride, a->n_pages,
+                    a->v_page_stride, box_rows, 1, "v_cache");
   if (rc != MOE_OK) return rc;
   int spread = 1;
   while (spread < kMaxSpread && h->n_kv_heads % (2 * spread) == 0) spread *= 2;
-  const AttnParams p{*a,        h->n_kv_heads, h->n_heads / h->n_kv_heads, spread, h->status,
-                     h->part_o, h->part_ml,    h->cuts};
+  const AttnParams p{*a, h->n_kv_heads, group, tokens, spread, h->status, h->part_o, h->part_ml, h->cuts};
   if (a->dtype == MOE_DTYPE_BF16)
-    return h->head_dim == 64 ? launch_attn<__nv_bfloat16, 64>(h, p, k_map, v_map, stream)
-                             : launch_attn<__nv_bfloat16, 128>(h, p, k_map, v_map, stream);
-  return h->head_dim == 64 ? launch_attn<__half, 64>(h, p, k_map, v_map, stream)
-                           : launch_attn<__half, 128>(h, p, k_map, v_map, stream);
+    return h->head_dim == 64 ? launch_attn<__nv_bfloat16, 64>(h, p, maps, stream)
+                             : launch_attn<__nv_bfloat16, 128>(h, p, maps, stream);
+  return h->head_dim == 64 ? launch_attn<__half, 64>(h, p, maps, stream)
+                           : launch_attn<__half, 128>(h, p, maps, stream);
 }
 
 int moe_attn_get_status(moe_attn_t* h) {
