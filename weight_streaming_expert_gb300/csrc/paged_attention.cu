@@ -53,7 +53,7 @@ constexpr int kAttnThreads = 352;          // two softmax warpgroups, the MMA wa
 constexpr int kMmaWarp = 8, kCopyWarp = 9, kQueryWarp = 10;
 constexpr int kMaxBatch = 4096;
 constexpr int kMaxStages = 10;
-constexpr uint32_t kHeadBytes = 2048;      // barriers, plan and the exchange area before the tiles
+constexpr uint32_t kStagingBytes = 8 * 4096;  // 32 rows of 128 bytes for each softmax warp
 constexpr float kRescaleLog2 = 8.f;
 constexpr int kJoinRows = 4, kJoinGroups = 4;  // rows of a joining CTA, and threads that share a row's parts
 constexpr int kMaxSpread = 8;              // key/value heads that neighbouring CTAs work on side by side
@@ -147,12 +147,6 @@ __device__ __forceinline__ int units_of(const AttnParams& p, const Seq& s, int i
   return max(1, (end + kTile - 1) / kTile);
 }
 
-// x / y, in 32 bits where they do: a 64-bit division takes some hundred
-// instructions on the way to the first copy.
-__device__ __forceinline__ long long quotient(long long x, long long y) {
-  return (x | y) >> 32 ? x / y : (long long)((uint32_t)x / (uint32_t)y);
-}
-
 // A CTA's next piece of work.
 struct Item {
   int b, h, tile, u0, u1, units;
@@ -163,20 +157,20 @@ struct Item {
 // the same one, each for a head of its own: what they read of a position lies
 // side by side in memory and is read at about the same time.
 struct Plan {
-  long long start, todo;  // where this CTA's share begins, and its length
-  long long share;        // of every CTA but the last
-  int b, h, tile, u0;     // h counts groups of `spread` heads
+  int start, todo;     // where this CTA's share begins, and its length
+  int share;           // of every CTA but the last
+  int b, h, tile, u0;  // h counts groups of `spread` heads
+  Seq s;               // sequence b
 };
 
 template <int kTiles>
 struct Walk {
   const AttnParams& p;
-  int b, h, tile, u0;
-  long long todo;
+  int b, h, tile, u0, todo;
   Seq s;
   int loaded;
   __device__ Walk(const AttnParams& p_, const Plan& plan)
-      : p(p_), b(plan.b), h(plan.h), tile(plan.tile), u0(plan.u0), todo(plan.todo), loaded(-1) {}
+      : p(p_), b(plan.b), h(plan.h), tile(plan.tile), u0(plan.u0), todo(plan.todo), s(plan.s), loaded(plan.b) {}
   __device__ bool next(Item& it) {
     if (todo <= 0) return false;
     for (;;) {
@@ -193,13 +187,64 @@ struct Walk {
     it.b = b, it.h = h * p.spread + (int)blockIdx.x % p.spread, it.tile = tile, it.s = s;
     it.units = units_of<kTiles>(p, s, tile);
     it.u0 = u0;
-    it.u1 = (int)min((long long)it.units, u0 + todo);
+    it.u1 = min(it.units, u0 + todo);
     todo -= it.u1 - it.u0;
     u0 = 0;
     ++tile;
     return true;
   }
 };
+
+// Sum of the lanes' values up to this one's.
+__device__ __forceinline__ int scan_up(int v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, v, m);
+    if (lane >= m) v += o;
+  }
+  return v;
+}
+
+// Where this CTA's share begins, found by each warp for itself: lane l has the
+// sequences l * per, .., whose costs (one head's units) cost(b) gives and sum
+// to `sum`.
+template <int kTiles, typename Cost>
+__device__ __forceinline__ Plan make_plan(const AttnParams& p, int per, int sum, Cost cost) {
+  const int lane = threadIdx.x & 31;
+  const int upto = scan_up(sum);
+  const int heads = p.n_kv_heads / p.spread, shares = gridDim.x / p.spread;
+  const int total = __shfl_sync(0xffffffffu, upto, 31) * heads;
+  Plan plan{};
+  // equal shares of whole units: fewer CTAs, and cuts, where there are few
+  plan.share = (unsigned)(total + shares - 1) / (unsigned)shares;
+  plan.start = min(total, plan.share * (int)(blockIdx.x / p.spread));
+  plan.todo = min(total - plan.start, plan.share);
+  if (plan.todo == 0) return plan;
+  int at = (upto - sum) * heads, own = 0, b = lane * per;
+  const bool mine = plan.start >= at && plan.start < upto * heads;
+  if (mine)
+    for (own = cost(b); plan.start >= at + own * heads; own = cost(++b)) at += own * heads;
+  const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+  plan.b = __shfl_sync(0xffffffffu, b, src);
+  int rest = plan.start - __shfl_sync(0xffffffffu, at, src);
+  own = __shfl_sync(0xffffffffu, own, src);
+  plan.s = load_seq(p, plan.b);
+  plan.h = (unsigned)rest / (unsigned)own;
+  rest -= plan.h * own;
+  for (int tile = lane;; tile += 32) {  // 32 items at a time
+    const int u = tile * kTiles * p.tokens < plan.s.n ? units_of<kTiles>(p, plan.s, tile) : 0;
+    const int to = scan_up(u);
+    const unsigned past = __ballot_sync(0xffffffffu, to > rest);
+    if (past) {
+      const int first = __ffs(past) - 1;
+      plan.tile = __shfl_sync(0xffffffffu, tile, first);
+      plan.u0 = rest - __shfl_sync(0xffffffffu, to - u, first);
+      return plan;
+    }
+    rest -= __shfl_sync(0xffffffffu, to, 31);
+  }
+}
 
 // The n lowest bits of a word (none below 0, all from 32 on).
 __device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
@@ -233,9 +278,11 @@ struct Layout {
   static constexpr uint32_t kTileBytes = kTile * D * 2;          // one tile of Q, K or V
   static constexpr int kQTiles = kPair ? 2 : 1;
   static constexpr int kRows = kQTiles * kTile;                   // query rows of an item
-  static constexpr int kFit = (int)((232448 - 1024 - kHeadBytes) / kTileBytes) - kQTiles;
+  // barriers and the staging area (split: the exchange of both chains' statistics) before the tiles
+  static constexpr uint32_t kHead = 1024 + (kPair ? kStagingBytes : 2048u);
+  static constexpr int kFit = (int)((232448 - kHead) / kTileBytes) - kQTiles;
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
-  static constexpr uint32_t kSmem = 1024 + kHeadBytes + (kQTiles + kStages) * kTileBytes;
+  static constexpr uint32_t kSmem = kHead + (kQTiles + kStages) * kTileBytes;
 };
 
 template <typename T, int D, bool kPair>
@@ -245,8 +292,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   using L = Layout<D, kPair>;
   constexpr int kTiles = L::kQTiles, kRows = L::kRows, kStages = L::kStages;
   constexpr uint32_t kTileBytes = L::kTileBytes, kPanel = kTile * 128;
-  extern __shared__ uint8_t raw_smem[];
-  uint8_t* smem = raw_smem + (1024 - (smem_u32(raw_smem) & 1023)) % 1024;
+  extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle goes by address bits up to 9
   const uint32_t sb = smem_u32(smem);
   auto full = [&](int s) { return sb + 8u * s; };
   auto empty = [&](int s) { return sb + 80u + 8u * s; };
@@ -258,10 +304,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const uint32_t drained = sb + 272u;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + 280);
   int* gone = reinterpret_cast<int*>(smem + 284);
-  Plan& plan = *reinterpret_cast<Plan*>(smem + 288);
-  float2* exchange = reinterpret_cast<float2*>(smem + 1024);        // [128]: the odd chain's (m, sum)
-  const uint32_t q_at = sb + kHeadBytes, ring = q_at + L::kQTiles * kTileBytes;
-  uint8_t* ring_smem = smem + kHeadBytes + L::kQTiles * kTileBytes;
+  uint8_t* staging = smem + 1024;                          // [8][32 rows][128 bytes]: of the softmax warps
+  float2* exchange = reinterpret_cast<float2*>(staging);   // [2][128]: both chains' (m, sum)
+  const uint32_t q_at = sb + L::kHead, ring = q_at + L::kQTiles * kTileBytes;
+  uint8_t* ring_smem = smem + L::kHead + L::kQTiles * kTileBytes;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const moe_attn_args_t& a = p.a;
 
@@ -292,19 +338,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   pdl_wait();
   pdl_launch_dependents();
 
-  // ---- the plan: cost of each sequence (of one key/value head), their prefix
-  // sums, and where this CTA's share begins
-  long long* cost = reinterpret_cast<long long*>(ring_smem);  // the ring is not in use yet
-  {
-    // sequences of few row tiles: one thread each; of many: one warp each
-    const bool wide = a.max_q_len > 4 * kTiles * p.tokens;
-    const int step = wide ? kAttnThreads / 32 : kAttnThreads;
-    for (int b = wide ? warp : tid; b < a.batch; b += step) {
+  // ---- the plan, from the cost of each sequence (of one key/value head)
+  Plan plan;
+  const bool wide = a.max_q_len > 4 * kTiles * p.tokens;  // sequences of many items: a warp each
+  if (a.batch <= 32 && !wide) {
+    int sum = 0;
+    if (lane < a.batch) {
+      const Seq s = load_seq(p, lane);
+      if (s.bad && blockIdx.x == 0) atomicOr(p.status, kAttnBadLength);
+      for (int i = 0; i * kTiles * p.tokens < s.n; ++i) sum += units_of<kTiles>(p, s, i);
+    }
+    plan = make_plan<kTiles>(p, 1, sum, [&](int) { return sum; });
+  } else {
+    int* cost = reinterpret_cast<int*>(ring_smem);  // the ring is not in use yet
+    for (int b = wide ? warp : tid; b < a.batch; b += wide ? kAttnThreads / 32 : kAttnThreads) {
       const Seq s = load_seq(p, b);
-      if (s.bad && (!wide || lane == 0) && blockIdx.x == 0) atomicOr(p.status, kAttnBadLength);
-      long long sum = 0;
-      const int tiles = (s.n + kTiles * p.tokens - 1) / (kTiles * p.tokens);
-      for (int i = wide ? lane : 0; i < tiles; i += wide ? 32 : 1) sum += units_of<kTiles>(p, s, i);
+      if (s.bad && blockIdx.x == 0) atomicOr(p.status, kAttnBadLength);
+      int sum = 0;
+      for (int i = wide ? lane : 0; i * kTiles * p.tokens < s.n; i += wide ? 32 : 1) sum += units_of<kTiles>(p, s, i);
       if (wide) {
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
@@ -312,48 +363,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (!wide || lane == 0) cost[b] = sum;
     }
     __syncthreads();
-    if (warp == 0) {
-      // lane l: sequences [l * per, (l + 1) * per)
-      const int per = (a.batch + 31) / 32;
-      const int b0 = min(a.batch, lane * per), b1 = min(a.batch, b0 + per);
-      long long sum = 0;
-      for (int b = b0; b < b1; ++b) sum += cost[b];
-      long long upto = sum;
-#pragma unroll
-      for (int m = 1; m < 32; m <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, upto, m);
-        if (lane >= m) upto += o;
-      }
-      const int heads = p.n_kv_heads / p.spread, shares = gridDim.x / p.spread, c = blockIdx.x / p.spread;
-      const long long total = __shfl_sync(0xffffffffu, upto, 31) * heads;
-      // equal shares of whole units: fewer CTAs, and cuts, where there are few
-      const long long share = quotient(total + shares - 1, shares);
-      const long long start = share * c, end = min(total, start + share);
-      if (lane == 0) {
-        plan.start = start;
-        plan.todo = max(0ll, end - start);
-        plan.share = share;
-      }
-      long long at = (upto - sum) * heads;
-      if (end > start && start >= at && start < upto * heads) {  // one lane
-        int b = b0;
-        while (start >= at + cost[b] * heads) at += cost[b++] * heads;
-        const Seq s = load_seq(p, b);
-        const long long h = quotient(start - at, cost[b]);
-        long long rest = start - at - h * cost[b];
-        int tile = 0;
-        for (int u; rest >= (u = units_of<kTiles>(p, s, tile)); ++tile) rest -= u;
-        plan.b = b;
-        plan.h = (int)h;
-        plan.tile = tile;
-        plan.u0 = (int)rest;
-      }
-    }
-    fence_proxy_async_smem();  // the plan's scratch becomes the ring
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
+    const int per = (a.batch + 31) / 32;
+    int sum = 0;
+    for (int b = lane * per; b < min(a.batch, (lane + 1) * per); ++b) sum += cost[b];
+    plan = make_plan<kTiles>(p, per, sum, [&](int b) { return cost[b]; });
+    fence_proxy_async_smem();  // the costs' place becomes the ring
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const Waiter wait{gone, p.status};
   if (tid == 0) p.cuts[blockIdx.x].parts = 0;
@@ -477,15 +495,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int local = kPair ? chain * kTile + r : r;  // row of the item
       float f0 = 1.f, f1 = 0.f;
       if (!kPair) {
-        // both chains' (m, l): the odd one's through shared memory, the even
-        // one's back; then each chain's warps write half of the columns
-        if (chain == 1) exchange[r] = make_float2(m, l);
+        // each chain's warps then write half of the columns
+        exchange[chain * kTile + r] = make_float2(m, l);
         named_sync(1, 256);
-        const float2 odd = exchange[r];
-        named_sync(1, 256);
-        if (chain == 0) exchange[r] = make_float2(m, l);
-        named_sync(1, 256);
-        const float2 even = exchange[r];
+        const float2 even = exchange[r], odd = exchange[kTile + r];
+        named_sync(1, 256);  // before it is written over
         m = fmaxf(even.x, odd.x);
         f0 = even.x == -INFINITY ? 0.f : exp2_approx((even.x - m) * c);
         f1 = odd.x == -INFINITY ? 0.f : exp2_approx((odd.x - m) * c);
@@ -502,9 +516,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         constexpr int kBlocks = kPair ? D / 32 : D / 64;  // 32-column blocks of this warp
         const int block0 = kPair ? 0 : chain * kBlocks;
         const uint32_t even_at = tmem + lane_at + 2 * kTile + (kPair ? chain * D : 0);
-        T* out = static_cast<T*>(a.out) + (long long)(it.s.q0 + token) * a.out_token_stride +
-                 head * a.out_head_stride;
-        float4* part = reinterpret_cast<float4*>(p.part_o) + ((long long)slot * kRows + local) * (D / 4);
+        // Rows are 256 bytes or more apart, so a warp's lanes would write 32
+        // places at a time: by way of shared memory eight lanes write 128 bytes
+        // of a row.  The split form has few rows and rather another stage.
+        uint8_t* mine = staging + warp * 4096;
+        auto put = [&](int chunk, uint4 v) {
+          *reinterpret_cast<uint4*>(mine + lane * 128 + (chunk ^ (lane & 7)) * 16) = v;
+        };
+        auto flush = [&](char* to) {  // this lane's 128 bytes, nullptr: none
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = i * 4 + lane / 8;
+            char* dst = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), row));
+            const uint4 v = *reinterpret_cast<const uint4*>(mine + row * 128 + ((lane & 7) ^ (row & 7)) * 16);
+            if (dst) *reinterpret_cast<uint4*>(dst + (lane & 7) * 16) = v;
+          }
+          __syncwarp();
+        };
+        char* out = reinterpret_cast<char*>(static_cast<T*>(a.out) + (long long)(it.s.q0 + token) * a.out_token_stride +
+                                            head * a.out_head_stride);
+        char* part = reinterpret_cast<char*>(p.part_o + ((long long)slot * kRows + local) * D);
 #pragma unroll
         for (int i = 0; i < kBlocks; ++i) {
           uint32_t o[32];
@@ -519,13 +551,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               o[k] = __float_as_uint((f0 != 0.f ? __uint_as_float(o[k]) * f0 : 0.f) +
                                      (f1 != 0.f ? __uint_as_float(o1[k]) * f1 : 0.f));
           }
-          if (!valid) continue;
           if (cut) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              part[8 * (block0 + i) + k] =
-                  make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]), __uint_as_float(o[4 * k + 2]),
-                              __uint_as_float(o[4 * k + 3]));
+            for (int k = 0; k < 8; ++k) {
+              const uint4 v = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+              if (kPair)
+                put(k, v);
+              else if (valid)
+                *reinterpret_cast<uint4*>(part + 128 * (block0 + i) + 16 * k) = v;
+            }
+            if (kPair) flush(valid ? part + 128 * (block0 + i) : nullptr);
           } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -534,8 +569,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
               for (int j = 0; j < 4; ++j)
                 w[j] = pack<T>(__uint_as_float(o[8 * k + 2 * j]) * norm, __uint_as_float(o[8 * k + 2 * j + 1]) * norm);
-              *reinterpret_cast<uint4*>(out + 32 * (block0 + i) + 8 * k) = v;
+              if (kPair)
+                put((i & 1) * 4 + k, v);
+              else if (valid)
+                *reinterpret_cast<uint4*>(out + 64 * (block0 + i) + 16 * k) = v;
             }
+            if (kPair && (i & 1)) flush(valid ? out + 64 * (block0 + i - 1) : nullptr);
           }
         }
         if (valid && (kPair || chain == 0)) {
@@ -548,8 +587,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       if (cut && it.u0 == 0 && tid == 0) {
         // this share ends inside the tile: which share holds its last unit
-        const long long last = plan.start + (plan.todo - walk.todo) - n + it.units - 1;
-        const int e = (int)quotient(last, plan.share);
+        const int last = plan.start + (plan.todo - walk.todo) - n + it.units - 1;
+        const int e = (unsigned)last / (unsigned)plan.share;
         p.cuts[blockIdx.x] = Cut{e - (int)blockIdx.x / p.spread + 1, it.b, it.h, it.tile};
       }
       if (!kPair) named_sync(1, 256);  // both chains' sums are read before the next item's
@@ -561,14 +600,30 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // ---- copies: per 128 positions one box per page and 64 columns, a lane each
     constexpr int kHalves = D / 64;
     const int box_rows = min(a.page_size, kTile), per_tile = kTile / box_rows;
+    const int pages_log2 = 31 - __clz(a.page_size);
     const int box = lane / kHalves, half = lane % kHalves;
     int filled = 0;
+    // The table's entries come 32 at a time, an entry per lane, and a window
+    // ahead of their use: `even` and `odd` hold the windows of those numbers.
+    int even = 0, odd = 0, have = 0;
+    auto fetch = [&](int window) {
+      const int i = window * 32 + lane;
+      const int page = (long long)i * a.page_size < it.s.kv ? a.block_table[(long long)it.b * a.table_stride + i] : -1;
+      if (window & 1)
+        odd = page;
+      else
+        even = page;
+      have = window;
+    };
+    auto start_item = [&]() {
+      fetch((it.u0 * kTile >> pages_log2) / 32);
+      fetch(have + 1);
+    };
     auto load = [&](const CUtensorMap* map, int u) {
       const int stage = filled % kStages, round = filled / kStages;
-      const int pos = u * kTile + box * box_rows;
+      const int pos = u * kTile + box * box_rows, i = pos >> pages_log2, window = (u * kTile >> pages_log2) / 32;
+      int page = __shfl_sync(0xffffffffu, window & 1 ? odd : even, i & 31);
       const bool mine = box < per_tile && pos < it.s.kv;
-      int page = 0;
-      if (mine) page = a.block_table[(long long)it.b * a.table_stride + pos / a.page_size];
       if (mine && (unsigned)page >= (unsigned)a.n_pages) {
         atomicOr(p.status, kAttnBadPage);
         page = a.n_pages;  // outside the tensor: reads as zeros
@@ -579,21 +634,28 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       __syncwarp();
       if (mine)
         tma_load_3d(ring + stage * kTileBytes + half * kPanel + box * box_rows * 128, map, it.h * D + half * 64,
-                    pos % a.page_size, page, full(stage));
+                    pos & (a.page_size - 1), page, full(stage));
       ++filled;
+      return window;
+    };
+    // values come last of a position's copies: what is before their window is done with
+    auto load_values = [&](int u) {
+      const int window = load(&v_map, u);
+      if (window == have) fetch(window + 1);
     };
     while (walk.next(it)) {
       const int n = it.u1 - it.u0;
+      start_item();
       if (kPair) {
         for (int j = 0; j < n; ++j) {
           load(&k_map, it.u0 + j);
-          load(&v_map, it.u0 + j);
+          load_values(it.u0 + j);
         }
       } else {
         load(&k_map, it.u0);
         if (n > 1) load(&k_map, it.u0 + 1);
         for (int j = 0; j < n; ++j) {
-          load(&v_map, it.u0 + j);
+          load_values(it.u0 + j);
           if (j + 2 < n) load(&k_map, it.u0 + j + 2);
         }
       }
@@ -994,6 +1056,11 @@ int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t strea
        a->k_row_stride | a->v_page_stride | a->v_row_stride) & 7)
     return fail(MOE_ERR_INVALID_ARG, "every stride must be a multiple of 8 elements (16 bytes)");
   if (a->n_tokens > (1 << 30)) return fail(MOE_ERR_UNSUPPORTED, "n_tokens = %d is too many", a->n_tokens);
+  // units of work, at most: they are counted in 32 bits
+  const double units = ((double)a->n_tokens * h->n_heads / (2 * kTile - 2 * h->n_heads / h->n_kv_heads + 2) +
+                        (double)a->batch * h->n_kv_heads) *
+                       ((double)a->table_stride * a->page_size / kTile + 1);
+  if (units > 2e9) return fail(MOE_ERR_UNSUPPORTED, "too much work for one call: split the tokens");
   if (a->batch > kMaxBatch) return fail(MOE_ERR_UNSUPPORTED, "batch = %d exceeds %d", a->batch, kMaxBatch);
   const int group = h->n_heads / h->n_kv_heads, columns = h->n_kv_heads * h->head_dim;
   const int tokens = kTile / group, box_rows = std::min(a->page_size, kTile);
