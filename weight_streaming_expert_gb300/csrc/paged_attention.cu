@@ -12,12 +12,15 @@
 //
 // A tile is up to 128 query rows: as many whole tokens of the chunk as fit,
 // each with the heads that share a key/value head, so that a page is read once
-// for all of them.  Per 128
-// positions one warp issues S = Q K^T into TMEM (128 x 128 fp32), four warps
+// for all of them.  Per 64
+// positions one warp issues S = Q K^T into TMEM (128 x 64 fp32), four warps
 // turn S into probabilities, one row a thread with no exchange between
 // threads, and write them over S as the 16-bit A operand of O += P V, which
-// stays in TMEM.  Two such chains run in turn, so that one's products cover
-// the other's exponentials:
+// stays in TMEM.  A chain has two buffers of 64 positions, so that the next
+// scores are ready when a step's softmax ends (S as 128 x 64 takes 400 clocks
+// where 128 x 128 takes 264 for the same positions, but waiting for it took
+// more: 3060 clocks for 256 rows by 128 positions).  Two such chains run side
+// by side:
 //   pair   two tiles of rows over the same positions (chunks of many rows);
 //   split  one tile, the even 128 positions in one chain and the odd ones in
 //          the other, merged at the end (chunks of up to 128 rows, which are
@@ -145,6 +148,13 @@ __device__ __forceinline__ int units_of(const AttnParams& p, const Seq& s, int i
   const int last = min(s.n, (i + 1) * kTiles * p.tokens) - 1;
   const int end = p.a.tree_mask ? s.kv : min(s.kv, max(0, s.base + last + 1));
   return max(1, (end + kTile - 1) / kTile);
+}
+
+// The same value in every lane, told to the compiler: MMAs take their operands
+// from uniform registers, and a move there per operand took longer than the MMA.
+template <typename X>
+__device__ __forceinline__ X uniform(X v) {
+  return __shfl_sync(0xffffffffu, v, 0);
 }
 
 // A CTA's next piece of work.
@@ -298,17 +308,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   auto empty = [&](int s) { return sb + 80u + 8u * s; };
   auto q_full = [&](int t) { return sb + 160u + 8u * t; };
   auto q_empty = [&](int t) { return sb + 176u + 8u * t; };
-  auto s_full = [&](int t) { return sb + 192u + 8u * t; };
-  auto p_full = [&](int t, int half) { return sb + 208u + 16u * t + 8u * half; };
-  auto o_done = [&](int t, int half) { return sb + 240u + 16u * t + 8u * half; };
-  const uint32_t drained = sb + 272u;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + 280);
-  int* gone = reinterpret_cast<int*>(smem + 284);
+  // of a chain and one of its two score buffers
+  auto s_full = [&](int chain, int half) { return sb + 192u + 16u * chain + 8u * half; };
+  auto p_full = [&](int chain, int half) { return sb + 224u + 16u * chain + 8u * half; };
+  auto o_done = [&](int chain, int half) { return sb + 256u + 16u * chain + 8u * half; };
+  const uint32_t drained = sb + 288u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + 296);
+  int* gone = reinterpret_cast<int*>(smem + 300);
   uint8_t* staging = smem + 1024;                          // [8][32 rows][128 bytes]: of the softmax warps
   float2* exchange = reinterpret_cast<float2*>(staging);   // [2][128]: both chains' (m, sum)
   const uint32_t q_at = sb + L::kHead, ring = q_at + L::kQTiles * kTileBytes;
   uint8_t* ring_smem = smem + L::kHead + L::kQTiles * kTileBytes;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
   const moe_attn_args_t& a = p.a;
 
   if (tid == 0) {
@@ -319,8 +330,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(q_full(t), 1);
       mbar_init(q_empty(t), 1);
-      mbar_init(s_full(t), 1);
       for (int half = 0; half < 2; ++half) {
+        mbar_init(s_full(t, half), 1);
         mbar_init(p_full(t, half), 4);
         mbar_init(o_done(t, half), 1);
       }
@@ -372,7 +383,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
   const Waiter wait{gone, p.status};
   if (tid == 0) p.cuts[blockIdx.x].parts = 0;
 
@@ -398,6 +409,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const unsigned long long bits = a.tree_mask && valid ? (unsigned long long)a.tree_mask[it.s.q0 + token] : 0ull;
       const int end = !valid ? 0 : a.tree_mask ? it.s.kv : min(it.s.kv, max(0, it.s.base + token + 1));
       const int plain = a.tree_mask ? max(0, min(it.s.base, end)) : end;
+      const int warp_plain = __reduce_min_sync(0xffffffffu, plain);
       float m = -INFINITY, l = 0.f;
       int done = 0;  // tiles of this chain in this item
       // One step: 64 positions, straight through with or without masking (a
@@ -434,9 +446,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           m = high;
         }
         if ((done > 0 || half > 0) && __any_sync(0xffffffffu, shrink != 1.f)) {
-          // the products so far have to be in before their sums shrink: those
-          // of the tiles before are, for this tile's scores came after them
-          if (half > 0) wait(o_done(chain, 0), (tiles[0] * (1 - chain) + tiles[1] * chain + done) & 1);
+          // the products so far have to be in before their sums shrink: the
+          // last step's, for these scores came after the ones before
+          wait(o_done(chain, half ^ 1), (tiles[0] * (1 - chain) + tiles[1] * chain + done - (half ^ 1)) & 1);
           tc_fence_after();
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
@@ -462,20 +474,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             sum[k & 1] = add2(sum[k & 1], pair_of(x, y));
             packed[k] = pack<T>(x, y);
           }
-          tmem_st16(s_at + kHalf / 2 * half + 16 * i, packed);
+          tmem_st16(s_at + kHalf * half + 16 * i, packed);
         }
         sum[0] = add2(sum[0], sum[1]);
         l += low_of(sum[0]) + high_of(sum[0]);
         tmem_wait_st();
       };
       for (int u = kPair ? it.u0 : it.u0 + chain; u < it.u1; u += kPair ? 1 : 2) {
-        wait(s_full(chain), (tiles[0] * (1 - chain) + tiles[1] * chain + done) & 1);
-        tc_fence_after();
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           const int first_pos = u * kTile + half * kHalf;
+          wait(s_full(chain, half), (tiles[0] * (1 - chain) + tiles[1] * chain + done) & 1);
+          tc_fence_after();
           if (warp_valid) {
-            if (__any_sync(0xffffffffu, plain < first_pos + kHalf))
+            if (warp_plain < first_pos + kHalf)
               softmax_step(half, first_pos, std::true_type{});
             else
               softmax_step(half, first_pos, std::false_type{});
@@ -507,7 +519,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       tiles[0] += count0;
       tiles[1] += count1;
-      // the last tile's products (the one's before are in)
+      // the last step's products (which come after all the others)
       if (!kPair || chain == 0) wait(o_done(0, 1), (tiles[0] - 1) & 1);
       if (kPair ? chain == 1 : count1 > 0) wait(o_done(1, 1), (tiles[1] - 1) & 1);
       tc_fence_after();
@@ -693,48 +705,49 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     } else if (warp == kMmaWarp) {
     Walk<kTiles> walk(p, plan);
     Item it{};
-    // ---- products, issued by lane 0
-    constexpr uint32_t kDescS = mma_desc(std::is_same<T, __nv_bfloat16>::value, false, kTile, kTile);
-    constexpr uint32_t kDescO = mma_desc(std::is_same<T, __nv_bfloat16>::value, true, kTile, D);
-    int taken = 0, q_round = 0, p_round[2] = {0, 0};  // p_round: units of a chain
+    // ---- products, issued by one lane
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr uint32_t kDescS = mma_desc(kBf16, false, kTile, kHalf), kDescO = mma_desc(kBf16, true, kTile, D);
+    int taken = 0, q_round = 0;
+    uint32_t p_parity = 0;  // bit 2 chain + half: of the next probabilities
     auto next_stage = [&]() {
       const int stage = taken % kStages;
       wait(full(stage), (taken / kStages) & 1);
       ++taken;
       return stage;
     };
-    auto scores = [&](int chain, int q_tile, int stage) {
-      if (lane == 0) {
-        const uint64_t qd = smem_desc(q_at + q_tile * kTileBytes, 16, 1024), kd = smem_desc(ring + stage * kTileBytes, 16, 1024);
+    // S of 64 of a stage's positions, into the chain's buffer of that half
+    auto scores = [&](int chain, int half, int q_tile, int stage) {
+      if (elected()) {
+        const uint64_t qd = smem_desc(q_at + q_tile * kTileBytes, 16, 1024);
+        const uint64_t kd = smem_desc(ring + stage * kTileBytes + half * kHalf * 128, 16, 1024);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k / 4) * kPanel + (k % 4) * 32;
-          mma_ss(tmem + chain * kTile, qd + off / 16, kd + off / 16, kDescS, k > 0);
+          const uint32_t off = ((k / 4) * kPanel + (k % 4) * 32) / 16;
+          mma_ss(tmem + chain * kTile + half * kHalf, qd + off, kd + off, kDescS, k > 0);
         }
-        mma_commit(s_full(chain));
+        mma_commit(s_full(chain, half));
       }
     };
-    auto products = [&](int chain, int stage, bool add) {
-      const uint32_t parity = p_round[chain]++ & 1;
+    auto products = [&](int chain, int half, int stage, bool add) {
+      wait(p_full(chain, half), (p_parity >> (2 * chain + half)) & 1);
+      p_parity ^= 1u << (2 * chain + half);
+      tc_fence_after();
+      if (elected()) {
+        const uint64_t vd = smem_desc(ring + stage * kTileBytes + half * kHalf * 128, kPanel, 1024);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        wait(p_full(chain, half), parity);
-        tc_fence_after();
-        if (lane == 0) {
-          const uint64_t vd = smem_desc(ring + stage * kTileBytes, kPanel, 1024);
-#pragma unroll
-          for (int k = half * (kHalf / 16); k < (half + 1) * (kHalf / 16); ++k)
-            mma_ts(tmem + 2 * kTile + chain * D, tmem + chain * kTile + k * 8, vd + k * 128, kDescO, add || k > 0);
-          mma_commit(o_done(chain, half));
-        }
+        for (int k = 0; k < kHalf / 16; ++k)
+          mma_ts(tmem + 2 * kTile + chain * D, tmem + chain * kTile + half * kHalf + k * 8, vd + k * 128, kDescO,
+                 add || k > 0);
+        mma_commit(o_done(chain, half));
       }
     };
     auto release = [&](int stage) {
-      if (lane == 0) mma_commit(empty(stage));
+      if (elected()) mma_commit(empty(stage));
     };
     // the item's scores are all issued: its queries make room for the next
     auto release_queries = [&]() {
-      if (lane == 0) {
+      if (elected()) {
         mma_commit(q_empty(0));
         if (kPair) mma_commit(q_empty(1));
       }
@@ -754,55 +767,65 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       return stage;
     };
-    while (walk.next(it)) {
-      const int n = it.u1 - it.u0;
+    while (uniform((int)walk.next(it))) {
+      const int n = uniform(it.u1 - it.u0);
       wait(q_full(0), q_round & 1);
+      if (kPair) wait(q_full(1), q_round & 1);
+      int ks[2], vs[2];
+      // scores go two steps ahead of the products: a chain's softmax finds the
+      // next scores ready while the MMAs of its last step are still to come
       if (kPair) {
-        int ks = next_stage();
+        ks[0] = next_stage();
         tc_fence_after();
-        scores(0, 0, ks);
-        wait(q_full(1), q_round & 1);
-        scores(1, 1, ks);
-        release(ks);
+        for (int step = 0; step < 4; ++step) scores(step & 1, step >> 1, step & 1, ks[0]);
+        release(ks[0]);
         if (n == 1) release_queries();
         for (int j = 0; j < n; ++j) {
-          const int vs = value_stage(it.u0 + j);
-          products(0, vs, j > 0);
-          if (j + 1 < n) {
-            ks = next_stage();
-            scores(0, 0, ks);
+#pragma unroll
+          for (int step = 0; step < 4; ++step) {
+            const int chain = step & 1, half = step >> 1;
+            if (step == 0) vs[0] = value_stage(it.u0 + j);
+            products(chain, half, vs[0], j > 0 || half > 0);
+            if (j + 1 < n) {
+              if (step == 0) ks[0] = next_stage();
+              scores(chain, half, chain, ks[0]);
+            }
           }
-          products(1, vs, j > 0);
-          release(vs);
-          if (j + 1 < n) {
-            scores(1, 1, ks);
-            release(ks);
-            if (j + 2 == n) release_queries();
-          }
+          release(vs[0]);
+          if (j + 1 < n) release(ks[0]);
+          if (j + 2 == n) release_queries();
         }
       } else {
-        for (int j = 0; j < min(n, 2); ++j) {
-          const int ks = next_stage();
+        for (int i = 0; i < min(n, 2); ++i) {
+          ks[0] = next_stage();
           tc_fence_after();
-          scores(j, 0, ks);
-          release(ks);
-          if (j + 1 == n) release_queries();
+          scores(i, 0, 0, ks[0]);
+          scores(i, 1, 0, ks[0]);
+          release(ks[0]);
         }
-        for (int j = 0; j < n; ++j) {
-          const int vs = value_stage(it.u0 + j);
-          products(j & 1, vs, j > 1);
-          release(vs);
-          if (j + 2 < n) {
-            const int ks = next_stage();
-            scores(j & 1, 0, ks);
-            release(ks);
-            if (j + 3 == n) release_queries();
+        if (n <= 2) release_queries();
+        for (int i0 = 0; i0 < n; i0 += 2) {
+#pragma unroll
+          for (int step = 0; step < 4; ++step) {
+            const int chain = step & 1, half = step >> 1, i = i0 + chain;
+            if (i >= n) continue;
+            if (half == 0) vs[chain] = value_stage(it.u0 + i);
+            products(chain, half, vs[chain], i0 > 0 || half > 0);
+            if (i + 2 < n) {
+              if (half == 0) ks[chain] = next_stage();
+              scores(chain, half, 0, ks[chain]);
+            }
+            if (half == 1) {
+              release(vs[chain]);
+              if (i + 2 < n) release(ks[chain]);
+              if (i + 3 == n) release_queries();
+            }
           }
         }
       }
       ++q_round;
     }
-    if (lane == 0) mma_commit(drained);
+    if (elected()) mma_commit(drained);
     unsigned long long waited;
     mbar_wait(drained, 0, &waited);
     __syncwarp();

@@ -14,6 +14,13 @@
 
 namespace wse {
 
+// True in one lane of a converged warp, always the same one.
+__device__ __forceinline__ bool elected() {
+  uint32_t yes;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(yes));
+  return yes != 0;
+}
+
 // One elected warp allocates, and the same warp frees.
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_dst, uint32_t columns) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(columns)
