@@ -4,7 +4,6 @@ into the paged cache (``QKNormRope``) and attention of new tokens over it
 library's kernels.  Nothing here is differentiable."""
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 from fractions import Fraction
@@ -12,39 +11,59 @@ from fractions import Fraction
 import torch
 
 from . import native as N
-from .layer import _ptr, _stream_ptr
 
 _DTYPES = {torch.bfloat16: N.MOE_DTYPE_BF16, torch.float16: N.MOE_DTYPE_FP16}
-_NO_CONTEXT = contextlib.nullcontext()
 _TWO_PI = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
 
-
-def _on(device, stream):
-    """Context in which outputs are allocated: the call's device and stream, so
-    that the allocator orders their reuse after the kernel."""
-    if stream is not None:
-        return torch.cuda.stream(stream)
-    if device.type != "cuda":
-        return _NO_CONTEXT
-    return _NO_CONTEXT if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+# The calls below cost a few microseconds of GPU time where there are few
+# tokens, so what the host does before each counts: one expression looks the
+# arguments over, and only where it finds something are they gone through one
+# by one for the message.
 
 
-def _heads(name, t, dtype, device, dim):
+def _raw_stream(index, stream):
+    """The stream a call runs on, as an integer."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+class _On:
+    """Device and stream of a call that are not the current ones: outputs are
+    allocated, and the kernel is launched, inside."""
+
+    def __init__(self, index, stream):
+        self._contexts = [torch.cuda.device(index)] + ([] if stream is None else [torch.cuda.stream(stream)])
+
+    def __enter__(self):
+        for c in self._contexts:
+            c.__enter__()
+
+    def __exit__(self, *e):
+        for c in reversed(self._contexts):
+            c.__exit__(*e)
+
+
+def _elsewhere(index, stream):
+    """Whether a call on GPU `index` and `stream` needs `_On`."""
+    return stream is not None or torch._C._cuda_getDevice() != index
+
+
+def _heads(name, t, dtype, index, dim):
     """t: [tokens, heads, dim], each head's values contiguous."""
-    if t.dim() != 3 or t.dtype != dtype or t.device != device or t.shape[2] != dim or (t.stride(2) != 1 and dim > 1):
-        raise ValueError(f"{name} must be a {dtype} CUDA tensor [tokens, heads, {dim}] with contiguous heads")
+    if t.dim() != 3 or t.dtype != dtype or t.get_device() != index or t.shape[2] != dim or t.stride(2) != 1:
+        raise ValueError(f"{name} must be a {dtype} tensor [tokens, heads, {dim}] with contiguous heads on cuda:{index}")
 
 
-def _cache(name, t, dtype, device, dim):
-    """t: [pages, page_size, kv_heads, dim], each row contiguous."""
-    if (t.dim() != 4 or t.dtype != dtype or t.device != device or t.shape[3] != dim or t.stride(3) != 1
-            or (t.shape[2] > 1 and t.stride(2) != dim)):
-        raise ValueError(f"{name} must be a {dtype} CUDA tensor [pages, page_size, kv_heads, {dim}] with contiguous rows")
+def _cache(name, t, dtype, index, heads, dim):
+    """t: [pages, page_size, heads, dim], each row contiguous."""
+    if (t.dim() != 4 or t.dtype != dtype or t.get_device() != index or t.shape[2:] != (heads, dim)
+            or t.stride()[2:] != (dim, 1)):
+        raise ValueError(f"{name} must be a {dtype} tensor [pages, page_size, {heads}, {dim}] with contiguous rows "
+                         f"on cuda:{index}")
 
 
-def _plain(name, t, dtype, device, *shape):
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor {list(shape)}")
+def _plain(name, t, dtype, index, *shape):
+    if t.dtype != dtype or t.get_device() != index or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on cuda:{index}")
 
 
 class QKNormRope:
@@ -70,48 +89,72 @@ class QKNormRope:
         self.head_dim, self.rotary_dim, self.interleaved, self.eps = head_dim, rotary_dim, bool(interleaved), float(eps)
         # turns per position as whole parts of 2^64, as signed words
         turns = [round(Fraction(f) / _TWO_PI * (1 << 64)) % (1 << 64) for f in inv_freq]
-        device = torch.device(device)
-        self.turns = torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
+        words = [t - (1 << 64) if t >> 63 else t for t in turns]
+        self.turns = torch.tensor(words, dtype=torch.int64).to(device)
         self.device = self.turns.device
+        self._turns_ptr = self.turns.data_ptr()
 
     def forward(self, q, k, v, q_weight, k_weight, positions, slots, k_cache, v_cache, q_out=None, stream=None):
         """q [T, Hq, D], k and v [T, Hk, D] (views of one projection are fine),
         weights [D] or None, positions int32 [T], slots int64 [T] (a negative
         slot writes nothing), caches [pages, page_size, Hk, D].  Returns q_out
         (a new contiguous tensor, or the given one; it may be q)."""
+        index = self.turns.get_device()
+        if _elsewhere(index, stream):
+            with _On(index, stream):
+                return self._forward(index, q, k, v, q_weight, k_weight, positions, slots, k_cache, v_cache, q_out)
+        return self._forward(index, q, k, v, q_weight, k_weight, positions, slots, k_cache, v_cache, q_out)
+
+    def _forward(self, index, q, k, v, q_weight, k_weight, positions, slots, k_cache, v_cache, q_out):
         T, Hq, D = q.shape
-        dt, dev = q.dtype, q.device
-        if dt not in _DTYPES or dev != self.device or D != self.head_dim:
-            raise ValueError(f"q must be a bf16 or fp16 tensor [tokens, heads, {self.head_dim}] on {self.device}")
-        _heads("q", q, dt, dev, D)
-        _heads("k", k, dt, dev, D)
-        _heads("v", v, dt, dev, D)
-        _cache("k_cache", k_cache, dt, dev, D)
-        _cache("v_cache", v_cache, dt, dev, D)
-        Hk = k.shape[1]
-        if k.shape != v.shape or k.shape[0] != T or k_cache.shape != v_cache.shape or k_cache.shape[2] != Hk:
-            raise ValueError("q, k, v and the caches must agree in tokens and heads")
-        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-            if w is not None:
-                _plain(name, w, dt, dev, D)
-        _plain("positions", positions, torch.int32, dev, T)
-        _plain("slots", slots, torch.int64, dev, T)
-        with _on(dev, stream):
-            if q_out is None:
-                q_out = torch.empty((T, Hq, D), dtype=dt, device=dev)
-            else:
-                _heads("q_out", q_out, dt, dev, D)
-                if q_out.shape != q.shape:
-                    raise ValueError("q_out must have q's shape")
-            a = N.moe_qk_norm_rope_args_t(
-                _DTYPES[dt], T, Hq, Hk, D, self.rotary_dim, self.interleaved, self.eps, q.data_ptr(), k.data_ptr(),
-                v.data_ptr(), q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
-                None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
-                self.turns.data_ptr(), positions.data_ptr(), slots.data_ptr(), q_out.data_ptr(), q_out.stride(0),
-                q_out.stride(1), k_cache.data_ptr(), v_cache.data_ptr(), k_cache.stride(0), k_cache.stride(1),
-                v_cache.stride(0), v_cache.stride(1), k_cache.shape[0], k_cache.shape[1])
-            N.check("moe_qk_norm_rope", N.lib().moe_qk_norm_rope(ctypes.byref(a), _stream_ptr(stream)))
+        dt = q.dtype
+        pages, page_size, Hk, _ = shape = k_cache.shape
+        tokens = (T,)
+        qs, ks, vs, kc, vc = q.stride(), k.stride(), v.stride(), k_cache.stride(), v_cache.stride()
+        if not (dt in _DTYPES and D == self.head_dim and k.shape == v.shape == (T, Hk, D) and v_cache.shape == shape
+                and shape[3] == D and k.dtype is dt and v.dtype is dt and k_cache.dtype is dt and v_cache.dtype is dt
+                and qs[2] == ks[2] == vs[2] == 1 and kc[2:] == vc[2:] == (D, 1)
+                and q.get_device() == k.get_device() == v.get_device() == k_cache.get_device() == v_cache.get_device()
+                == positions.get_device() == slots.get_device() == index
+                and positions.dtype is torch.int32 and positions.shape == tokens and positions.is_contiguous()
+                and slots.dtype is torch.int64 and slots.shape == tokens and slots.is_contiguous()):
+            self._explain(index, q, k, v, positions, slots, k_cache, v_cache)
+        w = (D,)
+        if q_weight is not None and not (q_weight.dtype is dt and q_weight.shape == w and q_weight.is_contiguous()
+                                         and q_weight.get_device() == index):
+            _plain("q_weight", q_weight, dt, index, D)
+        if k_weight is not None and not (k_weight.dtype is dt and k_weight.shape == w and k_weight.is_contiguous()
+                                         and k_weight.get_device() == index):
+            _plain("k_weight", k_weight, dt, index, D)
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+        else:
+            _heads("q_out", q_out, dt, index, D)
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must have q's shape")
+        os = q_out.stride()
+        a = N.moe_qk_norm_rope_args_t(
+            _DTYPES[dt], T, Hq, Hk, D, self.rotary_dim, self.interleaved, self.eps, q.data_ptr(), k.data_ptr(),
+            v.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], None if q_weight is None else q_weight.data_ptr(),
+            None if k_weight is None else k_weight.data_ptr(), self._turns_ptr, positions.data_ptr(), slots.data_ptr(),
+            q_out.data_ptr(), os[0], os[1], k_cache.data_ptr(), v_cache.data_ptr(), kc[0], kc[1], vc[0], vc[1], pages,
+            page_size)
+        status = N.lib().moe_qk_norm_rope(ctypes.byref(a), torch._C._cuda_getCurrentRawStream(index))
+        if status:
+            N.check("moe_qk_norm_rope", status)
         return q_out
+
+    def _explain(self, index, q, k, v, positions, slots, k_cache, v_cache):
+        T, D, dt = q.shape[0], self.head_dim, q.dtype
+        if dt not in _DTYPES:
+            raise ValueError("q must be bf16 or fp16")
+        for name, t in (("q", q), ("k", k), ("v", v)):
+            _heads(name, t, dt, index, D)
+        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+            _cache(name, t, dt, index, k.shape[1], D)
+        _plain("positions", positions, torch.int32, index, T)
+        _plain("slots", slots, torch.int64, index, T)
+        raise ValueError("q, k, v and the caches must agree in tokens, heads and pages")
 
     __call__ = forward
 
@@ -123,6 +166,7 @@ class PagedAttention:
     def __init__(self, n_heads: int, n_kv_heads: int, head_dim: int, device="cuda"):
         self.n_heads, self.n_kv_heads, self.head_dim = n_heads, n_kv_heads, head_dim
         self.device = torch.empty(0, device=device).device
+        self._index = self.device.index
         with torch.cuda.device(self.device):
             h = N.lib().moe_attn_create(n_heads, n_kv_heads, head_dim)
         if not h:
@@ -137,43 +181,64 @@ class PagedAttention:
         D ** -0.5; tree_mask: int64 [T], bit j of a token's word set where it
         sees its chunk's token j, instead of the chain (chunks up to 64).
         Returns out [T, Hq, D], with ``return_lse`` also fp32 [T, Hq]."""
-        T, Hq, D = q.shape
-        dt, dev = q.dtype, q.device
-        if dt not in _DTYPES or dev != self.device or Hq != self.n_heads or D != self.head_dim:
-            raise ValueError(f"q must be a bf16 or fp16 tensor [tokens, {self.n_heads}, {self.head_dim}] on {self.device}")
-        _heads("q", q, dt, dev, D)
-        _cache("k_cache", k_cache, dt, dev, D)
-        _cache("v_cache", v_cache, dt, dev, D)
-        if k_cache.shape != v_cache.shape or k_cache.shape[2] != self.n_kv_heads:
-            raise ValueError(f"the caches must have one shape, with {self.n_kv_heads} heads")
-        if block_table.dim() != 2:
-            raise ValueError("block_table must be [batch, pages]")
-        B = block_table.shape[0]
-        if block_table.dtype != torch.int32 or block_table.device != dev or block_table.stride(1) != 1:
-            raise ValueError("block_table must be an int32 CUDA tensor [batch, pages] with contiguous rows")
-        _plain("q_starts", q_starts, torch.int32, dev, B + 1)
-        _plain("kv_lens", kv_lens, torch.int32, dev, B)
+        index = self._index
+        if _elsewhere(index, stream):
+            with _On(index, stream):
+                return self._forward(q, k_cache, v_cache, block_table, q_starts, kv_lens, max_q_len, scale, tree_mask,
+                                     out, return_lse)
+        return self._forward(q, k_cache, v_cache, block_table, q_starts, kv_lens, max_q_len, scale, tree_mask, out,
+                             return_lse)
+
+    def _forward(self, q, k_cache, v_cache, block_table, q_starts, kv_lens, max_q_len, scale, tree_mask, out,
+                 return_lse):
+        index, D, dt, dev = self._index, self.head_dim, q.dtype, q.device
+        T = q.shape[0]
+        B, width = block_table.shape
+        shape = k_cache.shape
+        qs, kc, vc, bs = q.stride(), k_cache.stride(), v_cache.stride(), block_table.stride()
+        if not (dt in _DTYPES and q.shape == (T, self.n_heads, D) and qs[2] == 1 and len(shape) == 4
+                and shape[2] == self.n_kv_heads and shape[3] == D and v_cache.shape == shape and k_cache.dtype is dt
+                and v_cache.dtype is dt and kc[2:] == vc[2:] == (D, 1) and block_table.dtype is torch.int32
+                and bs[1] == 1 and q_starts.dtype is torch.int32 and q_starts.shape == (B + 1,)
+                and q_starts.is_contiguous() and kv_lens.dtype is torch.int32 and kv_lens.shape == (B,)
+                and kv_lens.is_contiguous()
+                and q.get_device() == k_cache.get_device() == v_cache.get_device() == block_table.get_device()
+                == q_starts.get_device() == kv_lens.get_device() == index):
+            self._explain(q, k_cache, v_cache, block_table, q_starts, kv_lens)
         if tree_mask is not None:
-            _plain("tree_mask", tree_mask, torch.int64, dev, T)
-        lse = None
-        with _on(dev, stream):
-            if out is None:
-                out = torch.empty((T, Hq, D), dtype=dt, device=dev)
-            else:
-                _heads("out", out, dt, dev, D)
-                if out.shape != q.shape:
-                    raise ValueError("out must have q's shape")
-            if return_lse:
-                lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
-            a = N.moe_attn_args_t(
-                _DTYPES[dt], B, T, max_q_len, D ** -0.5 if scale is None else scale, q.data_ptr(), q.stride(0),
-                q.stride(1), k_cache.data_ptr(), v_cache.data_ptr(), k_cache.stride(0), k_cache.stride(1),
-                v_cache.stride(0), v_cache.stride(1), k_cache.shape[0], k_cache.shape[1], block_table.data_ptr(),
-                block_table.stride(0) if B > 1 else block_table.shape[1], q_starts.data_ptr(), kv_lens.data_ptr(),
-                None if tree_mask is None else tree_mask.data_ptr(), out.data_ptr(), out.stride(0), out.stride(1),
-                None if lse is None else lse.data_ptr())
-            N.check("moe_attn_forward", N.lib().moe_attn_forward(self._h, ctypes.byref(a), _stream_ptr(stream)))
+            _plain("tree_mask", tree_mask, torch.int64, index, T)
+        if out is None:
+            out = torch.empty((T, self.n_heads, D), dtype=dt, device=dev)
+        else:
+            _heads("out", out, dt, index, D)
+            if out.shape != q.shape:
+                raise ValueError("out must have q's shape")
+        lse = torch.empty((T, self.n_heads), dtype=torch.float32, device=dev) if return_lse else None
+        os = out.stride()
+        a = N.moe_attn_args_t(
+            _DTYPES[dt], B, T, max_q_len, D ** -0.5 if scale is None else scale, q.data_ptr(), qs[0], qs[1],
+            k_cache.data_ptr(), v_cache.data_ptr(), kc[0], kc[1], vc[0], vc[1], shape[0], shape[1],
+            block_table.data_ptr(), bs[0] if B > 1 else width, q_starts.data_ptr(), kv_lens.data_ptr(),
+            None if tree_mask is None else tree_mask.data_ptr(), out.data_ptr(), os[0], os[1],
+            None if lse is None else lse.data_ptr())
+        status = N.lib().moe_attn_forward(self._h, ctypes.byref(a), torch._C._cuda_getCurrentRawStream(index))
+        if status:
+            N.check("moe_attn_forward", status)
         return (out, lse) if return_lse else out
+
+    def _explain(self, q, k_cache, v_cache, block_table, q_starts, kv_lens):
+        index, D, dt = self._index, self.head_dim, q.dtype
+        if dt not in _DTYPES or q.dim() != 3 or q.shape[1] != self.n_heads:
+            raise ValueError(f"q must be a bf16 or fp16 tensor [tokens, {self.n_heads}, {D}]")
+        _heads("q", q, dt, index, D)
+        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+            _cache(name, t, dt, index, self.n_kv_heads, D)
+        if block_table.dtype != torch.int32 or block_table.get_device() != index or block_table.stride(1) != 1:
+            raise ValueError(f"block_table must be an int32 tensor [batch, pages] with contiguous rows on cuda:{index}")
+        B = block_table.shape[0]
+        _plain("q_starts", q_starts, torch.int32, index, B + 1)
+        _plain("kv_lens", kv_lens, torch.int32, index, B)
+        raise ValueError("the caches must have one shape")
 
     __call__ = forward
 

@@ -8,46 +8,56 @@ import heapq
 import torch
 
 from . import native as N
-from .attention import _on, _plain
-from .layer import _ptr, _stream_ptr
+from .attention import _elsewhere, _On, _plain
 
 
 def _pools(k_pool, v_pool):
-    for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
-        if t.dim() != 5 or not t.is_cuda or t[0, 0].numel() != t.stride(1) or not t[0, 0].is_contiguous():
-            raise ValueError(f"{name} must be a CUDA tensor [layers, pages, page_size, kv_heads, dim] of contiguous pages")
-    if k_pool.shape != v_pool.shape or k_pool.dtype != v_pool.dtype or k_pool.device != v_pool.device:
+    """Strides in bytes of (layer, page) of both pools, the rows' bytes, the GPU."""
+    shape, ks, vs = k_pool.shape, k_pool.stride(), v_pool.stride()
+    index = k_pool.get_device()
+    if len(shape) != 5 or index < 0:
+        raise ValueError("the pools must be CUDA tensors [layers, pages, page_size, kv_heads, dim]")
+    if v_pool.shape != shape or v_pool.dtype != k_pool.dtype or v_pool.get_device() != index:
         raise ValueError("the pools must have one shape, type and device")
+    row = shape[3] * shape[4]
+    inner = (row, shape[4], 1)
+    if ks[2:] != inner or vs[2:] != inner:
+        raise ValueError("the pools' pages must be contiguous")
+    e = k_pool.element_size()
+    return ks[0] * e, vs[0] * e, ks[1] * e, vs[1] * e, row * e, index
+
+
+def _copy(name, dtype, k_pool, v_pool, src, dst, stream):
+    k_layer, v_layer, k_page, v_page, row, index = _pools(k_pool, v_pool)
+    layers, pages, page_size = k_pool.shape[:3]
+    n = src.shape[0]
+    _plain("src", src, dtype, index, n)
+    _plain("dst", dst, dtype, index, n)
+    sizes = (pages, page_size * row) if dtype is torch.int32 else (pages, page_size, row)
+    call = getattr(N.lib(), name)
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            status = call(k_pool.data_ptr(), v_pool.data_ptr(), layers, k_layer, v_layer, k_page, v_page, *sizes,
+                          src.data_ptr(), dst.data_ptr(), n, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        status = call(k_pool.data_ptr(), v_pool.data_ptr(), layers, k_layer, v_layer, k_page, v_page, *sizes,
+                      src.data_ptr(), dst.data_ptr(), n, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        N.check(name, status)
 
 
 def copy_pages(k_pool, v_pool, src, dst, stream=None):
     """Page dst[i] := page src[i] in every layer of both pools [L, P, page_size,
-    Hk, D]; src, dst: int32 CUDA tensors [n].  No page may be in dst twice or
-    in both lists."""
-    _pools(k_pool, v_pool)
-    n, e = src.shape[0], k_pool.element_size()
-    _plain("src", src, torch.int32, k_pool.device, n)
-    _plain("dst", dst, torch.int32, k_pool.device, n)
-    with _on(k_pool.device, stream):
-        N.check("moe_copy_pages", N.lib().moe_copy_pages(
-            _ptr(k_pool), _ptr(v_pool), k_pool.shape[0], k_pool.stride(0) * e, v_pool.stride(0) * e,
-            k_pool.stride(1) * e, v_pool.stride(1) * e, k_pool.shape[1], k_pool.stride(1) * e, _ptr(src), _ptr(dst), n,
-            _stream_ptr(stream)))
+    Hk, D] (pages contiguous, layers and pages any distance apart); src, dst:
+    int32 CUDA tensors [n].  No page may be in dst twice or in both lists."""
+    _copy("moe_copy_pages", torch.int32, k_pool, v_pool, src, dst, stream)
 
 
 def copy_rows(k_pool, v_pool, src, dst, stream=None):
     """Cache rows dst[i] := src[i] in every layer of both pools, as if all were
     read before any is written; src, dst: int64 CUDA tensors [n] of slots (page
     * page_size + row), n up to 64, no slot in dst twice."""
-    _pools(k_pool, v_pool)
-    n, e = src.shape[0], k_pool.element_size()
-    _plain("src", src, torch.int64, k_pool.device, n)
-    _plain("dst", dst, torch.int64, k_pool.device, n)
-    with _on(k_pool.device, stream):
-        N.check("moe_copy_rows", N.lib().moe_copy_rows(
-            _ptr(k_pool), _ptr(v_pool), k_pool.shape[0], k_pool.stride(0) * e, v_pool.stride(0) * e,
-            k_pool.stride(1) * e, v_pool.stride(1) * e, k_pool.shape[1], k_pool.shape[2], k_pool.stride(2) * e,
-            _ptr(src), _ptr(dst), n, _stream_ptr(stream)))
+    _copy("moe_copy_rows", torch.int64, k_pool, v_pool, src, dst, stream)
 
 
 class PageTable:
@@ -180,15 +190,17 @@ class PagedKVCache:
         self.v = torch.zeros(shape, dtype=dtype, device=device)
         self.device = self.k.device
 
-    def _device(self, values, dtype):
+    def _device(self, values, dtype, stream):
         t = torch.tensor(values, dtype=dtype)
-        return t.pin_memory().to(self.device, non_blocking=True) if self.device.type == "cuda" else t
+        if self.device.type != "cuda":
+            return t
+        with _On(self.device.index, stream):
+            return t.pin_memory().to(self.device, non_blocking=True)
 
     def _copy(self, copies, stream):
         if copies:
-            with _on(self.device, stream):
-                src, dst = self._device(list(zip(*copies)), torch.int32)
-                copy_pages(self.k, self.v, src, dst, stream)
+            src, dst = self._device(list(zip(*copies)), torch.int32, stream)
+            copy_pages(self.k, self.v, src, dst, stream)
 
     def open(self) -> int:
         return self.table.open()
@@ -201,8 +213,7 @@ class PagedKVCache:
         device.  A last page that a fork shares is copied first."""
         slots, copies = self.table.extend(seq, n)
         self._copy(copies, stream)
-        with _on(self.device, stream):
-            return self._device(slots, torch.int64)
+        return self._device(slots, torch.int64, stream)
 
     def truncate(self, seq: int, length: int):
         self.table.truncate(seq, length)
@@ -226,10 +237,9 @@ class PagedKVCache:
             self._copy(self.table.unshare(seq, moves[0][1], moves[-1][1] + 1), stream)
         for at in range(0, len(moves), N.MOE_COPY_ROWS_MAX):  # ascending blocks: a block's rows are read before later ones land
             part = moves[at:at + N.MOE_COPY_ROWS_MAX]
-            with _on(self.device, stream):
-                src = self._device(self.table.slots(seq, [a for a, _ in part]), torch.int64)
-                dst = self._device(self.table.slots(seq, [b for _, b in part]), torch.int64)
-                copy_rows(self.k, self.v, src, dst, stream)
+            slots = [self.table.slots(seq, at) for at in zip(*part)]
+            src, dst = self._device(slots, torch.int64, stream)
+            copy_rows(self.k, self.v, src, dst, stream)
         self.table.truncate(seq, start + len(accepted))
 
     def compact(self, stream=None) -> int:
@@ -244,6 +254,5 @@ class PagedKVCache:
         the sequences, on the device."""
         pages = [self.table.pages(s) for s in seqs]
         width = max([1] + [len(p) for p in pages])
-        with _on(self.device, stream):
-            table = self._device([p + [-1] * (width - len(p)) for p in pages], torch.int32).view(len(pages), width)
-            return table, self._device([self.length(s) for s in seqs], torch.int32)
+        table = self._device([p + [-1] * (width - len(p)) for p in pages], torch.int32, stream).view(len(pages), width)
+        return table, self._device([self.length(s) for s in seqs], torch.int32, stream)

@@ -937,27 +937,70 @@ MapEncode map_encode() {
   return fn;
 }
 
-// A three-dimensional map of 16-bit elements, innermost contiguous, whose boxes
-// are 64 columns of `rows` by `slabs`.
-int encode_map(CUtensorMap* map, int dtype, const void* base, int columns, int d1, int64_t stride1, int d2,
-               int64_t stride2, int rows, int slabs, const char* what) {
-  const MapEncode encode = map_encode();
-  if (!encode) return fail(MOE_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
-  const cuuint64_t dims[3] = {(cuuint64_t)columns, (cuuint64_t)d1, (cuuint64_t)d2};
-  const cuuint64_t strides[2] = {(cuuint64_t)stride1 * 2, (cuuint64_t)stride2 * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)rows, (cuuint32_t)slabs};
-  const cuuint32_t steps[3] = {1, 1, 1};
-  const CUresult r =
-      encode(map, dtype == MOE_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-             const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? MOE_OK
-                           : fail(MOE_ERR_INVALID_ARG, "no tensor map for the strides of %s (driver error %d)", what, (int)r);
-}
-
 struct Maps {
   CUtensorMap q, k, v;
 };
+
+using MapReplace = CUresult (*)(CUtensorMap*, void*);
+
+MapReplace map_replace() {
+  static const MapReplace fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapReplaceAddress", &f, 12000, cudaEnableDefault, &r) != cudaSuccess)
+      f = nullptr;
+    return reinterpret_cast<MapReplace>(f);
+  }();
+  return fn;
+}
+
+// What a map says apart from its address, and the map: encoding one takes some
+// microseconds of the host, giving one another address a fraction of that.
+struct Shape {
+  int dtype, columns, d1, d2, rows, slabs;
+  int64_t stride1, stride2;
+  bool operator==(const Shape& o) const {
+    return dtype == o.dtype && columns == o.columns && d1 == o.d1 && d2 == o.d2 && rows == o.rows &&
+           slabs == o.slabs && stride1 == o.stride1 && stride2 == o.stride2;
+  }
+};
+// A three-dimensional map of 16-bit elements, innermost contiguous, whose boxes
+// are 64 columns of `rows` by `slabs`.
+int encode_map(CUtensorMap* map, const Shape& s, const void* base, const char* what) {
+  const MapEncode encode = map_encode();
+  if (!encode) return fail(MOE_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
+  const cuuint64_t dims[3] = {(cuuint64_t)s.columns, (cuuint64_t)s.d1, (cuuint64_t)s.d2};
+  const cuuint64_t strides[2] = {(cuuint64_t)s.stride1 * 2, (cuuint64_t)s.stride2 * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)s.rows, (cuuint32_t)s.slabs};
+  const cuuint32_t steps[3] = {1, 1, 1};
+  const CUresult r =
+      encode(map, s.dtype == MOE_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+             const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS
+             ? MOE_OK
+             : fail(MOE_ERR_INVALID_ARG, "no tensor map for the strides of %s (driver error %d)", what, (int)r);
+}
+
+struct KnownMap {
+  Shape shape{};
+  CUtensorMap map;
+};
+
+int map_for(KnownMap& known, const Shape& s, const void* base, CUtensorMap* map, const char* what) {
+  if (!(known.shape == s)) {
+    const int rc = encode_map(&known.map, s, base, what);
+    if (rc != MOE_OK) {
+      known.shape = Shape{};
+      return rc;
+    }
+    known.shape = s;
+  }
+  *map = known.map;
+  const MapReplace replace = map_replace();
+  const CUresult r = replace ? replace(map, const_cast<void*>(base)) : CUDA_ERROR_NOT_FOUND;
+  return r == CUDA_SUCCESS ? MOE_OK : fail(MOE_ERR_CUDA, "no tensor map at the address of %s (driver error %d)", what, (int)r);
+}
 
 }  // namespace
 }  // namespace wse
@@ -970,6 +1013,7 @@ struct moe_attn {
   float* part_o = nullptr;
   float2* part_ml = nullptr;
   Cut* cuts = nullptr;
+  KnownMap q_map, k_map, v_map;
 };
 
 namespace {
@@ -1088,14 +1132,15 @@ int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t strea
   const int group = h->n_heads / h->n_kv_heads, columns = h->n_kv_heads * h->head_dim;
   const int tokens = kTile / group, box_rows = std::min(a->page_size, kTile);
   Maps maps;
-  int rc = encode_map(&maps.q, a->dtype, a->q, h->head_dim, h->n_heads, a->q_head_stride, a->n_tokens,
-                      a->q_token_stride, group, tokens, "q");
+  int rc = map_for(h->q_map, {a->dtype, h->head_dim, h->n_heads, a->n_tokens, group, tokens, a->q_head_stride,
+                              a->q_token_stride},
+                   a->q, &maps.q, "q");
   if (rc == MOE_OK)
-    rc = encode_map(&maps.k, a->dtype, a->k_cache, columns, a->page_size, a->k_row_stride, a->n_pages,
-                    a->k_page_stride, box_rows, 1, "k_cache");
+    rc = map_for(h->k_map, {a->dtype, columns, a->page_size, a->n_pages, box_rows, 1, a->k_row_stride, a->k_page_stride},
+                 a->k_cache, &maps.k, "k_cache");
   if (rc == MOE_OK)
-    rc = encode_map(&maps.v, a->dtype, a->v_cache, columns, a->page_size, a->v_row_stride, a->n_pages,
-                    a->v_page_stride, box_rows, 1, "v_cache");
+    rc = map_for(h->v_map, {a->dtype, columns, a->page_size, a->n_pages, box_rows, 1, a->v_row_stride, a->v_page_stride},
+                 a->v_cache, &maps.v, "v_cache");
   if (rc != MOE_OK) return rc;
   int spread = 1;
   while (spread < kMaxSpread && h->n_kv_heads % (2 * spread) == 0) spread *= 2;

@@ -95,6 +95,8 @@ def library_path() -> str:
 def lib(build_if_missing: bool = True):
     """The loaded C library with its prototypes declared."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

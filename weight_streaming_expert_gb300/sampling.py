@@ -5,8 +5,7 @@ from __future__ import annotations
 import torch
 
 from . import native as N
-from .attention import _on, _plain
-from .layer import _ptr, _stream_ptr
+from .attention import _elsewhere, _On, _plain
 
 
 def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, return_probs: bool = False,
@@ -17,24 +16,33 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
     and min_p, top_p >= 1 is off.  Returns int32 tokens [M] (-1 for a row
     without a logit above -inf), with ``return_probs`` also each token's
     probability among those that stayed, fp32 [M]."""
-    if logits.dim() != 2 or logits.dtype != torch.float32 or not logits.is_cuda or logits.stride(1) != 1:
+    index = logits.get_device()
+    if index < 0 or logits.dim() != 2 or logits.dtype != torch.float32 or logits.stride(1) != 1:
         raise ValueError("logits must be an fp32 CUDA tensor [rows, vocab] with contiguous rows")
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return _sample(index, logits, u, temperature, top_k, top_p, min_p, tokens, return_probs)
+    return _sample(index, logits, u, temperature, top_k, top_p, min_p, tokens, return_probs)
+
+
+def _sample(index, logits, u, temperature, top_k, top_p, min_p, tokens, return_probs):
     M, V = logits.shape
     dev = logits.device
-    _plain("u", u, torch.float32, dev, M)
+    _plain("u", u, torch.float32, index, M)
     for name, t, dt in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
                         ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
         if t is not None:
-            _plain(name, t, dt, dev, M)
-    probs = None
-    with _on(dev, stream):
-        if tokens is None:
-            tokens = torch.empty(M, dtype=torch.int32, device=dev)
-        else:
-            _plain("tokens", tokens, torch.int32, dev, M)
-        if return_probs:
-            probs = torch.empty(M, dtype=torch.float32, device=dev)
-        N.check("moe_sample", N.lib().moe_sample(_ptr(logits), logits.stride(0), M, V, _ptr(u), _ptr(temperature),
-                                                 _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(tokens), _ptr(probs),
-                                                 _stream_ptr(stream)))
+            _plain(name, t, dt, index, M)
+    if tokens is None:
+        tokens = torch.empty(M, dtype=torch.int32, device=dev)
+    else:
+        _plain("tokens", tokens, torch.int32, index, M)
+    probs = torch.empty(M, dtype=torch.float32, device=dev) if return_probs else None
+    status = N.lib().moe_sample(
+        logits.data_ptr(), logits.stride(0), M, V, u.data_ptr(), None if temperature is None else temperature.data_ptr(),
+        None if top_k is None else top_k.data_ptr(), None if top_p is None else top_p.data_ptr(),
+        None if min_p is None else min_p.data_ptr(), tokens.data_ptr(), None if probs is None else probs.data_ptr(),
+        torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        N.check("moe_sample", status)
     return (tokens, probs) if return_probs else tokens
