@@ -59,6 +59,7 @@ constexpr int kMaxStages = 10;
 constexpr uint32_t kStagingBytes = 8 * 4096;  // 32 rows of 128 bytes for each softmax warp
 constexpr float kRescaleLog2 = 8.f;
 constexpr int kJoinRows = 4, kJoinGroups = 4;  // rows of a joining CTA, and threads that share a row's parts
+constexpr int kFewParts = 4;
 constexpr int kMaxSpread = 8;              // key/value heads that neighbouring CTAs work on side by side
 
 template <typename T>
@@ -104,10 +105,10 @@ __device__ __forceinline__ void max3(float& top, uint32_t x, uint32_t y) {
   asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(__uint_as_float(x)), "f"(__uint_as_float(y)));
 }
 
-// A tile that was cut at the end of CTA c's share: joined from its partial
-// sums in CTAs c, c + 1, .., c + parts - 1 (0: no such tile).
+// A tile that was cut at the end of CTA c's share: joined from the partial sums
+// of CTAs c, c + spread, .., `parts` of them (0: no such tile).
 struct Cut {
-  int parts, b, h, tile;
+  int parts, c, b, h, tile;
 };
 constexpr int kMaxParts = 1024;            // CTAs, which is at least the shares of one tile
 
@@ -119,7 +120,8 @@ struct AttnParams {
   int* status;
   float* part_o;    // [CTAs][2][rows of an item][D]: unnormalised sums
   float2* part_ml;  // [CTAs][2][rows of an item]: (m, sum of p)
-  Cut* cuts;        // [CTAs]
+  Cut* cuts;        // [CTAs]: by the CTA, or by_item
+  bool by_item;     // one item per sequence and head, no more than CTAs: cut b * heads + h is that item's
 };
 
 // One sequence as the kernel takes it: lengths that do not fit are cut.
@@ -385,7 +387,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot);
   const Waiter wait{gone, p.status};
-  if (tid == 0) p.cuts[blockIdx.x].parts = 0;
+  if (p.by_item) {
+    // items that are not cut say so where they begin; these have no items
+    if (blockIdx.x == 0)
+      for (int i = tid; i < a.batch * p.n_kv_heads; i += kAttnThreads)
+        if (load_seq(p, i / p.n_kv_heads).n == 0) p.cuts[i].parts = 0;
+  } else if (tid == 0) {
+    p.cuts[blockIdx.x].parts = 0;
+  }
 
   if (warp < kMmaWarp) {
     Walk<kTiles> walk(p, plan);
@@ -597,11 +606,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f;
         }
       }
-      if (cut && it.u0 == 0 && tid == 0) {
-        // this share ends inside the tile: which share holds its last unit
-        const int last = plan.start + (plan.todo - walk.todo) - n + it.units - 1;
-        const int e = (unsigned)last / (unsigned)plan.share;
-        p.cuts[blockIdx.x] = Cut{e - (int)blockIdx.x / p.spread + 1, it.b, it.h, it.tile};
+      if (it.u0 == 0 && tid == 0) {
+        const int at = p.by_item ? it.b * p.n_kv_heads + it.h : blockIdx.x;
+        if (cut) {
+          // this share ends inside the tile: which share holds its last unit
+          const int last = plan.start + (plan.todo - walk.todo) - n + it.units - 1;
+          const int e = (unsigned)last / (unsigned)plan.share;
+          p.cuts[at] = Cut{e - (int)blockIdx.x / p.spread + 1, (int)blockIdx.x, it.b, it.h, it.tile};
+        } else if (p.by_item) {
+          p.cuts[at].parts = 0;
+        }
       }
       if (!kPair) named_sync(1, 256);  // both chains' sums are read before the next item's
     }
@@ -837,8 +851,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 }
 
 // Joins the tiles that shares have cut: out = sum_i O_i 2^(c (m_i - m)) / sum_i
-// l_i 2^(c (m_i - m)) in the order of the shares.  Block (c, y): of the tile
-// that was cut at the end of CTA c's share, 4 rows at a time.  What it costs is
+// l_i 2^(c (m_i - m)) in the order of the shares.  Block (i, y): of cut i, 4
+// rows at a time.  What it costs is
 // the latency of its reads, so all of a row's statistics are read at once, by
 // the lanes of a warp, and then its parts by four threads per column, whose
 // sums are added in order.
@@ -862,9 +876,53 @@ __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4) join_kernel(c
     return in_tile < p.tokens ? (cut.tile * (kRows / kTile) + row / kTile) * p.tokens + in_tile : s.n;
   };
   const float c = a.scale * 1.4426950408889634f;
-  auto slot = [&](int i) { return 2ll * (blockIdx.x + i * p.spread) + (i == 0 ? 1 : 0); };
-  const int r0 = blockIdx.y * kJoinRows;
-  {
+  auto write = [&](int row, int token, int column, float4 o, float norm, float lse) {
+    const int head = cut.h * p.group + row % kTile % p.group;
+    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (long long)(s.q0 + token) * a.out_token_stride +
+                              head * a.out_head_stride + column * 4) =
+        make_uint2(pack<T>(o.x * norm, o.y * norm), pack<T>(o.z * norm, o.w * norm));
+    if (a.lse && column == 0) a.lse[(long long)(s.q0 + token) * (p.group * p.n_kv_heads) + head] = lse;
+  };
+  auto slot = [&](int i) { return 2ll * (cut.c + i * p.spread) + (i == 0 ? 1 : 0); };
+  // Few parts (tiles of long chunks, cut once or twice): a thread reads all of
+  // its column's at once.
+  if (cut.parts <= kFewParts) {
+    constexpr int kAtOnce = kJoinRows * kJoinGroups;
+    for (int r = blockIdx.y * kAtOnce + tid / kColumns; r < kRows; r += gridDim.y * kAtOnce) {
+      const int token = token_of(r);
+      if (token >= s.n) continue;
+      float2 ml[kFewParts];
+      float4 v[kFewParts];
+#pragma unroll
+      for (int i = 0; i < kFewParts; ++i) {
+        ml[i] = make_float2(-INFINITY, 0.f);
+        if (i < cut.parts) {
+          ml[i] = p.part_ml[slot(i) * kRows + r];
+          v[i] = reinterpret_cast<const float4*>(p.part_o)[(slot(i) * kRows + r) * kColumns + column];
+        }
+      }
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int i = 0; i < kFewParts; ++i) m = fmaxf(m, ml[i].x);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kFewParts; ++i) {
+        if (ml[i].x == -INFINITY) continue;  // a part in which the row sees nothing, or none
+        const float f = exp2_approx((ml[i].x - m) * c);
+        l = fmaf(ml[i].y, f, l);
+        o.x = fmaf(v[i].x, f, o.x);
+        o.y = fmaf(v[i].y, f, o.y);
+        o.z = fmaf(v[i].z, f, o.z);
+        o.w = fmaf(v[i].w, f, o.w);
+      }
+      write(r, token, column, o, l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l),
+            l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f);
+    }
+    return;
+  }
+  for (int r0 = blockIdx.y * kJoinRows; r0 < kRows; r0 += gridDim.y * kJoinRows) {
+    if (token_of(r0) >= s.n && r0 / kTile == (r0 + kJoinRows - 1) / kTile && token_of(r0 + kJoinRows - 1) >= s.n)
+      continue;  // for the whole block
     if (warp < kJoinRows && token_of(r0 + warp) < s.n) {
       float m = -INFINITY, l = 0.f;
       for (int i = lane; i < cut.parts; i += 32) m = fmaxf(m, p.part_ml[slot(i) * kRows + r0 + warp].x);
@@ -911,14 +969,9 @@ __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4) join_kernel(c
         o.z += v.z;
         o.w += v.w;
       }
-      const float norm = total[row].x;
-      const int head = cut.h * p.group + (r0 + row) % kTile % p.group;
-      *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (long long)(s.q0 + token) * a.out_token_stride +
-                                head * a.out_head_stride + column * 4) =
-          make_uint2(pack<T>(o.x * norm, o.y * norm), pack<T>(o.z * norm, o.w * norm));
-      if (a.lse && column == 0)
-        a.lse[(long long)(s.q0 + token) * (p.group * p.n_kv_heads) + head] = total[row].y;
+      write(r0 + row, token, column, o, total[row].x, total[row].y);
     }
+    __syncthreads();  // before the next rows' factors are written
   }
 }
 
@@ -1044,8 +1097,11 @@ int launch_attn(const moe_attn* h, const AttnParams& p, const Maps& maps, moe_st
   const int rc = launch_pdl(paged_attention_kernel<T, D, kPair>, dim3(grid), dim3(kAttnThreads), L::kSmem, stream,
                             1, p, maps.q, maps.k, maps.v);
   if (rc != MOE_OK) return rc;
+  // cuts by item: as many blocks as their rows have use for, for the latency;
+  // else most of the blocks find no cut
   const int rows = kPair ? L::kRows : std::min(p.a.max_q_len, p.tokens) * p.group;
-  return launch_pdl(join_kernel<T, D, L::kRows>, dim3(grid, (rows + kJoinRows - 1) / kJoinRows),
+  const dim3 blocks = p.by_item ? dim3(p.a.batch * p.n_kv_heads, (rows + kJoinRows - 1) / kJoinRows) : dim3(grid, 16);
+  return launch_pdl(join_kernel<T, D, L::kRows>, blocks,
                     dim3(kJoinRows * kJoinGroups * D / 4), 0, stream, 1, p);
 }
 
@@ -1144,7 +1200,9 @@ int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t strea
   if (rc != MOE_OK) return rc;
   int spread = 1;
   while (spread < kMaxSpread && h->n_kv_heads % (2 * spread) == 0) spread *= 2;
-  const AttnParams p{*a, h->n_kv_heads, group, tokens, spread, h->status, h->part_o, h->part_ml, h->cuts};
+  const bool one_item = a->max_q_len <= (a->max_q_len > tokens ? 2 : 1) * tokens;
+  const AttnParams p{*a,       h->n_kv_heads, group,      tokens,  spread,
+                     h->status, h->part_o,     h->part_ml, h->cuts, one_item && a->batch * h->n_kv_heads <= h->n_sms};
   if (a->dtype == MOE_DTYPE_BF16)
     return h->head_dim == 64 ? launch_attn<__nv_bfloat16, 64>(h, p, maps, stream)
                              : launch_attn<__nv_bfloat16, 128>(h, p, maps, stream);
