@@ -437,31 +437,40 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
   // does, exp gives 1 either way; where d / t overflows the remainder is NaN,
   // which counts as infinitely far below like an infinite d.
   const float inverse = __frcp_rn(t);
-  const bool tame = t > 1e-4f && t < 1e4f;
-  // weights of four keys, without a branch between them
-  auto weights = [&](const uint32_t (&key)[4], u64 (&w)[4]) {
-    float d[4], z[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) d[j] = logit_of(key[j]) - top;
+  const bool tame = t > 1e-4f && t < 1e4f && top < INFINITY;
+  // exp((l - l0) / t) of four keys, without a branch between them; 0 for what
+  // is infinitely far below (also at an infinite temperature)
+  auto exps = [&](const uint32_t (&key)[4], float (&e)[4]) {
+    float z[4];
     if (tame) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float q = d[j] * inverse;
-        z[j] = fmaf(fmaf(-q, t, d[j]), inverse, q);
+        const float d = logit_of(key[j]) - top, q = d * inverse;
+        z[j] = fmaf(fmaf(-q, t, d), inverse, q);
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) z[j] = d[j] / t;
+      for (int j = 0; j < 4; ++j) z[j] = key[j] == top_key ? 0.f : (logit_of(key[j]) - top) / t;  // top may be infinite
     }
 #pragma unroll
+    for (int j = 0; j < 4; ++j) e[j] = fmaxf(expf(z[j]), 0.f);  // of NaN and 0: 0
+  };
+  // floor(2^38 e) as a high and a low word of 19 bits (e = 1: 2^19 and 0).
+  // Adding 2^23 towards minus infinity leaves the whole part in the low bits,
+  // and both remainders are exact; conversions would take four times as long.
+  auto split = [](float e, uint32_t& high, uint32_t& low) {
+    const float h = __fadd_rd(e * 0x1p19f, 0x1p23f);
+    high = __float_as_uint(h) & 0x7fffffu;
+    low = __float_as_uint(__fadd_rd(fmaf(e, 0x1p38f, (h - 0x1p23f) * -0x1p19f), 0x1p23f)) & 0x7fffffu;
+  };
+  auto weights = [&](const uint32_t (&key)[4], u64 (&w)[4]) {
+    float e[4];
+    exps(key, e);
+#pragma unroll
     for (int j = 0; j < 4; ++j) {
-      // infinitely far below (also at an infinite temperature): 0; the top,
-      // also an infinite one: 1
-      const float x = expf(z[j]);
-      const float e = key[j] == top_key ? 1.f : z[j] == z[j] ? x : 0.f;
-      // floor(2^38 e) in two parts: both steps are exact
-      const uint32_t high = (uint32_t)(e * 0x1p19f);
-      w[j] = ((u64)high << 19) + (uint32_t)fmaf(e, 0x1p38f, (float)high * -0x1p19f);
+      uint32_t high, low;
+      split(e[j], high, low);
+      w[j] = ((u64)high << 19) + low;
     }
   };
   auto weight = [&](uint32_t key) {
@@ -470,22 +479,31 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
     weights(k, w);
     return w[0];
   };
-  // weight of this thread's keys above `bar`
-  auto mass_above = [&](uint32_t bar) {
-    u64 sum = 0;
-    c.each4([&](int, const uint32_t (&key)[4]) {
-      if (max(max(key[0], key[1]), max(key[2], key[3])) <= bar) return;
-      u64 w[4];
-      weights(key, w);
+  // Weight of this thread's keys from `bar` on, of at least `least`, up to id
+  // tie_end for those of key bar itself.  A thread has at most 1025 keys, whose
+  // high and low words sum to less than 2^32.
+  auto mass_from = [&](uint32_t bar, float least, int tie_end) {
+    uint32_t high = 0, low = 0;
+    c.each4([&](int i, const uint32_t (&key)[4]) {
+      if (max(max(key[0], key[1]), max(key[2], key[3])) < bar) return;
+      float e[4];
+      exps(key, e);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sum += key[j] > bar ? w[j] : 0;
+      for (int j = 0; j < 4; ++j) {
+        bool stays = key[j] >= bar && e[j] >= least;
+        if (tie_end != kAllTies) stays = stays && (key[j] != bar || c.id(i + j) <= tie_end);
+        uint32_t h, l;
+        split(stays ? e[j] : 0.f, h, l);
+        high += h;
+        low += l;
+      }
     });
-    return sum;
+    return ((u64)high << 19) + low;
   };
 
   const bool by_count = k > 0 && k < a.vocab, by_mass = p < 1.f;
   u64 above, at, total, row_mass = 0;
-  if (by_mass && !by_count) c.team_scan(mass_above(0), row_mass);  // top-p's share is of the whole row
+  if (by_mass && !by_count) c.team_scan(mass_from(0, 0.f, kAllTies), row_mass);  // top-p's share is of the whole row
   if (size > 1 && (by_count || by_mass)) {
     // the keys above `bar`: at most kList, those of this thread
     uint32_t bar;
@@ -496,7 +514,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
       for (int j = 0; j < 4; ++j) count += key[j] > bar;
     });
     const int to = (int)c.team_scan(count, total);
-    if (by_mass && !by_count) c.team_scan(mass_above(bar), in_list);
+    if (by_mass && !by_count) c.team_scan(mass_from(bar + 1, 0.f, kAllTies), in_list);
     if (tid == 0) s.shared[0] = by_mass && !by_count ? whole_of((double)p * (double)row_mass) : 0;
     __syncthreads();
     if (total > 0 && (by_count ? (u64)k <= total : s.shared[0] <= in_list)) {
@@ -532,7 +550,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
   }
   if (by_mass) {
     if (by_count) {
-      c.team_scan(mass_above(thr), row_mass);
+      c.team_scan(mass_from(thr + 1, 0.f, kAllTies), row_mass);
       row_mass += ties * weight(thr);
     }
     // 64-bit arithmetic is slow on this GPU: one thread does it for all
@@ -576,42 +594,42 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
     c.sync();
     tie_end = s.tie_end;
   }
-  // ceil(2^38 min_p), exact in fp32: a power of two times it
-  const u64 least = min_p > 0.f ? (u64)ceilf(fminf(min_p, 1.f) * kOne) : 0;
-
-  // weights of keys i .. i + 3, 0 where the token does not stay
-  auto staying = [&](int i, const uint32_t (&key)[4], u64 (&w)[4]) {
-    weights(key, w);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (w[j] < least || key[j] < thr || (key[j] == thr && tie_end != kAllTies && c.id(i + j) > tie_end)) w[j] = 0;
-  };
-  u64 sum = 0;
-  c.each4([&](int i, const uint32_t (&key)[4]) {
-    if (max(max(key[0], key[1]), max(key[2], key[3])) < thr) return;
-    u64 w[4];
-    staying(i, key, w);
-    sum += (w[0] + w[1]) + (w[2] + w[3]);
-  });
+  // w >= min_p 2^38 is e >= the least multiple of 2^-38 that is not below
+  // min_p: exact in fp32, as 2^38 e and min_p have 24 bits
+  const float least = min_p > 0.f ? ceilf(fminf(min_p, 1.f) * kOne) * 0x1p-38f : 0.f;
+  const u64 sum = mass_from(thr, least, tie_end);
   u64 before = c.team_scan(sum, total);
   if (tid == 0) s.shared[0] = min((u64)((double)u * (double)total), total - 1);
   __syncthreads();
   const u64 wanted = s.shared[0];
-  if (wanted >= before && wanted < before + sum) {  // the token is one of this thread's
-    bool found = false;
-    c.each4([&](int i, const uint32_t (&key)[4]) {
-      u64 w[4];
-      staying(i, key, w);
+  const unsigned here = __ballot_sync(0xffffffffu, wanted >= before && wanted < before + sum);
+  if (here) {  // the token is one of a thread's of this warp: its lanes look through them
+    const int src = __ffs(here) - 1, from = __shfl_sync(0xffffffffu, c.i0, src), to = __shfl_sync(0xffffffffu, c.i1, src);
+    before = __shfl_sync(0xffffffffu, before, src);
+    for (int i = from + c.lane;; i += 32) {
+      const uint32_t key[4] = {i < to ? c.key(i) : 0u, 0u, 0u, 0u};
+      float e[4];
+      exps(key, e);
+      const bool stays = i < to && key[0] >= thr && e[0] >= least && (key[0] != thr || c.id(i) <= tie_end);
+      uint32_t high, low;
+      split(stays ? e[0] : 0.f, high, low);
+      const u64 w = ((u64)high << 19) + low;
+      u64 upto = w;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        before += w[j];
-        if (!found && before > wanted) {
-          found = true;
-          a.tokens[m] = c.id(i + j);
-          if (a.probs) a.probs[m] = quotient(w[j], total);
-        }
+      for (int d = 1; d < 32; d <<= 1) {
+        const u64 o = __shfl_up_sync(0xffffffffu, upto, d);
+        if (c.lane >= d) upto += o;
       }
-    });
+      const unsigned past = __ballot_sync(0xffffffffu, before + upto > wanted);
+      if (past) {
+        if (c.lane == __ffs(past) - 1) {
+          a.tokens[m] = c.id(i);
+          if (a.probs) a.probs[m] = quotient(w, total);
+        }
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, upto, 31);
+    }
   }
   c.sync();  // no CTA leaves while another may read its sums
 }
@@ -637,7 +655,7 @@ extern "C" int moe_sample(const float* logits, int64_t row_stride, int rows, int
   int rc = check_device();
   if (rc != MOE_OK) return rc;
   int cluster = kMaxCluster;
-  while (cluster > 1 && (rows * cluster > 1024 || (vocab + cluster - 1) / cluster < kSampleThreads) &&
+  while (cluster > 1 && (rows * cluster > 256 || (vocab + cluster - 1) / cluster < kSampleThreads) &&
          (vocab + cluster / 2 - 1) / (cluster / 2) <= kMaxSlice)
     cluster /= 2;
   SampleArgs a{logits, row_stride, vocab, (vocab + cluster - 1) / cluster, u, temperature, top_k, top_p, min_p,
