@@ -112,7 +112,7 @@ typedef struct {
 
 /*
  * Errors found on the device (a page outside the cache, whose positions then
- * count as zeros; a length beyond the table, which is cut to it; a chunk
+ * count as zeros; a length beyond the table or 2^30, which is cut; a chunk
  * longer than max_q_len, whose tokens beyond it are not computed; a bounded
  * wait that ran out) set the handle's sticky status word.
  */

@@ -8,12 +8,15 @@
  *               subtraction, division and exp in fp32.  Whole numbers: their
  *               sums do not depend on the order of addition, so the same
  *               inputs give the same token on any grid.
- *   temperature <= 0: greedy, the largest logit (probability 1).
+ *               What is infinitely far below l0 weighs nothing, at any
+ *               temperature.
+ *   temperature not above 0: greedy, the largest logit (probability 1).
  *   top_k       > 0: only the top_k largest logits stay.
  *   top_p       < 1: of those, by falling logit, each stays whose preceding
  *               weights sum to less than top_p times their total (the first
  *               always does).
- *   min_p       > 0: of those, each stays with w_i >= min_p * 2^38.
+ *   min_p       > 0: of those, each stays with w_i >= min_p * 2^38 (above 1
+ *               counts as 1).
  *   The token is the lowest id whose running sum of the staying weights, by
  *   id, exceeds floor(u * total); its probability is w / total.
  * Equal logits go to the lower id first throughout.  A row without any logit

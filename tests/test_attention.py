@@ -318,6 +318,36 @@ def test_graph_replay_other_stream_and_changed_lengths():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hk", [(3, 3), (12, 6), (16, 16), (128, 1), (96, 2), (100, 1)])
+def test_more_head_layouts(Hq, Hk):
+    # heads that neighbouring CTAs share out, and groups of which one token fills a tile
+    run(Case([2, 5, 1], [300, 70, 513], Hq, Hk, 64, 16, "fp16", seed=Hq))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch,q_len", [(33, 1), (100, 3), (300, 1), (40, 30)])
+def test_many_sequences(batch, q_len):
+    g = torch.Generator().manual_seed(batch)
+    lens = torch.randint(0, 400, (batch,), generator=g).tolist()
+    q = torch.randint(0, q_len + 1, (batch,), generator=g).tolist()
+    run(Case(q, [max(n, m) if i % 7 else n for i, (n, m) in enumerate(zip(lens, q))], 8, 2, 64, 32, seed=batch))
+
+
+@pytest.mark.gpu
+def test_one_handle_over_calls_of_every_kind():
+    """What a call leaves in the handle's workspace is not another's."""
+    from weight_streaming_expert_gb300 import PagedAttention
+    attn = PagedAttention(8, 2, 128, device=DEV)
+    cases = [Case([6, 6], [4000, 900], 8, 2, 128, 64, seed=1), Case([0, 6], [4000, 20], 8, 2, 128, 64, seed=2),
+             Case([300], [2000], 8, 2, 128, 16, "fp16", seed=3), Case([1] * 90, [700] * 90, 8, 2, 128, 32, seed=4),
+             Case([64, 0, 2], [64, 500, 5000], 8, 2, 128, 16, seed=5), Case([6, 6], [4000, 0], 8, 2, 128, 64, seed=6)]
+    for c in cases + cases[::-1]:
+        out, lse = attn(return_lse=True, **c.inputs())
+        assert attn.status() == 0
+        c.check(out, lse, c.q.dtype)
+
+
+@pytest.mark.gpu
 def test_same_bits_every_time():
     c = Case([1] * 7, [3000, 2, 800, 1500, 77, 4000, 129], 32, 4, 128, 16, seed=16)
     first = run(c)

@@ -39,6 +39,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <new>
 #include <type_traits>
 
 #include "attention.h"
@@ -133,7 +134,7 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
   const moe_attn_args_t& a = p.a;
   Seq s;
   const int q0 = a.q_starts[b], q1 = a.q_starts[b + 1], kv = a.kv_lens[b];
-  const long long room = (long long)a.table_stride * a.page_size;
+  const long long room = min(1ll << 30, (long long)a.table_stride * a.page_size);
   s.q0 = max(0, min(q0, a.n_tokens));
   s.n = max(0, min(min(q1, a.n_tokens) - s.q0, a.max_q_len));
   s.kv = (int)max(0ll, min((long long)kv, room));
@@ -1130,7 +1131,11 @@ moe_attn_t* moe_attn_create(int n_heads, int n_kv_heads, int head_dim) {
     return nullptr;
   }
   if (check_device() != MOE_OK) return nullptr;
-  auto* h = new moe_attn;
+  auto* h = new (std::nothrow) moe_attn;
+  if (!h) {
+    fail(MOE_ERR_OOM, "attention handle: out of memory");
+    return nullptr;
+  }
   h->n_heads = n_heads;
   h->n_kv_heads = n_kv_heads;
   h->head_dim = head_dim;
