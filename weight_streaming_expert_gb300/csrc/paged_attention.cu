@@ -16,15 +16,19 @@
 // positions one warp issues S = Q K^T into TMEM (128 x 64 fp32), four warps
 // turn S into probabilities, one row a thread with no exchange between
 // threads, and write them over S as the 16-bit A operand of O += P V, which
-// stays in TMEM.  A chain has two buffers of 64 positions, so that the next
-// scores are ready when a step's softmax ends (S as 128 x 64 takes 400 clocks
-// where 128 x 128 takes 264 for the same positions, but waiting for it took
-// more: 3060 clocks for 256 rows by 128 positions).  Two such chains run side
-// by side:
+// stays in TMEM.  Two such chains run side by side, so that one's products
+// cover the other's exponentials:
 //   pair   two tiles of rows over the same positions (chunks of many rows);
 //   split  one tile, the even 128 positions in one chain and the odd ones in
 //          the other, merged at the end (chunks of up to 128 rows, which are
 //          bound by reading the cache).
+// A chain has two buffers of 64 positions.  In the pair form the next scores go
+// into the one while the softmax works on the other: S as 128 x 64 takes 413
+// clocks where 128 x 128 takes 268 for the same positions (the MMA then waits
+// for its operands in shared memory), but a chain that waited for its scores
+// took 3060 clocks for 128 positions and now takes 2800 (8192 tokens over
+// 16384, 32/4 heads of 128: 1375 us before, 1205 us).  The split form waits
+// for memory anyway and takes both buffers' scores at once.
 // One warp copies the pages with TMA into a ring of 128-position tiles, another
 // the queries of the next tile.
 //
@@ -722,7 +726,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     Item it{};
     // ---- products, issued by one lane
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-    constexpr uint32_t kDescS = mma_desc(kBf16, false, kTile, kHalf), kDescO = mma_desc(kBf16, true, kTile, D);
+    constexpr uint32_t kDescS = mma_desc(kBf16, false, kTile, kPair ? kHalf : kTile), kDescO = mma_desc(kBf16, true, kTile, D);
     int taken = 0, q_round = 0;
     uint32_t p_parity = 0;  // bit 2 chain + half: of the next probabilities
     auto next_stage = [&]() {
@@ -731,7 +735,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       ++taken;
       return stage;
     };
-    // S of 64 of a stage's positions, into the chain's buffer of that half
+    // S of 64 of a stage's positions, into the chain's buffer of that half; in
+    // the split form (half = 0) of all 128, into both
     auto scores = [&](int chain, int half, int q_tile, int stage) {
       if (elected()) {
         const uint64_t qd = smem_desc(q_at + q_tile * kTileBytes, 16, 1024);
@@ -742,6 +747,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           mma_ss(tmem + chain * kTile + half * kHalf, qd + off, kd + off, kDescS, k > 0);
         }
         mma_commit(s_full(chain, half));
+        if (!kPair) mma_commit(s_full(chain, 1));
       }
     };
     auto products = [&](int chain, int half, int stage, bool add) {
@@ -815,26 +821,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           ks[0] = next_stage();
           tc_fence_after();
           scores(i, 0, 0, ks[0]);
-          scores(i, 1, 0, ks[0]);
           release(ks[0]);
         }
         if (n <= 2) release_queries();
         for (int i0 = 0; i0 < n; i0 += 2) {
 #pragma unroll
           for (int step = 0; step < 4; ++step) {
-            const int chain = step & 1, half = step >> 1, i = i0 + chain;
+            const int chain = step >> 1, half = step & 1, i = i0 + chain;
             if (i >= n) continue;
             if (half == 0) vs[chain] = value_stage(it.u0 + i);
             products(chain, half, vs[chain], i0 > 0 || half > 0);
+            if (half == 0) continue;
+            release(vs[chain]);
             if (i + 2 < n) {
-              if (half == 0) ks[chain] = next_stage();
-              scores(chain, half, 0, ks[chain]);
+              ks[0] = next_stage();
+              scores(chain, 0, 0, ks[0]);
+              release(ks[0]);
             }
-            if (half == 1) {
-              release(vs[chain]);
-              if (i + 2 < n) release(ks[chain]);
-              if (i + 3 == n) release_queries();
-            }
+            if (i + 3 == n) release_queries();
           }
         }
       }
