@@ -40,14 +40,16 @@ __device__ __forceinline__ float to_f32<__half>(__half v) {
   return __half2float(v);
 }
 template <typename T>
-__device__ __forceinline__ T from_f32(float v);
+__device__ __forceinline__ uint32_t pack2(float x, float y);
 template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
-  return __float2bfloat16_rn(v);
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float x, float y) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 template <>
-__device__ __forceinline__ __half from_f32<__half>(float v) {
-  return __float2half_rn(v);
+__device__ __forceinline__ uint32_t pack2<__half>(float x, float y) {
+  const __half2 v = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 template <typename T, int D, bool kInterleaved>
@@ -154,12 +156,8 @@ __global__ void __launch_bounds__(kRopeThreads, D == 256 ? 3 : 4) qk_norm_rope_k
           x_b = y_b;
         }
       }
-      uint2 o0, o1;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        reinterpret_cast<T*>(&o0)[j] = from_f32<T>(x[j]);
-        reinterpret_cast<T*>(&o1)[j] = from_f32<T>(x[4 + j]);
-      }
+      const uint2 o0 = make_uint2(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]));
+      const uint2 o1 = make_uint2(pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
       T* o = h < a.n_heads ? q_out + h * a.q_out_head_stride : k_out + (h - a.n_heads) * D;
       if (h < a.n_heads || keep) {
         *reinterpret_cast<uint2*>(o + lo) = o0;
@@ -176,8 +174,13 @@ int launch_rope(const moe_qk_norm_rope_args_t& a, moe_stream_t stream) {
   if (a.head_dim == 64) kernel = il ? qk_norm_rope_kernel<T, 64, true> : qk_norm_rope_kernel<T, 64, false>;
   else if (a.head_dim == 128) kernel = il ? qk_norm_rope_kernel<T, 128, true> : qk_norm_rope_kernel<T, 128, false>;
   else kernel = il ? qk_norm_rope_kernel<T, 256, true> : qk_norm_rope_kernel<T, 256, false>;
-  // few tokens: all warps of a CTA on one token, for the latency; many: a warp each
-  const int warps = a.n_tokens <= 512 ? kRopeWarps : 1, tokens = kRopeWarps / warps;
+  // Several warps share a token as long as all CTAs are resident at once (4 per
+  // SM): 1001 tokens of 16 + 4 heads of 64 take 4.0 us with 2 or 4 warps each,
+  // 4.9 with one.  Beyond that a warp each, which works the angles out once:
+  // 16384 tokens of 32 + 8 heads of 128 take 74 us, with 2 warps 78, 4 90.
+  int warps = kRopeWarps;
+  while (warps > 1 && (long long)a.n_tokens * warps > 152ll * 4 * kRopeWarps) warps /= 2;
+  const int tokens = kRopeWarps / warps;
   return launch_pdl(kernel, dim3((unsigned)((a.n_tokens + tokens - 1) / tokens)), dim3(kRopeThreads), 0, stream, 1, a,
                     warps);
 }
