@@ -53,14 +53,14 @@ __device__ __forceinline__ uint32_t pack2<__half>(float x, float y) {
 }
 
 template <typename T, int D, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads, D == 256 ? 3 : 4) qk_norm_rope_kernel(const __grid_constant__ moe_qk_norm_rope_args_t a,
-                                                                     int warps_per_token) {
+__global__ void __launch_bounds__(kRopeThreads, D == 256 ? 3 : 4) qk_norm_rope_kernel(
+    const __grid_constant__ moe_qk_norm_rope_args_t a, int warps_per_token) {
   constexpr int kLanes = D / 8;               // lanes of a head
-  constexpr int kHeads = 32 / kLanes;         // heads of a warp at a time
+  constexpr int kHeads = 32 / kLanes;         // heads of a group: what a warp does at a time
   __shared__ float2 turn[kRopeWarps][D / 2];  // (cos, sin) of the warp's token
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = lane % kLanes;
+  const int lane = threadIdx.x & 31, part = lane % kLanes, sub = lane / kLanes;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // tells the compiler that it is uniform
   const long long t = (long long)blockIdx.x * (kRopeWarps / warps_per_token) + warp / warps_per_token;
-  const int n_qk = a.n_heads + a.n_kv_heads, n_all = n_qk + a.n_kv_heads;
   const int pairs = a.rotary_dim / 2;
   pdl_wait();
   pdl_launch_dependents();
@@ -77,30 +77,37 @@ __global__ void __launch_bounds__(kRopeThreads, D == 256 ? 3 : 4) qk_norm_rope_k
   const long long slot = a.n_kv_heads > 0 ? a.slots[t] : -1;
   const bool keep = slot >= 0 && slot < (long long)a.n_pages * a.page_size;
   const long long page = keep ? slot / a.page_size : 0, row = keep ? slot % a.page_size : 0;
-  const T* q = static_cast<const T*>(a.q) + t * a.q_token_stride;
-  const T* k = static_cast<const T*>(a.k) + t * a.k_token_stride;
-  const T* v = static_cast<const T*>(a.v) + t * a.v_token_stride;
-  T* q_out = static_cast<T*>(a.q_out) + t * a.q_out_token_stride;
-  T* k_out = static_cast<T*>(a.k_cache) + page * a.k_page_stride + row * a.k_row_stride;
-  T* v_out = static_cast<T*>(a.v_cache) + page * a.v_page_stride + row * a.v_row_stride;
-  const T* qw = static_cast<const T*>(a.q_weight);
-  const T* kw = static_cast<const T*>(a.k_weight);
+  // of each kind (queries, keys, values) where this lane's values of head
+  // `sub` begin, in and out
+  const T* from[3] = {static_cast<const T*>(a.q) + t * a.q_token_stride + sub * a.q_head_stride + lo,
+                      static_cast<const T*>(a.k) + t * a.k_token_stride + sub * a.k_head_stride + lo,
+                      static_cast<const T*>(a.v) + t * a.v_token_stride + sub * a.v_head_stride + lo};
+  T* to[3] = {static_cast<T*>(a.q_out) + t * a.q_out_token_stride + sub * a.q_out_head_stride + lo,
+              static_cast<T*>(a.k_cache) + page * a.k_page_stride + row * a.k_row_stride + sub * D + lo,
+              static_cast<T*>(a.v_cache) + page * a.v_page_stride + row * a.v_row_stride + sub * D + lo};
+  const int apart = hi - lo;
 
-  const int step = warps_per_token * kHeads;
-  const int h0 = (warp % warps_per_token) * kHeads + lane / kLanes;
+  // groups of heads of one kind, so that what differs by kind is decided once
+  // for the warp: of queries, then of keys, then of values
+  const int q_groups = (a.n_heads + kHeads - 1) / kHeads, kv_groups = (a.n_kv_heads + kHeads - 1) / kHeads;
+  const int groups = q_groups + 2 * kv_groups;
+  auto kind_of = [&](int g) { return g < q_groups ? 0 : g < q_groups + kv_groups ? 1 : 2; };
+  auto head_of = [&](int g, int kind) {
+    return (kind == 0 ? g : kind == 1 ? g - q_groups : g - q_groups - kv_groups) * kHeads;
+  };
   float2 cs[4];
   bool first = true;
-  for (int base = h0 - lane / kLanes; base < n_all; base += kRopeLoads * step) {
+  for (int g0 = warp % warps_per_token; g0 < groups; g0 += kRopeLoads * warps_per_token) {
     uint2 x0[kRopeLoads], x1[kRopeLoads];
 #pragma unroll
     for (int i = 0; i < kRopeLoads; ++i) {
-      const int h = base + i * step + lane / kLanes;
-      if (h >= n_all) continue;
-      const T* p = h < a.n_heads ? q + h * a.q_head_stride
-                   : h < n_qk    ? k + (h - a.n_heads) * a.k_head_stride
-                                 : v + (h - n_qk) * a.v_head_stride;
-      x0[i] = *reinterpret_cast<const uint2*>(p + lo);
-      x1[i] = *reinterpret_cast<const uint2*>(p + hi);
+      const int g = g0 + i * warps_per_token, kind = kind_of(g), head = head_of(g, kind);
+      if (g >= groups || head + sub >= (kind == 0 ? a.n_heads : a.n_kv_heads)) continue;
+      const T* p = kind == 0   ? from[0] + head * a.q_head_stride
+                   : kind == 1 ? from[1] + head * a.k_head_stride
+                               : from[2] + head * a.v_head_stride;
+      x0[i] = *reinterpret_cast<const uint2*>(p);
+      x1[i] = *reinterpret_cast<const uint2*>(p + apart);
     }
     if (first) {
       first = false;
@@ -116,52 +123,48 @@ __global__ void __launch_bounds__(kRopeThreads, D == 256 ? 3 : 4) qk_norm_rope_k
     }
 #pragma unroll
     for (int i = 0; i < kRopeLoads; ++i) {
-      if (base + i * step >= n_all) break;  // the whole warp
-      const int h = base + i * step + lane / kLanes;
-      const T* e0 = reinterpret_cast<const T*>(&x0[i]);
-      const T* e1 = reinterpret_cast<const T*>(&x1[i]);
-      float x[8];
+      const int g = g0 + i * warps_per_token, kind = kind_of(g), head = head_of(g, kind);
+      if (g >= groups) break;
+      const bool valid = head + sub < (kind == 0 ? a.n_heads : a.n_kv_heads) && (kind == 0 || keep);
+      uint2 o0 = x0[i], o1 = x1[i];
+      if (kind < 2) {
+        const T* e0 = reinterpret_cast<const T*>(&x0[i]);
+        const T* e1 = reinterpret_cast<const T*>(&x1[i]);
+        float x[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = to_f32<T>(e0[j]), x[4 + j] = to_f32<T>(e1[j]);
-      float sq = 0.f;
+        for (int j = 0; j < 4; ++j) x[j] = to_f32<T>(e0[j]), x[4 + j] = to_f32<T>(e1[j]);
+        const T* w = static_cast<const T*>(kind == 0 ? a.q_weight : a.k_weight);
+        if (w) {
+          float sq = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sq = fmaf(x[j], x[j], sq);
+          for (int j = 0; j < 8; ++j) sq = fmaf(x[j], x[j], sq);
 #pragma unroll
-      for (int m = kLanes / 2; m > 0; m >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, m);
-      if (h >= n_all) continue;
-      if (h >= n_qk) {
-        if (keep) {
-          *reinterpret_cast<uint2*>(v_out + (h - n_qk) * D + lo) = x0[i];
-          *reinterpret_cast<uint2*>(v_out + (h - n_qk) * D + hi) = x1[i];
+          for (int m = kLanes / 2; m > 0; m >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, m);
+          const float r = rsqrtf(sq * (1.f / D) + a.eps);
+          const uint2 w0 = *reinterpret_cast<const uint2*>(w + lo), w1 = *reinterpret_cast<const uint2*>(w + hi);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            x[j] *= r * to_f32<T>(reinterpret_cast<const T*>(&w0)[j]);
+            x[4 + j] *= r * to_f32<T>(reinterpret_cast<const T*>(&w1)[j]);
+          }
         }
-        continue;
-      }
-      const T* w = h < a.n_heads ? qw : kw;
-      if (w) {
-        const float r = rsqrtf(sq * (1.f / D) + a.eps);
-        const uint2 w0 = *reinterpret_cast<const uint2*>(w + lo), w1 = *reinterpret_cast<const uint2*>(w + hi);
+        if (turns) {  // others stay as they are: 0 * inf must not reach them
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[j] *= r * to_f32<T>(reinterpret_cast<const T*>(&w0)[j]);
-          x[4 + j] *= r * to_f32<T>(reinterpret_cast<const T*>(&w1)[j]);
+          for (int j = 0; j < 4; ++j) {
+            float& x_a = x[kInterleaved ? 2 * j : j];
+            float& x_b = x[kInterleaved ? 2 * j + 1 : 4 + j];
+            const float y_a = fmaf(-x_b, cs[j].y, x_a * cs[j].x), y_b = fmaf(x_a, cs[j].y, x_b * cs[j].x);
+            x_a = y_a;
+            x_b = y_b;
+          }
         }
+        o0 = make_uint2(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]));
+        o1 = make_uint2(pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
       }
-      if (turns) {  // others stay as they are: 0 * inf must not reach them
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float& x_a = x[kInterleaved ? 2 * j : j];
-          float& x_b = x[kInterleaved ? 2 * j + 1 : 4 + j];
-          const float y_a = fmaf(-x_b, cs[j].y, x_a * cs[j].x), y_b = fmaf(x_a, cs[j].y, x_b * cs[j].x);
-          x_a = y_a;
-          x_b = y_b;
-        }
-      }
-      const uint2 o0 = make_uint2(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]));
-      const uint2 o1 = make_uint2(pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
-      T* o = h < a.n_heads ? q_out + h * a.q_out_head_stride : k_out + (h - a.n_heads) * D;
-      if (h < a.n_heads || keep) {
-        *reinterpret_cast<uint2*>(o + lo) = o0;
-        *reinterpret_cast<uint2*>(o + hi) = o1;
+      if (valid) {
+        T* o = kind == 0 ? to[0] + head * a.q_out_head_stride : kind == 1 ? to[1] + head * D : to[2] + head * D;
+        *reinterpret_cast<uint2*>(o) = o0;
+        *reinterpret_cast<uint2*>(o + apart) = o1;
       }
     }
   }
