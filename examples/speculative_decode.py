@@ -55,10 +55,12 @@ class Model:
         self.weights = []
         for _ in range(c.layers):
             self.weights.append(dict(
-                norm1=1 + rand(c.hidden, std=0.1), norm2=1 + rand(c.hidden, std=0.1), qkv=rand(c.hidden, width, std=0.08),
+                norm1=1 + rand(c.hidden, std=0.1), norm2=1 + rand(c.hidden, std=0.1),
+                qkv=rand(c.hidden, width, std=0.08),
                 out=rand(c.heads * c.head_dim, c.hidden, std=0.08), q_norm=1 + rand(c.head_dim, std=0.1),
                 k_norm=1 + rand(c.head_dim, std=0.1), router=rand(c.experts, c.hidden, std=0.1),
-                gate_up=rand(c.experts, 2 * c.inter, c.hidden, std=0.08), down=rand(c.experts, c.hidden, c.inter, std=0.08)))
+                gate_up=rand(c.experts, 2 * c.inter, c.hidden, std=0.08),
+                down=rand(c.experts, c.hidden, c.inter, std=0.08)))
         self.norm = 1 + rand(c.hidden, std=0.1)
         self.head_weight = rand(c.vocab, c.hidden, std=0.15)
         self.moe = [MoELayer(w["router"], w["gate_up"], w["down"], c.topk) for w in self.weights]

@@ -391,7 +391,8 @@ def args(**change):
 REFUSED = [("dtype", 2, 1, "dtype"), ("batch", -1, 1, "batch"), ("n_tokens", -1, 1, "n_tokens"),
            ("scale", 0.0, 1, "scale"), ("scale", -1.0, 1, "scale"), ("scale", math.inf, 1, "scale"),
            ("scale", math.nan, 1, "scale"), ("page_size", 0, 2, "page_size"), ("page_size", 48, 2, "page_size"),
-           ("page_size", 8, 2, "page_size"), ("n_pages", 0, 1, "n_pages"), ("q", None, 1, "null"), ("q", 8, 1, "aligned"),
+           ("page_size", 8, 2, "page_size"), ("n_pages", 0, 1, "n_pages"), ("q", None, 1, "null"),
+           ("q", 8, 1, "aligned"),
            ("k_cache", 24, 1, "aligned"), ("v_cache", None, 1, "null"), ("out", 20, 1, "aligned"),
            ("block_table", None, 1, "block_table"), ("q_starts", 2, 1, "q_starts"), ("kv_lens", None, 1, "kv_lens"),
            ("q_token_stride", 4, 1, "stride"), ("k_row_stride", 65, 1, "stride"), ("v_page_stride", 1, 1, "stride"),
@@ -433,7 +434,8 @@ def test_python_refusals():
     x = c.inputs()
     bad = dict(q=[x["q"].float(), x["q"][:, :3], x["q"].transpose(1, 2), x["q"].cpu()],
                k_cache=[x["k_cache"].half(), x["k_cache"][:, :, :1], x["k_cache"][..., :32]],
-               block_table=[x["block_table"].long(), x["block_table"][0]], q_starts=[x["q_starts"].long(), x["kv_lens"]],
+               block_table=[x["block_table"].long(), x["block_table"][0]],
+               q_starts=[x["q_starts"].long(), x["kv_lens"]],
                kv_lens=[x["q_starts"]], tree_mask=[torch.zeros(3, dtype=torch.int64, device=DEV)],
                out=[torch.empty(2, 4, 64, device=DEV), torch.empty(1, 4, 64, dtype=torch.bfloat16, device=DEV)])
     for name, values in bad.items():

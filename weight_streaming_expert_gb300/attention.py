@@ -50,7 +50,8 @@ def _elsewhere(index, stream):
 def _heads(name, t, dtype, index, dim):
     """t: [tokens, heads, dim], each head's values contiguous."""
     if t.dim() != 3 or t.dtype != dtype or t.get_device() != index or t.shape[2] != dim or t.stride(2) != 1:
-        raise ValueError(f"{name} must be a {dtype} tensor [tokens, heads, {dim}] with contiguous heads on cuda:{index}")
+        raise ValueError(f"{name} must be a {dtype} tensor [tokens, heads, {dim}] with contiguous heads on "
+                         f"cuda:{index}")
 
 
 def _cache(name, t, dtype, index, heads, dim):

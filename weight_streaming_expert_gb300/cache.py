@@ -235,7 +235,8 @@ class PagedKVCache:
         moves = [(start + i, start + at) for at, i in enumerate(accepted) if i != at]
         if moves:
             self._copy(self.table.unshare(seq, moves[0][1], moves[-1][1] + 1), stream)
-        for at in range(0, len(moves), N.MOE_COPY_ROWS_MAX):  # ascending blocks: a block's rows are read before later ones land
+        # blocks in ascending order: what a block writes lies before all that later ones read
+        for at in range(0, len(moves), N.MOE_COPY_ROWS_MAX):
             part = moves[at:at + N.MOE_COPY_ROWS_MAX]
             slots = [self.table.slots(seq, at) for at in zip(*part)]
             src, dst = self._device(slots, torch.int64, stream)

@@ -12,12 +12,12 @@
 //
 // A tile is up to 128 query rows: as many whole tokens of the chunk as fit,
 // each with the heads that share a key/value head, so that a page is read once
-// for all of them.  Per 64
-// positions one warp issues S = Q K^T into TMEM (128 x 64 fp32), four warps
-// turn S into probabilities, one row a thread with no exchange between
-// threads, and write them over S as the 16-bit A operand of O += P V, which
-// stays in TMEM.  Two such chains run side by side, so that one's products
-// cover the other's exponentials:
+// for all of them.  Per 64 positions one warp issues S = Q K^T into TMEM (128 x
+// 64 fp32), four warps turn S into probabilities, one row a thread with no
+// exchange between threads, and write them over S as the 16-bit A operand of
+// O += P V, which stays in TMEM (each probability is rounded once to the
+// element type; scores, statistics and sums are fp32).  Two such chains run
+// side by side, so that one's products cover the other's exponentials:
 //   pair   two tiles of rows over the same positions (chunks of many rows);
 //   split  one tile, the even 128 positions in one chain and the odd ones in
 //          the other, merged at the end (chunks of up to 128 rows, which are
@@ -39,6 +39,16 @@
 // graph adapts to lengths that change.  A tile that a boundary cuts leaves
 // unnormalised sums with their m; a second, small kernel joins them in a fixed
 // order.
+//
+// What bounds it, and what it reaches on one GB300 (copy 6687 GB/s, bf16 GEMM
+// 1897 TFLOP/s in a burst and 1727 sustained):
+//   long chunks      the tensor pipe: 2650 of the 2800 clocks per 256 rows by
+//                    128 positions are MMAs.  8192 tokens over 16384: 1.17 ms,
+//                    1410 TFLOP/s.
+//   long decoding    reading the cache: 32 sequences of 2,000 to 32,768
+//                    positions, one token each: 131 us, 6.3 TB/s.
+//   short calls      latencies: the plan, the first pages, one softmax, the
+//                    join: 6 tokens over 8192: 14 us, of which memory needs 2.5.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -554,7 +564,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int row = i * 4 + lane / 8;
-            char* dst = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), row));
+            const auto at = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), row);
+            char* dst = reinterpret_cast<char*>(at);
             const uint4 v = *reinterpret_cast<const uint4*>(mine + row * 128 + ((lane & 7) ^ (row & 7)) * 16);
             if (dst) *reinterpret_cast<uint4*>(dst + (lane & 7) * 16) = v;
           }
@@ -626,76 +637,77 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
   } else {
     if (warp == kCopyWarp) {
-    Walk<kTiles> walk(p, plan);
-    Item it{};
-    // ---- copies: per 128 positions one box per page and 64 columns, a lane each
-    constexpr int kHalves = D / 64;
-    const int box_rows = min(a.page_size, kTile), per_tile = kTile / box_rows;
-    const int pages_log2 = 31 - __clz(a.page_size);
-    const int box = lane / kHalves, half = lane % kHalves;
-    int filled = 0;
-    // The table's entries come 32 at a time, an entry per lane, and a window
-    // ahead of their use: `even` and `odd` hold the windows of those numbers.
-    int even = 0, odd = 0, have = 0;
-    auto fetch = [&](int window) {
-      const int i = window * 32 + lane;
-      const int page = (long long)i * a.page_size < it.s.kv ? a.block_table[(long long)it.b * a.table_stride + i] : -1;
-      if (window & 1)
-        odd = page;
-      else
-        even = page;
-      have = window;
-    };
-    auto start_item = [&]() {
-      fetch((it.u0 * kTile >> pages_log2) / 32);
-      fetch(have + 1);
-    };
-    auto load = [&](const CUtensorMap* map, int u) {
-      const int stage = filled % kStages, round = filled / kStages;
-      const int pos = u * kTile + box * box_rows, i = pos >> pages_log2, window = (u * kTile >> pages_log2) / 32;
-      int page = __shfl_sync(0xffffffffu, window & 1 ? odd : even, i & 31);
-      const bool mine = box < per_tile && pos < it.s.kv;
-      if (mine && (unsigned)page >= (unsigned)a.n_pages) {
-        atomicOr(p.status, kAttnBadPage);
-        page = a.n_pages;  // outside the tensor: reads as zeros
-      }
-      if (round > 0) wait(empty(stage), (round - 1) & 1);
-      const unsigned boxes = __popc(__ballot_sync(0xffffffffu, mine));
-      if (lane == 0) mbar_arrive_expect_tx(full(stage), boxes * box_rows * 128u);
-      __syncwarp();
-      if (mine)
-        tma_load_3d(ring + stage * kTileBytes + half * kPanel + box * box_rows * 128, map, it.h * D + half * 64,
-                    pos & (a.page_size - 1), page, full(stage));
-      ++filled;
-      return window;
-    };
-    // values come last of a position's copies: what is before their window is done with
-    auto load_values = [&](int u) {
-      const int window = load(&v_map, u);
-      if (window == have) fetch(window + 1);
-    };
-    while (walk.next(it)) {
-      const int n = it.u1 - it.u0;
-      start_item();
-      if (kPair) {
-        for (int j = 0; j < n; ++j) {
-          load(&k_map, it.u0 + j);
-          load_values(it.u0 + j);
+      Walk<kTiles> walk(p, plan);
+      Item it{};
+      // ---- copies: per 128 positions one box per page and 64 columns, a lane each
+      constexpr int kHalves = D / 64;
+      const int box_rows = min(a.page_size, kTile), per_tile = kTile / box_rows;
+      const int pages_log2 = 31 - __clz(a.page_size);
+      const int box = lane / kHalves, half = lane % kHalves;
+      int filled = 0;
+      // The table's entries come 32 at a time, an entry per lane, and a window
+      // ahead of their use: `even` and `odd` hold the windows of those numbers.
+      int even = 0, odd = 0, have = 0;
+      auto fetch = [&](int window) {
+        const int i = window * 32 + lane;
+        const bool used = (long long)i * a.page_size < it.s.kv;
+        const int page = used ? a.block_table[(long long)it.b * a.table_stride + i] : -1;
+        if (window & 1)
+          odd = page;
+        else
+          even = page;
+        have = window;
+      };
+      auto start_item = [&]() {
+        fetch((it.u0 * kTile >> pages_log2) / 32);
+        fetch(have + 1);
+      };
+      auto load = [&](const CUtensorMap* map, int u) {
+        const int stage = filled % kStages, round = filled / kStages;
+        const int pos = u * kTile + box * box_rows, i = pos >> pages_log2, window = (u * kTile >> pages_log2) / 32;
+        int page = __shfl_sync(0xffffffffu, window & 1 ? odd : even, i & 31);
+        const bool mine = box < per_tile && pos < it.s.kv;
+        if (mine && (unsigned)page >= (unsigned)a.n_pages) {
+          atomicOr(p.status, kAttnBadPage);
+          page = a.n_pages;  // outside the tensor: reads as zeros
         }
-      } else {
-        load(&k_map, it.u0);
-        if (n > 1) load(&k_map, it.u0 + 1);
-        for (int j = 0; j < n; ++j) {
-          load_values(it.u0 + j);
-          if (j + 2 < n) load(&k_map, it.u0 + j + 2);
+        if (round > 0) wait(empty(stage), (round - 1) & 1);
+        const unsigned boxes = __popc(__ballot_sync(0xffffffffu, mine));
+        if (lane == 0) mbar_arrive_expect_tx(full(stage), boxes * box_rows * 128u);
+        __syncwarp();
+        if (mine)
+          tma_load_3d(ring + stage * kTileBytes + half * kPanel + box * box_rows * 128, map, it.h * D + half * 64,
+                      pos & (a.page_size - 1), page, full(stage));
+        ++filled;
+        return window;
+      };
+      // values come last of a position's copies: what is before their window is done with
+      auto load_values = [&](int u) {
+        const int window = load(&v_map, u);
+        if (window == have) fetch(window + 1);
+      };
+      while (walk.next(it)) {
+        const int n = it.u1 - it.u0;
+        start_item();
+        if (kPair) {
+          for (int j = 0; j < n; ++j) {
+            load(&k_map, it.u0 + j);
+            load_values(it.u0 + j);
+          }
+        } else {
+          load(&k_map, it.u0);
+          if (n > 1) load(&k_map, it.u0 + 1);
+          for (int j = 0; j < n; ++j) {
+            load_values(it.u0 + j);
+            if (j + 2 < n) load(&k_map, it.u0 + j + 2);
+          }
         }
       }
-    }
-    // no copy is in flight when the CTA ends, also after a wait has given up
-    for (int f = max(0, filled - kStages); f < filled; ++f) {
-      unsigned long long waited;
-      mbar_wait(full(f % kStages), (f / kStages) & 1, &waited);
-    }
+      // no copy is in flight when the CTA ends, also after a wait has given up
+      for (int f = max(0, filled - kStages); f < filled; ++f) {
+        unsigned long long waited;
+        mbar_wait(full(f % kStages), (f / kStages) & 1, &waited);
+      }
     } else if (warp >= kQueryWarp) {
       // ---- queries, of a tile as one box of its tokens, the heads of a group
       // and 64 columns.  Past the sequence's last token it reads what follows,
@@ -722,132 +734,133 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (round > 0)
         for (int t = 0; t < kTiles; ++t) mbar_wait(q_full(t), (round - 1) & 1, &waited);
     } else if (warp == kMmaWarp) {
-    Walk<kTiles> walk(p, plan);
-    Item it{};
-    // ---- products, issued by one lane
-    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-    constexpr uint32_t kDescS = mma_desc(kBf16, false, kTile, kPair ? kHalf : kTile), kDescO = mma_desc(kBf16, true, kTile, D);
-    int taken = 0, q_round = 0;
-    uint32_t p_parity = 0;  // bit 2 chain + half: of the next probabilities
-    auto next_stage = [&]() {
-      const int stage = taken % kStages;
-      wait(full(stage), (taken / kStages) & 1);
-      ++taken;
-      return stage;
-    };
-    // S of 64 of a stage's positions, into the chain's buffer of that half; in
-    // the split form (half = 0) of all 128, into both
-    auto scores = [&](int chain, int half, int q_tile, int stage) {
-      if (elected()) {
-        const uint64_t qd = smem_desc(q_at + q_tile * kTileBytes, 16, 1024);
-        const uint64_t kd = smem_desc(ring + stage * kTileBytes + half * kHalf * 128, 16, 1024);
+      Walk<kTiles> walk(p, plan);
+      Item it{};
+      // ---- products, issued by one lane
+      constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+      constexpr uint32_t kDescS = mma_desc(kBf16, false, kTile, kPair ? kHalf : kTile);
+      constexpr uint32_t kDescO = mma_desc(kBf16, true, kTile, D);
+      int taken = 0, q_round = 0;
+      uint32_t p_parity = 0;  // bit 2 chain + half: of the next probabilities
+      auto next_stage = [&]() {
+        const int stage = taken % kStages;
+        wait(full(stage), (taken / kStages) & 1);
+        ++taken;
+        return stage;
+      };
+      // S of 64 of a stage's positions, into the chain's buffer of that half; in
+      // the split form (half = 0) of all 128, into both
+      auto scores = [&](int chain, int half, int q_tile, int stage) {
+        if (elected()) {
+          const uint64_t qd = smem_desc(q_at + q_tile * kTileBytes, 16, 1024);
+          const uint64_t kd = smem_desc(ring + stage * kTileBytes + half * kHalf * 128, 16, 1024);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = ((k / 4) * kPanel + (k % 4) * 32) / 16;
-          mma_ss(tmem + chain * kTile + half * kHalf, qd + off, kd + off, kDescS, k > 0);
-        }
-        mma_commit(s_full(chain, half));
-        if (!kPair) mma_commit(s_full(chain, 1));
-      }
-    };
-    auto products = [&](int chain, int half, int stage, bool add) {
-      wait(p_full(chain, half), (p_parity >> (2 * chain + half)) & 1);
-      p_parity ^= 1u << (2 * chain + half);
-      tc_fence_after();
-      if (elected()) {
-        const uint64_t vd = smem_desc(ring + stage * kTileBytes + half * kHalf * 128, kPanel, 1024);
-#pragma unroll
-        for (int k = 0; k < kHalf / 16; ++k)
-          mma_ts(tmem + 2 * kTile + chain * D, tmem + chain * kTile + half * kHalf + k * 8, vd + k * 128, kDescO,
-                 add || k > 0);
-        mma_commit(o_done(chain, half));
-      }
-    };
-    auto release = [&](int stage) {
-      if (elected()) mma_commit(empty(stage));
-    };
-    // the item's scores are all issued: its queries make room for the next
-    auto release_queries = [&]() {
-      if (elected()) {
-        mma_commit(q_empty(0));
-        if (kPair) mma_commit(q_empty(1));
-      }
-    };
-    // Rows of the cache past the sequence's end hold anything, and 0 * NaN is
-    // NaN: they become zeros.
-    auto value_stage = [&](int u) {
-      const int stage = next_stage(), valid = max(0, it.s.kv - u * kTile);
-      if (valid < kTile) {
-        uint8_t* v = ring_smem + stage * kTileBytes;
-        for (int i = lane; i < (kTile - valid) * (D / 8); i += 32) {
-          const int row = valid + i / (D / 8), c = i % (D / 8);
-          *reinterpret_cast<uint4*>(v + (c / 8) * kPanel + row * 128 + (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      return stage;
-    };
-    while (uniform((int)walk.next(it))) {
-      const int n = uniform(it.u1 - it.u0);
-      wait(q_full(0), q_round & 1);
-      if (kPair) wait(q_full(1), q_round & 1);
-      int ks[2], vs[2];
-      // scores go two steps ahead of the products: a chain's softmax finds the
-      // next scores ready while the MMAs of its last step are still to come
-      if (kPair) {
-        ks[0] = next_stage();
-        tc_fence_after();
-        for (int step = 0; step < 4; ++step) scores(step & 1, step >> 1, step & 1, ks[0]);
-        release(ks[0]);
-        if (n == 1) release_queries();
-        for (int j = 0; j < n; ++j) {
-#pragma unroll
-          for (int step = 0; step < 4; ++step) {
-            const int chain = step & 1, half = step >> 1;
-            if (step == 0) vs[0] = value_stage(it.u0 + j);
-            products(chain, half, vs[0], j > 0 || half > 0);
-            if (j + 1 < n) {
-              if (step == 0) ks[0] = next_stage();
-              scores(chain, half, chain, ks[0]);
-            }
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k / 4) * kPanel + (k % 4) * 32) / 16;
+            mma_ss(tmem + chain * kTile + half * kHalf, qd + off, kd + off, kDescS, k > 0);
           }
-          release(vs[0]);
-          if (j + 1 < n) release(ks[0]);
-          if (j + 2 == n) release_queries();
+          mma_commit(s_full(chain, half));
+          if (!kPair) mma_commit(s_full(chain, 1));
         }
-      } else {
-        for (int i = 0; i < min(n, 2); ++i) {
+      };
+      auto products = [&](int chain, int half, int stage, bool add) {
+        wait(p_full(chain, half), (p_parity >> (2 * chain + half)) & 1);
+        p_parity ^= 1u << (2 * chain + half);
+        tc_fence_after();
+        if (elected()) {
+          const uint64_t vd = smem_desc(ring + stage * kTileBytes + half * kHalf * 128, kPanel, 1024);
+#pragma unroll
+          for (int k = 0; k < kHalf / 16; ++k)
+            mma_ts(tmem + 2 * kTile + chain * D, tmem + chain * kTile + half * kHalf + k * 8, vd + k * 128, kDescO,
+                   add || k > 0);
+          mma_commit(o_done(chain, half));
+        }
+      };
+      auto release = [&](int stage) {
+        if (elected()) mma_commit(empty(stage));
+      };
+      // the item's scores are all issued: its queries make room for the next
+      auto release_queries = [&]() {
+        if (elected()) {
+          mma_commit(q_empty(0));
+          if (kPair) mma_commit(q_empty(1));
+        }
+      };
+      // Rows of the cache past the sequence's end hold anything, and 0 * NaN is
+      // NaN: they become zeros.
+      auto value_stage = [&](int u) {
+        const int stage = next_stage(), valid = max(0, it.s.kv - u * kTile);
+        if (valid < kTile) {
+          uint8_t* v = ring_smem + stage * kTileBytes;
+          for (int i = lane; i < (kTile - valid) * (D / 8); i += 32) {
+            const int row = valid + i / (D / 8), c = i % (D / 8);
+            *reinterpret_cast<uint4*>(v + (c / 8) * kPanel + row * 128 + (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        return stage;
+      };
+      while (uniform((int)walk.next(it))) {
+        const int n = uniform(it.u1 - it.u0);
+        wait(q_full(0), q_round & 1);
+        if (kPair) wait(q_full(1), q_round & 1);
+        int ks[2], vs[2];
+        // scores go two steps ahead of the products: a chain's softmax finds the
+        // next scores ready while the MMAs of its last step are still to come
+        if (kPair) {
           ks[0] = next_stage();
           tc_fence_after();
-          scores(i, 0, 0, ks[0]);
+          for (int step = 0; step < 4; ++step) scores(step & 1, step >> 1, step & 1, ks[0]);
           release(ks[0]);
-        }
-        if (n <= 2) release_queries();
-        for (int i0 = 0; i0 < n; i0 += 2) {
+          if (n == 1) release_queries();
+          for (int j = 0; j < n; ++j) {
 #pragma unroll
-          for (int step = 0; step < 4; ++step) {
-            const int chain = step >> 1, half = step & 1, i = i0 + chain;
-            if (i >= n) continue;
-            if (half == 0) vs[chain] = value_stage(it.u0 + i);
-            products(chain, half, vs[chain], i0 > 0 || half > 0);
-            if (half == 0) continue;
-            release(vs[chain]);
-            if (i + 2 < n) {
-              ks[0] = next_stage();
-              scores(chain, 0, 0, ks[0]);
-              release(ks[0]);
+            for (int step = 0; step < 4; ++step) {
+              const int chain = step & 1, half = step >> 1;
+              if (step == 0) vs[0] = value_stage(it.u0 + j);
+              products(chain, half, vs[0], j > 0 || half > 0);
+              if (j + 1 < n) {
+                if (step == 0) ks[0] = next_stage();
+                scores(chain, half, chain, ks[0]);
+              }
             }
-            if (i + 3 == n) release_queries();
+            release(vs[0]);
+            if (j + 1 < n) release(ks[0]);
+            if (j + 2 == n) release_queries();
+          }
+        } else {
+          for (int i = 0; i < min(n, 2); ++i) {
+            ks[0] = next_stage();
+            tc_fence_after();
+            scores(i, 0, 0, ks[0]);
+            release(ks[0]);
+          }
+          if (n <= 2) release_queries();
+          for (int i0 = 0; i0 < n; i0 += 2) {
+#pragma unroll
+            for (int step = 0; step < 4; ++step) {
+              const int chain = step >> 1, half = step & 1, i = i0 + chain;
+              if (i >= n) continue;
+              if (half == 0) vs[chain] = value_stage(it.u0 + i);
+              products(chain, half, vs[chain], i0 > 0 || half > 0);
+              if (half == 0) continue;
+              release(vs[chain]);
+              if (i + 2 < n) {
+                ks[0] = next_stage();
+                scores(chain, 0, 0, ks[0]);
+                release(ks[0]);
+              }
+              if (i + 3 == n) release_queries();
+            }
           }
         }
+        ++q_round;
       }
-      ++q_round;
-    }
-    if (elected()) mma_commit(drained);
-    unsigned long long waited;
-    mbar_wait(drained, 0, &waited);
-    __syncwarp();
+      if (elected()) mma_commit(drained);
+      unsigned long long waited;
+      mbar_wait(drained, 0, &waited);
+      __syncwarp();
     }
   }
   tc_fence_before();
@@ -857,10 +870,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
 // Joins the tiles that shares have cut: out = sum_i O_i 2^(c (m_i - m)) / sum_i
 // l_i 2^(c (m_i - m)) in the order of the shares.  Block (i, y): of cut i, 4
-// rows at a time.  What it costs is
-// the latency of its reads, so all of a row's statistics are read at once, by
-// the lanes of a warp, and then its parts by four threads per column, whose
-// sums are added in order.
+// rows at a time.  What it costs is the latency of its reads, so all of a
+// row's statistics are read at once, by the lanes of a warp, and then its
+// parts by four threads per column, whose sums are added in order.
 template <typename T, int D, int kRows>
 __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4) join_kernel(const __grid_constant__ AttnParams p) {
   constexpr int kColumns = D / 4;
@@ -926,8 +938,7 @@ __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4) join_kernel(c
     return;
   }
   for (int r0 = blockIdx.y * kJoinRows; r0 < kRows; r0 += gridDim.y * kJoinRows) {
-    if (token_of(r0) >= s.n && r0 / kTile == (r0 + kJoinRows - 1) / kTile && token_of(r0 + kJoinRows - 1) >= s.n)
-      continue;  // for the whole block
+    if (token_of(r0) >= s.n) continue;  // nor does a later row of the four have a token
     if (warp < kJoinRows && token_of(r0 + warp) < s.n) {
       float m = -INFINITY, l = 0.f;
       for (int i = lane; i < cut.parts; i += 32) m = fmaxf(m, p.part_ml[slot(i) * kRows + r0 + warp].x);
@@ -1057,7 +1068,9 @@ int map_for(KnownMap& known, const Shape& s, const void* base, CUtensorMap* map,
   *map = known.map;
   const MapReplace replace = map_replace();
   const CUresult r = replace ? replace(map, const_cast<void*>(base)) : CUDA_ERROR_NOT_FOUND;
-  return r == CUDA_SUCCESS ? MOE_OK : fail(MOE_ERR_CUDA, "no tensor map at the address of %s (driver error %d)", what, (int)r);
+  return r == CUDA_SUCCESS
+             ? MOE_OK
+             : fail(MOE_ERR_CUDA, "no tensor map at the address of %s (driver error %d)", what, (int)r);
 }
 
 }  // namespace
@@ -1171,7 +1184,8 @@ int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t strea
     return fail(MOE_ERR_INVALID_ARG, "dtype = %d: must be MOE_DTYPE_BF16 or MOE_DTYPE_FP16", a->dtype);
   if (a->batch < 0 || a->n_tokens < 0 || a->max_q_len < 0 || a->table_stride < 0)
     return fail(MOE_ERR_INVALID_ARG, "batch, n_tokens, max_q_len and table_stride must be 0 or more");
-  if (!(a->scale > 0.f) || !(a->scale < INFINITY)) return fail(MOE_ERR_INVALID_ARG, "scale must be positive and finite");
+  if (!(a->scale > 0.f) || !(a->scale < INFINITY))
+    return fail(MOE_ERR_INVALID_ARG, "scale must be positive and finite");
   if (a->page_size != 16 && a->page_size != 32 && a->page_size != 64 && a->page_size != 128 && a->page_size != 256)
     return fail(MOE_ERR_UNSUPPORTED, "page_size = %d: must be 16, 32, 64, 128 or 256", a->page_size);
   if (a->tree_mask && a->max_q_len > 64)
@@ -1201,10 +1215,12 @@ int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t strea
                               a->q_token_stride},
                    a->q, &maps.q, "q");
   if (rc == MOE_OK)
-    rc = map_for(h->k_map, {a->dtype, columns, a->page_size, a->n_pages, box_rows, 1, a->k_row_stride, a->k_page_stride},
+    rc = map_for(h->k_map, {a->dtype, columns, a->page_size, a->n_pages, box_rows, 1, a->k_row_stride,
+                            a->k_page_stride},
                  a->k_cache, &maps.k, "k_cache");
   if (rc == MOE_OK)
-    rc = map_for(h->v_map, {a->dtype, columns, a->page_size, a->n_pages, box_rows, 1, a->v_row_stride, a->v_page_stride},
+    rc = map_for(h->v_map, {a->dtype, columns, a->page_size, a->n_pages, box_rows, 1, a->v_row_stride,
+                            a->v_page_stride},
                  a->v_cache, &maps.v, "v_cache");
   if (rc != MOE_OK) return rc;
   int spread = 1;

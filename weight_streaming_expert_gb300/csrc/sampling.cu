@@ -16,6 +16,10 @@
 // filter cuts among the 2048 largest logits, as it mostly does, one pass of
 // bins finds those, the CTAs hand them to the first one in the order of their
 // ids, and it goes on alone with the same code.
+//
+// 6 rows of 157184 logits: greedy 4.4 us, unfiltered 9.0 us, top-k 50 22 us,
+// top-k 50 and top-p 0.95 31 us, top-p 0.95 alone (a cut among 20,000 logits)
+// 40 us; the logits' bytes are 0.6 us of that.
 #include <cooperative_groups.h>
 
 #include <cstddef>
@@ -112,7 +116,8 @@ struct Team {
   }
   // Keys in shared memory: of the slice after the struct, or the list's.
   __device__ __forceinline__ uint32_t cached(int i) const {
-    return reinterpret_cast<const uint32_t*>(&s)[(alone ? (int)offsetof(Shared, list_key) : (int)sizeof(Shared)) / 4 + i];
+    const int first = alone ? (int)offsetof(Shared, list_key) : (int)sizeof(Shared);
+    return reinterpret_cast<const uint32_t*>(&s)[first / 4 + i];
   }
   __device__ __forceinline__ uint32_t key(int i) const { return kCached || alone ? cached(i) : key_of(row[i]); }
   // f(i, keys i .. i + 3) for this thread's keys, four at a time so that their
@@ -604,7 +609,8 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
   const u64 wanted = s.shared[0];
   const unsigned here = __ballot_sync(0xffffffffu, wanted >= before && wanted < before + sum);
   if (here) {  // the token is one of a thread's of this warp: its lanes look through them
-    const int src = __ffs(here) - 1, from = __shfl_sync(0xffffffffu, c.i0, src), to = __shfl_sync(0xffffffffu, c.i1, src);
+    const int src = __ffs(here) - 1;
+    const int from = __shfl_sync(0xffffffffu, c.i0, src), to = __shfl_sync(0xffffffffu, c.i1, src);
     before = __shfl_sync(0xffffffffu, before, src);
     for (int i = from + c.lane;; i += 32) {
       const uint32_t key[4] = {i < to ? c.key(i) : 0u, 0u, 0u, 0u};
@@ -654,6 +660,9 @@ extern "C" int moe_sample(const float* logits, int64_t row_stride, int rows, int
     return fail(MOE_ERR_INVALID_ARG, "row_stride = %lld is smaller than vocab", (long long)row_stride);
   int rc = check_device();
   if (rc != MOE_OK) return rc;
+  // CTAs of a row: as many as run at once (two per SM), for every exchange
+  // costs each of them the same (64 rows of 157184, top-k: 95 us with 16, 73 us
+  // with 4; 6 rows, every filter: 32 us with 8, 31 us with 16)
   int cluster = kMaxCluster;
   while (cluster > 1 && (rows * cluster > 256 || (vocab + cluster - 1) / cluster < kSampleThreads) &&
          (vocab + cluster / 2 - 1) / (cluster / 2) <= kMaxSlice)
@@ -675,5 +684,6 @@ extern "C" int moe_sample(const float* logits, int64_t row_stride, int rows, int
     if (e == cudaSuccess) ready = dev;
   }
   if (e != cudaSuccess) return fail_cuda(e, "sampling set-up");
-  return launch_pdl(cached ? sample_kernel<true> : sample_kernel<false>, dim3((unsigned)(rows * cluster)), dim3(kSampleThreads), smem, stream, cluster, a);
+  return launch_pdl(cached ? sample_kernel<true> : sample_kernel<false>, dim3((unsigned)(rows * cluster)),
+                    dim3(kSampleThreads), smem, stream, cluster, a);
 }

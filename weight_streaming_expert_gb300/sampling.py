@@ -39,9 +39,9 @@ def _sample(index, logits, u, temperature, top_k, top_p, min_p, tokens, return_p
         _plain("tokens", tokens, torch.int32, index, M)
     probs = torch.empty(M, dtype=torch.float32, device=dev) if return_probs else None
     status = N.lib().moe_sample(
-        logits.data_ptr(), logits.stride(0), M, V, u.data_ptr(), None if temperature is None else temperature.data_ptr(),
-        None if top_k is None else top_k.data_ptr(), None if top_p is None else top_p.data_ptr(),
-        None if min_p is None else min_p.data_ptr(), tokens.data_ptr(), None if probs is None else probs.data_ptr(),
+        logits.data_ptr(), logits.stride(0), M, V, u.data_ptr(),
+        None if temperature is None else temperature.data_ptr(), None if top_k is None else top_k.data_ptr(),
+        None if top_p is None else top_p.data_ptr(), None if min_p is None else min_p.data_ptr(), tokens.data_ptr(), None if probs is None else probs.data_ptr(),
         torch._C._cuda_getCurrentRawStream(index))
     if status:
         N.check("moe_sample", status)
