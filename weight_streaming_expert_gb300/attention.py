@@ -1,7 +1,8 @@
 """Python face of include/attention.h: norms and rotation of queries and keys
 into the paged cache (``QKNormRope``) and attention of new tokens over it
-(``PagedAttention``).  Argument marshalling only: the work runs in the
-library's kernels.  Nothing here is differentiable."""
+(``PagedAttention``).  The arguments are looked over and passed on by the
+extension module (csrc/python_calls.cpp); where it finds that one does not fit,
+this side says which.  Nothing here is differentiable."""
 from __future__ import annotations
 
 import ctypes
@@ -14,17 +15,6 @@ from . import native as N
 
 _DTYPES = {torch.bfloat16: N.MOE_DTYPE_BF16, torch.float16: N.MOE_DTYPE_FP16}
 _TWO_PI = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
-
-# The calls below cost a few microseconds of GPU time where there are few
-# tokens, so what the host does before each counts: one expression looks the
-# arguments over, and only where it finds something are they gone through one
-# by one for the message.
-
-
-def _raw_stream(index, stream):
-    """The stream a call runs on, as an integer."""
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-
 
 class _On:
     """Device and stream of a call that are not the current ones: outputs are
@@ -93,69 +83,40 @@ class QKNormRope:
         words = [t - (1 << 64) if t >> 63 else t for t in turns]
         self.turns = torch.tensor(words, dtype=torch.int64).to(device)
         self.device = self.turns.device
-        self._turns_ptr = self.turns.data_ptr()
+        self._index = self.turns.get_device()
 
     def forward(self, q, k, v, q_weight, k_weight, positions, slots, k_cache, v_cache, q_out=None, stream=None):
         """q [T, Hq, D], k and v [T, Hk, D] (views of one projection are fine),
         weights [D] or None, positions int32 [T], slots int64 [T] (a negative
         slot writes nothing), caches [pages, page_size, Hk, D].  Returns q_out
         (a new contiguous tensor, or the given one; it may be q)."""
-        index = self.turns.get_device()
+        index = self._index
         if _elsewhere(index, stream):
             with _On(index, stream):
-                return self._forward(index, q, k, v, q_weight, k_weight, positions, slots, k_cache, v_cache, q_out)
-        return self._forward(index, q, k, v, q_weight, k_weight, positions, slots, k_cache, v_cache, q_out)
+                return self.forward(q, k, v, q_weight, k_weight, positions, slots, k_cache, v_cache, q_out)
+        got = N.calls().qk_norm_rope(index, torch._C._cuda_getCurrentRawStream(index), self.head_dim, self.rotary_dim,
+                                     self.interleaved, self.eps, self.turns, q, k, v, q_weight, k_weight, positions,
+                                     slots, k_cache, v_cache, q_out)
+        if isinstance(got, int):
+            if got < 0:
+                self._explain(index, q, k, v, q_weight, k_weight, positions, slots, k_cache, v_cache, q_out)
+            N.check("moe_qk_norm_rope", got)
+        return got if q_out is None else q_out
 
-    def _forward(self, index, q, k, v, q_weight, k_weight, positions, slots, k_cache, v_cache, q_out):
-        T, Hq, D = q.shape
-        dt = q.dtype
-        pages, page_size, Hk, _ = shape = k_cache.shape
-        tokens = (T,)
-        qs, ks, vs, kc, vc = q.stride(), k.stride(), v.stride(), k_cache.stride(), v_cache.stride()
-        if not (dt in _DTYPES and D == self.head_dim and k.shape == v.shape == (T, Hk, D) and v_cache.shape == shape
-                and shape[3] == D and k.dtype is dt and v.dtype is dt and k_cache.dtype is dt and v_cache.dtype is dt
-                and qs[2] == ks[2] == vs[2] == 1 and kc[2:] == vc[2:] == (D, 1)
-                and q.get_device() == k.get_device() == v.get_device() == k_cache.get_device() == v_cache.get_device()
-                == positions.get_device() == slots.get_device() == index
-                and positions.dtype is torch.int32 and positions.shape == tokens and positions.is_contiguous()
-                and slots.dtype is torch.int64 and slots.shape == tokens and slots.is_contiguous()):
-            self._explain(index, q, k, v, positions, slots, k_cache, v_cache)
-        w = (D,)
-        if q_weight is not None and not (q_weight.dtype is dt and q_weight.shape == w and q_weight.is_contiguous()
-                                         and q_weight.get_device() == index):
-            _plain("q_weight", q_weight, dt, index, D)
-        if k_weight is not None and not (k_weight.dtype is dt and k_weight.shape == w and k_weight.is_contiguous()
-                                         and k_weight.get_device() == index):
-            _plain("k_weight", k_weight, dt, index, D)
-        if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
-        else:
-            _heads("q_out", q_out, dt, index, D)
-            if q_out.shape != q.shape:
-                raise ValueError("q_out must have q's shape")
-        os = q_out.stride()
-        a = N.moe_qk_norm_rope_args_t(
-            _DTYPES[dt], T, Hq, Hk, D, self.rotary_dim, self.interleaved, self.eps, q.data_ptr(), k.data_ptr(),
-            v.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], None if q_weight is None else q_weight.data_ptr(),
-            None if k_weight is None else k_weight.data_ptr(), self._turns_ptr, positions.data_ptr(), slots.data_ptr(),
-            q_out.data_ptr(), os[0], os[1], k_cache.data_ptr(), v_cache.data_ptr(), kc[0], kc[1], vc[0], vc[1], pages,
-            page_size)
-        status = N.lib().moe_qk_norm_rope(ctypes.byref(a), torch._C._cuda_getCurrentRawStream(index))
-        if status:
-            N.check("moe_qk_norm_rope", status)
-        return q_out
-
-    def _explain(self, index, q, k, v, positions, slots, k_cache, v_cache):
+    def _explain(self, index, q, k, v, q_weight, k_weight, positions, slots, k_cache, v_cache, q_out):
         T, D, dt = q.shape[0], self.head_dim, q.dtype
         if dt not in _DTYPES:
             raise ValueError("q must be bf16 or fp16")
-        for name, t in (("q", q), ("k", k), ("v", v)):
+        for name, t in (("q", q), ("k", k), ("v", v)) + ((("q_out", q_out),) if q_out is not None else ()):
             _heads(name, t, dt, index, D)
         for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
             _cache(name, t, dt, index, k.shape[1], D)
+        for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if t is not None:
+                _plain(name, t, dt, index, D)
         _plain("positions", positions, torch.int32, index, T)
         _plain("slots", slots, torch.int64, index, T)
-        raise ValueError("q, k, v and the caches must agree in tokens, heads and pages")
+        raise ValueError("q, k, v, q_out and the caches must agree in tokens, heads and pages")
 
     __call__ = forward
 
@@ -173,6 +134,7 @@ class PagedAttention:
         if not h:
             raise N.MoEError("moe_attn_create", N.MOE_ERR_INVALID_ARG, N.last_error())
         self._h = ctypes.c_void_p(h)
+        self._handle = h
 
     def forward(self, q, k_cache, v_cache, block_table, q_starts, kv_lens, max_q_len: int, scale: float | None = None,
                 tree_mask=None, out=None, return_lse: bool = False, stream=None):
@@ -185,61 +147,37 @@ class PagedAttention:
         index = self._index
         if _elsewhere(index, stream):
             with _On(index, stream):
-                return self._forward(q, k_cache, v_cache, block_table, q_starts, kv_lens, max_q_len, scale, tree_mask,
-                                     out, return_lse)
-        return self._forward(q, k_cache, v_cache, block_table, q_starts, kv_lens, max_q_len, scale, tree_mask, out,
-                             return_lse)
-
-    def _forward(self, q, k_cache, v_cache, block_table, q_starts, kv_lens, max_q_len, scale, tree_mask, out,
-                 return_lse):
-        index, D, dt, dev = self._index, self.head_dim, q.dtype, q.device
-        T = q.shape[0]
-        B, width = block_table.shape
-        shape = k_cache.shape
-        qs, kc, vc, bs = q.stride(), k_cache.stride(), v_cache.stride(), block_table.stride()
-        if not (dt in _DTYPES and q.shape == (T, self.n_heads, D) and qs[2] == 1 and len(shape) == 4
-                and shape[2] == self.n_kv_heads and shape[3] == D and v_cache.shape == shape and k_cache.dtype is dt
-                and v_cache.dtype is dt and kc[2:] == vc[2:] == (D, 1) and block_table.dtype is torch.int32
-                and bs[1] == 1 and q_starts.dtype is torch.int32 and q_starts.shape == (B + 1,)
-                and q_starts.is_contiguous() and kv_lens.dtype is torch.int32 and kv_lens.shape == (B,)
-                and kv_lens.is_contiguous()
-                and q.get_device() == k_cache.get_device() == v_cache.get_device() == block_table.get_device()
-                == q_starts.get_device() == kv_lens.get_device() == index):
-            self._explain(q, k_cache, v_cache, block_table, q_starts, kv_lens)
-        if tree_mask is not None:
-            _plain("tree_mask", tree_mask, torch.int64, index, T)
+                return self.forward(q, k_cache, v_cache, block_table, q_starts, kv_lens, max_q_len, scale, tree_mask,
+                                    out, return_lse)
+        got = N.calls().attention(index, torch._C._cuda_getCurrentRawStream(index), self._handle, self.n_heads,
+                                  self.n_kv_heads, self.head_dim, q, k_cache, v_cache, block_table, q_starts, kv_lens,
+                                  max_q_len, self.head_dim ** -0.5 if scale is None else scale, tree_mask, out,
+                                  return_lse)
+        if isinstance(got, int):
+            if got < 0:
+                self._explain(q, k_cache, v_cache, block_table, q_starts, kv_lens, max_q_len, tree_mask, out)
+            N.check("moe_attn_forward", got)
         if out is None:
-            out = torch.empty((T, self.n_heads, D), dtype=dt, device=dev)
-        else:
-            _heads("out", out, dt, index, D)
-            if out.shape != q.shape:
-                raise ValueError("out must have q's shape")
-        lse = torch.empty((T, self.n_heads), dtype=torch.float32, device=dev) if return_lse else None
-        os = out.stride()
-        a = N.moe_attn_args_t(
-            _DTYPES[dt], B, T, max_q_len, D ** -0.5 if scale is None else scale, q.data_ptr(), qs[0], qs[1],
-            k_cache.data_ptr(), v_cache.data_ptr(), kc[0], kc[1], vc[0], vc[1], shape[0], shape[1],
-            block_table.data_ptr(), bs[0] if B > 1 else width, q_starts.data_ptr(), kv_lens.data_ptr(),
-            None if tree_mask is None else tree_mask.data_ptr(), out.data_ptr(), os[0], os[1],
-            None if lse is None else lse.data_ptr())
-        status = N.lib().moe_attn_forward(self._h, ctypes.byref(a), torch._C._cuda_getCurrentRawStream(index))
-        if status:
-            N.check("moe_attn_forward", status)
-        return (out, lse) if return_lse else out
+            return got
+        return (out, got[1]) if return_lse else out
 
-    def _explain(self, q, k_cache, v_cache, block_table, q_starts, kv_lens):
+    def _explain(self, q, k_cache, v_cache, block_table, q_starts, kv_lens, max_q_len, tree_mask, out):
         index, D, dt = self._index, self.head_dim, q.dtype
         if dt not in _DTYPES or q.dim() != 3 or q.shape[1] != self.n_heads:
             raise ValueError(f"q must be a bf16 or fp16 tensor [tokens, {self.n_heads}, {D}]")
         _heads("q", q, dt, index, D)
         for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
             _cache(name, t, dt, index, self.n_kv_heads, D)
-        if block_table.dtype != torch.int32 or block_table.get_device() != index or block_table.stride(1) != 1:
+        if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.get_device() != index or block_table.stride(1) != 1:
             raise ValueError(f"block_table must be an int32 tensor [batch, pages] with contiguous rows on cuda:{index}")
         B = block_table.shape[0]
         _plain("q_starts", q_starts, torch.int32, index, B + 1)
         _plain("kv_lens", kv_lens, torch.int32, index, B)
-        raise ValueError("the caches must have one shape")
+        if tree_mask is not None:
+            _plain("tree_mask", tree_mask, torch.int64, index, q.shape[0])
+        if out is not None:
+            _heads("out", out, dt, index, D)
+        raise ValueError("the caches must have one shape, out q's, and max_q_len must be an int of 0 or more")
 
     __call__ = forward
 

@@ -11,53 +11,37 @@ from . import native as N
 from .attention import _elsewhere, _On, _plain
 
 
-def _pools(k_pool, v_pool):
-    """Strides in bytes of (layer, page) of both pools, the rows' bytes, the GPU."""
-    shape, ks, vs = k_pool.shape, k_pool.stride(), v_pool.stride()
+def _copy(name, rows, k_pool, v_pool, src, dst, stream):
     index = k_pool.get_device()
-    if len(shape) != 5 or index < 0:
-        raise ValueError("the pools must be CUDA tensors [layers, pages, page_size, kv_heads, dim]")
-    if v_pool.shape != shape or v_pool.dtype != k_pool.dtype or v_pool.get_device() != index:
-        raise ValueError("the pools must have one shape, type and device")
-    row = shape[3] * shape[4]
-    inner = (row, shape[4], 1)
-    if ks[2:] != inner or vs[2:] != inner:
-        raise ValueError("the pools' pages must be contiguous")
-    e = k_pool.element_size()
-    return ks[0] * e, vs[0] * e, ks[1] * e, vs[1] * e, row * e, index
-
-
-def _copy(name, dtype, k_pool, v_pool, src, dst, stream):
-    k_layer, v_layer, k_page, v_page, row, index = _pools(k_pool, v_pool)
-    layers, pages, page_size = k_pool.shape[:3]
-    n = src.shape[0]
-    _plain("src", src, dtype, index, n)
-    _plain("dst", dst, dtype, index, n)
-    sizes = (pages, page_size * row) if dtype is torch.int32 else (pages, page_size, row)
-    call = getattr(N.lib(), name)
-    if _elsewhere(index, stream):
+    if index >= 0 and _elsewhere(index, stream):
         with _On(index, stream):
-            status = call(k_pool.data_ptr(), v_pool.data_ptr(), layers, k_layer, v_layer, k_page, v_page, *sizes,
-                          src.data_ptr(), dst.data_ptr(), n, torch._C._cuda_getCurrentRawStream(index))
-    else:
-        status = call(k_pool.data_ptr(), v_pool.data_ptr(), layers, k_layer, v_layer, k_page, v_page, *sizes,
-                      src.data_ptr(), dst.data_ptr(), n, torch._C._cuda_getCurrentRawStream(index))
-    if status:
-        N.check(name, status)
+            return _copy(name, rows, k_pool, v_pool, src, dst, None)
+    status = N.calls().copy(torch._C._cuda_getCurrentRawStream(index) if index >= 0 else 0, rows, k_pool, v_pool, src,
+                            dst)
+    if status < 0:
+        shape = k_pool.shape
+        if len(shape) != 5 or index < 0:
+            raise ValueError("the pools must be CUDA tensors [layers, pages, page_size, kv_heads, dim]")
+        if v_pool.shape != shape or v_pool.dtype != k_pool.dtype or v_pool.get_device() != index:
+            raise ValueError("the pools must have one shape, type and device")
+        for n, t in (("src", src), ("dst", dst)):
+            _plain(n, t, torch.int64 if rows else torch.int32, index, src.shape[0])
+        raise ValueError("the pools' pages must be contiguous")
+    N.check(name, status)
 
 
 def copy_pages(k_pool, v_pool, src, dst, stream=None):
     """Page dst[i] := page src[i] in every layer of both pools [L, P, page_size,
     Hk, D] (pages contiguous, layers and pages any distance apart); src, dst:
     int32 CUDA tensors [n].  No page may be in dst twice or in both lists."""
-    _copy("moe_copy_pages", torch.int32, k_pool, v_pool, src, dst, stream)
+    _copy("moe_copy_pages", False, k_pool, v_pool, src, dst, stream)
 
 
 def copy_rows(k_pool, v_pool, src, dst, stream=None):
     """Cache rows dst[i] := src[i] in every layer of both pools, as if all were
     read before any is written; src, dst: int64 CUDA tensors [n] of slots (page
     * page_size + row), n up to 64, no slot in dst twice."""
-    _copy("moe_copy_rows", torch.int64, k_pool, v_pool, src, dst, stream)
+    _copy("moe_copy_rows", True, k_pool, v_pool, src, dst, stream)
 
 
 class PageTable:

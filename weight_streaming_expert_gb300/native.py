@@ -8,6 +8,8 @@ is no Python or CPU fallback: if the library is missing or fails to load,
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -101,7 +103,7 @@ def lib(build_if_missing: bool = True):
         if _lib is not None:
             return _lib
         path = build_lib.LIB
-        if not os.path.exists(path):
+        if not (os.path.exists(path) and os.path.exists(build_lib.CALLS)):
             if not build_if_missing:
                 raise RuntimeError(f"CUDA library not built: {path}")
             build_lib.build()
@@ -179,6 +181,26 @@ def lib(build_if_missing: bool = True):
         L.moe_last_error.restype = ctypes.c_char_p
         _lib = L
         return L
+
+
+_calls = None
+
+
+def calls():
+    """The extension module of the attention and sampling calls
+    (``_build/wse_calls.so``, csrc/python_calls.cpp), loaded on first use."""
+    global _calls
+    if _calls is None:
+        lib()  # it is linked against the library
+        with _lock:
+            if not os.path.exists(build_lib.CALLS):
+                raise RuntimeError(f"extension module not built: {build_lib.CALLS}")
+            loader = importlib.machinery.ExtensionFileLoader("wse_calls", build_lib.CALLS)
+            spec = importlib.util.spec_from_file_location("wse_calls", build_lib.CALLS, loader=loader)
+            module = importlib.util.module_from_spec(spec)
+            loader.exec_module(module)
+            _calls = module
+    return _calls
 
 
 def last_error() -> str:

@@ -1,5 +1,6 @@
 """Python face of include/sampling.h: the next token of each row of logits.
-Argument marshalling only: the work runs in the library's kernel."""
+The arguments are looked over and passed on by the extension module
+(csrc/python_calls.cpp)."""
 from __future__ import annotations
 
 import torch
@@ -17,32 +18,27 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
     without a logit above -inf), with ``return_probs`` also each token's
     probability among those that stayed, fp32 [M]."""
     index = logits.get_device()
+    if index >= 0 and _elsewhere(index, stream):
+        with _On(index, stream):
+            return sample(logits, u, temperature, top_k, top_p, min_p, tokens, return_probs)
+    got = N.calls().sample(torch._C._cuda_getCurrentRawStream(index) if index >= 0 else 0, logits, u, temperature,
+                           top_k, top_p, min_p, tokens, return_probs)
+    if isinstance(got, int):
+        if got < 0:
+            _explain(index, logits, u, temperature, top_k, top_p, min_p, tokens)
+        N.check("moe_sample", got)
+    if tokens is None:
+        return got
+    return (tokens, got[1]) if return_probs else tokens
+
+
+def _explain(index, logits, u, temperature, top_k, top_p, min_p, tokens):
     if index < 0 or logits.dim() != 2 or logits.dtype != torch.float32 or logits.stride(1) != 1:
         raise ValueError("logits must be an fp32 CUDA tensor [rows, vocab] with contiguous rows")
-    if _elsewhere(index, stream):
-        with _On(index, stream):
-            return _sample(index, logits, u, temperature, top_k, top_p, min_p, tokens, return_probs)
-    return _sample(index, logits, u, temperature, top_k, top_p, min_p, tokens, return_probs)
-
-
-def _sample(index, logits, u, temperature, top_k, top_p, min_p, tokens, return_probs):
-    M, V = logits.shape
-    dev = logits.device
-    _plain("u", u, torch.float32, index, M)
-    for name, t, dt in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
-                        ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
-        if t is not None:
+    M = logits.shape[0]
+    for name, t, dt in (("u", u, torch.float32), ("temperature", temperature, torch.float32),
+                        ("top_k", top_k, torch.int32), ("top_p", top_p, torch.float32),
+                        ("min_p", min_p, torch.float32), ("tokens", tokens, torch.int32)):
+        if t is not None or name == "u":
             _plain(name, t, dt, index, M)
-    if tokens is None:
-        tokens = torch.empty(M, dtype=torch.int32, device=dev)
-    else:
-        _plain("tokens", tokens, torch.int32, index, M)
-    probs = torch.empty(M, dtype=torch.float32, device=dev) if return_probs else None
-    status = N.lib().moe_sample(
-        logits.data_ptr(), logits.stride(0), M, V, u.data_ptr(),
-        None if temperature is None else temperature.data_ptr(), None if top_k is None else top_k.data_ptr(),
-        None if top_p is None else top_p.data_ptr(), None if min_p is None else min_p.data_ptr(), tokens.data_ptr(), None if probs is None else probs.data_ptr(),
-        torch._C._cuda_getCurrentRawStream(index))
-    if status:
-        N.check("moe_sample", status)
-    return (tokens, probs) if return_probs else tokens
+    raise ValueError("an argument of sample is not a tensor, or has over 2^31 elements")
