@@ -363,10 +363,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tma_prefetch_map(&k_map);
     tma_prefetch_map(&v_map);
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = uniform(*tmem_slot);
+  const Waiter wait{gone, p.status};
   pdl_wait();
   pdl_launch_dependents();
 
-  // ---- the plan, from the cost of each sequence (of one key/value head)
+  // ---- the plan, from the cost of each sequence (of one key/value head); few
+  // sequences: every warp makes it by itself and goes on without the others
   Plan plan;
   const bool wide = a.max_q_len > 4 * kTiles * p.tokens;  // sequences of many items: a warp each
   if (a.batch <= 32 && !wide) {
@@ -396,12 +402,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     for (int b = lane * per; b < min(a.batch, (lane + 1) * per); ++b) sum += cost[b];
     plan = make_plan<kTiles>(p, per, sum, [&](int b) { return cost[b]; });
     fence_proxy_async_smem();  // the costs' place becomes the ring
+    __syncthreads();
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = uniform(*tmem_slot);
-  const Waiter wait{gone, p.status};
   if (p.by_item) {
     // items that are not cut say so where they begin; these have no items
     if (blockIdx.x == 0)
@@ -873,8 +875,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // rows at a time.  What it costs is the latency of its reads, so all of a
 // row's statistics are read at once, by the lanes of a warp, and then its
 // parts by four threads per column, whose sums are added in order.
-template <typename T, int D, int kRows>
-__global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4) join_kernel(const __grid_constant__ AttnParams p) {
+//
+// Cuts by item are few and wait for nothing but these reads, so a thread may
+// have many under way (128 registers: 13.3 us for 6 tokens over 8192, with 64
+// registers 14.4) as long as all blocks run at once; of the blocks by CTA two
+// or more share an SM (ragged chunks: 143 us, with 128 registers 152).
+template <typename T, int D, int kRows, bool kByItem>
+__global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4, kByItem ? 128 / D * 2 - 1 : 256 / D)
+    join_kernel(const __grid_constant__ AttnParams p) {
   constexpr int kColumns = D / 4;
   __shared__ float factor[kJoinRows][kMaxParts];
   __shared__ float4 sums[kJoinGroups - 1][kJoinRows][kColumns];
@@ -882,11 +890,15 @@ __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4) join_kernel(c
   const moe_attn_args_t& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int column = tid % kColumns, row = tid / kColumns % kJoinRows, part = tid / (kColumns * kJoinRows);
+  // the lengths are no output of the kernel before, which starts this one only
+  // after it has waited for what came before itself
+  Seq s;
+  if (kByItem) s = load_seq(p, blockIdx.x / p.n_kv_heads);
   pdl_wait();
   pdl_launch_dependents();
   const Cut cut = p.cuts[blockIdx.x];
   if (cut.parts == 0) return;
-  const Seq s = load_seq(p, cut.b);
+  if (!kByItem) s = load_seq(p, cut.b);
   // rows of the item in use: of the pair's second tile from 128 on
   auto token_of = [&](int row) {
     const int in_tile = row % kTile / p.group;
@@ -939,6 +951,19 @@ __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4) join_kernel(c
   }
   for (int r0 = blockIdx.y * kJoinRows; r0 < kRows; r0 += gridDim.y * kJoinRows) {
     if (token_of(r0) >= s.n) continue;  // nor does a later row of the four have a token
+    const int token = token_of(r0 + row);
+    const bool mine = token < s.n;
+    // the first parts' sums are on their way while the factors are worked out
+    constexpr int kAhead = 8;
+    const int per = (cut.parts + kJoinGroups - 1) / kJoinGroups;
+    const int first = part * per, end = min(cut.parts, first + per);
+    auto sums_of = [&](int i) {
+      return reinterpret_cast<const float4*>(p.part_o)[(slot(i) * kRows + r0 + row) * kColumns + column];
+    };
+    float4 ahead[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (mine && first + i < end) ahead[i] = sums_of(first + i);
     if (warp < kJoinRows && token_of(r0 + warp) < s.n) {
       float m = -INFINITY, l = 0.f;
       for (int i = lane; i < cut.parts; i += 32) m = fmaxf(m, p.part_ml[slot(i) * kRows + r0 + warp].x);
@@ -957,22 +982,21 @@ __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4) join_kernel(c
                                   l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f);
     }
     __syncthreads();
-    const int token = token_of(r0 + row);
-    const bool mine = token < s.n;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (mine) {
-      const int per = (cut.parts + kJoinGroups - 1) / kJoinGroups;
-#pragma unroll 8
-      for (int i = part * per; i < min(cut.parts, (part + 1) * per); ++i) {
+      auto add = [&](int i, float4 v) {
         const float f = factor[row][i];
-        const float4 v = reinterpret_cast<const float4*>(p.part_o)[(slot(i) * kRows + r0 + row) * kColumns + column];
-        if (f != 0.f) {
-          o.x = fmaf(v.x, f, o.x);
-          o.y = fmaf(v.y, f, o.y);
-          o.z = fmaf(v.z, f, o.z);
-          o.w = fmaf(v.w, f, o.w);
-        }
-      }
+        if (f == 0.f) return;
+        o.x = fmaf(v.x, f, o.x);
+        o.y = fmaf(v.y, f, o.y);
+        o.z = fmaf(v.z, f, o.z);
+        o.w = fmaf(v.w, f, o.w);
+      };
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (first + i < end) add(first + i, ahead[i]);
+#pragma unroll 4
+      for (int i = first + kAhead; i < end; ++i) add(i, sums_of(i));
       if (part > 0) sums[part - 1][row][column] = o;
     }
     __syncthreads();
@@ -1115,12 +1139,14 @@ int launch_attn(const moe_attn* h, const AttnParams& p, const Maps& maps, moe_st
   const int rc = launch_pdl(paged_attention_kernel<T, D, kPair>, dim3(grid), dim3(kAttnThreads), L::kSmem, stream,
                             1, p, maps.q, maps.k, maps.v);
   if (rc != MOE_OK) return rc;
-  // cuts by item: as many blocks as their rows have use for, for the latency;
-  // else most of the blocks find no cut
+  const dim3 threads(kJoinRows * kJoinGroups * D / 4);
+  // cuts by item: as many blocks as their rows have use for; else most of the
+  // blocks find no cut
   const int rows = kPair ? L::kRows : std::min(p.a.max_q_len, p.tokens) * p.group;
-  const dim3 blocks = p.by_item ? dim3(p.a.batch * p.n_kv_heads, (rows + kJoinRows - 1) / kJoinRows) : dim3(grid, 16);
-  return launch_pdl(join_kernel<T, D, L::kRows>, blocks,
-                    dim3(kJoinRows * kJoinGroups * D / 4), 0, stream, 1, p);
+  if (p.by_item)
+    return launch_pdl(join_kernel<T, D, L::kRows, true>,
+                      dim3(p.a.batch * p.n_kv_heads, (rows + kJoinRows - 1) / kJoinRows), threads, 0, stream, 1, p);
+  return launch_pdl(join_kernel<T, D, L::kRows, false>, dim3(grid, 16), threads, 0, stream, 1, p);
 }
 
 template <typename T, int D>
