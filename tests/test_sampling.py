@@ -132,6 +132,29 @@ def test_larger_vocabularies_and_many_rows():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("V", [40960, 40961, 655360, 655361])
+def test_where_a_slice_leaves_shared_memory(V):
+    check(logits(len(SETTINGS), V, V), SETTINGS, torch.rand(len(SETTINGS), generator=torch.Generator().manual_seed(V)),
+          real=False)
+    # rows enough for one CTA each
+    rows = [SETTINGS[i % len(SETTINGS)] for i in range(160)]
+    if V < 50000:
+        check(logits(160, V, V + 1), rows, torch.rand(160, generator=torch.Generator().manual_seed(1)), real=False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [512, 513, 2048, 2049, 20000])
+@pytest.mark.parametrize("tied", [False, True])
+def test_lengths_of_what_stays(V, tied):
+    """Cuts on both sides of the lengths at which the kernel goes on another way."""
+    rows = [(1.0, k, p, 0.0) for k in (2, 63, 64, 65, 511, 512, 513, 1024, 2047, 2048, 2049) for p in (1.0, 0.9, 0.2)]
+    rows += [(t, 0, p, 0.0) for t in (0.5, 1.0, 4.0) for p in (0.1, 0.3, 0.5, 0.7, 0.99)]
+    x = logits(len(rows), V, V)
+    u = torch.rand(len(rows), generator=torch.Generator().manual_seed(V))
+    check(x.round() if tied else x, rows, u, real=False)
+
+
+@pytest.mark.gpu
 def test_borders_of_the_uniform_number():
     x = torch.zeros(6, 1024, device=DEV)  # equal weights: token floor(u * 1024)
     u = torch.tensor([0.0, 1 / 1024, 0.5, 1 - 2.0 ** -24, 0.25 - 2.0 ** -26, 1.0])

@@ -15,12 +15,16 @@
 // what remains is the latency of the exchanges (one takes 1-3 us).  So where a
 // filter cuts among the 2048 largest logits, as it mostly does, one pass of
 // bins finds those down to the cut, the CTAs hand them to the first one in the
-// order of their ids, and it goes on alone.  Up to 256 of them it sorts, which
-// places both cuts at once, and strikes out what lies behind.
+// order of their ids, and it goes on alone.  Up to 512 of them it sorts, which
+// places both cuts at once, and strikes out what lies behind (top-k 50
+// and top-p 0.95: 19 us instead of 31; sorting 2048 would take longer than the
+// passes of bins, top-p 0.5 alone 42 us instead of 31).
 //
-// 6 rows of 157184 logits: greedy 4.4 us, unfiltered 9.0 us, top-k 50 22 us,
-// top-k 50 and top-p 0.95 31 us, top-p 0.95 alone (a cut among 20,000 logits)
-// 40 us; the logits' bytes are 0.6 us of that.
+// 6 rows of 157184 logits: greedy 4.4 us, unfiltered 8.9 us, top-k 50 16 us,
+// top-k 50 and top-p 0.95 17 us, top-p 0.95 alone (a cut among 20,000 logits)
+// 37 us; the logits' bytes are 0.6 us of that.  The kernel for slices in
+// shared memory may use 128 registers, as only one such CTA fits an SM: at 64
+// it spills, 19 us instead of 17 for both filters.
 #include <cooperative_groups.h>
 
 #include <cstddef>
@@ -40,10 +44,10 @@ constexpr int kBarBits = 10;             // of the pass that finds the kList lar
 constexpr int kWindowBits = 24;          // the first pass looks at the 2^24 keys from the largest: two to three octaves
 constexpr int kMaxCluster = 16;
 constexpr float kOne = 274877906944.f;   // 2^38
-constexpr int kMaxCached = 36864;        // logits of a slice that fit in shared memory
+constexpr int kMaxCached = 40960;        // logits of a slice that fit in shared memory
 constexpr uint32_t kKeyNegInf = 0x007fffffu;
 constexpr int kList = 2048;              // largest logits that one CTA can go on with
-constexpr int kSorted = 256;              // of them, where sorting is faster than more passes of bins
+constexpr int kSorted = 512;             // of them, where sorting is faster than more passes of bins
 constexpr int kAllTies = 0x7fffffff;
 constexpr int kLimbBits = 13;            // of a weight (39 bits) in a bin's three words
 constexpr int kMaxSlice = 1 << (32 - kLimbBits);  // a slice's sums of 13-bit parts fit a word
@@ -416,7 +420,7 @@ __device__ float quotient(u64 x, u64 y) {
 }
 
 template <bool kCached>
-__global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kSampleThreads, kCached ? 1 : 2) sample_kernel(const SampleArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& s = *reinterpret_cast<Shared*>(smem);
   uint32_t* cache = reinterpret_cast<uint32_t*>(smem + sizeof(Shared));
@@ -667,7 +671,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
     const int src = __ffs(here) - 1;
     const int from = __shfl_sync(0xffffffffu, c.i0, src), to = __shfl_sync(0xffffffffu, c.i1, src);
     before = __shfl_sync(0xffffffffu, before, src);
-    for (int i = from + c.lane;; i += 32) {
+    for (int i = from + c.lane; i - c.lane < to; i += 32) {
       const uint32_t key[4] = {i < to ? c.key(i) : 0u, 0u, 0u, 0u};
       float e[4];
       exps(key, e);
@@ -715,13 +719,16 @@ extern "C" int moe_sample(const float* logits, int64_t row_stride, int rows, int
     return fail(MOE_ERR_INVALID_ARG, "row_stride = %lld is smaller than vocab", (long long)row_stride);
   int rc = check_device();
   if (rc != MOE_OK) return rc;
-  // CTAs of a row: as many as run at once (two per SM), for every exchange
-  // costs each of them the same (64 rows of 157184, top-k: 95 us with 16, 73 us
-  // with 4; 6 rows, every filter: 32 us with 8, 31 us with 16)
+  // CTAs of a row: as many as run at once, one per SM, for every exchange costs
+  // each of them the same (16 rows of 157184, top-k: 39 us with 16, 34 us with
+  // 8), but not so few that a slice leaves shared memory (64 rows: 51 us with 4,
+  // in two waves; 68 us with 2, which read the row from L2 in every pass)
   int cluster = kMaxCluster;
-  while (cluster > 1 && (rows * cluster > 256 || (vocab + cluster - 1) / cluster < kSampleThreads) &&
-         (vocab + cluster / 2 - 1) / (cluster / 2) <= kMaxSlice)
+  while (cluster > 1 && (rows * cluster > 152 || (vocab + cluster - 1) / cluster < kSampleThreads) &&
+         (vocab + cluster / 2 - 1) / (cluster / 2) <= kMaxCached)
     cluster /= 2;
+  static_assert(MOE_SAMPLE_MAX_VOCAB / kMaxCluster <= kMaxSlice && kMaxCached <= kMaxSlice);
+  static_assert(sizeof(Shared) + kMaxCached * 4 <= 227 * 1024);
   SampleArgs a{logits, row_stride, vocab, (vocab + cluster - 1) / cluster, u, temperature, top_k, top_p, min_p,
                tokens, probs};
   const bool cached = a.slice <= kMaxCached;
