@@ -10,13 +10,20 @@
 // wraps modulo a whole turn by itself, so the angle has an error of
 // position * 2^-65 turns and the 32 leading bits go to sincospif.
 //
-// Bound by memory: 2 bytes in and 2 out per value.  A warp handles a token, or
+// 2 bytes in and 2 out per value.  A warp handles a token, or
 // a share of its heads where there are few tokens; D/8 lanes share a head.  A
 // lane holds four values of a head's first half and their four partners of the
 // second (or four adjacent pairs), so a pair turns inside a thread and only
 // the sum of squares crosses lanes.  The sines and cosines of a token are
 // computed once by the warp, two or so per lane, while its first heads are on
 // their way, and no warp waits for another.
+//
+// The norm's weights are multiplied into the sines and cosines once per token
+// and kind, and the products are done on two fp32 values at a time: the kernel
+// is bound by issuing instructions before it is by memory.  16384 tokens of 32
+// + 8 heads of 128: 59 us, 5.6 TB/s; with weights and turns one after the other
+// and single products 73 us, 70 % of the issue slots.  6 tokens: 3.2 us, a
+// launch and two reads one after the other.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -52,6 +59,29 @@ __device__ __forceinline__ uint32_t pack2<__half>(float x, float y) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Two fp32 values side by side, whose products are one instruction.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair_of(float x, float y) {
+  f32x2 v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+  return v;
+}
+__device__ __forceinline__ float2 both(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 x, f32x2 y) {
+  f32x2 v;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(x), "l"(y));
+  return v;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 x, f32x2 y, f32x2 z) {
+  f32x2 v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(x), "l"(y), "l"(z));
+  return v;
+}
+
 template <typename T, int D, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads, D == 256 ? 3 : 4) qk_norm_rope_kernel(
     const __grid_constant__ moe_qk_norm_rope_args_t a, int warps_per_token) {
@@ -74,18 +104,10 @@ __global__ void __launch_bounds__(kRopeThreads, D == 256 ? 3 : 4) qk_norm_rope_k
     lo = turns ? part * 4 : part * 4 + pairs;
     hi = turns ? part * 4 + pairs : part * 4 + D / 2;
   }
+  const int apart = hi - lo;
   const long long slot = a.n_kv_heads > 0 ? a.slots[t] : -1;
   const bool keep = slot >= 0 && slot < (long long)a.n_pages * a.page_size;
-  const long long page = keep ? slot / a.page_size : 0, row = keep ? slot % a.page_size : 0;
-  // of each kind (queries, keys, values) where this lane's values of head
-  // `sub` begin, in and out
-  const T* from[3] = {static_cast<const T*>(a.q) + t * a.q_token_stride + sub * a.q_head_stride + lo,
-                      static_cast<const T*>(a.k) + t * a.k_token_stride + sub * a.k_head_stride + lo,
-                      static_cast<const T*>(a.v) + t * a.v_token_stride + sub * a.v_head_stride + lo};
-  T* to[3] = {static_cast<T*>(a.q_out) + t * a.q_out_token_stride + sub * a.q_out_head_stride + lo,
-              static_cast<T*>(a.k_cache) + page * a.k_page_stride + row * a.k_row_stride + sub * D + lo,
-              static_cast<T*>(a.v_cache) + page * a.v_page_stride + row * a.v_row_stride + sub * D + lo};
-  const int apart = hi - lo;
+  const long long page = keep ? slot / a.page_size : 0, row = keep ? slot - page * a.page_size : 0;
 
   // groups of heads of one kind, so that what differs by kind is decided once
   // for the warp: of queries, then of keys, then of values
@@ -93,24 +115,131 @@ __global__ void __launch_bounds__(kRopeThreads, D == 256 ? 3 : 4) qk_norm_rope_k
   const int groups = q_groups + 2 * kv_groups;
   auto kind_of = [&](int g) { return g < q_groups ? 0 : g < q_groups + kv_groups ? 1 : 2; };
   auto head_of = [&](int g, int kind) {
-    return (kind == 0 ? g : kind == 1 ? g - q_groups : g - q_groups - kv_groups) * kHeads;
+    return (kind == 0 ? g : kind == 1 ? g - q_groups : g - q_groups - kv_groups) * kHeads + sub;
   };
-  float2 cs[4];
-  bool first = true;
-  for (int g0 = warp % warps_per_token; g0 < groups; g0 += kRopeLoads * warps_per_token) {
+  // where this lane's values of a head begin, in and out
+  auto from = [&](int kind, int head) {
+    const long long at = kind == 0   ? t * a.q_token_stride + head * a.q_head_stride
+                         : kind == 1 ? t * a.k_token_stride + head * a.k_head_stride
+                                     : t * a.v_token_stride + head * a.v_head_stride;
+    return static_cast<const T*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) + at + lo;
+  };
+  auto to = [&](int kind, int head) {
+    const long long at = kind == 0   ? t * a.q_out_token_stride + head * a.q_out_head_stride
+                         : kind == 1 ? page * a.k_page_stride + row * a.k_row_stride + head * D
+                                     : page * a.v_page_stride + row * a.v_row_stride + head * D;
+    return static_cast<T*>(kind == 0 ? a.q_out : kind == 1 ? a.k_cache : a.v_cache) + at + lo;
+  };
+
+  // what a head's values are multiplied with: norm weight times cosine or sine,
+  // for this lane's pairs, two at a time.  Halves: own[0, 1] and cross[0, 1]
+  // make the first of a pair, own[2, 3] and cross[2, 3] the second, with `own`
+  // on that value itself.  Adjacent: own on (x_a, x_a), cross on (x_b, x_b).
+  f32x2 own[4], cross[4];
+  int made = -1;  // the kind that they are of
+  auto factors_of = [&](int kind) {
+    if (kind == made) return;
+    made = kind;
+    float w[8], c[4], sn[4];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = 1.f;
+    if (const T* weight = static_cast<const T*>(kind == 0 ? a.q_weight : a.k_weight)) {
+      const uint2 w0 = *reinterpret_cast<const uint2*>(weight + lo), w1 = *reinterpret_cast<const uint2*>(weight + hi);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        w[j] = to_f32<T>(reinterpret_cast<const T*>(&w0)[j]);
+        w[4 + j] = to_f32<T>(reinterpret_cast<const T*>(&w1)[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 cs = turns ? turn[warp][part * 4 + j] : make_float2(1.f, 0.f);
+      c[j] = cs.x;
+      sn[j] = cs.y;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (kInterleaved) {
+        const float wa = w[2 * j], wb = w[2 * j + 1];
+        own[j] = turns ? pair_of(wa * c[j], wa * sn[j]) : pair_of(wa, wb);
+        cross[j] = pair_of(-wb * sn[j], wb * c[j]);
+      } else {
+        const int n = 2 * (j & 1);  // of pairs n, n + 1
+        const float* wo = w + (j < 2 ? 0 : 4);
+        const float* wc = w + (j < 2 ? 4 : 0);
+        const float sign = j < 2 ? -1.f : 1.f;
+        own[j] = pair_of(wo[n] * c[n], wo[n + 1] * c[n + 1]);
+        cross[j] = pair_of(sign * wc[n] * sn[n], sign * wc[n + 1] * sn[n + 1]);
+      }
+    }
+  };
+  // a group's values, normed and turned
+  auto finish = [&](uint2& v0, uint2& v1, bool norm) {
+    const T* e0 = reinterpret_cast<const T*>(&v0);
+    const T* e1 = reinterpret_cast<const T*>(&v1);
+    f32x2 x[4], y[4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      x[j] = pair_of(to_f32<T>(e0[2 * j]), to_f32<T>(e0[2 * j + 1]));
+      x[2 + j] = pair_of(to_f32<T>(e1[2 * j]), to_f32<T>(e1[2 * j + 1]));
+    }
+    if (norm) {
+      f32x2 sq2 = mul2(x[0], x[0]);
+#pragma unroll
+      for (int j = 1; j < 4; ++j) sq2 = fma2(x[j], x[j], sq2);
+      float sq = both(sq2).x + both(sq2).y;
+#pragma unroll
+      for (int m = kLanes / 2; m > 0; m >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, m);
+      const float r = rsqrtf(sq * (1.f / D) + a.eps);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = mul2(x[j], pair_of(r, r));
+    }
+    if (turns) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (kInterleaved) {
+          const float2 v = both(x[j]);
+          y[j] = fma2(pair_of(v.y, v.y), cross[j], mul2(pair_of(v.x, v.x), own[j]));
+        } else {
+          y[j] = fma2(x[j ^ 2], cross[j], mul2(x[j], own[j]));
+        }
+      }
+    } else {  // 0 * inf must not reach these
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = mul2(x[j], own[j]);
+    }
+    v0 = make_uint2(pack2<T>(both(y[0]).x, both(y[0]).y), pack2<T>(both(y[1]).x, both(y[1]).y));
+    v1 = make_uint2(pack2<T>(both(y[2]).x, both(y[2]).y), pack2<T>(both(y[3]).x, both(y[3]).y));
+  };
+  auto load = [&](uint2& v0, uint2& v1, const T* p) {
+    v0 = *reinterpret_cast<const uint2*>(p);
+    v1 = *reinterpret_cast<const uint2*>(p + apart);
+  };
+  auto store = [&](T* p, uint2 v0, uint2 v1) {
+    *reinterpret_cast<uint2*>(p) = v0;
+    *reinterpret_cast<uint2*>(p + apart) = v1;
+  };
+
+  const int g_first = warp % warps_per_token, whole = a.n_heads / kHeads;
+  const long long q_step = (long long)warps_per_token * kHeads * a.q_head_stride;
+  const long long out_step = (long long)warps_per_token * kHeads * a.q_out_head_stride;
+  const T* q = from(0, g_first * kHeads + sub);
+  T* out = to(0, g_first * kHeads + sub);
+  for (int g0 = g_first; g0 < groups; g0 += kRopeLoads * warps_per_token) {
+    const bool queries = g0 + (kRopeLoads - 1) * warps_per_token < whole;  // whole groups of them
     uint2 x0[kRopeLoads], x1[kRopeLoads];
 #pragma unroll
     for (int i = 0; i < kRopeLoads; ++i) {
-      const int g = g0 + i * warps_per_token, kind = kind_of(g), head = head_of(g, kind);
-      if (g >= groups || head + sub >= (kind == 0 ? a.n_heads : a.n_kv_heads)) continue;
-      const T* p = kind == 0   ? from[0] + head * a.q_head_stride
-                   : kind == 1 ? from[1] + head * a.k_head_stride
-                               : from[2] + head * a.v_head_stride;
-      x0[i] = *reinterpret_cast<const uint2*>(p);
-      x1[i] = *reinterpret_cast<const uint2*>(p + apart);
+      const int g = g0 + i * warps_per_token;
+      if (queries) {
+        load(x0[i], x1[i], q);
+        q += q_step;
+      } else if (g < groups) {
+        const int kind = kind_of(g), head = head_of(g, kind);
+        if (head < (kind == 0 ? a.n_heads : a.n_kv_heads)) load(x0[i], x1[i], from(kind, head));
+      }
     }
-    if (first) {
-      first = false;
+    if (g0 == g_first) {
       for (int i = lane; i < pairs; i += 32) {
         const unsigned long long at = (unsigned long long)(long long)a.positions[t] * a.turns[i];
         float sn, c;
@@ -118,54 +247,28 @@ __global__ void __launch_bounds__(kRopeThreads, D == 256 ? 3 : 4) qk_norm_rope_k
         turn[warp][i] = make_float2(c, sn);
       }
       __syncwarp();
+    }
+    if (queries) {
+      factors_of(0);
+      const bool norm = a.q_weight != nullptr;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) cs[j] = turns ? turn[warp][part * 4 + j] : make_float2(1.f, 0.f);
+      for (int i = 0; i < kRopeLoads; ++i) {
+        finish(x0[i], x1[i], norm);
+        store(out, x0[i], x1[i]);
+        out += out_step;
+      }
+      continue;
     }
 #pragma unroll
     for (int i = 0; i < kRopeLoads; ++i) {
-      const int g = g0 + i * warps_per_token, kind = kind_of(g), head = head_of(g, kind);
+      const int g = g0 + i * warps_per_token;
       if (g >= groups) break;
-      const bool valid = head + sub < (kind == 0 ? a.n_heads : a.n_kv_heads) && (kind == 0 || keep);
-      uint2 o0 = x0[i], o1 = x1[i];
+      const int kind = kind_of(g), head = head_of(g, kind);
       if (kind < 2) {
-        const T* e0 = reinterpret_cast<const T*>(&x0[i]);
-        const T* e1 = reinterpret_cast<const T*>(&x1[i]);
-        float x[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = to_f32<T>(e0[j]), x[4 + j] = to_f32<T>(e1[j]);
-        const T* w = static_cast<const T*>(kind == 0 ? a.q_weight : a.k_weight);
-        if (w) {
-          float sq = 0.f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) sq = fmaf(x[j], x[j], sq);
-#pragma unroll
-          for (int m = kLanes / 2; m > 0; m >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, m);
-          const float r = rsqrtf(sq * (1.f / D) + a.eps);
-          const uint2 w0 = *reinterpret_cast<const uint2*>(w + lo), w1 = *reinterpret_cast<const uint2*>(w + hi);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x[j] *= r * to_f32<T>(reinterpret_cast<const T*>(&w0)[j]);
-            x[4 + j] *= r * to_f32<T>(reinterpret_cast<const T*>(&w1)[j]);
-          }
-        }
-        if (turns) {  // others stay as they are: 0 * inf must not reach them
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float& x_a = x[kInterleaved ? 2 * j : j];
-            float& x_b = x[kInterleaved ? 2 * j + 1 : 4 + j];
-            const float y_a = fmaf(-x_b, cs[j].y, x_a * cs[j].x), y_b = fmaf(x_a, cs[j].y, x_b * cs[j].x);
-            x_a = y_a;
-            x_b = y_b;
-          }
-        }
-        o0 = make_uint2(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]));
-        o1 = make_uint2(pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
+        factors_of(kind);
+        finish(x0[i], x1[i], (kind == 0 ? a.q_weight : a.k_weight) != nullptr);
       }
-      if (valid) {
-        T* o = kind == 0 ? to[0] + head * a.q_out_head_stride : kind == 1 ? to[1] + head * D : to[2] + head * D;
-        *reinterpret_cast<uint2*>(o) = o0;
-        *reinterpret_cast<uint2*>(o + apart) = o1;
-      }
+      if (head < (kind == 0 ? a.n_heads : a.n_kv_heads) && (kind == 0 || keep)) store(to(kind, head), x0[i], x1[i]);
     }
   }
 }
@@ -178,9 +281,9 @@ int launch_rope(const moe_qk_norm_rope_args_t& a, moe_stream_t stream) {
   else if (a.head_dim == 128) kernel = il ? qk_norm_rope_kernel<T, 128, true> : qk_norm_rope_kernel<T, 128, false>;
   else kernel = il ? qk_norm_rope_kernel<T, 256, true> : qk_norm_rope_kernel<T, 256, false>;
   // Several warps share a token as long as all CTAs are resident at once (4 per
-  // SM): 1001 tokens of 16 + 4 heads of 64 take 4.0 us with 2 or 4 warps each,
-  // 4.9 with one.  Beyond that a warp each, which works the angles out once:
-  // 16384 tokens of 32 + 8 heads of 128 take 74 us, with 2 warps 78, 4 90.
+  // SM): 1001 tokens of 16 + 4 heads of 64 take 4.4 us with 4 warps each, 5.3
+  // with 8.  Beyond that a warp each, which works the angles out once: 16384
+  // tokens of 32 + 8 heads of 128 take 59 us, with 2 warps 64, with 4 76.
   int warps = kRopeWarps;
   while (warps > 1 && (long long)a.n_tokens * warps > 152ll * 4 * kRopeWarps) warps /= 2;
   const int tokens = kRopeWarps / warps;
