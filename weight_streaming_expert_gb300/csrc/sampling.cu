@@ -77,7 +77,7 @@ __device__ __forceinline__ float logit_of(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
-struct Shared {
+struct alignas(16) Shared {
   uint32_t hist[3][kBins];   // counts, or the sums of the weights' 13-bit parts, then 64-bit sums over the first two
   uint32_t list_key[kList];  // of the first CTA: the largest logits, by id
   int list_id[kList];
@@ -111,6 +111,7 @@ struct Team {
   bool alone;       // it does, with the list: its keys and their ids
   const float* row; // before that, the slice's logits, whose ids are begin, begin + 1, ..
   int begin;
+  int shift;        // and how far into the memory after the struct their keys begin
   int warp, lane;
   unsigned phase;
   int i0, i1;            // this thread's keys
@@ -122,8 +123,8 @@ struct Team {
   }
   // Keys in shared memory: of the slice after the struct, or the list's.
   __device__ __forceinline__ uint32_t cached(int i) const {
-    const int first = alone ? (int)offsetof(Shared, list_key) : (int)sizeof(Shared);
-    return reinterpret_cast<const uint32_t*>(&s)[first / 4 + i];
+    const int first = alone ? (int)offsetof(Shared, list_key) / 4 : (int)sizeof(Shared) / 4 + shift;
+    return reinterpret_cast<const uint32_t*>(&s)[first + i];
   }
   __device__ __forceinline__ uint32_t key(int i) const { return kCached || alone ? cached(i) : key_of(row[i]); }
   // f(i, keys i .. i + 3) for this thread's keys, four at a time so that their
@@ -423,7 +424,6 @@ template <bool kCached>
 __global__ void __launch_bounds__(kSampleThreads, kCached ? 1 : 2) sample_kernel(const SampleArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& s = *reinterpret_cast<Shared*>(smem);
-  uint32_t* cache = reinterpret_cast<uint32_t*>(smem + sizeof(Shared));
   const int tid = threadIdx.x;
   cg::cluster_group cluster = cg::this_cluster();
   const int size = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -435,18 +435,40 @@ __global__ void __launch_bounds__(kSampleThreads, kCached ? 1 : 2) sample_kernel
   const int k = a.top_k ? a.top_k[m] : 0;
   const int begin = min(rank * a.slice, a.vocab), n = min(a.slice, a.vocab - begin);
   const float* row = a.logits + m * a.row_stride + begin;
-  Team<kCached> c{s, cluster, rank, size, false, row, begin, tid >> 5, tid & 31, 0, 0, 0};
+  const int shift = (int)(reinterpret_cast<uintptr_t>(row) / 4) & 3;  // logits from a 16-byte border on
+  uint32_t* cache = reinterpret_cast<uint32_t*>(smem + sizeof(Shared)) + shift;
+  Team<kCached> c{s, cluster, rank, size, false, row, begin, shift, tid >> 5, tid & 31, 0, 0, 0};
   c.split(n);
 
   // the row's largest logit, the lowest id first
-  u64 best = 0;
-#pragma unroll 8
-  for (int i = tid; i < n; i += kSampleThreads) {
-    const uint32_t key = key_of(row[i]);
+  uint32_t best_key = 0;
+  int best_i = 0;
+  auto take = [&](int i, uint32_t key) {
     if (kCached) cache[i] = key;
-    best = max(best, (u64)key << 32 | (uint32_t)~(begin + i));
+    if (key > best_key) best_key = key, best_i = i;
+  };
+  // four at a time from the first one at a 16-byte border
+  const int head = min(n, -c.shift & 3), fours = (n - head) / 4;
+  if (tid < head) take(tid, key_of(row[tid]));
+  constexpr int kLoads = 8;  // in flight
+  for (int g0 = tid; g0 < fours; g0 += kLoads * kSampleThreads) {
+    float4 v[kLoads];
+#pragma unroll
+    for (int l = 0; l < kLoads; ++l)
+      if (g0 + l * kSampleThreads < fours)
+        v[l] = reinterpret_cast<const float4*>(row + head)[g0 + l * kSampleThreads];
+#pragma unroll
+    for (int l = 0; l < kLoads; ++l) {
+      const int g = g0 + l * kSampleThreads, i = head + 4 * g;
+      if (g >= fours) break;
+      const uint4 key = make_uint4(key_of(v[l].x), key_of(v[l].y), key_of(v[l].z), key_of(v[l].w));
+      if (kCached) reinterpret_cast<uint4*>(cache + head)[g] = key;
+      const uint32_t most = max(max(key.x, key.y), max(key.z, key.w));
+      if (most > best_key) best_key = most, best_i = i + (key.x == most ? 0 : key.y == most ? 1 : key.z == most ? 2 : 3);
+    }
   }
-  best = warp_max(best);
+  if (tid < n - head - 4 * fours) take(head + 4 * fours + tid, key_of(row[head + 4 * fours + tid]));
+  u64 best = warp_max((u64)best_key << 32 | (uint32_t)~(begin + best_i));
   if (c.lane == 0) s.sums[c.warp] = best;
   __syncthreads();
 #pragma unroll
@@ -728,11 +750,11 @@ extern "C" int moe_sample(const float* logits, int64_t row_stride, int rows, int
          (vocab + cluster / 2 - 1) / (cluster / 2) <= kMaxCached)
     cluster /= 2;
   static_assert(MOE_SAMPLE_MAX_VOCAB / kMaxCluster <= kMaxSlice && kMaxCached <= kMaxSlice);
-  static_assert(sizeof(Shared) + kMaxCached * 4 <= 227 * 1024);
+  static_assert(sizeof(Shared) % 16 == 0 && sizeof(Shared) + (kMaxCached + 3) * 4 <= 227 * 1024);
   SampleArgs a{logits, row_stride, vocab, (vocab + cluster - 1) / cluster, u, temperature, top_k, top_p, min_p,
                tokens, probs};
   const bool cached = a.slice <= kMaxCached;
-  const size_t smem = sizeof(Shared) + (cached ? (size_t)a.slice * 4 : 0);
+  const size_t smem = sizeof(Shared) + (cached ? (size_t)(a.slice + 3) * 4 : 0);
   static thread_local int ready = -1;  // device whose kernel attributes this thread has set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -740,7 +762,7 @@ extern "C" int moe_sample(const float* logits, int64_t row_stride, int rows, int
     for (auto kernel : {sample_kernel<true>, sample_kernel<false>}) {
       if (e == cudaSuccess)
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)sizeof(Shared) + kMaxCached * 4);
+                                 (int)sizeof(Shared) + (kMaxCached + 3) * 4);
       if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     }
     if (e == cudaSuccess) ready = dev;
