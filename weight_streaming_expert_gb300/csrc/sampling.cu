@@ -20,7 +20,7 @@
 // and top-p 0.95: 19 us instead of 31; sorting 2048 would take longer than the
 // passes of bins, top-p 0.5 alone 42 us instead of 31).
 //
-// 6 rows of 157184 logits: greedy 4.4 us, unfiltered 8.9 us, top-k 50 16 us,
+// 6 rows of 157184 logits: greedy 3.8 us, unfiltered 8.4 us, top-k 50 16 us,
 // top-k 50 and top-p 0.95 17 us, top-p 0.95 alone (a cut among 20,000 logits)
 // 37 us; the logits' bytes are 0.6 us of that.  The kernel for slices in
 // shared memory may use 128 registers, as only one such CTA fits an SM: at 64
@@ -741,33 +741,48 @@ extern "C" int moe_sample(const float* logits, int64_t row_stride, int rows, int
     return fail(MOE_ERR_INVALID_ARG, "row_stride = %lld is smaller than vocab", (long long)row_stride);
   int rc = check_device();
   if (rc != MOE_OK) return rc;
-  // CTAs of a row: as many as run at once, one per SM, for every exchange costs
-  // each of them the same (16 rows of 157184, top-k: 39 us with 16, 34 us with
-  // 8), but not so few that a slice leaves shared memory (64 rows: 51 us with 4,
-  // in two waves; 68 us with 2, which read the row from L2 in every pass)
-  int cluster = kMaxCluster;
-  while (cluster > 1 && (rows * cluster > 152 || (vocab + cluster - 1) / cluster < kSampleThreads) &&
-         (vocab + cluster / 2 - 1) / (cluster / 2) <= kMaxCached)
-    cluster /= 2;
   static_assert(MOE_SAMPLE_MAX_VOCAB / kMaxCluster <= kMaxSlice && kMaxCached <= kMaxSlice);
   static_assert(sizeof(Shared) % 16 == 0 && sizeof(Shared) + (kMaxCached + 3) * 4 <= 227 * 1024);
-  SampleArgs a{logits, row_stride, vocab, (vocab + cluster - 1) / cluster, u, temperature, top_k, top_p, min_p,
-               tokens, probs};
-  const bool cached = a.slice <= kMaxCached;
-  const size_t smem = sizeof(Shared) + (cached ? (size_t)(a.slice + 3) * 4 : 0);
-  static thread_local int ready = -1;  // device whose kernel attributes this thread has set
+  constexpr int kSmem = (int)sizeof(Shared) + (kMaxCached + 3) * 4;
+  static thread_local int ready = -1;                // device that this thread has set up
+  static thread_local int resident[kMaxCluster + 1];  // clusters of a size that run at once there
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && ready != dev) {
     for (auto kernel : {sample_kernel<true>, sample_kernel<false>}) {
-      if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)sizeof(Shared) + (kMaxCached + 3) * 4);
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
       if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    }
+    for (int size = 2; size <= kMaxCluster && e == cudaSuccess; size *= 2) {
+      cudaLaunchAttribute in_clusters{};
+      in_clusters.id = cudaLaunchAttributeClusterDimension;
+      in_clusters.val.clusterDim.x = size;
+      in_clusters.val.clusterDim.y = in_clusters.val.clusterDim.z = 1;
+      cudaLaunchConfig_t config{};
+      config.gridDim = dim3((unsigned)size);
+      config.blockDim = dim3(kSampleThreads);
+      config.dynamicSmemBytes = kSmem;
+      config.attrs = &in_clusters;
+      config.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&resident[size], sample_kernel<true>, &config);
     }
     if (e == cudaSuccess) ready = dev;
   }
   if (e != cudaSuccess) return fail_cuda(e, "sampling set-up");
+  // CTAs of a row: as many as let all rows run at once, a CTA per SM (7
+  // clusters of 16, 15 of 8, 36 of 4, 76 of 2: the groups of SMs that a cluster
+  // cannot leave are not all whole): 16 rows of 157184, top-k 50: 32 us with 8,
+  // in two waves, 25 us with 4 (top-p 0.95 54 and 65 us).  But not so few that a slice leaves shared memory:
+  // 64 rows 48 us with 4, in two waves, 68 us with 2, which read the row from
+  // L2 in every pass.
+  int cluster = kMaxCluster;
+  while (cluster > 1 && (rows > resident[cluster] || (vocab + cluster - 1) / cluster < kSampleThreads) &&
+         (vocab + cluster / 2 - 1) / (cluster / 2) <= kMaxCached)
+    cluster /= 2;
+  SampleArgs a{logits, row_stride, vocab, (vocab + cluster - 1) / cluster, u, temperature, top_k, top_p, min_p,
+               tokens, probs};
+  const bool cached = a.slice <= kMaxCached;
+  const size_t smem = sizeof(Shared) + (cached ? (size_t)(a.slice + 3) * 4 : 0);
   return launch_pdl(cached ? sample_kernel<true> : sample_kernel<false>, dim3((unsigned)(rows * cluster)),
                     dim3(kSampleThreads), smem, stream, cluster, a);
 }
