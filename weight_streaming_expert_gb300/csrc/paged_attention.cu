@@ -33,7 +33,7 @@
 // the queries of the next tile.
 //
 // The work is a list of (sequence, key/value head, tile of rows, 128
-// positions) in that order.  Every CTA takes an equal contiguous share of it,
+// positions) in that order.  Every CTA takes a contiguous share of equal cost,
 // computed on the device from the lengths that the call finds there: one long
 // sequence spreads over all SMs, many short ones share an SM, and a captured
 // graph adapts to lengths that change.  A tile that a boundary cuts leaves
@@ -48,7 +48,7 @@
 //   long decoding    reading the cache: 32 sequences of 2,000 to 32,768
 //                    positions, one token each: 131 us, 6.3 TB/s.
 //   short calls      latencies: the plan, the first pages, one softmax, the
-//                    join: 6 tokens over 8192: 14 us, of which memory needs 2.5.
+//                    join: 6 tokens over 8192: 13 us, of which memory needs 2.5.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -174,6 +174,14 @@ __device__ __forceinline__ X uniform(X v) {
   return __shfl_sync(0xffffffffu, v, 0);
 }
 
+// What an item costs besides its units, in units: its queries, the first scores
+// and the last sums, which nothing overlaps.  In the pair form as much as two
+// units: ragged chunks of 900 to 1500 tokens over 1500 to 6000 take 145 us with
+// 0, 124 with 1, 119 with 2, 120 with 3.  In the split form, whose copies run
+// ahead, nothing to speak of (decode batch 130 us with 0 and 131 with 1 or 2).
+template <int kTiles>
+constexpr int kItemCost = kTiles == 2 ? 2 : 0;
+
 // A CTA's next piece of work.
 struct Item {
   int b, h, tile, u0, u1, units;
@@ -184,20 +192,20 @@ struct Item {
 // the same one, each for a head of its own: what they read of a position lies
 // side by side in memory and is read at about the same time.
 struct Plan {
-  int start, todo;     // where this CTA's share begins, and its length
+  int start, todo;     // where this CTA's share begins, and its length, in units of cost
   int share;           // of every CTA but the last
-  int b, h, tile, u0;  // h counts groups of `spread` heads
+  int b, h, tile, at;  // h counts groups of `spread` heads; what of the item others have done
   Seq s;               // sequence b
 };
 
 template <int kTiles>
 struct Walk {
   const AttnParams& p;
-  int b, h, tile, u0, todo;
+  int b, h, tile, at, todo;
   Seq s;
   int loaded;
   __device__ Walk(const AttnParams& p_, const Plan& plan)
-      : p(p_), b(plan.b), h(plan.h), tile(plan.tile), u0(plan.u0), todo(plan.todo), s(plan.s), loaded(plan.b) {}
+      : p(p_), b(plan.b), h(plan.h), tile(plan.tile), at(plan.at), todo(plan.todo), s(plan.s), loaded(plan.b) {}
   __device__ bool next(Item& it) {
     if (todo <= 0) return false;
     for (;;) {
@@ -213,12 +221,13 @@ struct Walk {
     }
     it.b = b, it.h = h * p.spread + (int)blockIdx.x % p.spread, it.tile = tile, it.s = s;
     it.units = units_of<kTiles>(p, s, tile);
-    it.u0 = u0;
-    it.u1 = min(it.units, u0 + todo);
-    todo -= it.u1 - it.u0;
-    u0 = 0;
+    const int to = min(it.units + kItemCost<kTiles>, at + todo);
+    todo -= to - at;
+    it.u0 = max(0, at - kItemCost<kTiles>);
+    it.u1 = max(0, to - kItemCost<kTiles>);
+    at = 0;
     ++tile;
-    return true;
+    return it.u1 > 0;  // a share that ends before the item's first unit leaves it to the next
   }
 };
 
@@ -260,13 +269,13 @@ __device__ __forceinline__ Plan make_plan(const AttnParams& p, int per, int sum,
   plan.h = (unsigned)rest / (unsigned)own;
   rest -= plan.h * own;
   for (int tile = lane;; tile += 32) {  // 32 items at a time
-    const int u = tile * kTiles * p.tokens < plan.s.n ? units_of<kTiles>(p, plan.s, tile) : 0;
+    const int u = tile * kTiles * p.tokens < plan.s.n ? units_of<kTiles>(p, plan.s, tile) + kItemCost<kTiles> : 0;
     const int to = scan_up(u);
     const unsigned past = __ballot_sync(0xffffffffu, to > rest);
     if (past) {
       const int first = __ffs(past) - 1;
       plan.tile = __shfl_sync(0xffffffffu, tile, first);
-      plan.u0 = rest - __shfl_sync(0xffffffffu, to - u, first);
+      plan.at = rest - __shfl_sync(0xffffffffu, to - u, first);
       return plan;
     }
     rest -= __shfl_sync(0xffffffffu, to, 31);
@@ -380,7 +389,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (lane < a.batch) {
       const Seq s = load_seq(p, lane);
       if (s.bad && blockIdx.x == 0) atomicOr(p.status, kAttnBadLength);
-      for (int i = 0; i * kTiles * p.tokens < s.n; ++i) sum += units_of<kTiles>(p, s, i);
+      for (int i = 0; i * kTiles * p.tokens < s.n; ++i) sum += units_of<kTiles>(p, s, i) + kItemCost<kTiles>;
     }
     plan = make_plan<kTiles>(p, 1, sum, [&](int) { return sum; });
   } else {
@@ -389,7 +398,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const Seq s = load_seq(p, b);
       if (s.bad && blockIdx.x == 0) atomicOr(p.status, kAttnBadLength);
       int sum = 0;
-      for (int i = wide ? lane : 0; i * kTiles * p.tokens < s.n; i += wide ? 32 : 1) sum += units_of<kTiles>(p, s, i);
+      for (int i = wide ? lane : 0; i * kTiles * p.tokens < s.n; i += wide ? 32 : 1)
+        sum += units_of<kTiles>(p, s, i) + kItemCost<kTiles>;
       if (wide) {
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
@@ -879,7 +889,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // Cuts by item are few and wait for nothing but these reads, so a thread may
 // have many under way (128 registers: 13.3 us for 6 tokens over 8192, with 64
 // registers 14.4) as long as all blocks run at once; of the blocks by CTA two
-// or more share an SM (ragged chunks: 143 us, with 128 registers 152).
+// or more share an SM (ragged chunks: 9 us less than with 128 registers).
 template <typename T, int D, int kRows, bool kByItem>
 __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4, kByItem ? 128 / D * 2 - 1 : 256 / D)
     join_kernel(const __grid_constant__ AttnParams p) {

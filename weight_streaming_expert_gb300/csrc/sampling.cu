@@ -464,7 +464,8 @@ __global__ void __launch_bounds__(kSampleThreads, kCached ? 1 : 2) sample_kernel
       const uint4 key = make_uint4(key_of(v[l].x), key_of(v[l].y), key_of(v[l].z), key_of(v[l].w));
       if (kCached) reinterpret_cast<uint4*>(cache + head)[g] = key;
       const uint32_t most = max(max(key.x, key.y), max(key.z, key.w));
-      if (most > best_key) best_key = most, best_i = i + (key.x == most ? 0 : key.y == most ? 1 : key.z == most ? 2 : 3);
+      if (most > best_key)
+        best_key = most, best_i = i + (key.x == most ? 0 : key.y == most ? 1 : key.z == most ? 2 : 3);
     }
   }
   if (tid < n - head - 4 * fours) take(head + 4 * fours + tid, key_of(row[head + 4 * fours + tid]));
