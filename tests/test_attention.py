@@ -334,6 +334,18 @@ def test_many_sequences(batch, q_len):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("batch", [1, 2, 7, 23, 61, 90])
+def test_shares_that_end_anywhere_in_an_item(batch):
+    """Items of one to some units, so that the CTAs' shares end before, at and
+    behind the first unit of one."""
+    g = torch.Generator().manual_seed(batch)
+    draw = lambda lo, hi: int(torch.randint(lo, hi, (1,), generator=g))
+    q_lens = [draw(20, 260) for _ in range(batch)]
+    q_lens[0] = 259
+    run(chain(q_lens, [m + draw(-10, 600) for m in q_lens], 4, 2, 64, 32, "fp16", batch))
+
+
+@pytest.mark.gpu
 def test_one_handle_over_calls_of_every_kind():
     """What a call leaves in the handle's workspace is not another's."""
     from weight_streaming_expert_gb300 import PagedAttention
