@@ -22,7 +22,7 @@
 //
 // 6 rows of 157184 logits: greedy 3.8 us, unfiltered 8.4 us, top-k 50 16 us,
 // top-k 50 and top-p 0.95 17 us, top-p 0.95 alone (a cut among 20,000 logits)
-// 37 us; the logits' bytes are 0.6 us of that.  The kernel for slices in
+// 34 us; the logits' bytes are 0.6 us of that.  The kernel for slices in
 // shared memory may use 128 registers, as only one such CTA fits an SM: at 64
 // it spills, 19 us instead of 17 for both filters.
 #include <cooperative_groups.h>
@@ -231,10 +231,10 @@ struct Team {
 
   // The smallest key K in [lo, hi] of the row (of non-zero measure) with
   // measure(keys in (K, hi]) < target; `above` is that measure and `at` the
-  // measure of K itself.  0 < target <= measure of the whole range, and hi is
-  // in the row.  With kOnce only as far as the first bin that holds it: lo and
-  // `found` are that bin's smallest and largest possible keys, `above` the
-  // measure above the bin, `at` the bin's.
+  // measure of K itself.  0 < target <= measure of the whole range.  With kOnce
+  // only as far as the first bin that holds it: lo and `found` are that bin's
+  // smallest and largest possible keys, `above` the measure above the bin, `at`
+  // the bin's.
   // kParts: words of a bin, 1 for counts and 3 for weights (a 64-bit add in
   // shared memory is a loop of compare-and-swap, three 32-bit adds are not).
   template <int kParts, int kBits, bool kOnce, typename Measure>
@@ -571,17 +571,19 @@ __global__ void __launch_bounds__(kSampleThreads, kCached ? 1 : 2) sample_kernel
     c.team_scan(mass_from(0, 0.f, kAllTies), total);
     target = share_of(total);
   }
+  // the first cut is in [cut_lo, cut_hi], with `before_cut` above
+  uint32_t cut_lo = 0, cut_hi = top_key;
+  u64 before_cut = 0;
   if (by_count ? k <= kList : by_mass) {
-    // the keys from `bar` on, down to the bin that the first cut falls into,
-    // and how many of them this thread has
-    uint32_t bar = 0, bin_top;
+    // the keys down to the bin that the first cut falls into, and how many of
+    // them this thread has
     if (a.vocab > kList) {
       if (by_count)
-        c.template select<1, kBarBits, true>(bar, top_key, (u64)k, Ones{}, bin_top, above, at);
+        c.template select<1, kBarBits, true>(cut_lo, top_key, (u64)k, Ones{}, cut_hi, before_cut, at);
       else
-        c.template select<3, kBarBits, true>(bar, top_key, target, weights, bin_top, above, at);
+        c.template select<3, kBarBits, true>(cut_lo, top_key, target, weights, cut_hi, before_cut, at);
     }
-    bar = max(bar, 1u);  // 0 is no key
+    const uint32_t bar = max(cut_lo, 1u);  // 0 is no key
     u64 count = 0;
     c.each4([&](int, const uint32_t (&key)[4]) {
 #pragma unroll
@@ -637,18 +639,19 @@ __global__ void __launch_bounds__(kSampleThreads, kCached ? 1 : 2) sample_kernel
   int tie_end = kAllTies;
   u64 ties = 0, same = 0;  // how many of the `same` tokens of key thr stay
   if (by_count && !sorted) {
-    uint32_t lo = 0;
-    c.template select<1, kBinBits, false>(lo, top_key, (u64)k, Ones{}, thr, above, at);
-    ties = (u64)k - above;  // at most `at`: k is reached there
+    c.template select<1, kBinBits, false>(cut_lo, cut_hi, (u64)k - before_cut, Ones{}, thr, above, at);
+    ties = (u64)k - before_cut - above;  // at most `at`: k is reached there
     same = at;
   }
   if (by_mass && !sorted) {
     if (by_count) {
       c.team_scan(mass_from(thr + 1, 0.f, kAllTies), total);
       target = share_of(total + ties * weight(thr));
+      cut_lo = thr, cut_hi = top_key, before_cut = 0;
     }
-    uint32_t key, lo = same ? thr : 0;
-    c.template select<3, kBinBits, false>(lo, top_key, target, weights, key, above, at);
+    uint32_t key;
+    target -= before_cut;
+    c.template select<3, kBinBits, false>(cut_lo, cut_hi, target, weights, key, above, at);
     const u64 w = weight(key);
     if (at == w) {
       ties = same = 1;
@@ -773,7 +776,7 @@ extern "C" int moe_sample(const float* logits, int64_t row_stride, int rows, int
   // CTAs of a row: as many as let all rows run at once, a CTA per SM (7
   // clusters of 16, 15 of 8, 36 of 4, 76 of 2: the groups of SMs that a cluster
   // cannot leave are not all whole): 16 rows of 157184, top-k 50: 32 us with 8,
-  // in two waves, 25 us with 4 (top-p 0.95 54 and 65 us).  But not so few that a slice leaves shared memory:
+  // in two waves, 25 us with 4 (top-p 0.95 54 and 56 us).  But not so few that a slice leaves shared memory:
   // 64 rows 48 us with 4, in two waves, 68 us with 2, which read the row from
   // L2 in every pass.
   int cluster = kMaxCluster;
