@@ -12,7 +12,7 @@
 // A row belongs to one thread-block cluster: its CTAs take contiguous slices
 // of the vocabulary, hold them in shared memory, and exchange maxima, bins and
 // sums through distributed shared memory.  The row is read from memory once;
-// what remains is the latency of the exchanges (one takes 1-3 us).  So where a
+// what remains is the latency of the exchanges (one takes about 1 us).  So where a
 // filter cuts among the 2048 largest logits, as it mostly does, one pass of
 // bins finds those down to the cut, the CTAs hand them to the first one in the
 // order of their ids, and it goes on alone.  Up to 512 of them it sorts, which
@@ -20,7 +20,7 @@
 // and top-p 0.95: 19 us instead of 31; sorting 2048 would take longer than the
 // passes of bins, top-p 0.5 alone 42 us instead of 31).
 //
-// 6 rows of 157184 logits: greedy 3.8 us, unfiltered 8.4 us, top-k 50 16 us,
+// 6 rows of 157184 logits: greedy 3.3 us, unfiltered 8.0 us, top-k 50 16 us,
 // top-k 50 and top-p 0.95 17 us, top-p 0.95 alone (a cut among 20,000 logits)
 // 34 us; the logits' bytes are 0.6 us of that.  The kernel for slices in
 // shared memory may use 128 registers, as only one such CTA fits an SM: at 64
@@ -82,8 +82,7 @@ struct alignas(16) Shared {
   uint32_t list_key[kList];  // of the first CTA: the largest logits, by id
   int list_id[kList];
   u64 sums[kSampleWarps];    // of this CTA's warps
-  u64 scan[2][3];            // read by the other CTAs: the CTA's values of an exchange, alternating
-  u64 result[6];             // of an exchange, for this CTA's threads
+  u64 scan[2][kMaxCluster];  // written by the other CTAs: their values of an exchange, alternating
   u64 found[3];              // written by the CTA that found it: a pass's bin, the measure before it, its own
   u64 shared[2];             // of this CTA: what one thread computes for the others
   int tie_end;               // written by the CTA that found it
@@ -99,6 +98,9 @@ __device__ __forceinline__ u64 warp_max(u64 v) {
   for (int m = 16; m > 0; m >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, m));
   return v;
 }
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 
 // The CTAs that work on a row, and this one's part of it: n keys, of which each
 // thread has `run` in a row (an odd number: consecutive threads then read
@@ -179,54 +181,27 @@ struct Team {
   }
   // The same over the team.
   __device__ u64 team_scan(u64 v, u64& total) {
-    u64 mine, below;
+    u64 mine;
     const u64 before = cta_scan(v, mine);
-    exchange(mine, below, total);
-    return below + before;
-  }
-  // Over the team: the sums of the CTAs' values before this one, and of all.
-  // One warp reads the others' memory (a read there is slow, and its
-  // bandwidth too small for every warp to do it).  Two slots in turn: a slot
-  // is written again only after another exchange, which every CTA enters
-  // after it has read this one.
-  template <int kValues>
-  __device__ void exchange(const u64 (&mine)[kValues], u64 (&below)[kValues], u64 (&total)[kValues]) {
     if (size == 1) {
-      for (int q = 0; q < kValues; ++q) below[q] = 0, total[q] = mine[q];
-      return;
+      total = mine;
+      return before;
     }
-    phase ^= 1;
-    if (threadIdx.x == 0)
-      for (int q = 0; q < kValues; ++q) s.scan[phase][q] = mine[q];
-    cluster.sync();
-    if (warp == 0) {
-#pragma unroll
-      for (int q = 0; q < kValues; ++q) {
-        const u64 v = lane < size ? *cluster.map_shared_rank(&s.scan[phase][q], lane) : 0;
-        const u64 b = warp_sum(lane < rank ? v : 0), t = warp_sum(v);
-        if (lane == 0) s.result[q] = b, s.result[3 + q] = t;
-      }
-    }
-    __syncthreads();
-    for (int q = 0; q < kValues; ++q) below[q] = s.result[q], total[q] = s.result[3 + q];
+    const u64 other = exchange(mine);
+    total = warp_sum(other);
+    return warp_sum(lane < rank ? other : 0) + before;
   }
-  __device__ void exchange(u64 mine, u64& below, u64& total) {
-    u64 b[1], t[1];
-    exchange<1>({mine}, b, t);
-    below = b[0];
-    total = t[0];
-  }
-  __device__ u64 team_max(u64 mine) {
-    if (size == 1) return mine;
+  __device__ u64 team_max(u64 mine) { return size == 1 ? mine : warp_max(exchange(mine)); }
+  // Each CTA's value, the same for all of its threads, to every other: lane r
+  // gets CTA r's, 0 past the last.  The values are written into the others'
+  // memory, which nobody waits for, instead of read out of it, which takes
+  // about half a microsecond.  Two slots in turn: a slot is written again only
+  // after another exchange, which every CTA enters after it has read this one.
+  __device__ u64 exchange(u64 mine) {
     phase ^= 1;
-    if (threadIdx.x == 0) s.scan[phase][0] = mine;
+    if (warp == 0 && lane < size) *cluster.map_shared_rank(&s.scan[phase][rank], lane) = mine;
     cluster.sync();
-    if (warp == 0) {
-      const u64 v = warp_max(lane < size ? *cluster.map_shared_rank(&s.scan[phase][0], lane) : 0);
-      if (lane == 0) s.result[0] = v;
-    }
-    __syncthreads();
-    return s.result[0];
+    return lane < size ? s.scan[phase][lane] : 0;
   }
 
   // The smallest key K in [lo, hi] of the row (of non-zero measure) with
@@ -332,7 +307,6 @@ struct Team {
         above += total;
         hi = from - 1;
         from = lo;
-        sync();  // the sums are read before the next pass writes them
         continue;
       }
       before += above;
@@ -428,6 +402,7 @@ __global__ void __launch_bounds__(kSampleThreads, kCached ? 1 : 2) sample_kernel
   cg::cluster_group cluster = cg::this_cluster();
   const int size = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const long long m = blockIdx.x / size;
+  cluster_arrive();
   pdl_wait();
   pdl_launch_dependents();
   const float t = a.temperature ? a.temperature[m] : 1.f, p = a.top_p ? a.top_p[m] : 1.f;
@@ -474,6 +449,7 @@ __global__ void __launch_bounds__(kSampleThreads, kCached ? 1 : 2) sample_kernel
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kSampleWarps; ++w) best = max(best, s.sums[w]);
+  cluster_wait();  // every CTA of the cluster has begun, before the first writes into another's memory
   best = c.team_max(best);
   const uint32_t top_key = (uint32_t)(best >> 32);
   const float top = logit_of(top_key);
@@ -482,7 +458,6 @@ __global__ void __launch_bounds__(kSampleThreads, kCached ? 1 : 2) sample_kernel
       a.tokens[m] = top_key <= kKeyNegInf ? -1 : (int)~(uint32_t)best;
       if (a.probs) a.probs[m] = top_key <= kKeyNegInf ? 0.f : 1.f;
     }
-    c.sync();  // the others may still read this CTA's maximum
     return;
   }
   // d / t, correctly rounded like the operator: a quotient off by at most one
@@ -722,7 +697,7 @@ __global__ void __launch_bounds__(kSampleThreads, kCached ? 1 : 2) sample_kernel
       before += __shfl_sync(0xffffffffu, upto, 31);
     }
   }
-  c.sync();  // no CTA leaves while another may read its sums
+  // whoever leaves has passed a barrier after all that others do in its memory
 }
 
 }  // namespace
