@@ -454,3 +454,18 @@ def test_python_refusals():
         for v in values:
             with pytest.raises(ValueError):
                 attn(**{**x, name: v})
+
+
+@pytest.mark.gpu
+def test_a_closed_handle_is_refused():
+    from weight_streaming_expert_gb300 import PagedAttention
+    from weight_streaming_expert_gb300.native import MoEError
+    c = Case([2], [40], 4, 2, 64, 16)
+    attn = PagedAttention(4, 2, 64, device=DEV)
+    attn(**c.inputs())
+    torch.cuda.synchronize()
+    attn.close()
+    attn.close()
+    with pytest.raises(MoEError):
+        attn(**c.inputs())
+    assert attn.status() != 0

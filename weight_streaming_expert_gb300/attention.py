@@ -168,7 +168,8 @@ class PagedAttention:
         _heads("q", q, dt, index, D)
         for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
             _cache(name, t, dt, index, self.n_kv_heads, D)
-        if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.get_device() != index or block_table.stride(1) != 1:
+        if (block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.get_device() != index
+                or block_table.stride(1) != 1):
             raise ValueError(f"block_table must be an int32 tensor [batch, pages] with contiguous rows on cuda:{index}")
         B = block_table.shape[0]
         _plain("q_starts", q_starts, torch.int32, index, B + 1)
@@ -188,7 +189,7 @@ class PagedAttention:
     def close(self):
         if getattr(self, "_h", None):
             N.lib().moe_attn_destroy(self._h)
-            self._h = None
+            self._h, self._handle = None, 0
 
     def __del__(self):
         try:

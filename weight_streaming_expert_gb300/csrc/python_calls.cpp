@@ -11,6 +11,7 @@
 // PyTorch is used for the tensors' metadata and memory only.
 #include <ATen/ATen.h>
 #include <Python.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "attention.h"
@@ -129,7 +130,8 @@ PyObject* attention(Args x) {
   const int64_t T = q.size(0), B = table.size(0);
   if (dtype_of(q) < 0 || !heads(q, type, T, Hq, dim, gpu) || !cache(k_cache, type, Hk, dim, gpu) ||
       !cache(v_cache, type, Hk, dim, gpu) || !k_cache.sizes().equals(v_cache.sizes()) ||
-      table.scalar_type() != at::kInt || !on(table, gpu) || table.stride(1) != 1 || !plain(starts, at::kInt, B + 1, gpu) ||
+      table.scalar_type() != at::kInt || !on(table, gpu) || table.stride(1) != 1 ||
+      !plain(starts, at::kInt, B + 1, gpu) ||
       !plain(kv_lens, at::kInt, B, gpu) || (tree.defined() && !plain(tree, at::kLong, T, gpu)) ||
       (out.defined() && !heads(out, type, T, Hq, dim, gpu)) || !fits_int(T) || !fits_int(B) || !fits_int(max_q) ||
       !fits_int(k_cache.size(0)) || !fits_int(k_cache.size(1)) || !fits_int(table.stride(0)))
@@ -166,8 +168,8 @@ PyObject* copy(Args x) {
     if (t->stride(2) != row || t->stride(3) != k.size(4) || t->stride(4) != 1) return number(kDoesNotFit);
   const auto s = reinterpret_cast<moe_stream_t>(stream);
   const int status =
-      rows ? moe_copy_rows(k.data_ptr(), v.data_ptr(), (int)k.size(0), k.stride(0) * e, v.stride(0) * e, k.stride(1) * e,
-                           v.stride(1) * e, (int)k.size(1), (int)k.size(2), row * e, ptr<int64_t>(src),
+      rows ? moe_copy_rows(k.data_ptr(), v.data_ptr(), (int)k.size(0), k.stride(0) * e, v.stride(0) * e,
+                           k.stride(1) * e, v.stride(1) * e, (int)k.size(1), (int)k.size(2), row * e, ptr<int64_t>(src),
                            ptr<int64_t>(dst), (int)n, s)
            : moe_copy_pages(k.data_ptr(), v.data_ptr(), (int)k.size(0), k.stride(0) * e, v.stride(0) * e,
                             k.stride(1) * e, v.stride(1) * e, (int)k.size(1), k.size(2) * row * e, ptr<int32_t>(src),
@@ -200,15 +202,13 @@ PyObject* sample(Args x) {
   return l ? Py_BuildValue("(NN)", o, l) : (Py_DECREF(o), nullptr);
 }
 
-// C++ exceptions (of an allocation, say) become Python's.
+// C++ exceptions (of an allocation, say) become the Python ones that PyTorch's
+// own calls raise.
 template <PyObject* (*kCall)(Args)>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  try {
-    return kCall(Args{args, n});
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-    return nullptr;
-  }
+  HANDLE_TH_ERRORS
+  return kCall(Args{args, n});
+  END_HANDLE_TH_ERRORS
 }
 
 template <PyObject* (*kCall)(Args)>
