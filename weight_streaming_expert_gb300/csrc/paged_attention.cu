@@ -282,6 +282,11 @@ __device__ __forceinline__ Plan make_plan(const AttnParams& p, int per, int sum,
   }
 }
 
+// Whether a row has seen nothing where these are its largest score and its sum.
+// A row whose scores are all NaN has no largest one either, but its sum is NaN,
+// which has to show.
+__device__ __forceinline__ bool nothing_seen(float2 ml) { return ml.x == -INFINITY && ml.y == 0.f; }
+
 // The n lowest bits of a word (none below 0, all from 32 on).
 __device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
 
@@ -542,6 +547,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int slot = 2 * blockIdx.x + (it.u0 == 0 ? 1 : 0);
       const int local = kPair ? chain * kTile + r : r;  // row of the item
       float f0 = 1.f, f1 = 0.f;
+      bool seen0 = true, seen1 = true;
       if (!kPair) {
         // each chain's warps then write half of the columns
         exchange[chain * kTile + r] = make_float2(m, l);
@@ -549,6 +555,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const float2 even = exchange[r], odd = exchange[kTile + r];
         named_sync(1, 256);  // before it is written over
         m = fmaxf(even.x, odd.x);
+        seen0 = !nothing_seen(even), seen1 = !nothing_seen(odd);
         f0 = even.x == -INFINITY ? 0.f : exp2_approx((even.x - m) * c);
         f1 = odd.x == -INFINITY ? 0.f : exp2_approx((odd.x - m) * c);
         l = even.y * f0 + odd.y * f1;
@@ -597,8 +604,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             tmem_wait_ld();
 #pragma unroll
             for (int k = 0; k < 32; ++k)
-              o[k] = __float_as_uint((f0 != 0.f ? __uint_as_float(o[k]) * f0 : 0.f) +
-                                     (f1 != 0.f ? __uint_as_float(o1[k]) * f1 : 0.f));
+              o[k] = __float_as_uint((seen0 ? __uint_as_float(o[k]) * f0 : 0.f) +
+                                     (seen1 ? __uint_as_float(o1[k]) * f1 : 0.f));
           }
           if (cut) {
 #pragma unroll
@@ -923,6 +930,7 @@ __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4, kByItem ? 128
     if (a.lse && column == 0) a.lse[(long long)(s.q0 + token) * (p.group * p.n_kv_heads) + head] = lse;
   };
   auto slot = [&](int i) { return 2ll * (cut.c + i * p.spread) + (i == 0 ? 1 : 0); };
+  auto factor_of = [&](float part_m, float m) { return part_m == -INFINITY ? 0.f : exp2_approx((part_m - m) * c); };
   // Few parts (tiles of long chunks, cut once or twice): a thread reads all of
   // its column's at once.
   if (cut.parts <= kFewParts) {
@@ -946,8 +954,8 @@ __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4, kByItem ? 128
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < kFewParts; ++i) {
-        if (ml[i].x == -INFINITY) continue;  // a part in which the row sees nothing, or none
-        const float f = exp2_approx((ml[i].x - m) * c);
+        if (nothing_seen(ml[i])) continue;
+        const float f = factor_of(ml[i].x, m);
         l = fmaf(ml[i].y, f, l);
         o.x = fmaf(v[i].x, f, o.x);
         o.y = fmaf(v[i].y, f, o.y);
@@ -981,8 +989,8 @@ __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4, kByItem ? 128
       for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
       for (int i = lane; i < cut.parts; i += 32) {
         const float2 ml = p.part_ml[slot(i) * kRows + r0 + warp];
-        const float f = ml.x == -INFINITY ? 0.f : exp2_approx((ml.x - m) * c);
-        factor[warp][i] = f;
+        const float f = factor_of(ml.x, m);
+        factor[warp][i] = nothing_seen(ml) ? -1.f : f;
         l += ml.y * f;
       }
 #pragma unroll
@@ -996,7 +1004,7 @@ __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4, kByItem ? 128
     if (mine) {
       auto add = [&](int i, float4 v) {
         const float f = factor[row][i];
-        if (f == 0.f) return;
+        if (f < 0.f) return;
         o.x = fmaf(v.x, f, o.x);
         o.y = fmaf(v.y, f, o.y);
         o.z = fmaf(v.z, f, o.z);
