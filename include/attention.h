@@ -100,14 +100,16 @@ typedef struct {
   const void* v_cache;
   int64_t k_page_stride, k_row_stride, v_page_stride, v_row_stride; /* elements */
   int n_pages, page_size;  /* page_size: 16, 32, 64, 128 or 256 */
-  const int32_t* block_table; /* device [batch][table_stride]; entries past a sequence's pages are not read */
-  int table_stride;        /* pages a row of the table holds */
+  const int32_t* block_table; /* device, row b at block_table + b*table_stride; entries past a sequence's pages are not
+                              read.  May be NULL where a row holds no pages */
+  int table_stride;        /* from one row to the next; 0: the sequences share one row */
   const int32_t* q_starts; /* device [batch+1], ascending */
   const int32_t* kv_lens;  /* device [batch] */
   const int64_t* tree_mask;/* device [n_tokens] or NULL */
   void* out;
   int64_t out_token_stride, out_head_stride;
   float* lse;              /* NULL, or device [n_tokens][n_heads]: natural log of the sum of exp(scale q.k) */
+  int table_pages;         /* pages a row of the table holds; 0: table_stride of them */
 } moe_attn_args_t;
 
 /*

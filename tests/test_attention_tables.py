@@ -1,0 +1,79 @@
+"""Block tables and lengths of other shapes than a full, contiguous table with
+ascending starts: a table that sequences share, a view of a wider one, starts
+that make no sense."""
+import math
+
+import pytest
+import torch
+
+from tests.test_attention import DEV, Case, args
+
+INT_MIN = -2 ** 31
+
+
+def outputs(c, attn=None, **change):
+    from weight_streaming_expert_gb300 import PagedAttention
+    attn = attn or PagedAttention(c.Hq, c.Hk, c.D, device=DEV)
+    return attn(return_lse=True, **{**c.inputs(), **change})
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("q_lens,n", [([1, 1, 1], 300), ([4, 2], 700), ([90, 40], 95)])
+def test_a_table_that_all_sequences_share(q_lens, n):
+    from weight_streaming_expert_gb300 import PagedAttention
+    c = Case(q_lens, [n] * len(q_lens), 8, 2, 128, 16, seed=n)
+    attn = PagedAttention(8, 2, 128, device=DEV)
+    one = c.inputs()["block_table"][:1]
+    copied = one.repeat(len(q_lens), 1)
+    out, lse = outputs(c, attn, block_table=copied)
+    assert attn.status() == 0 and lse.isfinite().all()
+    got, got_lse = outputs(c, attn, block_table=one.expand(len(q_lens), -1))
+    assert attn.status() == 0
+    assert torch.equal(got, out) and torch.equal(got_lse, lse)
+
+
+@pytest.mark.gpu
+def test_a_length_past_the_width_of_a_view():
+    """It is cut and reported; what lies beside the view is not read."""
+    from weight_streaming_expert_gb300 import PagedAttention
+    from weight_streaming_expert_gb300 import native as N
+    c = Case([2, 3], [64, 64], 4, 2, 64, 16, "fp16", seed=1)
+    attn = PagedAttention(4, 2, 64, device=DEV)
+    x = c.inputs()
+    wide = torch.full((2, 11), 1 << 30, dtype=torch.int32, device=DEV)  # no pages of this cache
+    wide[:, 3:7] = x["block_table"]
+    out, lse = outputs(c, attn, block_table=wide[:, 3:7])
+    assert attn.status() == 0 and torch.equal(out, outputs(c, attn)[0])
+    for lens in ([64, 65], [80, 64], [64, 1 << 30]):
+        kv_lens = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        got, _ = outputs(c, attn, block_table=wide[:, 3:7], kv_lens=kv_lens)
+        assert attn.status() == N.MOE_ERR_INVALID_ARG
+        assert "length" in N.last_error() and "page" not in N.last_error()
+        assert got.isfinite().all()
+
+
+@pytest.mark.gpu
+def test_a_table_without_columns():
+    from weight_streaming_expert_gb300 import PagedAttention
+    from weight_streaming_expert_gb300 import native as N
+    c = Case([2, 1], [0, 0], 4, 2, 64, 16, seed=2)
+    attn = PagedAttention(4, 2, 64, device=DEV)
+    for B in (1, 2):
+        i = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)
+        empty = torch.zeros(B, 0, dtype=torch.int32, device=DEV)
+        starts = i(0, 3) if B == 1 else i(0, 2, 3)
+        out, lse = outputs(c, attn, block_table=empty, q_starts=starts, kv_lens=i(*[0] * B), max_q_len=3)
+        assert attn.status() == 0 and (out == 0).all() and (lse == -math.inf).all()
+        outputs(c, attn, block_table=empty, q_starts=starts, kv_lens=i(*[9] * B), max_q_len=3)
+        assert attn.status() == N.MOE_ERR_INVALID_ARG
+
+
+def test_refusals_of_tables():
+    import ctypes
+
+    from weight_streaming_expert_gb300 import native as N
+    fake = ctypes.cast(ctypes.create_string_buffer(4096), ctypes.c_void_p)
+    call = lambda **k: N.lib().moe_attn_forward(fake, ctypes.byref(args(**k)), None)
+    assert call(table_pages=-1) == N.MOE_ERR_INVALID_ARG and "table_pages" in N.last_error()
+    assert call(table_stride=-1) == N.MOE_ERR_INVALID_ARG and "table_stride" in N.last_error()
+    assert call(table_pages=1, block_table=None) == N.MOE_ERR_INVALID_ARG and "block_table" in N.last_error()

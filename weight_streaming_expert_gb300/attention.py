@@ -139,8 +139,9 @@ class PagedAttention:
     def forward(self, q, k_cache, v_cache, block_table, q_starts, kv_lens, max_q_len: int, scale: float | None = None,
                 tree_mask=None, out=None, return_lse: bool = False, stream=None):
         """q [T, Hq, D]; caches [pages, page_size, Hk, D]; block_table int32
-        [B, pages of a row]; q_starts int32 [B + 1]; kv_lens int32 [B] (the new
-        tokens included); max_q_len: at least the longest chunk; scale: default
+        [B, pages of a row] (a view of a wider table, or one row expanded, is
+        fine); q_starts int32 [B + 1]; kv_lens int32 [B] (the new tokens
+        included); max_q_len: at least the longest chunk; scale: default
         D ** -0.5; tree_mask: int64 [T], bit j of a token's word set where it
         sees its chunk's token j, instead of the chain (chunks up to 64).
         Returns out [T, Hq, D], with ``return_lse`` also fp32 [T, Hq]."""

@@ -148,7 +148,7 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
   const moe_attn_args_t& a = p.a;
   Seq s;
   const int q0 = a.q_starts[b], q1 = a.q_starts[b + 1], kv = a.kv_lens[b];
-  const long long room = min(1ll << 30, (long long)a.table_stride * a.page_size);
+  const long long room = min(1ll << 30, (long long)a.table_pages * a.page_size);
   s.q0 = max(0, min(q0, a.n_tokens));
   s.n = max(0, min(min(q1, a.n_tokens) - s.q0, a.max_q_len));
   s.kv = (int)max(0ll, min((long long)kv, room));
@@ -1226,8 +1226,8 @@ int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t strea
   if (!h || !a) return fail(MOE_ERR_INVALID_ARG, "null handle or arguments");
   if (a->dtype != MOE_DTYPE_BF16 && a->dtype != MOE_DTYPE_FP16)
     return fail(MOE_ERR_INVALID_ARG, "dtype = %d: must be MOE_DTYPE_BF16 or MOE_DTYPE_FP16", a->dtype);
-  if (a->batch < 0 || a->n_tokens < 0 || a->max_q_len < 0 || a->table_stride < 0)
-    return fail(MOE_ERR_INVALID_ARG, "batch, n_tokens, max_q_len and table_stride must be 0 or more");
+  if (a->batch < 0 || a->n_tokens < 0 || a->max_q_len < 0 || a->table_stride < 0 || a->table_pages < 0)
+    return fail(MOE_ERR_INVALID_ARG, "batch, n_tokens, max_q_len, table_stride and table_pages must be 0 or more");
   if (!(a->scale > 0.f) || !(a->scale < INFINITY))
     return fail(MOE_ERR_INVALID_ARG, "scale must be positive and finite");
   if (a->page_size != 16 && a->page_size != 32 && a->page_size != 64 && a->page_size != 128 && a->page_size != 256)
@@ -1239,7 +1239,8 @@ int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t strea
   if (!a->q || !a->k_cache || !a->v_cache || !a->out || !aligned(a->q, 16) || !aligned(a->k_cache, 16) ||
       !aligned(a->v_cache, 16) || !aligned(a->out, 16))
     return fail(MOE_ERR_INVALID_ARG, "q, out and the caches must be non-null and 16-byte aligned");
-  if (!a->block_table || !a->q_starts || !a->kv_lens || !aligned(a->block_table, 4) || !aligned(a->q_starts, 4) ||
+  const int table_pages = a->table_pages > 0 ? a->table_pages : a->table_stride;
+  if ((!a->block_table && table_pages > 0) || !a->q_starts || !a->kv_lens || !aligned(a->block_table, 4) || !aligned(a->q_starts, 4) ||
       !aligned(a->kv_lens, 4) || !aligned(a->tree_mask, 8) || !aligned(a->lse, 4))
     return fail(MOE_ERR_INVALID_ARG, "block_table, q_starts and kv_lens must be non-null, and all aligned");
   if ((a->q_token_stride | a->q_head_stride | a->out_token_stride | a->out_head_stride | a->k_page_stride |
@@ -1249,7 +1250,7 @@ int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t strea
   // units of work, at most: they are counted in 32 bits
   const double units = ((double)a->n_tokens * h->n_heads / (2 * kTile - 2 * h->n_heads / h->n_kv_heads + 2) +
                         (double)a->batch * h->n_kv_heads) *
-                       ((double)a->table_stride * a->page_size / kTile + 1);
+                       ((double)table_pages * a->page_size / kTile + 1);
   if (units > 2e9) return fail(MOE_ERR_UNSUPPORTED, "too much work for one call: split the tokens");
   if (a->batch > kMaxBatch) return fail(MOE_ERR_UNSUPPORTED, "batch = %d exceeds %d", a->batch, kMaxBatch);
   const int group = h->n_heads / h->n_kv_heads, columns = h->n_kv_heads * h->head_dim;
@@ -1270,8 +1271,9 @@ int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t strea
   int spread = 1;
   while (spread < kMaxSpread && h->n_kv_heads % (2 * spread) == 0) spread *= 2;
   const bool one_item = a->max_q_len <= (a->max_q_len > tokens ? 2 : 1) * tokens;
-  const AttnParams p{*a,       h->n_kv_heads, group,      tokens,  spread,
-                     h->status, h->part_o,     h->part_ml, h->cuts, one_item && a->batch * h->n_kv_heads <= h->n_sms};
+  AttnParams p{*a,       h->n_kv_heads, group,      tokens,  spread,
+               h->status, h->part_o,     h->part_ml, h->cuts, one_item && a->batch * h->n_kv_heads <= h->n_sms};
+  p.a.table_pages = table_pages;
   if (a->dtype == MOE_DTYPE_BF16)
     return h->head_dim == 64 ? launch_attn<__nv_bfloat16, 64>(h, p, maps, stream)
                              : launch_attn<__nv_bfloat16, 128>(h, p, maps, stream);

@@ -128,22 +128,24 @@ PyObject* attention(Args x) {
   if (x.bad || q.dim() != 3 || table.dim() != 2) return number(kDoesNotFit);
   const auto type = q.scalar_type();
   const int64_t T = q.size(0), B = table.size(0);
+  // a row's distance and its pages are two things: rows may be shared, or part of a wider table
+  const int64_t row_step = B > 1 && table.size(1) > 0 ? table.stride(0) : 0;
   if (dtype_of(q) < 0 || !heads(q, type, T, Hq, dim, gpu) || !cache(k_cache, type, Hk, dim, gpu) ||
       !cache(v_cache, type, Hk, dim, gpu) || !k_cache.sizes().equals(v_cache.sizes()) ||
       table.scalar_type() != at::kInt || !on(table, gpu) || table.stride(1) != 1 ||
       !plain(starts, at::kInt, B + 1, gpu) ||
       !plain(kv_lens, at::kInt, B, gpu) || (tree.defined() && !plain(tree, at::kLong, T, gpu)) ||
       (out.defined() && !heads(out, type, T, Hq, dim, gpu)) || !fits_int(T) || !fits_int(B) || !fits_int(max_q) ||
-      !fits_int(k_cache.size(0)) || !fits_int(k_cache.size(1)) || !fits_int(table.stride(0)))
+      !fits_int(k_cache.size(0)) || !fits_int(k_cache.size(1)) || !fits_int(row_step) || !fits_int(table.size(1)))
     return number(kDoesNotFit);
   if (!out.defined()) out = at::empty({T, Hq, dim}, q.options());
   if (want_lse) lse = at::empty({T, Hq}, q.options().dtype(at::kFloat));
   const moe_attn_args_t a{dtype_of(q), (int)B, (int)T, (int)max_q, (float)scale, q.data_ptr(), q.stride(0), q.stride(1),
                           k_cache.data_ptr(), v_cache.data_ptr(), k_cache.stride(0), k_cache.stride(1),
                           v_cache.stride(0), v_cache.stride(1), (int)k_cache.size(0), (int)k_cache.size(1),
-                          ptr<int32_t>(table), (int)(B > 1 ? table.stride(0) : table.size(1)), ptr<int32_t>(starts),
-                          ptr<int32_t>(kv_lens), ptr<int64_t>(tree), out.data_ptr(), out.stride(0), out.stride(1),
-                          ptr<float>(lse)};
+                          ptr<int32_t>(table), (int)row_step, ptr<int32_t>(starts), ptr<int32_t>(kv_lens),
+                          ptr<int64_t>(tree), out.data_ptr(), out.stride(0), out.stride(1), ptr<float>(lse),
+                          (int)table.size(1)};
   const int status =
       moe_attn_forward(reinterpret_cast<moe_attn_t*>(handle), &a, reinterpret_cast<moe_stream_t>(stream));
   if (status != MOE_OK) return number(status);

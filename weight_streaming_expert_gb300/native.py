@@ -81,7 +81,7 @@ class moe_attn_args_t(ctypes.Structure):
                 ("k_page_stride", _l), ("k_row_stride", _l), ("v_page_stride", _l), ("v_row_stride", _l),
                 ("n_pages", _i), ("page_size", _i), ("block_table", _p), ("table_stride", _i), ("q_starts", _p),
                 ("kv_lens", _p), ("tree_mask", _p), ("out", _p), ("out_token_stride", _l), ("out_head_stride", _l),
-                ("lse", _p)]
+                ("lse", _p), ("table_pages", _i)]
 
 
 class MoEError(RuntimeError):
