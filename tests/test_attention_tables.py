@@ -77,3 +77,29 @@ def test_refusals_of_tables():
     assert call(table_pages=-1) == N.MOE_ERR_INVALID_ARG and "table_pages" in N.last_error()
     assert call(table_stride=-1) == N.MOE_ERR_INVALID_ARG and "table_stride" in N.last_error()
     assert call(table_pages=1, block_table=None) == N.MOE_ERR_INVALID_ARG and "block_table" in N.last_error()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", ["chain", "tree", "chunk"])
+def test_starts_that_make_no_sense(form):
+    """They are reported; rows past the last token are not touched, and the
+    sequences whose starts are right keep their results."""
+    from weight_streaming_expert_gb300 import PagedAttention
+    from weight_streaming_expert_gb300 import native as N
+    lens = [90, 40] if form == "chunk" else [3, 2]
+    tree = [1, 3, 5, 1, 3] if form == "tree" else None
+    c = Case(lens, [200, 150], 8, 2, 64, 16, "fp16", seed=3, tree=tree)
+    T, first = sum(lens), lens[0]
+    attn = PagedAttention(8, 2, 64, device=DEV)
+    good, _ = outputs(c, attn)
+    assert attn.status() == 0
+    for starts, right in (([0, first, INT_MIN], True), ([0, first, INT_MIN + first - 1], True),
+                          ([0, first, -1], True), ([0, first, 1], True), ([INT_MIN, first, T], False),
+                          ([0, 2 ** 31 - 1, T], False), ([2 ** 31 - 1, INT_MIN, 2 ** 31 - 1], False),
+                          ([-5, T + 7, INT_MIN], False), ([T, T, T + 1], False)):
+        out = torch.full((2 * T + 300, 8, 64), 7.0, dtype=torch.float16, device=DEV)
+        outputs(c, attn, q_starts=torch.tensor(starts, dtype=torch.int32, device=DEV), out=out[:T])
+        assert attn.status() == N.MOE_ERR_INVALID_ARG and "length" in N.last_error(), starts
+        assert (out[T:] == 7).all() and out.isfinite().all(), starts
+        if right:
+            assert torch.equal(out[:first], good[:first]), starts

@@ -150,12 +150,12 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
   const int q0 = a.q_starts[b], q1 = a.q_starts[b + 1], kv = a.kv_lens[b];
   const long long room = min(1ll << 30, (long long)a.table_pages * a.page_size);
   s.q0 = max(0, min(q0, a.n_tokens));
-  s.n = max(0, min(min(q1, a.n_tokens) - s.q0, a.max_q_len));
+  s.n = max(0, min(max(0, min(q1, a.n_tokens)) - s.q0, a.max_q_len));  // both in 0..n_tokens: no overflow
   s.kv = (int)max(0ll, min((long long)kv, room));
   s.bad = s.q0 != q0 || (long long)s.n != (long long)q1 - q0 || s.kv != kv;
   // the chunk's place goes by the lengths as given; what was cut is hidden
   const long long base = (long long)kv - ((long long)q1 - q0);
-  s.base = (int)max(-(1ll << 30), min(base, 1ll << 30));
+  s.base = (int)max(-(1ll << 30), min(base, (1ll << 30) - 1));  // base + a token's number stays in 32 bits
   return s;
 }
 // 128-position tiles that item i of a sequence visits (at least one, which
