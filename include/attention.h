@@ -117,6 +117,10 @@ typedef struct {
  * count as zeros; a length beyond the table or 2^30, which is cut; a chunk
  * longer than max_q_len, whose tokens beyond it are not computed; a bounded
  * wait that ran out) set the handle's sticky status word.
+ *
+ * MOE_ERR_UNSUPPORTED for a batch above 4096, and for more than 2e9 tiles of work, counted with as many positions as
+ * a row of the table could hold (a tile: 128 positions of a key/value head for 2 * (128 / group) tokens, half as many
+ * where max_q_len is no more than that): 2^20 tokens of 32/4 heads and tables of 2^20 positions are half of it.
  */
 int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t stream);
 

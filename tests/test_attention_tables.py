@@ -103,3 +103,36 @@ def test_starts_that_make_no_sense(form):
         assert (out[T:] == 7).all() and out.isfinite().all(), starts
         if right:
             assert torch.equal(out[:first], good[:first]), starts
+
+
+@pytest.mark.gpu
+def test_many_heads_over_one_in_a_long_table():
+    """A table of a million positions does not make a chunk too much work: 128
+    heads of a token fill a tile, so 8192 tokens are 4096 items of at most 8192
+    tiles of positions."""
+    from weight_streaming_expert_gb300 import PagedAttention
+    g = torch.Generator(device=DEV).manual_seed(4)
+    rand = lambda *s: torch.randn(*s, generator=g, device=DEV).bfloat16()
+    T, page = 8192, 64
+    q, k, v = rand(T, 128, 64), rand(T // page, page, 1, 64), rand(T // page, page, 1, 64)
+    i = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    narrow = torch.arange(T // page, dtype=torch.int32, device=DEV)[None]
+    wide = torch.full((1, (1 << 20) // page), -1, dtype=torch.int32, device=DEV)
+    wide[:, :T // page] = narrow
+    attn = PagedAttention(128, 1, 64, device=DEV)
+    want = attn(q, k, v, narrow, i(0, T), i(T), T)
+    got = attn(q, k, v, wide, i(0, T), i(T), T)
+    assert attn.status() == 0 and torch.equal(got, want)
+
+
+@pytest.mark.gpu
+def test_too_much_work_is_refused():
+    from weight_streaming_expert_gb300 import PagedAttention
+    from weight_streaming_expert_gb300 import native as N
+    attn = PagedAttention(64, 64, 64, device=DEV)
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, device=DEV)
+    table = z(1, 1, dt=torch.int32).expand(1, 1 << 22)  # 2^30 positions: 2^23 tiles
+    q = z(1024, 64, 64)  # 4 items of 64 heads
+    with pytest.raises(N.MoEError, match="too much work"):
+        attn(q, z(1, 256, 64, 64), z(1, 256, 64, 64), table.contiguous(), z(2, dt=torch.int32), z(1, dt=torch.int32),
+             1024)

@@ -1247,14 +1247,14 @@ int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t strea
        a->k_row_stride | a->v_page_stride | a->v_row_stride) & 7)
     return fail(MOE_ERR_INVALID_ARG, "every stride must be a multiple of 8 elements (16 bytes)");
   if (a->n_tokens > (1 << 30)) return fail(MOE_ERR_UNSUPPORTED, "n_tokens = %d is too many", a->n_tokens);
-  // units of work, at most: they are counted in 32 bits
-  const double units = ((double)a->n_tokens * h->n_heads / (2 * kTile - 2 * h->n_heads / h->n_kv_heads + 2) +
-                        (double)a->batch * h->n_kv_heads) *
-                       ((double)table_pages * a->page_size / kTile + 1);
-  if (units > 2e9) return fail(MOE_ERR_UNSUPPORTED, "too much work for one call: split the tokens");
   if (a->batch > kMaxBatch) return fail(MOE_ERR_UNSUPPORTED, "batch = %d exceeds %d", a->batch, kMaxBatch);
   const int group = h->n_heads / h->n_kv_heads, columns = h->n_kv_heads * h->head_dim;
   const int tokens = kTile / group, box_rows = std::min(a->page_size, kTile);
+  // units of cost, at most: they are counted in 32 bits
+  const double item_tokens = (a->max_q_len > tokens ? 2. : 1.) * tokens;
+  const double item_cost = std::min(1073741824., (double)table_pages * a->page_size) / kTile + 1 + kItemCost<2>;
+  if ((a->n_tokens / item_tokens + a->batch) * h->n_kv_heads * item_cost > 2e9)
+    return fail(MOE_ERR_UNSUPPORTED, "too much work for one call: split the tokens");
   Maps maps;
   int rc = map_for(h->q_map, {a->dtype, h->head_dim, h->n_heads, a->n_tokens, group, tokens, a->q_head_stride,
                               a->q_token_stride},
