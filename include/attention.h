@@ -115,8 +115,9 @@ typedef struct {
 /*
  * Errors found on the device (a page outside the cache, whose positions then
  * count as zeros; a length beyond the table or 2^30, which is cut; a chunk
- * longer than max_q_len, whose tokens beyond it are not computed; a bounded
- * wait that ran out) set the handle's sticky status word.
+ * longer than max_q_len, whose tokens beyond it are not computed; chunks that
+ * overlap, and where they make more work than the limit below nothing is
+ * computed; a bounded wait that ran out) set the handle's sticky status word.
  *
  * MOE_ERR_UNSUPPORTED for a batch above 4096, and for more than 2e9 tiles of work, counted with as many positions as
  * a row of the table could hold (a tile: 128 positions of a key/value head for 2 * (128 / group) tokens, half as many

@@ -136,3 +136,31 @@ def test_too_much_work_is_refused():
     with pytest.raises(N.MoEError, match="too much work"):
         attn(q, z(1, 256, 64, 64), z(1, 256, 64, 64), table.contiguous(), z(2, dt=torch.int32), z(1, dt=torch.int32),
              1024)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch,T,Hq,Hk,positions", [(4096, 4096, 8, 2, 1 << 24), (32, 256, 20, 5, 1 << 30)])
+def test_overlapping_chunks_that_are_too_much_work(batch, T, Hq, Hk, positions):
+    """Every second sequence names all tokens, over all positions that its row
+    of the table could hold: more work than 32 bits count, of which nothing is
+    done."""
+    from weight_streaming_expert_gb300 import PagedAttention
+    from weight_streaming_expert_gb300 import native as N
+    attn = PagedAttention(Hq, Hk, 64, device=DEV)
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device=DEV)
+    i = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    k = z(2, 256, Hk, 64)
+    table = torch.zeros(1, positions // 256, dtype=torch.int32, device=DEV).expand(batch, -1)
+    starts = torch.zeros(batch + 1, dtype=torch.int32, device=DEV)
+    starts[1::2] = T
+    lens = torch.full((batch,), positions, dtype=torch.int32, device=DEV)
+    out = torch.full((T, Hq, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    attn(z(T, Hq, 64), k, k, table, starts, lens, T, out=out)
+    assert attn.status() == N.MOE_ERR_INVALID_ARG and "length" in N.last_error()
+    assert (out == 7).all()
+    # without the overlap the same tables are fine
+    starts[1:] = T
+    lens.fill_(300)
+    lens[0] = T
+    attn(z(T, Hq, 64), k, k, table, starts, lens, T, out=out)
+    assert attn.status() == 0 and (out == 0).all()

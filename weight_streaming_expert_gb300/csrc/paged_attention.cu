@@ -53,6 +53,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cmath>
 #include <new>
 #include <type_traits>
 
@@ -125,6 +126,7 @@ __device__ __forceinline__ void max3(float& top, uint32_t x, uint32_t y) {
 struct Cut {
   int parts, c, b, h, tile;
 };
+constexpr double kMaxUnits = 2e9;          // of a call: they are counted in 32 bits
 constexpr int kMaxParts = 1024;            // CTAs, which is at least the shares of one tile
 
 struct AttnParams {
@@ -136,7 +138,8 @@ struct AttnParams {
   float* part_o;    // [CTAs][2][rows of an item][D]: unnormalised sums
   float2* part_ml;  // [CTAs][2][rows of an item]: (m, sum of p)
   Cut* cuts;        // [CTAs]: by the CTA, or by_item
-  bool by_item;     // one item per sequence and head, no more than CTAs: cut b * heads + h is that item's
+  bool by_item;     // one item per sequence and head, no more than CTAs: cut b * heads + h is that item's; `fits` holds
+  bool fits;        // the units' sum stays in 32 bits even where sequences name the same tokens
 };
 
 // One sequence as the kernel takes it: lengths that do not fit are cut.
@@ -244,12 +247,22 @@ __device__ __forceinline__ int scan_up(int v) {
 
 // Where this CTA's share begins, found by each warp for itself: lane l has the
 // sequences l * per, .., whose costs (one head's units) cost(b) gives and sum
-// to `sum`.
+// to `lane_sum`.
 template <int kTiles, typename Cost>
-__device__ __forceinline__ Plan make_plan(const AttnParams& p, int per, int sum, Cost cost) {
+__device__ __forceinline__ Plan make_plan(const AttnParams& p, int per, long long lane_sum, Cost cost) {
   const int lane = threadIdx.x & 31;
-  const int upto = scan_up(sum);
   const int heads = p.n_kv_heads / p.spread, shares = gridDim.x / p.spread;
+  if (!p.fits) {
+    // the host's limit holds for chunks that do not overlap
+    long long all = lane_sum;
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) all += __shfl_xor_sync(0xffffffffu, all, m);
+    if ((double)all * p.n_kv_heads > kMaxUnits) {
+      if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.status, kAttnBadLength);
+      return Plan{};
+    }
+  }
+  const int sum = (int)lane_sum, upto = scan_up(sum);
   const int total = __shfl_sync(0xffffffffu, upto, 31) * heads;
   Plan plan{};
   // equal shares of whole units: fewer CTAs, and cuts, where there are few
@@ -413,7 +426,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     __syncthreads();
     const int per = (a.batch + 31) / 32;
-    int sum = 0;
+    long long sum = 0;
     for (int b = lane * per; b < min(a.batch, (lane + 1) * per); ++b) sum += cost[b];
     plan = make_plan<kTiles>(p, per, sum, [&](int b) { return cost[b]; });
     fence_proxy_async_smem();  // the costs' place becomes the ring
@@ -1250,11 +1263,11 @@ int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t strea
   if (a->batch > kMaxBatch) return fail(MOE_ERR_UNSUPPORTED, "batch = %d exceeds %d", a->batch, kMaxBatch);
   const int group = h->n_heads / h->n_kv_heads, columns = h->n_kv_heads * h->head_dim;
   const int tokens = kTile / group, box_rows = std::min(a->page_size, kTile);
-  // units of cost, at most: they are counted in 32 bits
   const double item_tokens = (a->max_q_len > tokens ? 2. : 1.) * tokens;
   const double item_cost = std::min(1073741824., (double)table_pages * a->page_size) / kTile + 1 + kItemCost<2>;
-  if ((a->n_tokens / item_tokens + a->batch) * h->n_kv_heads * item_cost > 2e9)
+  if ((a->n_tokens / item_tokens + a->batch) * h->n_kv_heads * item_cost > kMaxUnits)
     return fail(MOE_ERR_UNSUPPORTED, "too much work for one call: split the tokens");
+  const bool fits = a->batch * std::ceil(a->max_q_len / item_tokens) * h->n_kv_heads * item_cost <= kMaxUnits;
   Maps maps;
   int rc = map_for(h->q_map, {a->dtype, h->head_dim, h->n_heads, a->n_tokens, group, tokens, a->q_head_stride,
                               a->q_token_stride},
@@ -1272,7 +1285,8 @@ int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t strea
   while (spread < kMaxSpread && h->n_kv_heads % (2 * spread) == 0) spread *= 2;
   const bool one_item = a->max_q_len <= (a->max_q_len > tokens ? 2 : 1) * tokens;
   AttnParams p{*a,       h->n_kv_heads, group,      tokens,  spread,
-               h->status, h->part_o,     h->part_ml, h->cuts, one_item && a->batch * h->n_kv_heads <= h->n_sms};
+               h->status, h->part_o,     h->part_ml, h->cuts, one_item && a->batch * h->n_kv_heads <= h->n_sms,
+               fits};
   p.a.table_pages = table_pages;
   if (a->dtype == MOE_DTYPE_BF16)
     return h->head_dim == 64 ? launch_attn<__nv_bfloat16, 64>(h, p, maps, stream)
