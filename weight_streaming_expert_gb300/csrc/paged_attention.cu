@@ -248,18 +248,18 @@ __device__ __forceinline__ int scan_up(int v) {
 // Where this CTA's share begins, found by each warp for itself: lane l has the
 // sequences l * per, .., whose costs (one head's units) cost(b) gives and sum
 // to `lane_sum`.
-template <int kTiles, typename Cost>
+template <int kTiles, bool kChecked, typename Cost>
 __device__ __forceinline__ Plan make_plan(const AttnParams& p, int per, long long lane_sum, Cost cost) {
   const int lane = threadIdx.x & 31;
   const int heads = p.n_kv_heads / p.spread, shares = gridDim.x / p.spread;
-  if (!p.fits) {
+  if (kChecked && !p.fits) {
     // the host's limit holds for chunks that do not overlap
     long long all = lane_sum;
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) all += __shfl_xor_sync(0xffffffffu, all, m);
     if ((double)all * p.n_kv_heads > kMaxUnits) {
       if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.status, kAttnBadLength);
-      return Plan{};
+      lane_sum = 0;  // no work for anyone (an early return here costs the long chunk 4 %)
     }
   }
   const int sum = (int)lane_sum, upto = scan_up(sum);
@@ -402,14 +402,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   // sequences: every warp makes it by itself and goes on without the others
   Plan plan;
   const bool wide = a.max_q_len > 4 * kTiles * p.tokens;  // sequences of many items: a warp each
-  if (a.batch <= 32 && !wide) {
+  if (a.batch <= 32 && !wide && p.fits) {
     int sum = 0;
     if (lane < a.batch) {
       const Seq s = load_seq(p, lane);
       if (s.bad && blockIdx.x == 0) atomicOr(p.status, kAttnBadLength);
       for (int i = 0; i * kTiles * p.tokens < s.n; ++i) sum += units_of<kTiles>(p, s, i) + kItemCost<kTiles>;
     }
-    plan = make_plan<kTiles>(p, 1, sum, [&](int) { return sum; });
+    plan = make_plan<kTiles, false>(p, 1, sum, [&](int) { return sum; });
   } else {
     int* cost = reinterpret_cast<int*>(ring_smem);  // the ring is not in use yet
     for (int b = wide ? warp : tid; b < a.batch; b += wide ? kAttnThreads / 32 : kAttnThreads) {
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int per = (a.batch + 31) / 32;
     long long sum = 0;
     for (int b = lane * per; b < min(a.batch, (lane + 1) * per); ++b) sum += cost[b];
-    plan = make_plan<kTiles>(p, per, sum, [&](int b) { return cost[b]; });
+    plan = make_plan<kTiles, true>(p, per, sum, [&](int b) { return cost[b]; });
     fence_proxy_async_smem();  // the costs' place becomes the ring
     __syncthreads();
   }
