@@ -79,7 +79,9 @@ int moe_qk_norm_rope(const moe_qk_norm_rope_args_t* a, moe_stream_t stream);
  *   j < kv_len - n, or bit j - (kv_len - n) of tree_mask[token] is set,
  * and j < kv_len.  out = sum_j softmax_j(scale * q.k_j) v_j over the seen
  * positions, query head h with key/value head h / (n_heads / n_kv_heads).  A
- * token that sees nothing gets zeros (and -inf as its log-sum).
+ * token that sees nothing gets zeros (and -inf as its log-sum).  Keys and values
+ * that a token does not see may hold anything, infinities and NaN among them;
+ * those that it sees show.
  * Scores, softmax statistics and sums are fp32; the probabilities are rounded
  * to the element type for the second product; out is rounded once.
  */

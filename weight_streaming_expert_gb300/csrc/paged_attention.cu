@@ -68,8 +68,9 @@ enum : int { kAttnBadPage = 1, kAttnBadLength = 2, kAttnTimeout = 4 };
 
 constexpr int kTile = 128;                 // query rows of a tile, and positions
 constexpr int kHalf = 64;                  // positions of a softmax step
-constexpr int kAttnThreads = 352;          // two softmax warpgroups, the MMA warp, the copy warp, the query warp
-constexpr int kMmaWarp = 8, kCopyWarp = 9, kQueryWarp = 10;
+// Two softmax warpgroups, then a warp each for MMAs, copies and queries, and in
+// the pair form one for veiled values.
+constexpr int kMmaWarp = 8, kCopyWarp = 9, kQueryWarp = 10, kValueWarp = 11;
 constexpr int kMaxBatch = 4096;
 constexpr int kMaxStages = 10;
 constexpr uint32_t kStagingBytes = 8 * 4096;  // 32 rows of 128 bytes for each softmax warp
@@ -245,6 +246,58 @@ __device__ __forceinline__ int scan_up(int v) {
   return v;
 }
 
+// Positions that not every row of an item sees: those from `lo` on are hidden
+// from some rows, those from `hi` on from all.
+struct Veil {
+  int lo, hi;
+};
+template <int kTiles>
+__device__ __forceinline__ Veil veil_of(const AttnParams& p, const Seq& s, int item) {
+  if (p.a.tree_mask) return {max(0, min(s.base, s.kv)), s.kv};
+  const int first = item * kTiles * p.tokens, last = min(s.n, first + kTiles * p.tokens) - 1;
+  const int lo = max(0, min(s.base + first + 1, s.kv));
+  return {lo, max(lo, min(s.base + last + 1, s.kv))};
+}
+
+// Elements of a pair that are infinite or NaN: the top bit of each half.
+template <typename T>
+__device__ __forceinline__ uint32_t not_finite(uint32_t pair) {
+  constexpr uint32_t kExponent = std::is_same<T, __nv_bfloat16>::value ? 0x7f807f80u : 0x7c007c00u;
+  constexpr uint32_t kLowest = std::is_same<T, __nv_bfloat16>::value ? 0x00800080u : 0x04000400u;
+  return ((pair & kExponent) + kLowest) & 0x80008000u;  // all ones carry into the sign's place
+}
+template <typename T>
+__device__ __forceinline__ uint32_t not_finite(uint4 v) {
+  return not_finite<T>(v.x) | not_finite<T>(v.y) | not_finite<T>(v.z) | not_finite<T>(v.w);
+}
+
+// Values (128 rows of D in shared memory) whose rows from `lo` on are hidden from
+// some rows of the item and from `hi` on from all: a hidden row's probability is
+// 0, but 0 * inf and 0 * NaN are NaN.  Rows from `hi` on become zeros: past the
+// sequence's end they hold anything.  Of the others only infinities and NaN do;
+// true in the lanes that met one.  (Two plain loops: as one, with a branch, it
+// was late for the products, ragged chunks 131 us instead of 121.)
+template <typename T, int D>
+__device__ __forceinline__ bool clean_values(uint8_t* values, int lo, int hi) {
+  constexpr int kChunks = D / 8;  // of 16 bytes, of a row
+  const int lane = threadIdx.x & 31, past = min(max(hi, 0), kTile);
+  auto chunk = [&](int i) {
+    return reinterpret_cast<uint4*>(values + (i % kChunks / 8) * (kTile * 128) + i / kChunks * 128 + i % 8 * 16);
+  };
+  for (int i = past * kChunks + lane; i < kTile * kChunks; i += 32) *chunk(i) = make_uint4(0u, 0u, 0u, 0u);
+  bool found = false;
+#pragma unroll 1
+  for (int i = lo * kChunks + lane; i < past * kChunks; i += 32) {
+    uint4* at = chunk(i);
+    if (!not_finite<T>(*at)) continue;
+    found = true;
+    uint32_t* pairs = reinterpret_cast<uint32_t*>(at);
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) pairs[k] &= ~((not_finite<T>(pairs[k]) >> 15) * 0xffffu);
+  }
+  return found;
+}
+
 // Where this CTA's share begins, found by each warp for itself: lane l has the
 // sequences l * per, .., whose costs (one head's units) cost(b) gives and sum
 // to `lane_sum`.
@@ -323,12 +376,51 @@ struct Waiter {
   }
 };
 
+// Adds the infinities and NaN that clean_values has taken out of an item's
+// tiles u0 .. u1 - 1 to the rows that see them: whatever its weight, an infinity
+// is the sum's then.  For row r of the chain's columns, whose 16-bit output or
+// fp32 part (in place `slot`) is in memory already.  Hardly ever called.
+template <typename T, int D, bool kPair>
+__device__ __noinline__ void add_not_finite(const AttnParams& p, int b, int h, int tile, int u0, int u1, bool cut,
+                                            int slot, int chain, int r) {
+  constexpr int kTiles = kPair ? 2 : 1, kColumns = kPair ? D : D / 2;
+  const moe_attn_args_t& a = p.a;
+  const Seq s = load_seq(p, b);
+  const int token = (tile * kTiles + (kPair ? chain : 0)) * p.tokens + r / p.group;
+  if (r / p.group >= p.tokens || token >= s.n) return;
+  const Veil veil = veil_of<kTiles>(p, s, tile);
+  const int column0 = kPair ? 0 : chain * kColumns, local = kPair ? chain * kTile + r : r;
+  const long long row = s.q0 + token;
+  T* out = static_cast<T*>(a.out) + row * a.out_token_stride + (h * p.group + r % p.group) * a.out_head_stride + column0;
+  float* part = p.part_o + ((long long)slot * kTiles * kTile + local) * D + column0;
+  for (int pos = max(veil.lo, u0 * kTile); pos < min(veil.hi, u1 * kTile); ++pos) {
+    const int other = pos - s.base;  // the chunk's token at that position
+    if (a.tree_mask ? other >= 64 || (other >= 0 && !((a.tree_mask[row] >> other) & 1)) : other > token) continue;
+    const int page = a.block_table[(long long)b * a.table_stride + pos / a.page_size];
+    if ((unsigned)page >= (unsigned)a.n_pages) continue;
+    const T* v = static_cast<const T*>(a.v_cache) + page * a.v_page_stride + pos % a.page_size * a.v_row_stride +
+                 h * D + column0;
+    for (int column = 0; column < kColumns; column += 8) {
+      if (!not_finite<T>(*reinterpret_cast<const uint4*>(v + column))) continue;
+      for (int i = column; i < column + 8; ++i) {
+        const float x = (float)v[i];
+        if (fabsf(x) < INFINITY) continue;
+        if (cut)
+          part[i] += x;
+        else
+          out[i] = (T)((float)out[i] + x);
+      }
+    }
+  }
+}
+
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 template <int D, bool kPair>
 struct Layout {
+  static constexpr int kThreads = kPair ? 384 : 352;
   static constexpr uint32_t kTileBytes = kTile * D * 2;          // one tile of Q, K or V
   static constexpr int kQTiles = kPair ? 2 : 1;
   static constexpr int kRows = kQTiles * kTile;                   // query rows of an item
@@ -340,11 +432,11 @@ struct Layout {
 };
 
 template <typename T, int D, bool kPair>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+__global__ void __launch_bounds__(Layout<D, kPair>::kThreads, 1)
     paged_attention_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap q_map,
                            const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   using L = Layout<D, kPair>;
-  constexpr int kTiles = L::kQTiles, kRows = L::kRows, kStages = L::kStages;
+  constexpr int kTiles = L::kQTiles, kRows = L::kRows, kStages = L::kStages, kThreads = L::kThreads;
   constexpr uint32_t kTileBytes = L::kTileBytes, kPanel = kTile * 128;
   extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle goes by address bits up to 9
   const uint32_t sb = smem_u32(smem);
@@ -359,6 +451,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const uint32_t drained = sb + 288u;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + 296);
   int* gone = reinterpret_cast<int*>(smem + 300);
+  auto raw = [&](int s) { return sb + 304u + 8u * s; };  // pair form: in place of full(s) for veiled values
+  // the numbers of the last items with values that were not finite; the value
+  // warp is at most half a ring of items ahead of the softmax warps
+  constexpr int kItems = 8;
+  static_assert(kStages / 2 + 2 < kItems);
+  volatile int* left_out = reinterpret_cast<int*>(smem + 384);
   uint8_t* staging = smem + 1024;                          // [8][32 rows][128 bytes]: of the softmax warps
   float2* exchange = reinterpret_cast<float2*>(staging);   // [2][128]: both chains' (m, sum)
   const uint32_t q_at = sb + L::kHead, ring = q_at + L::kQTiles * kTileBytes;
@@ -370,7 +468,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     for (int s = 0; s < kStages; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
+      if (kPair) mbar_init(raw(s), 1);
     }
+    for (int i = 0; i < kItems; ++i) left_out[i] = -1;
     for (int t = 0; t < 2; ++t) {
       mbar_init(q_full(t), 1);
       mbar_init(q_empty(t), 1);
@@ -395,6 +495,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot);
   const Waiter wait{gone, p.status};
+  // A tile of an item's veiled values, by a warp, before the products read them.
+  auto clean = [&](int item, Veil veil, int u, int stage) {
+    const bool found = clean_values<T, D>(ring_smem + stage * kTileBytes, max(0, veil.lo - u * kTile),
+                                          veil.hi - u * kTile);
+    fence_proxy_async_smem();
+    if (__any_sync(0xffffffffu, found) && lane == 0) left_out[item % kItems] = item;
+    __syncwarp();
+  };
   pdl_wait();
   pdl_launch_dependents();
 
@@ -412,7 +520,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     plan = make_plan<kTiles, false>(p, 1, sum, [&](int) { return sum; });
   } else {
     int* cost = reinterpret_cast<int*>(ring_smem);  // the ring is not in use yet
-    for (int b = wide ? warp : tid; b < a.batch; b += wide ? kAttnThreads / 32 : kAttnThreads) {
+    for (int b = wide ? warp : tid; b < a.batch; b += wide ? kThreads / 32 : kThreads) {
       const Seq s = load_seq(p, b);
       if (s.bad && blockIdx.x == 0) atomicOr(p.status, kAttnBadLength);
       int sum = 0;
@@ -435,7 +543,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   if (p.by_item) {
     // items that are not cut say so where they begin; these have no items
     if (blockIdx.x == 0)
-      for (int i = tid; i < a.batch * p.n_kv_heads; i += kAttnThreads)
+      for (int i = tid; i < a.batch * p.n_kv_heads; i += kThreads)
         if (load_seq(p, i / p.n_kv_heads).n == 0) p.cuts[i].parts = 0;
   } else if (tid == 0) {
     p.cuts[blockIdx.x].parts = 0;
@@ -453,7 +561,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const float rescale = kRescaleLog2 / c;
     int tiles[2] = {0, 0};  // tiles of positions of the even and the odd chain before this item
     const int row_token = r / p.group, row_head = r - row_token * p.group;
-    while (walk.next(it)) {
+    for (int item = 0; walk.next(it); ++item) {
       const int token0 = (it.tile * kTiles + q_tile) * p.tokens;  // the tile's first, in the chunk
       const int token = token0 + row_token, head = it.h * p.group + row_head;
       const bool valid = row_token < p.tokens && token < it.s.n;
@@ -654,6 +762,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f;
         }
       }
+      if (left_out[item % kItems] == item)
+        add_not_finite<T, D, kPair>(p, it.b, it.h, it.tile, it.u0, it.u1, cut, slot, chain, r);
       if (it.u0 == 0 && tid == 0) {
         const int at = p.by_item ? it.b * p.n_kv_heads + it.h : blockIdx.x;
         if (cut) {
@@ -694,6 +804,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         fetch((it.u0 * kTile >> pages_log2) / 32);
         fetch(have + 1);
       };
+      int veiled = 0;  // the item's first tile of positions that not every row sees
       auto load = [&](const CUtensorMap* map, int u) {
         const int stage = filled % kStages, round = filled / kStages;
         const int pos = u * kTile + box * box_rows, i = pos >> pages_log2, window = (u * kTile >> pages_log2) / 32;
@@ -705,11 +816,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         if (round > 0) wait(empty(stage), (round - 1) & 1);
         const unsigned boxes = __popc(__ballot_sync(0xffffffffu, mine));
-        if (lane == 0) mbar_arrive_expect_tx(full(stage), boxes * box_rows * 128u);
+        const uint32_t bar = kPair && map == &v_map && u >= veiled ? raw(stage) : full(stage);
+        if (lane == 0) mbar_arrive_expect_tx(bar, boxes * box_rows * 128u);
         __syncwarp();
         if (mine)
           tma_load_3d(ring + stage * kTileBytes + half * kPanel + box * box_rows * 128, map, it.h * D + half * 64,
-                      pos & (a.page_size - 1), page, full(stage));
+                      pos & (a.page_size - 1), page, bar);
         ++filled;
         return window;
       };
@@ -721,6 +833,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       while (walk.next(it)) {
         const int n = it.u1 - it.u0;
         start_item();
+        if (kPair) veiled = veil_of<kTiles>(p, it.s, it.tile).lo / kTile;
         if (kPair) {
           for (int j = 0; j < n; ++j) {
             load(&k_map, it.u0 + j);
@@ -740,7 +853,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         unsigned long long waited;
         mbar_wait(full(f % kStages), (f / kStages) & 1, &waited);
       }
-    } else if (warp >= kQueryWarp) {
+    } else if (warp == kQueryWarp) {
       // ---- queries, of a tile as one box of its tokens, the heads of a group
       // and 64 columns.  Past the sequence's last token it reads what follows,
       // which no row that counts sees.
@@ -765,6 +878,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       unsigned long long waited;
       if (round > 0)
         for (int t = 0; t < kTiles; ++t) mbar_wait(q_full(t), (round - 1) & 1, &waited);
+    } else if (kPair && warp == kValueWarp) {
+      // ---- veiled values, ahead of the products that read them: an item's
+      // tokens veil one to three tiles, for which the MMA warp would stop.
+      // Their copies arrive at a barrier of their own, and this warp at the
+      // stage's.
+      Walk<kTiles> walk(p, plan);
+      Item it{};
+      int before = 0;           // tiles of keys and values of the items before this one
+      uint32_t raw_parity = 0;  // a bit per stage: of its next veiled values
+      for (int item = 0; walk.next(it); ++item) {
+        const Veil veil = veil_of<kTiles>(p, it.s, it.tile);
+        for (int u = max(it.u0, veil.lo / kTile); u < it.u1; ++u) {
+          const int stage = (before + 2 * (u - it.u0) + 1) % kStages;  // keys and values in turn
+          wait(raw(stage), (raw_parity >> stage) & 1);
+          raw_parity ^= 1u << stage;
+          clean(item, veil, u, stage);
+          if (lane == 0) mbar_arrive(full(stage));
+        }
+        before += 2 * (it.u1 - it.u0);
+      }
+      // no copy is in flight when the CTA ends, also after a wait has given up
+      unsigned long long waited;
+      for (int s = 0; s < kStages; ++s) mbar_wait(raw(s), (~raw_parity >> s) & 1, &waited);
     } else if (warp == kMmaWarp) {
       Walk<kTiles> walk(p, plan);
       Item it{};
@@ -772,7 +908,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
       constexpr uint32_t kDescS = mma_desc(kBf16, false, kTile, kPair ? kHalf : kTile);
       constexpr uint32_t kDescO = mma_desc(kBf16, true, kTile, D);
-      int taken = 0, q_round = 0;
+      int taken = 0, q_round = 0, item = 0;
+      Veil veil{};
       uint32_t p_parity = 0;  // bit 2 chain + half: of the next probabilities
       auto next_stage = [&]() {
         const int stage = taken % kStages;
@@ -818,23 +955,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (kPair) mma_commit(q_empty(1));
         }
       };
-      // Rows of the cache past the sequence's end hold anything, and 0 * NaN is
-      // NaN: they become zeros.
+      // the split form's few rows veil few positions: another warp for them comes
+      // later than this one (chain of 6: 14.1 us, with a warp 14.7)
       auto value_stage = [&](int u) {
-        const int stage = next_stage(), valid = max(0, it.s.kv - u * kTile);
-        if (valid < kTile) {
-          uint8_t* v = ring_smem + stage * kTileBytes;
-          for (int i = lane; i < (kTile - valid) * (D / 8); i += 32) {
-            const int row = valid + i / (D / 8), c = i % (D / 8);
-            *reinterpret_cast<uint4*>(v + (c / 8) * kPanel + row * 128 + (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
+        const int stage = next_stage();
+        if (!kPair && (u + 1) * kTile > veil.lo) clean(item, veil, u, stage);
         return stage;
       };
       while (uniform((int)walk.next(it))) {
         const int n = uniform(it.u1 - it.u0);
+        veil = veil_of<kTiles>(p, it.s, it.tile);
+        veil.lo = uniform(veil.lo), veil.hi = uniform(veil.hi);
         wait(q_full(0), q_round & 1);
         if (kPair) wait(q_full(1), q_round & 1);
         int ks[2], vs[2];
@@ -888,6 +1019,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
         }
         ++q_round;
+        ++item;
       }
       if (elected()) mma_commit(drained);
       unsigned long long waited;
@@ -1167,7 +1299,7 @@ template <typename T, int D, bool kPair>
 int launch_attn(const moe_attn* h, const AttnParams& p, const Maps& maps, moe_stream_t stream) {
   using L = Layout<D, kPair>;
   const int grid = h->n_sms / p.spread * p.spread;
-  const int rc = launch_pdl(paged_attention_kernel<T, D, kPair>, dim3(grid), dim3(kAttnThreads), L::kSmem, stream,
+  const int rc = launch_pdl(paged_attention_kernel<T, D, kPair>, dim3(grid), dim3(L::kThreads), L::kSmem, stream,
                             1, p, maps.q, maps.k, maps.v);
   if (rc != MOE_OK) return rc;
   const dim3 threads(kJoinRows * kJoinGroups * D / 4);
