@@ -164,3 +164,19 @@ def test_overlapping_chunks_that_are_too_much_work(batch, T, Hq, Hk, positions):
     lens[0] = T
     attn(z(T, Hq, 64), k, k, table, starts, lens, T, out=out)
     assert attn.status() == 0 and (out == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch", [2, 200])
+def test_a_longest_chunk_of_zero_is_reported(batch):
+    """As any other number that is smaller than a chunk."""
+    from weight_streaming_expert_gb300 import PagedAttention
+    from weight_streaming_expert_gb300 import native as N
+    c = Case([2] * batch, [30] * batch, 4, 2, 64, 16, seed=5)
+    attn = PagedAttention(4, 2, 64, device=DEV)
+    for longest in (1, 0):
+        outputs(c, attn, max_q_len=longest)
+        assert attn.status() == N.MOE_ERR_INVALID_ARG and "max_q_len" in N.last_error()
+    empty = torch.zeros(batch + 1, dtype=torch.int32, device=DEV)  # no chunk has a token
+    outputs(c, attn, max_q_len=0, q_starts=empty)
+    assert attn.status() == 0

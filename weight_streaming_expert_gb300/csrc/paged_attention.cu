@@ -1305,7 +1305,7 @@ int launch_attn(const moe_attn* h, const AttnParams& p, const Maps& maps, moe_st
   const dim3 threads(kJoinRows * kJoinGroups * D / 4);
   // cuts by item: as many blocks as their rows have use for; else most of the
   // blocks find no cut
-  const int rows = kPair ? L::kRows : std::min(p.a.max_q_len, p.tokens) * p.group;
+  const int rows = kPair ? L::kRows : std::max(1, std::min(p.a.max_q_len, p.tokens)) * p.group;
   if (p.by_item)
     return launch_pdl(join_kernel<T, D, L::kRows, true>,
                       dim3(p.a.batch * p.n_kv_heads, (rows + kJoinRows - 1) / kJoinRows), threads, 0, stream, 1, p);
@@ -1379,7 +1379,7 @@ int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t strea
     return fail(MOE_ERR_UNSUPPORTED, "page_size = %d: must be 16, 32, 64, 128 or 256", a->page_size);
   if (a->tree_mask && a->max_q_len > 64)
     return fail(MOE_ERR_UNSUPPORTED, "max_q_len = %d: a tree mask has 64 bits", a->max_q_len);
-  if (a->batch == 0 || a->n_tokens == 0 || a->max_q_len == 0) return MOE_OK;
+  if (a->batch == 0 || a->n_tokens == 0) return MOE_OK;
   if (a->n_pages < 1) return fail(MOE_ERR_INVALID_ARG, "n_pages = %d < 1", a->n_pages);
   if (!a->q || !a->k_cache || !a->v_cache || !a->out || !aligned(a->q, 16) || !aligned(a->k_cache, 16) ||
       !aligned(a->v_cache, 16) || !aligned(a->out, 16))
