@@ -87,7 +87,8 @@ int moe_qk_norm_rope(const moe_qk_norm_rope_args_t* a, moe_stream_t stream);
  */
 typedef struct moe_attn moe_attn_t; /* opaque; holds the workspace of split sequences */
 
-/* n_heads a multiple of n_kv_heads (up to 128 times), head_dim 64 or 128.  NULL on error. */
+/* On the current device, which has to be current in every forward.  n_heads a multiple of n_kv_heads (up to 128 times),
+ * head_dim 64 or 128.  NULL on error. */
 moe_attn_t* moe_attn_create(int n_heads, int n_kv_heads, int head_dim);
 
 typedef struct {
@@ -127,11 +128,11 @@ typedef struct {
  */
 int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t stream);
 
-/* Synchronises the device, then returns and clears the sticky status: MOE_OK, MOE_ERR_INVALID_ARG (bad pages or
+/* Synchronises the handle's device, then returns and clears the sticky status: MOE_OK, MOE_ERR_INVALID_ARG (bad pages or
  * lengths) or MOE_ERR_DEVICE_TIMEOUT; moe_last_error() names what was found. */
 int moe_attn_get_status(moe_attn_t* h);
 
-/* Frees the handle (NULL-safe); synchronises the device first. */
+/* Frees the handle (NULL-safe); synchronises its device first. */
 void moe_attn_destroy(moe_attn_t* h);
 
 /*

@@ -1266,7 +1266,7 @@ int map_for(KnownMap& known, const Shape& s, const void* base, CUtensorMap* map,
 using namespace wse;
 
 struct moe_attn {
-  int n_heads = 0, n_kv_heads = 0, head_dim = 0, n_sms = 0;
+  int n_heads = 0, n_kv_heads = 0, head_dim = 0, n_sms = 0, dev = 0;
   int* status = nullptr;
   float* part_o = nullptr;
   float2* part_ml = nullptr;
@@ -1345,9 +1345,8 @@ moe_attn_t* moe_attn_create(int n_heads, int n_kv_heads, int head_dim) {
   h->n_heads = n_heads;
   h->n_kv_heads = n_kv_heads;
   h->head_dim = head_dim;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->n_sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t e = cudaGetDevice(&h->dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->n_sms, cudaDevAttrMultiProcessorCount, h->dev);
   h->n_sms = std::min(h->n_sms, kMaxParts);
   if (e == cudaSuccess)
     e = head_dim == 64 ? allow_smem_both<__nv_bfloat16, 64>() : allow_smem_both<__nv_bfloat16, 128>();
@@ -1399,6 +1398,11 @@ int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t strea
   const double item_cost = std::min(1073741824., (double)table_pages * a->page_size) / kTile + 1 + kItemCost<2>;
   if ((a->n_tokens / item_tokens + a->batch) * h->n_kv_heads * item_cost > kMaxUnits)
     return fail(MOE_ERR_UNSUPPORTED, "too much work for one call: split the tokens");
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return fail_cuda(e, "cudaGetDevice");
+  if (dev != h->dev)
+    return fail(MOE_ERR_INVALID_ARG, "the handle belongs to device %d, the current device is %d", h->dev, dev);
   const bool fits = a->batch * std::ceil(a->max_q_len / item_tokens) * h->n_kv_heads * item_cost <= kMaxUnits;
   Maps maps;
   int rc = map_for(h->q_map, {a->dtype, h->head_dim, h->n_heads, a->n_tokens, group, tokens, a->q_head_stride,
@@ -1429,12 +1433,15 @@ int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t strea
 
 int moe_attn_get_status(moe_attn_t* h) {
   if (!h) return fail(MOE_ERR_INVALID_ARG, "null handle");
-  int st = 0;
+  int st = 0, current = 0;
   cudaError_t e;
-  if ((e = cudaDeviceSynchronize()) != cudaSuccess ||
-      (e = cudaMemcpy(&st, h->status, sizeof st, cudaMemcpyDeviceToHost)) != cudaSuccess ||
-      (e = cudaMemset(h->status, 0, sizeof st)) != cudaSuccess)
-    return fail_cuda(e, "attention status");
+  if ((e = cudaGetDevice(&current)) != cudaSuccess || (e = cudaSetDevice(h->dev)) != cudaSuccess)
+    return fail_cuda(e, "the handle's device");
+  if ((e = cudaDeviceSynchronize()) == cudaSuccess &&
+      (e = cudaMemcpy(&st, h->status, sizeof st, cudaMemcpyDeviceToHost)) == cudaSuccess)
+    e = cudaMemset(h->status, 0, sizeof st);
+  cudaSetDevice(current);
+  if (e != cudaSuccess) return fail_cuda(e, "attention status");
   if (st & kAttnTimeout) return fail(MOE_ERR_DEVICE_TIMEOUT, "a bounded wait of the attention kernel ran out");
   if (st)
     return fail(MOE_ERR_INVALID_ARG, "%s%s", st & kAttnBadPage ? "a block table names a page outside the cache; " : "",
@@ -1444,8 +1451,12 @@ int moe_attn_get_status(moe_attn_t* h) {
 
 void moe_attn_destroy(moe_attn_t* h) {
   if (!h) return;
+  int current = 0;
+  cudaGetDevice(&current);
+  cudaSetDevice(h->dev);
   cudaDeviceSynchronize();
   free_attn(h);
+  cudaSetDevice(current);
 }
 
 }  // extern "C"
