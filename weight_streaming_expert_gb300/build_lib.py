@@ -1,10 +1,11 @@
 """Builds the layer's shared library in-tree: _build/libwse.so (sm_103a).
 
 Each .cu file is compiled in parallel with nvcc, then linked into one shared
-library against the shared CUDA runtime.  The Python extension module of the
-attention and sampling calls, _build/wse_calls.so, is compiled beside them
-with g++ and linked against that library and PyTorch's.  Rebuilds only when a
-source or header is newer than the libraries.
+library against the shared CUDA runtime.  Beside it the Python extension module
+of the attention and sampling calls, _build/wse_calls.so, is compiled with g++
+and linked against that library and PyTorch's; the library needs neither, and is
+built also where the module cannot be.  Rebuilds only what is older than its
+sources and headers.
 
     python -m weight_streaming_expert_gb300.build_lib [--force] [--verbose]
 """
@@ -45,23 +46,37 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _headers():
+    return glob.glob(os.path.join(INCLUDE, "*.h"))
+
+
+def _library_inputs():
+    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + _headers()
+
+
 def _inputs():
-    return (_sources() + [CALLS_SOURCE] + glob.glob(os.path.join(CSRC, "*.cuh"))
-            + glob.glob(os.path.join(INCLUDE, "*.h")))
+    return _library_inputs() + [CALLS_SOURCE]
+
+
+def _newer(path: str, inputs) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in inputs)
+
+
+def _library_up_to_date() -> bool:
+    return _newer(LIB, _library_inputs())
+
+
+def _calls_up_to_date() -> bool:
+    return _newer(CALLS, [CALLS_SOURCE] + _headers())
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALLS):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
-    return all(os.path.getmtime(p) <= t for p in _inputs())
+    return _library_up_to_date() and _calls_up_to_date()
 
 
-def _torch_dir() -> str:
+def _torch_dir() -> str | None:
     spec = importlib.util.find_spec("torch")  # found, not imported: the headers are all that is wanted
-    if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("PyTorch not found: the Python calls are compiled against its headers")
-    return spec.submodule_search_locations[0]
+    return spec.submodule_search_locations[0] if spec is not None and spec.submodule_search_locations else None
 
 
 def _run(cmd, what):
@@ -79,8 +94,17 @@ def _compile_calls() -> str:
     return obj
 
 
-def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
-    if not force and up_to_date():
+def _link_calls(obj: str):
+    tmp = CALLS + f".tmp{os.getpid()}"
+    torch_lib = os.path.join(_torch_dir(), "lib")
+    _run(["g++", "-shared", "-o", tmp, obj, f"-L{BUILD}", "-lwse", "-Wl,-rpath,$ORIGIN", f"-L{torch_lib}",
+          "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{torch_lib}"], "link of the Python calls")
+    os.replace(tmp, CALLS)
+
+
+def build_library(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
+    """The C library alone."""
+    if not force and _library_up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -96,25 +120,33 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
         return obj, (r.stdout + r.stderr)
 
-    with ThreadPoolExecutor(max_workers=jobs or min(len(srcs) + 1, max(4, os.cpu_count() or 8))) as ex:
-        calls = ex.submit(_compile_calls)
+    with ThreadPoolExecutor(max_workers=jobs or min(len(srcs), max(4, os.cpu_count() or 8))) as ex:
         results = list(ex.map(compile_one, srcs))
-        calls_obj = calls.result()
     for src, (_, log) in zip(srcs, results):
         if verbose or "warning" in log:  # compiler warnings are shown, not swallowed
             sys.stderr.write(f"{os.path.basename(src)}:\n{log}")
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [cc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp] + [o for o, _ in results]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run([cc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp] + [o for o, _ in results], "link")
     os.replace(tmp, LIB)
-    tmp = CALLS + f".tmp{os.getpid()}"
-    torch_lib = os.path.join(_torch_dir(), "lib")
-    _run(["g++", "-shared", "-o", tmp, calls_obj, f"-L{BUILD}", "-lwse", "-Wl,-rpath,$ORIGIN", f"-L{torch_lib}",
-          "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{torch_lib}"], "link of the Python calls")
-    os.replace(tmp, CALLS)
     return LIB
+
+
+def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
+    """The library and the module of the Python calls.  Without PyTorch the
+    module is left out, with a note; what else keeps it from being built is
+    raised once the library is in place."""
+    if not force and _calls_up_to_date():
+        return build_library(verbose=verbose, jobs=jobs)
+    if _torch_dir() is None:
+        path = build_library(force, verbose, jobs)
+        sys.stderr.write("PyTorch not found: the module of the attention and sampling calls is not built\n")
+        return path
+    os.makedirs(BUILD, exist_ok=True)
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        calls = ex.submit(_compile_calls)  # beside the kernels
+        path = build_library(force, verbose, jobs)
+        _link_calls(calls.result())
+    return path
 
 
 if __name__ == "__main__":

@@ -103,10 +103,10 @@ def lib(build_if_missing: bool = True):
         if _lib is not None:
             return _lib
         path = build_lib.LIB
-        if not (os.path.exists(path) and os.path.exists(build_lib.CALLS)):
+        if not os.path.exists(path):
             if not build_if_missing:
                 raise RuntimeError(f"CUDA library not built: {path}")
-            build_lib.build()
+            build_lib.build_library()
         L = ctypes.CDLL(path)
         vp, ci, cu = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint
         i32p = ctypes.POINTER(ctypes.c_int32)
@@ -193,6 +193,8 @@ def calls():
     if _calls is None:
         lib()  # it is linked against the library
         with _lock:
+            if not os.path.exists(build_lib.CALLS):
+                build_lib.build()
             if not os.path.exists(build_lib.CALLS):
                 raise RuntimeError(f"extension module not built: {build_lib.CALLS}")
             loader = importlib.machinery.ExtensionFileLoader("wse_calls", build_lib.CALLS)
