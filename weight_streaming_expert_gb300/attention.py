@@ -37,8 +37,14 @@ def _elsewhere(index, stream):
     return stream is not None or torch._C._cuda_getDevice() != index
 
 
+def _tensor(name, t):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor, not {type(t).__name__}")
+
+
 def _heads(name, t, dtype, index, dim):
     """t: [tokens, heads, dim], each head's values contiguous."""
+    _tensor(name, t)
     if t.dim() != 3 or t.dtype != dtype or t.get_device() != index or t.shape[2] != dim or t.stride(2) != 1:
         raise ValueError(f"{name} must be a {dtype} tensor [tokens, heads, {dim}] with contiguous heads on "
                          f"cuda:{index}")
@@ -46,6 +52,7 @@ def _heads(name, t, dtype, index, dim):
 
 def _cache(name, t, dtype, index, heads, dim):
     """t: [pages, page_size, heads, dim], each row contiguous."""
+    _tensor(name, t)
     if (t.dim() != 4 or t.dtype != dtype or t.get_device() != index or t.shape[2:] != (heads, dim)
             or t.stride()[2:] != (dim, 1)):
         raise ValueError(f"{name} must be a {dtype} tensor [pages, page_size, {heads}, {dim}] with contiguous rows "
@@ -53,6 +60,7 @@ def _cache(name, t, dtype, index, heads, dim):
 
 
 def _plain(name, t, dtype, index, *shape):
+    _tensor(name, t)
     if t.dtype != dtype or t.get_device() != index or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on cuda:{index}")
 
@@ -91,6 +99,8 @@ class QKNormRope:
         slot writes nothing), caches [pages, page_size, Hk, D].  Returns q_out
         (a new contiguous tensor, or the given one; it may be q)."""
         index = self._index
+        if index < 0:
+            raise ValueError("the operator was made on the CPU: its calls need a GPU")
         if _elsewhere(index, stream):
             with _On(index, stream):
                 return self.forward(q, k, v, q_weight, k_weight, positions, slots, k_cache, v_cache, q_out)
@@ -104,7 +114,8 @@ class QKNormRope:
         return got if q_out is None else q_out
 
     def _explain(self, index, q, k, v, q_weight, k_weight, positions, slots, k_cache, v_cache, q_out):
-        T, D, dt = q.shape[0], self.head_dim, q.dtype
+        _tensor("q", q)
+        D, dt = self.head_dim, q.dtype
         if dt not in _DTYPES:
             raise ValueError("q must be bf16 or fp16")
         for name, t in (("q", q), ("k", k), ("v", v)) + ((("q_out", q_out),) if q_out is not None else ()):
@@ -114,8 +125,8 @@ class QKNormRope:
         for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
             if t is not None:
                 _plain(name, t, dt, index, D)
-        _plain("positions", positions, torch.int32, index, T)
-        _plain("slots", slots, torch.int64, index, T)
+        _plain("positions", positions, torch.int32, index, q.shape[0])
+        _plain("slots", slots, torch.int64, index, q.shape[0])
         raise ValueError("q, k, v, q_out and the caches must agree in tokens, heads and pages")
 
     __call__ = forward
@@ -163,12 +174,14 @@ class PagedAttention:
         return (out, got[1]) if return_lse else out
 
     def _explain(self, q, k_cache, v_cache, block_table, q_starts, kv_lens, max_q_len, tree_mask, out):
+        _tensor("q", q)
         index, D, dt = self._index, self.head_dim, q.dtype
         if dt not in _DTYPES or q.dim() != 3 or q.shape[1] != self.n_heads:
             raise ValueError(f"q must be a bf16 or fp16 tensor [tokens, {self.n_heads}, {D}]")
         _heads("q", q, dt, index, D)
         for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
             _cache(name, t, dt, index, self.n_kv_heads, D)
+        _tensor("block_table", block_table)
         if (block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.get_device() != index
                 or block_table.stride(1) != 1):
             raise ValueError(f"block_table must be an int32 tensor [batch, pages] with contiguous rows on cuda:{index}")
@@ -179,7 +192,8 @@ class PagedAttention:
             _plain("tree_mask", tree_mask, torch.int64, index, q.shape[0])
         if out is not None:
             _heads("out", out, dt, index, D)
-        raise ValueError("the caches must have one shape, out q's, and max_q_len must be an int of 0 or more")
+        raise ValueError("the caches must have one shape, out q's, max_q_len must be an int of 0 or more and scale a "
+                         "number")
 
     __call__ = forward
 

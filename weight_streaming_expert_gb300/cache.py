@@ -8,10 +8,11 @@ import heapq
 import torch
 
 from . import native as N
-from .attention import _elsewhere, _On, _plain
+from .attention import _elsewhere, _On, _plain, _tensor
 
 
 def _copy(name, rows, k_pool, v_pool, src, dst, stream):
+    _tensor("k_pool", k_pool)
     index = k_pool.get_device()
     if index >= 0 and _elsewhere(index, stream):
         with _On(index, stream):
@@ -19,13 +20,15 @@ def _copy(name, rows, k_pool, v_pool, src, dst, stream):
     status = N.calls().copy(torch._C._cuda_getCurrentRawStream(index) if index >= 0 else 0, rows, k_pool, v_pool, src,
                             dst)
     if status < 0:
+        for n, t in (("v_pool", v_pool), ("src", src), ("dst", dst)):
+            _tensor(n, t)
         shape = k_pool.shape
         if len(shape) != 5 or index < 0:
             raise ValueError("the pools must be CUDA tensors [layers, pages, page_size, kv_heads, dim]")
         if v_pool.shape != shape or v_pool.dtype != k_pool.dtype or v_pool.get_device() != index:
             raise ValueError("the pools must have one shape, type and device")
         for n, t in (("src", src), ("dst", dst)):
-            _plain(n, t, torch.int64 if rows else torch.int32, index, src.shape[0])
+            _plain(n, t, torch.int64 if rows else torch.int32, index, src.numel())
         raise ValueError("the pools' pages must be contiguous")
     N.check(name, status)
 

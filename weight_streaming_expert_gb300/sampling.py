@@ -6,7 +6,7 @@ from __future__ import annotations
 import torch
 
 from . import native as N
-from .attention import _elsewhere, _On, _plain
+from .attention import _elsewhere, _On, _plain, _tensor
 
 
 def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, return_probs: bool = False,
@@ -17,6 +17,7 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
     and min_p, top_p >= 1 is off.  Returns int32 tokens [M] (-1 for a row
     without a logit above -inf), with ``return_probs`` also each token's
     probability among those that stayed, fp32 [M]."""
+    _tensor("logits", logits)
     index = logits.get_device()
     if index >= 0 and _elsewhere(index, stream):
         with _On(index, stream):
@@ -33,7 +34,8 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
 
 
 def _explain(index, logits, u, temperature, top_k, top_p, min_p, tokens):
-    if index < 0 or logits.dim() != 2 or logits.dtype != torch.float32 or logits.stride(1) != 1:
+    if (index < 0 or logits.dim() != 2 or logits.dtype != torch.float32
+            or (logits.shape[1] > 1 and logits.stride(1) != 1)):
         raise ValueError("logits must be an fp32 CUDA tensor [rows, vocab] with contiguous rows")
     M = logits.shape[0]
     for name, t, dt in (("u", u, torch.float32), ("temperature", temperature, torch.float32),
