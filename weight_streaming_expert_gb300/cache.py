@@ -95,7 +95,8 @@ class PageTable:
         """Pages of its own for the positions start..end-1 that lie in shared
         ones, if `spare` more stay free; returns the copies (from, to)."""
         pages, P = self._pages[seq], self.page_size
-        shared = [i for i in range(start // P, min(len(pages), -(-end // P))) if self._refs[pages[i]] > 1]
+        last = min(len(pages), -(-end // P)) if start < end else 0
+        shared = [i for i in range(start // P, last) if self._refs[pages[i]] > 1]
         if len(shared) + spare > len(self._free):
             raise MemoryError(f"out of pages: {len(self._free)} are free")
         copies = [(pages[i], self._take()) for i in shared]
