@@ -50,6 +50,15 @@ inline int check_device() {
   return MOE_OK;
 }
 
+// SMs of the current device, asked once per device.
+inline int sm_count() {
+  static thread_local int of = -1, count = 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev != of && cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) of = dev;
+  return count;
+}
+
 // Launches `kernel` so that its prologue may overlap the end of the previous
 // kernel on the stream; the kernel waits with pdl_wait() before it touches
 // global memory.  cluster > 1: thread-block clusters of that many CTAs.

@@ -285,7 +285,8 @@ int launch_rope(const moe_qk_norm_rope_args_t& a, moe_stream_t stream) {
   // with 8.  Beyond that a warp each, which works the angles out once: 16384
   // tokens of 32 + 8 heads of 128 take 59 us, with 2 warps 64, with 4 76.
   int warps = kRopeWarps;
-  while (warps > 1 && (long long)a.n_tokens * warps > 152ll * 4 * kRopeWarps) warps /= 2;
+  const long long resident = 4ll * sm_count() * kRopeWarps;
+  while (warps > 1 && a.n_tokens * (long long)warps > resident) warps /= 2;
   const int tokens = kRopeWarps / warps;
   return launch_pdl(kernel, dim3((unsigned)((a.n_tokens + tokens - 1) / tokens)), dim3(kRopeThreads), 0, stream, 1, a,
                     warps);
