@@ -128,8 +128,8 @@ typedef struct {
  */
 int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t stream);
 
-/* Synchronises the handle's device, then returns and clears the sticky status: MOE_OK, MOE_ERR_INVALID_ARG (bad pages or
- * lengths) or MOE_ERR_DEVICE_TIMEOUT; moe_last_error() names what was found. */
+/* Synchronises the handle's device, then returns and clears the sticky status: MOE_OK, MOE_ERR_INVALID_ARG (bad pages
+ * or lengths) or MOE_ERR_DEVICE_TIMEOUT; moe_last_error() names what was found. */
 int moe_attn_get_status(moe_attn_t* h);
 
 /* Frees the handle (NULL-safe); synchronises its device first. */

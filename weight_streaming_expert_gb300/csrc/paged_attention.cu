@@ -15,9 +15,13 @@
 // for all of them.  Per 64 positions one warp issues S = Q K^T into TMEM (128 x
 // 64 fp32), four warps turn S into probabilities, one row a thread with no
 // exchange between threads, and write them over S as the 16-bit A operand of
-// O += P V, which stays in TMEM (each probability is rounded once to the
-// element type; scores, statistics and sums are fp32).  Two such chains run
-// side by side, so that one's products cover the other's exponentials:
+// O += P V, which stays in TMEM.  Each probability is rounded once to the
+// element type, as the MMA takes both operands in one 16-bit type: against 64
+// bits the outputs are then 1.35 times as far off as by their own rounding
+// alone; scores, statistics and sums are fp32.  Two such chains run side by
+// side, so that one's products cover the other's exponentials (two tiles in
+// turn, and rescaling only where the maximum has grown, are published ideas for
+// attention kernels):
 //   pair   two tiles of rows over the same positions (chunks of many rows);
 //   split  one tile, the even 128 positions in one chain and the odd ones in
 //          the other, merged at the end (chunks of up to 128 rows, which are
@@ -30,7 +34,8 @@
 // 16384, 32/4 heads of 128: 1375 us before, 1205 us).  The split form waits
 // for memory anyway and takes both buffers' scores at once.
 // One warp copies the pages with TMA into a ring of 128-position tiles, another
-// the queries of the next tile.
+// the queries of the next tile, and in the pair form a third looks through the
+// values of positions that some rows do not see.
 //
 // The work is a list of (sequence, key/value head, tile of rows, 128
 // positions) in that order.  Every CTA takes a contiguous share of equal cost,
@@ -44,9 +49,9 @@
 // 1897 TFLOP/s in a burst and 1727 sustained):
 //   long chunks      the tensor pipe: 2650 of the 2800 clocks per 256 rows by
 //                    128 positions are MMAs.  8192 tokens over 16384: 1.17 ms,
-//                    1410 TFLOP/s.
+//                    1410 TFLOP/s, in a graph, 1.19 ms as a call among others.
 //   long decoding    reading the cache: 32 sequences of 2,000 to 32,768
-//                    positions, one token each: 131 us, 6.3 TB/s.
+//                    positions, one token each: 132 us, 6.3 TB/s.
 //   short calls      latencies: the plan, the first pages, one softmax, the
 //                    join: 6 tokens over 8192: 13 us, of which memory needs 2.5.
 #include <cuda_bf16.h>
@@ -391,7 +396,8 @@ __device__ __noinline__ void add_not_finite(const AttnParams& p, int b, int h, i
   const Veil veil = veil_of<kTiles>(p, s, tile);
   const int column0 = kPair ? 0 : chain * kColumns, local = kPair ? chain * kTile + r : r;
   const long long row = s.q0 + token;
-  T* out = static_cast<T*>(a.out) + row * a.out_token_stride + (h * p.group + r % p.group) * a.out_head_stride + column0;
+  const int head = h * p.group + r % p.group;
+  T* out = static_cast<T*>(a.out) + row * a.out_token_stride + head * a.out_head_stride + column0;
   float* part = p.part_o + ((long long)slot * kTiles * kTile + local) * D + column0;
   for (int pos = max(veil.lo, u0 * kTile); pos < min(veil.hi, u1 * kTile); ++pos) {
     const int other = pos - s.base;  // the chunk's token at that position
@@ -1384,8 +1390,8 @@ int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t strea
       !aligned(a->v_cache, 16) || !aligned(a->out, 16))
     return fail(MOE_ERR_INVALID_ARG, "q, out and the caches must be non-null and 16-byte aligned");
   const int table_pages = a->table_pages > 0 ? a->table_pages : a->table_stride;
-  if ((!a->block_table && table_pages > 0) || !a->q_starts || !a->kv_lens || !aligned(a->block_table, 4) || !aligned(a->q_starts, 4) ||
-      !aligned(a->kv_lens, 4) || !aligned(a->tree_mask, 8) || !aligned(a->lse, 4))
+  if ((!a->block_table && table_pages > 0) || !a->q_starts || !a->kv_lens || !aligned(a->block_table, 4) ||
+      !aligned(a->q_starts, 4) || !aligned(a->kv_lens, 4) || !aligned(a->tree_mask, 8) || !aligned(a->lse, 4))
     return fail(MOE_ERR_INVALID_ARG, "block_table, q_starts and kv_lens must be non-null, and all aligned");
   if ((a->q_token_stride | a->q_head_stride | a->out_token_stride | a->out_head_stride | a->k_page_stride |
        a->k_row_stride | a->v_page_stride | a->v_row_stride) & 7)
