@@ -1,7 +1,9 @@
 /*
  * sampling.h -- C ABI of drawing each row's next token from its logits, with
  * temperature, top-k, top-p and min-p, from a given uniform number: the step
- * after the vocabulary projection of lm_head.h.
+ * after the vocabulary projection of lm_head.h.  Between the two
+ * moe_adjust_logits (at the end) applies penalties for repeated tokens, biases
+ * and a grammar's mask to the logits.
  *
  * Row m, with l its logits (NaN counts as -inf) and l0 the largest:
  *   weight      w_i = floor(2^38 * exp((l_i - l0) / temperature)), the
@@ -46,6 +48,44 @@ extern "C" {
 int moe_sample(const float* logits, int64_t row_stride, int rows, int vocab, const float* u, const float* temperature,
                const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens, float* probs,
                moe_stream_t stream);
+
+/*
+ * moe_adjust_logits -- row m of logits, x its value for token v, becomes
+ *   x / repetition if x > 0, else x * repetition, where v stands anywhere in
+ *                    the row's part of the history (prompt and answer);
+ *   x - frequency * (how often v stands in the answer);
+ *   x - presence     where it does at all;
+ *   x + bias         of the last entry for v in the row's part of the list;
+ *   -inf             where v's bit of the row's mask is 0 (whatever x was),
+ * each step in fp32 and rounded.  What is not given is left out; a NaN without
+ * a mask's 0 stays one.  The same inputs give the same bits every time.
+ * Asynchronous on `stream`, allocates nothing, can be captured into a graph.
+ */
+typedef struct {
+  const float* logits;     /* device, row m at logits + m*row_stride elements, 4-byte aligned */
+  int64_t row_stride;
+  float* out;              /* the same shape; may be logits itself (then only what changes is written), else may not
+                              overlap it */
+  int64_t out_stride;
+  int rows, vocab;         /* rows 0..65535 (0: no work), vocab 1..MOE_SAMPLE_MAX_VOCAB */
+  const int32_t* history;  /* device [n_history]: tokens; those outside the vocabulary are ignored; may be NULL */
+  int n_history;
+  const int32_t* spans;    /* device [rows][3]: (begin, answer, end), the row's history is begin..end-1, its answer
+                              answer..end-1; rows may share history; cut to 0..n_history.  Not NULL with history */
+  const float* repetition; /* device [rows] or NULL */
+  const float* presence;   /* device [rows] or NULL */
+  const float* frequency;  /* device [rows] or NULL */
+  const int32_t* bias_ids; /* device [n_biases], or NULL: tokens; those outside the vocabulary are ignored */
+  const float* bias_values;
+  int n_biases;
+  const int32_t* bias_starts; /* device [rows + 1]: row m has entries bias_starts[m] .. bias_starts[m+1]-1, cut to
+                              0..n_biases */
+  const uint32_t* allowed; /* device, row m at allowed + m*allowed_stride words: bit v % 32 of word v / 32; or NULL */
+  int64_t allowed_stride;  /* 0: the rows share one mask */
+} moe_adjust_logits_args_t;
+
+/* MOE_ERR_INVALID_ARG for bad pointers or sizes, MOE_ERR_CUDA if the launch fails. */
+int moe_adjust_logits(const moe_adjust_logits_args_t* a, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,225 @@
+// logits.cu -- penalties for repeated tokens, biases and grammar masks on
+// logits before the draw (include/sampling.h).
+//
+// Per row and token: x / r or x * r for tokens of the history, - f * count - p
+// for those of the answer, + bias, -inf where the mask says no.  A logit is
+// read and written once (8 bytes, and 1/8 of mask), so memory bounds large
+// batches and latencies small ones.
+//
+// A CTA takes kSlice tokens of a row.  It asks for their logits first, then
+// counts the row's history in a table in shared memory with a word per token
+// (whole numbers: any order gives the same), and meanwhile the logits arrive.
+// The history is read by each of a row's CTAs, from L2: 4,000 tokens are 16 KB
+// against the 32 KB of logits that a CTA moves.  Of several biases for a token
+// the last in the list holds: a second table takes the largest entry number.
+//
+// In place nothing is asked for ahead: only tokens that change are read, and
+// those that the mask forbids only written.
+#include "host_util.cuh"
+#include "sampling.h"
+
+namespace wse {
+namespace {
+
+constexpr int kLogitThreads = 256;
+constexpr int kLogitLoads = 4;                              // float4 of a thread
+constexpr int kSlice = kLogitThreads * kLogitLoads * 4;     // tokens of a CTA
+constexpr uint32_t kPromptOnly = 0x80000000u;               // of a count word: it stands in the prompt
+
+struct Span {
+  int begin, answer, end;
+};
+
+// (begin, answer, end) of a row, cut to the history.
+__device__ __forceinline__ Span span_of(const moe_adjust_logits_args_t& a, int row) {
+  const int32_t* s = a.spans + 3ll * row;
+  Span r;
+  r.begin = max(s[0], 0);
+  r.end = min(s[2], a.n_history);
+  r.answer = max(s[1], r.begin);
+  return r;
+}
+
+// The slice's tokens are numbered from the 16-byte boundary at or before the
+// row's first logit, so that a thread's four lie in one aligned load whatever
+// the row's address: token = number - shift.  kInPlace: out is logits.
+// kAligned: the output rows lie on the same remainder of 16 bytes.
+template <bool kInPlace, bool kAligned>
+__global__ void __launch_bounds__(kLogitThreads) adjust_logits_kernel(const __grid_constant__ moe_adjust_logits_args_t a) {
+  extern __shared__ uint4 table_words[];  // kSlice counts, then kSlice bias numbers (each only where given)
+  const int tid = threadIdx.x, row = blockIdx.y;
+  pdl_wait();
+  pdl_launch_dependents();
+  const float* in = a.logits + row * a.row_stride;
+  float* out = a.out + row * a.out_stride;
+  const int shift = (int)(reinterpret_cast<uintptr_t>(in) >> 2 & 3);
+  const int first = (int)blockIdx.x * kSlice - shift;  // token number 0 of the slice
+  const bool counts = a.history != nullptr, biases = a.bias_ids != nullptr;
+  uint32_t* count_of = reinterpret_cast<uint32_t*>(table_words);
+  int* bias_of = reinterpret_cast<int*>(count_of) + (counts ? kSlice : 0);
+  const uint32_t* allowed = a.allowed ? a.allowed + row * a.allowed_stride : nullptr;
+
+  // the thread's four tokens of load i, their bits of the mask (those past the
+  // vocabulary's ends are 0 in `inside`)
+  auto token_of = [&](int i) { return first + (i * kLogitThreads + tid) * 4; };
+  auto inside_of = [&](int v) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) bits |= (unsigned)(v + k) < (unsigned)a.vocab ? 1u << k : 0u;
+    return bits;
+  };
+  auto bits_of = [&](int v, uint32_t inside) {
+    if (!allowed || !inside) return inside;
+    const int v0 = max(v, 0), v3 = min(v + 3, a.vocab - 1);
+    const uint64_t words = allowed[v0 >> 5] | (uint64_t)allowed[v3 >> 5] << 32;
+    uint32_t bits = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int at = (v + k & 31) + ((v + k) >> 5 == v0 >> 5 ? 0 : 32);
+      bits |= (uint32_t)(words >> at & 1) << k;
+    }
+    return bits & inside;
+  };
+  auto load4 = [&](int v, uint32_t wanted) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (inside_of(v) == 15u) {
+      if (wanted) x = *reinterpret_cast<const float4*>(in + v);
+    } else {
+      if (wanted & 1) x.x = in[v];
+      if (wanted & 2) x.y = in[v + 1];
+      if (wanted & 4) x.z = in[v + 2];
+      if (wanted & 8) x.w = in[v + 3];
+    }
+    return x;
+  };
+
+  uint32_t allow[kLogitLoads];
+  float4 x[kLogitLoads];
+#pragma unroll
+  for (int i = 0; i < kLogitLoads; ++i) allow[i] = bits_of(token_of(i), inside_of(token_of(i)));
+  if (!kInPlace) {
+#pragma unroll
+    for (int i = 0; i < kLogitLoads; ++i) x[i] = load4(token_of(i), allow[i]);
+  }
+
+  // ---- the tables
+  if (counts || biases) {
+    const int words = ((counts ? kSlice : 0) + (biases ? kSlice : 0)) / 4;
+    for (int i = tid; i < words; i += kLogitThreads) table_words[i] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+    auto place_of = [&](int token) {  // in the slice, else past it
+      return (unsigned)token < (unsigned)a.vocab ? (unsigned)(token - first) : ~0u;
+    };
+    if (counts) {
+      const Span s = span_of(a, row);
+#pragma unroll 4
+      for (int i = s.begin + tid; i < s.end; i += kLogitThreads) {
+        const unsigned at = place_of(a.history[i]);
+        if (at >= (unsigned)kSlice) continue;
+        if (i >= s.answer)
+          atomicAdd(count_of + at, 1u);
+        else
+          atomicOr(count_of + at, kPromptOnly);
+      }
+    }
+    if (biases) {
+      const int from = max(a.bias_starts[row], 0), to = min(a.bias_starts[row + 1], a.n_biases);
+      for (int i = from + tid; i < to; i += kLogitThreads) {
+        const unsigned at = place_of(a.bias_ids[i]);
+        if (at < (unsigned)kSlice) atomicMax(bias_of + at, i - from + 1);
+      }
+    }
+    __syncthreads();
+  }
+
+  // ---- the logits
+  const float rep = a.repetition ? a.repetition[row] : 1.f, presence = a.presence ? a.presence[row] : 0.f;
+  const float frequency = a.frequency ? a.frequency[row] : 0.f;
+  auto adjusted = [&](float v, uint32_t word, int bias) {
+    if (word) {
+      if (a.repetition) v = v > 0.f ? __fdiv_rn(v, rep) : __fmul_rn(v, rep);
+      if (const uint32_t count = word & ~kPromptOnly) {
+        if (a.frequency) v = __fsub_rn(v, __fmul_rn(frequency, (float)count));
+        if (a.presence) v = __fsub_rn(v, presence);
+      }
+    }
+    if (bias) v = __fadd_rn(v, a.bias_values[max(a.bias_starts[row], 0) + bias - 1]);
+    return v;
+  };
+#pragma unroll
+  for (int i = 0; i < kLogitLoads; ++i) {
+    const int v = token_of(i), at = v - first;
+    const uint32_t inside = inside_of(v);
+    if (!inside) continue;
+    uint4 word = make_uint4(0u, 0u, 0u, 0u);
+    int4 bias = make_int4(0, 0, 0, 0);
+    if (counts) word = *reinterpret_cast<const uint4*>(count_of + at);
+    if (biases) bias = *reinterpret_cast<const int4*>(bias_of + at);
+    const uint32_t* w = &word.x;
+    const int* b = &bias.x;
+    uint32_t touched = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) touched |= w[k] || b[k] ? 1u << k : 0u;
+    if (kInPlace) {
+      const uint32_t change = touched & allow[i];
+      if (change) x[i] = load4(v, change);
+    }
+    float* p = &x[i].x;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (touched >> k & 1) p[k] = adjusted(p[k], w[k], b[k]);
+      if (!(allow[i] >> k & 1)) p[k] = -INFINITY;
+    }
+    if (kInPlace) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if ((inside >> k & 1) && ((touched >> k & 1) || !(allow[i] >> k & 1))) out[v + k] = p[k];
+    } else if (kAligned && inside == 15u) {
+      *reinterpret_cast<float4*>(out + v) = x[i];
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (inside >> k & 1) out[v + k] = p[k];
+    }
+  }
+}
+
+}  // namespace
+}  // namespace wse
+
+using namespace wse;
+
+extern "C" int moe_adjust_logits(const moe_adjust_logits_args_t* a, moe_stream_t stream) {
+  if (!a) return fail(MOE_ERR_INVALID_ARG, "null arguments");
+  if (a->rows < 0 || a->rows > 65535) return fail(MOE_ERR_INVALID_ARG, "rows = %d: must be in 0..65535", a->rows);
+  if (a->vocab < 1 || a->vocab > MOE_SAMPLE_MAX_VOCAB)
+    return fail(MOE_ERR_INVALID_ARG, "vocab = %d: must be in 1..%d", a->vocab, MOE_SAMPLE_MAX_VOCAB);
+  if (a->n_history < 0 || a->n_biases < 0)
+    return fail(MOE_ERR_INVALID_ARG, "n_history and n_biases must be 0 or more");
+  if (a->rows == 0) return MOE_OK;
+  if (!a->logits || !a->out || !aligned(a->logits, 4) || !aligned(a->out, 4))
+    return fail(MOE_ERR_INVALID_ARG, "logits and out must be non-null and 4-byte aligned");
+  if (a->history && !a->spans) return fail(MOE_ERR_INVALID_ARG, "a history needs spans");
+  if (a->bias_ids && (!a->bias_values || !a->bias_starts))
+    return fail(MOE_ERR_INVALID_ARG, "bias_ids need bias_values and bias_starts");
+  if (!aligned(a->history, 4) || !aligned(a->spans, 4) || !aligned(a->repetition, 4) || !aligned(a->presence, 4) ||
+      !aligned(a->frequency, 4) || !aligned(a->bias_ids, 4) || !aligned(a->bias_values, 4) ||
+      !aligned(a->bias_starts, 4) || !aligned(a->allowed, 4))
+    return fail(MOE_ERR_INVALID_ARG, "every array must be 4-byte aligned");
+  if (a->rows > 1 && (a->row_stride < 0 || a->out_stride < a->vocab))
+    return fail(MOE_ERR_INVALID_ARG, "row strides must be 0 or more, and out's rows may not overlap");
+  if (a->allowed_stride < 0) return fail(MOE_ERR_INVALID_ARG, "allowed_stride must be 0 or more");
+  const bool in_place = a->out == a->logits;
+  if (in_place && a->rows > 1 && a->out_stride != a->row_stride)
+    return fail(MOE_ERR_INVALID_ARG, "logits adjusted in place have one row stride");
+  const int rc = check_device();
+  if (rc != MOE_OK) return rc;
+  // up to three numbers before the first token, see `shift`
+  const unsigned slices = (unsigned)((a->vocab + 3 + kSlice - 1) / kSlice);
+  const size_t smem = ((a->history ? 4u : 0u) + (a->bias_ids ? 4u : 0u)) * kSlice;
+  const bool same = ((reinterpret_cast<uintptr_t>(a->logits) ^ reinterpret_cast<uintptr_t>(a->out)) & 15) == 0 &&
+                    (a->rows == 1 || ((a->row_stride ^ a->out_stride) & 3) == 0);
+  return launch_pdl(in_place ? adjust_logits_kernel<true, true>
+                             : same ? adjust_logits_kernel<false, true> : adjust_logits_kernel<false, false>,
+                    dim3(slices, (unsigned)a->rows), dim3(kLogitThreads), smem, stream, 1, *a);
+}

@@ -204,6 +204,42 @@ PyObject* sample(Args x) {
   return l ? Py_BuildValue("(NN)", o, l) : (Py_DECREF(o), nullptr);
 }
 
+PyObject* adjust_logits(Args x) {
+  const int64_t stream = x.integer();
+  const Tensor logits = x.tensor(), history = x.tensor(true), spans = x.tensor(true), repetition = x.tensor(true);
+  const Tensor presence = x.tensor(true), frequency = x.tensor(true), ids = x.tensor(true), values = x.tensor(true);
+  const Tensor starts = x.tensor(true), allowed = x.tensor(true);
+  Tensor out = x.tensor(true);
+  if (x.bad || logits.dim() != 2 || !logits.is_cuda()) return number(kDoesNotFit);
+  const int64_t gpu = logits.get_device(), M = logits.size(0), V = logits.size(1), words = (V + 31) / 32;
+  auto row = [&](const Tensor& t) { return !t.defined() || plain(t, at::kFloat, M, gpu); };
+  // [M, columns], rows any distance apart
+  auto rows_of = [&](const Tensor& t, at::ScalarType type, int64_t columns) {
+    return t.dim() == 2 && t.scalar_type() == type && on(t, gpu) && t.size(0) == M && t.size(1) == columns &&
+           (columns < 2 || t.stride(1) == 1);
+  };
+  if (!rows_of(logits, at::kFloat, V) || (out.defined() && !rows_of(out, at::kFloat, V)) || !row(repetition) ||
+      !row(presence) || !row(frequency) || history.defined() != spans.defined() ||
+      (history.defined() && (!plain(history, at::kInt, history.numel(), gpu) || !rows_of(spans, at::kInt, 3) ||
+                             !spans.is_contiguous() || !fits_int(history.numel()))) ||
+      ids.defined() != values.defined() || ids.defined() != starts.defined() ||
+      (ids.defined() && (!plain(ids, at::kInt, ids.numel(), gpu) || !plain(values, at::kFloat, ids.numel(), gpu) ||
+                         !plain(starts, at::kInt, M + 1, gpu) || !fits_int(ids.numel()))) ||
+      (allowed.defined() && !rows_of(allowed, at::kInt, words)) || !fits_int(M) || !fits_int(V))
+    return number(kDoesNotFit);
+  if (!out.defined()) out = at::empty({M, V}, logits.options());
+  const moe_adjust_logits_args_t a{ptr<float>(logits), logits.stride(0), ptr<float>(out), out.stride(0), (int)M, (int)V,
+                                   // an empty history or list has no address
+                                   history.defined() && history.numel() > 0 ? ptr<int32_t>(history) : nullptr,
+                                   history.defined() ? (int)history.numel() : 0, ptr<int32_t>(spans),
+                                   ptr<float>(repetition), ptr<float>(presence), ptr<float>(frequency),
+                                   ids.defined() && ids.numel() > 0 ? ptr<int32_t>(ids) : nullptr, ptr<float>(values),
+                                   ids.defined() ? (int)ids.numel() : 0, ptr<int32_t>(starts),
+                                   ptr<uint32_t>(allowed), allowed.defined() ? allowed.stride(0) : 0};
+  const int status = moe_adjust_logits(&a, reinterpret_cast<moe_stream_t>(stream));
+  return status == MOE_OK ? THPVariable_Wrap(std::move(out)) : number(status);
+}
+
 // C++ exceptions (of an allocation, say) become the Python ones that PyTorch's
 // own calls raise.
 template <PyObject* (*kCall)(Args)>
@@ -222,6 +258,7 @@ PyMethodDef methods[] = {{"qk_norm_rope", entry<qk_norm_rope>(), METH_FASTCALL, 
                          {"attention", entry<attention>(), METH_FASTCALL, nullptr},
                          {"copy", entry<copy>(), METH_FASTCALL, nullptr},
                          {"sample", entry<sample>(), METH_FASTCALL, nullptr},
+                         {"adjust_logits", entry<adjust_logits>(), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "wse_calls", nullptr, -1, methods};
 

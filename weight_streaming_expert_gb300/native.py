@@ -84,6 +84,13 @@ class moe_attn_args_t(ctypes.Structure):
                 ("lse", _p), ("table_pages", _i)]
 
 
+class moe_adjust_logits_args_t(ctypes.Structure):
+    _fields_ = [("logits", _p), ("row_stride", _l), ("out", _p), ("out_stride", _l), ("rows", _i), ("vocab", _i),
+                ("history", _p), ("n_history", _i), ("spans", _p), ("repetition", _p), ("presence", _p),
+                ("frequency", _p), ("bias_ids", _p), ("bias_values", _p), ("n_biases", _i), ("bias_starts", _p),
+                ("allowed", _p), ("allowed_stride", _l)]
+
+
 class MoEError(RuntimeError):
     def __init__(self, fn, status, msg):
         super().__init__(f"{fn}: {STATUS_NAMES.get(status, status)}: {msg}")
@@ -177,6 +184,8 @@ def lib(build_if_missing: bool = True):
         L.moe_copy_rows.restype = ci
         L.moe_sample.argtypes = [vp, i64, ci, ci, vp, vp, vp, vp, vp, vp, vp, vp]
         L.moe_sample.restype = ci
+        L.moe_adjust_logits.argtypes = [ctypes.POINTER(moe_adjust_logits_args_t), vp]
+        L.moe_adjust_logits.restype = ci
         L.moe_last_error.argtypes = []
         L.moe_last_error.restype = ctypes.c_char_p
         _lib = L
