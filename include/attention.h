@@ -70,6 +70,43 @@ typedef struct {
 
 int moe_qk_norm_rope(const moe_qk_norm_rope_args_t* a, moe_stream_t stream);
 
+/* The scales of one layer of the quantised cache: row r of page p and head h at
+ * scale + p*page_stride + h*head_stride + r, in bytes. */
+typedef struct {
+  void* k_scale;
+  void* v_scale;
+  int64_t k_page_stride, k_head_stride, v_page_stride, v_head_stride;
+} moe_cache_scales_t;
+
+/*
+ * The same with a quantised cache: a's caches hold codes (strides in bytes).
+ * Keys are quantised from their fp32 values after norm and rotation, not
+ * rounded to 16 bits in between.
+ */
+int moe_qk_norm_rope_e4m3(const moe_qk_norm_rope_args_t* a, const moe_cache_scales_t* s, moe_stream_t stream);
+
+/*
+ * moe_read_e4m3 -- rows of the quantised cache as 16-bit elements: token t of
+ * the outputs is what lies in slots[t], zeros for a slot outside [0, n_pages *
+ * page_size).  Exact in bf16; in fp16 rounded below 2^-14 and cut to +-65504.
+ */
+typedef struct {
+  int dtype;               /* MOE_DTYPE_* of the outputs */
+  int n, n_kv_heads;       /* 0: no work */
+  int head_dim;            /* 64, 128 or 256 */
+  const void* k_cache;     /* device, codes of one layer, 16-byte aligned */
+  const void* v_cache;
+  int64_t k_page_stride, k_row_stride, v_page_stride, v_row_stride; /* bytes, multiples of 16 */
+  moe_cache_scales_t scales;
+  int n_pages, page_size;
+  const int64_t* slots;    /* device [n] */
+  void* k_out;             /* device, token t head h at k_out + t*k_token_stride + h*k_head_stride elements, 16-byte */
+  void* v_out;             /* aligned */
+  int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride; /* multiples of 8 */
+} moe_read_e4m3_args_t;
+
+int moe_read_e4m3(const moe_read_e4m3_args_t* a, moe_stream_t stream);
+
 /*
  * Attention of new tokens over the paged cache.  Sequence b of the batch has
  * the new tokens q_starts[b] .. q_starts[b+1]-1 (n of them, any count) and
@@ -157,6 +194,17 @@ int moe_copy_pages(void* k_pool, void* v_pool, int n_layers, int64_t k_layer_str
 int moe_copy_rows(void* k_pool, void* v_pool, int n_layers, int64_t k_layer_stride, int64_t v_layer_stride,
                   int64_t k_page_stride, int64_t v_page_stride, int n_pages, int page_size, int64_t row_bytes,
                   const int64_t* src, const int64_t* dst, int n, moe_stream_t stream);
+
+/*
+ * moe_copy_scales -- the scales of rows that moe_copy_rows moves in a quantised
+ * cache: of slot dst[i] those of slot src[i], for every head and layer, as if
+ * all were read before any is written.  Strides in bytes; n <=
+ * MOE_COPY_ROWS_MAX.  (Whole pages of scales move with moe_copy_pages.)
+ */
+int moe_copy_scales(void* k_scales, void* v_scales, int n_layers, int64_t k_layer_stride, int64_t v_layer_stride,
+                    int64_t k_page_stride, int64_t v_page_stride, int64_t k_head_stride, int64_t v_head_stride,
+                    int n_pages, int page_size, int n_kv_heads, const int64_t* src, const int64_t* dst, int n,
+                    moe_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -13,7 +13,8 @@ import importlib
 
 _HOMES = {"MoELayer": "layer", "LmHead": "layer", "tp_slice": "layer", "combine_partials": "layer",
           "QKNormRope": "attention", "PagedAttention": "attention", "PagedKVCache": "cache", "PageTable": "cache",
-          "copy_pages": "cache", "copy_rows": "cache", "sample": "sampling",
+          "copy_pages": "cache", "copy_rows": "cache", "read_cache": "cache",
+          "sample": "sampling",
           "adjust_logits": "sampling"}
 __all__ = list(_HOMES)
 

@@ -59,6 +59,27 @@ def _cache(name, t, dtype, index, heads, dim):
                          f"on cuda:{index}")
 
 
+def _scale(name, t, cache, index):
+    """t: the scale bytes of a quantised cache [pages, page_size, heads, dim]."""
+    _tensor(name, t)
+    pages, page_size, heads = cache.shape[:3]
+    if (t.dtype != torch.uint8 or t.get_device() != index or t.shape != (pages, heads, page_size)
+            or (page_size > 1 and t.stride(2) != 1)):
+        raise ValueError(f"{name} must be a uint8 tensor [{pages}, {heads}, {page_size}] with contiguous rows on "
+                         f"cuda:{index}")
+
+
+def _caches(k_cache, v_cache, k_scale, v_scale, dtype, index, heads, dim):
+    """The caches of one layer: of `dtype`, or with scales of E4M3 codes."""
+    if k_scale is not None or v_scale is not None:
+        dtype = torch.float8_e4m3fn
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _cache(name, t, dtype, index, heads, dim)
+    if k_scale is not None or v_scale is not None:
+        for name, t, cache in (("k_scale", k_scale, k_cache), ("v_scale", v_scale, v_cache)):
+            _scale(name, t, cache, index)
+
+
 def _plain(name, t, dtype, index, *shape):
     _tensor(name, t)
     if t.dtype != dtype or t.get_device() != index or t.shape != shape or not t.is_contiguous():
@@ -93,35 +114,40 @@ class QKNormRope:
         self.device = self.turns.device
         self._index = self.turns.get_device()
 
-    def forward(self, q, k, v, q_weight, k_weight, positions, slots, k_cache, v_cache, q_out=None, stream=None):
+    def forward(self, q, k, v, q_weight, k_weight, positions, slots, k_cache, v_cache, q_out=None, stream=None,
+                k_scale=None, v_scale=None):
         """q [T, Hq, D], k and v [T, Hk, D] (views of one projection are fine),
         weights [D] or None, positions int32 [T], slots int64 [T] (a negative
         slot writes nothing), caches [pages, page_size, Hk, D].  Returns q_out
-        (a new contiguous tensor, or the given one; it may be q)."""
+        (a new contiguous tensor, or the given one; it may be q).  With k_scale
+        and v_scale (uint8 [pages, Hk, page_size]) the caches are quantised:
+        float8_e4m3fn codes, a power of two for each row of a head."""
         index = self._index
         if index < 0:
             raise ValueError("the operator was made on the CPU: its calls need a GPU")
         if _elsewhere(index, stream):
             with _On(index, stream):
-                return self.forward(q, k, v, q_weight, k_weight, positions, slots, k_cache, v_cache, q_out)
+                return self.forward(q, k, v, q_weight, k_weight, positions, slots, k_cache, v_cache, q_out, None,
+                                    k_scale, v_scale)
         got = N.calls().qk_norm_rope(index, torch._C._cuda_getCurrentRawStream(index), self.head_dim, self.rotary_dim,
                                      self.interleaved, self.eps, self.turns, q, k, v, q_weight, k_weight, positions,
-                                     slots, k_cache, v_cache, q_out)
+                                     slots, k_cache, v_cache, q_out, k_scale, v_scale)
         if isinstance(got, int):
             if got < 0:
-                self._explain(index, q, k, v, q_weight, k_weight, positions, slots, k_cache, v_cache, q_out)
+                self._explain(index, q, k, v, q_weight, k_weight, positions, slots, k_cache, v_cache, q_out, k_scale,
+                              v_scale)
             N.check("moe_qk_norm_rope", got)
         return got if q_out is None else q_out
 
-    def _explain(self, index, q, k, v, q_weight, k_weight, positions, slots, k_cache, v_cache, q_out):
+    def _explain(self, index, q, k, v, q_weight, k_weight, positions, slots, k_cache, v_cache, q_out, k_scale,
+                 v_scale):
         _tensor("q", q)
         D, dt = self.head_dim, q.dtype
         if dt not in _DTYPES:
             raise ValueError("q must be bf16 or fp16")
         for name, t in (("q", q), ("k", k), ("v", v)) + ((("q_out", q_out),) if q_out is not None else ()):
             _heads(name, t, dt, index, D)
-        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-            _cache(name, t, dt, index, k.shape[1], D)
+        _caches(k_cache, v_cache, k_scale, v_scale, dt, index, k.shape[1], D)
         for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
             if t is not None:
                 _plain(name, t, dt, index, D)

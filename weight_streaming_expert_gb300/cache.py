@@ -8,7 +8,7 @@ import heapq
 import torch
 
 from . import native as N
-from .attention import _elsewhere, _On, _plain, _tensor
+from .attention import _cache, _elsewhere, _heads, _On, _plain, _scale, _tensor
 
 
 def _copy(name, rows, k_pool, v_pool, src, dst, stream):
@@ -33,18 +33,91 @@ def _copy(name, rows, k_pool, v_pool, src, dst, stream):
     N.check(name, status)
 
 
-def copy_pages(k_pool, v_pool, src, dst, stream=None):
+def _scale_pools(k_pool, v_pool, k_scale, v_scale):
+    """Looks over the scales [L, P, Hk, page_size] of quantised pools."""
+    for name, t, pool_name, pool in (("k_scale", k_scale, "k_pool", k_pool), ("v_scale", v_scale, "v_pool", v_pool)):
+        _tensor(name, t)
+        _tensor(pool_name, pool)
+        if pool.dim() != 5:
+            raise ValueError("the pools must be CUDA tensors [layers, pages, page_size, kv_heads, dim]")
+        L, P, page_size, heads, _ = pool.shape
+        if (t.dtype != torch.uint8 or t.shape != (L, P, heads, page_size) or t.device != pool.device
+                or (page_size > 1 and t.stride(3) != 1)):
+            raise ValueError(f"{name} must be a uint8 tensor [{L}, {P}, {heads}, {page_size}] with contiguous rows "
+                             f"beside {pool_name}")
+
+
+def copy_pages(k_pool, v_pool, src, dst, stream=None, k_scale=None, v_scale=None):
     """Page dst[i] := page src[i] in every layer of both pools [L, P, page_size,
     Hk, D] (pages contiguous, layers and pages any distance apart); src, dst:
-    int32 CUDA tensors [n].  No page may be in dst twice or in both lists."""
+    int32 CUDA tensors [n].  No page may be in dst twice or in both lists.
+    k_scale, v_scale [L, P, Hk, page_size] (pages contiguous): those of
+    quantised pools, which move too."""
+    quantised = k_scale is not None or v_scale is not None
+    if quantised:
+        _scale_pools(k_pool, v_pool, k_scale, v_scale)
+        if any(t.stride(2) != t.shape[3] for t in (k_scale, v_scale)):
+            raise ValueError("the scales' pages must be contiguous")
     _copy("moe_copy_pages", False, k_pool, v_pool, src, dst, stream)
+    if quantised:
+        _copy("moe_copy_pages", False, k_scale.unsqueeze(2), v_scale.unsqueeze(2), src, dst, stream)
 
 
-def copy_rows(k_pool, v_pool, src, dst, stream=None):
+def copy_rows(k_pool, v_pool, src, dst, stream=None, k_scale=None, v_scale=None):
     """Cache rows dst[i] := src[i] in every layer of both pools, as if all were
     read before any is written; src, dst: int64 CUDA tensors [n] of slots (page
-    * page_size + row), n up to 64, no slot in dst twice."""
+    * page_size + row), n up to 64, no slot in dst twice.  k_scale, v_scale [L,
+    P, Hk, page_size]: those of quantised pools, which move too."""
+    quantised = k_scale is not None or v_scale is not None
+    if quantised:
+        _scale_pools(k_pool, v_pool, k_scale, v_scale)
     _copy("moe_copy_rows", True, k_pool, v_pool, src, dst, stream)
+    if quantised:
+        index = k_scale.get_device()
+        if _elsewhere(index, stream):
+            with _On(index, stream):
+                return _copy_scales(index, k_scale, v_scale, src, dst)
+        _copy_scales(index, k_scale, v_scale, src, dst)
+
+
+def _copy_scales(index, k_scale, v_scale, src, dst):
+    status = N.calls().copy_scales(torch._C._cuda_getCurrentRawStream(index), k_scale, v_scale, src, dst)
+    if status < 0:
+        raise ValueError("the scales must have one shape and device")
+    N.check("moe_copy_scales", status)
+
+
+def read_cache(k_cache, v_cache, k_scale, v_scale, slots, dtype=torch.bfloat16, k_out=None, v_out=None, stream=None):
+    """Rows of one layer of the quantised cache (float8_e4m3fn codes [pages,
+    page_size, Hk, D], scales uint8 [pages, Hk, page_size]) as keys and values
+    [n, Hk, D] of `dtype`: row i is what lies in slots[i] (int64 [n]), zeros for
+    a slot outside the cache.  Exact in bf16."""
+    _tensor("k_cache", k_cache)
+    index = k_cache.get_device()
+    if index >= 0 and _elsewhere(index, stream):
+        with _On(index, stream):
+            return read_cache(k_cache, v_cache, k_scale, v_scale, slots, dtype, k_out, v_out)
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("dtype must be bf16 or fp16")
+    got = N.calls().read_cache(torch._C._cuda_getCurrentRawStream(index) if index >= 0 else 0, dtype == torch.bfloat16,
+                               k_cache, v_cache, k_scale, v_scale, slots, k_out, v_out)
+    if isinstance(got, int):
+        if got < 0:
+            if k_cache.dim() != 4 or index < 0:
+                raise ValueError("k_cache must be a float8_e4m3fn CUDA tensor [pages, page_size, kv_heads, dim]")
+            heads, dim = k_cache.shape[2:]
+            for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+                _cache(name, t, torch.float8_e4m3fn, index, heads, dim)
+            for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+                _scale(name, t, k_cache, index)
+            _tensor("slots", slots)
+            _plain("slots", slots, torch.int64, index, slots.numel())
+            for name, t in (("k_out", k_out), ("v_out", v_out)):
+                if t is not None:
+                    _heads(name, t, dtype, index, dim)
+            raise ValueError("the caches must have one shape, and the outputs a row for each slot and head")
+        N.check("moe_read_e4m3", got)
+    return k_out if k_out is not None else got[0], v_out if v_out is not None else got[1]
 
 
 class PageTable:
@@ -165,6 +238,9 @@ class PageTable:
 class PagedKVCache:
     """Keys and values of ``n_layers`` layers, ``k`` and ``v`` [L, n_pages,
     page_size, n_kv_heads, head_dim], and the sequences that hold its pages.
+    With dtype float8_e4m3fn the cache is quantised: ``k_scale`` and ``v_scale``
+    (uint8 [L, n_pages, n_kv_heads, page_size]) hold a power of two for each row
+    of a head, else they are None; ``layer(i)`` is what the calls of a layer take.
     The moves run on the current stream (or ``stream``), before what the caller
     enqueues there next."""
 
@@ -176,7 +252,20 @@ class PagedKVCache:
         self.table = PageTable(n_pages, page_size, -(-max_len // page_size))
         self.k = torch.zeros(shape, dtype=dtype, device=device)
         self.v = torch.zeros(shape, dtype=dtype, device=device)
+        self.k_scale = self.v_scale = None
+        if dtype == torch.float8_e4m3fn:
+            shape = (n_layers, n_pages, n_kv_heads, page_size)
+            self.k_scale = torch.full(shape, 127, dtype=torch.uint8, device=device)
+            self.v_scale = torch.full(shape, 127, dtype=torch.uint8, device=device)
         self.device = self.k.device
+
+    def layer(self, i: int) -> dict:
+        """k_cache and v_cache of a layer, with its scales if it is quantised, as
+        named arguments of ``QKNormRope`` and ``PagedAttention``."""
+        caches = dict(k_cache=self.k[i], v_cache=self.v[i])
+        if self.k_scale is not None:
+            caches.update(k_scale=self.k_scale[i], v_scale=self.v_scale[i])
+        return caches
 
     def _device(self, values, dtype, stream):
         t = torch.tensor(values, dtype=dtype)
@@ -188,7 +277,7 @@ class PagedKVCache:
     def _copy(self, copies, stream):
         if copies:
             src, dst = self._device(list(zip(*copies)), torch.int32, stream)
-            copy_pages(self.k, self.v, src, dst, stream)
+            copy_pages(self.k, self.v, src, dst, stream, self.k_scale, self.v_scale)
 
     def open(self) -> int:
         return self.table.open()
@@ -228,7 +317,7 @@ class PagedKVCache:
             part = moves[at:at + N.MOE_COPY_ROWS_MAX]
             slots = [self.table.slots(seq, at) for at in zip(*part)]
             src, dst = self._device(slots, torch.int64, stream)
-            copy_rows(self.k, self.v, src, dst, stream)
+            copy_rows(self.k, self.v, src, dst, stream, self.k_scale, self.v_scale)
         self.table.truncate(seq, start + len(accepted))
 
     def compact(self, stream=None) -> int:

@@ -1,0 +1,181 @@
+// cache_e4m3.cu -- reading rows of the quantised cache back, and moving its
+// scales (include/attention.h).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "attention.h"
+#include "e4m3.cuh"
+#include "host_util.cuh"
+
+namespace wse {
+namespace {
+
+constexpr int kReadThreads = 256;
+constexpr int kReadUnits = 2;  // 16 codes each, that a thread has in flight
+
+// Sixteen codes times a power of two as 16-bit elements: exact in bf16; in fp16
+// rounded below 2^-14 and cut to its largest number.
+__device__ __forceinline__ void expand(uint4 codes, float scale, bool bf16, uint32_t (&o)[8]) {
+  const uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t half[2];
+    e4m3x4_to_f16x2(c[i], half[0], half[1]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float2 v = __half22float2(*reinterpret_cast<const __half2*>(&half[k]));
+      v.x *= scale;
+      v.y *= scale;
+      if (bf16) {
+        const __nv_bfloat162 r = __floats2bfloat162_rn(v.x, v.y);
+        o[2 * i + k] = *reinterpret_cast<const uint32_t*>(&r);
+      } else {
+        auto cut = [](float x) { return fabsf(x) > 65504.f ? copysignf(65504.f, x) : x; };  // a NaN stays
+        const __half2 r = __floats2half2_rn(cut(v.x), cut(v.y));
+        o[2 * i + k] = *reinterpret_cast<const uint32_t*>(&r);
+      }
+    }
+  }
+}
+
+// A thread takes 16 codes of a row; blockIdx.y: keys or values.  Bound by
+// memory: D + 1 bytes in and 2 D out for each row.
+__global__ void __launch_bounds__(kReadThreads)
+    read_e4m3_kernel(const __grid_constant__ moe_read_e4m3_args_t a) {
+  const bool values = blockIdx.y != 0;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int per_head = a.head_dim / 16, per_token = a.n_kv_heads * per_head;
+  const long long units = (long long)a.n * per_token;
+  const uint8_t* cache = static_cast<const uint8_t*>(values ? a.v_cache : a.k_cache);
+  const uint8_t* scales = static_cast<const uint8_t*>(values ? a.scales.v_scale : a.scales.k_scale);
+  const long long page_stride = values ? a.v_page_stride : a.k_page_stride;
+  const long long row_stride = values ? a.v_row_stride : a.k_row_stride;
+  const long long scale_page = values ? a.scales.v_page_stride : a.scales.k_page_stride;
+  const long long scale_head = values ? a.scales.v_head_stride : a.scales.k_head_stride;
+  char* out = static_cast<char*>(values ? a.v_out : a.k_out);
+  const long long token_stride = values ? a.v_token_stride : a.k_token_stride;
+  const long long head_stride = values ? a.v_head_stride : a.k_head_stride;
+  const long long first = (long long)blockIdx.x * kReadThreads * kReadUnits + threadIdx.x;
+  uint4 codes[kReadUnits];
+  uint32_t byte[kReadUnits];
+#pragma unroll
+  for (int i = 0; i < kReadUnits; ++i) {
+    const long long u = first + i * kReadThreads;
+    codes[i] = make_uint4(0u, 0u, 0u, 0u);
+    byte[i] = kScaleBias;
+    if (u >= units) continue;
+    const int t = (int)(u / per_token), in_token = (int)(u - (long long)t * per_token);
+    const int head = in_token / per_head;
+    const long long slot = a.slots[t];
+    if (slot < 0 || slot >= (long long)a.n_pages * a.page_size) continue;
+    const long long page = slot / a.page_size, row = slot - page * a.page_size;
+    codes[i] = *reinterpret_cast<const uint4*>(cache + page * page_stride + row * row_stride + in_token * 16);
+    byte[i] = scales[page * scale_page + head * scale_head + row];
+  }
+#pragma unroll
+  for (int i = 0; i < kReadUnits; ++i) {
+    const long long u = first + i * kReadThreads;
+    if (u >= units) continue;
+    const int t = (int)(u / per_token), in_token = (int)(u - (long long)t * per_token);
+    const int head = in_token / per_head, part = in_token - head * per_head;
+    uint32_t v[8];
+    expand(codes[i], power_of_two(exponent_of(byte[i])), a.dtype == MOE_DTYPE_BF16, v);
+    uint4* to = reinterpret_cast<uint4*>(out + (t * token_stride + head * head_stride + part * 16) * 2);
+    to[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    to[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+struct CopyScalesArgs {
+  uint8_t* pool[2];
+  int64_t layer_stride[2], page_stride[2], head_stride[2];
+  int64_t n_slots;
+  int page_size, n_heads, n;
+  const int64_t* src;
+  const int64_t* dst;
+};
+
+constexpr int kScaleHeads = kReadThreads / MOE_COPY_ROWS_MAX;  // of a CTA
+
+// One CTA moves the scales of all rows for kScaleHeads heads of a layer: every
+// thread has read its byte before any thread writes.
+__global__ void __launch_bounds__(kReadThreads) copy_scales_kernel(const CopyScalesArgs a) {
+  const int which = blockIdx.y & 1;
+  const long long layer = blockIdx.y >> 1;
+  const int i = threadIdx.x / kScaleHeads;
+  const long long head = (long long)blockIdx.x * kScaleHeads + threadIdx.x % kScaleHeads;
+  pdl_wait();
+  pdl_launch_dependents();
+  uint8_t* base = a.pool[which] + layer * a.layer_stride[which] + head * a.head_stride[which];
+  uint8_t v = 0;
+  long long d = -1;
+  if (i < a.n && head < a.n_heads) {
+    const long long s = a.src[i];
+    d = a.dst[i];
+    if (s < 0 || s >= a.n_slots || d >= a.n_slots) d = -1;
+    if (d >= 0) v = base[s / a.page_size * a.page_stride[which] + s % a.page_size];
+  }
+  __syncthreads();
+  if (d >= 0) base[d / a.page_size * a.page_stride[which] + d % a.page_size] = v;
+}
+
+}  // namespace
+}  // namespace wse
+
+using namespace wse;
+
+extern "C" {
+
+int moe_read_e4m3(const moe_read_e4m3_args_t* a, moe_stream_t stream) {
+  if (!a) return fail(MOE_ERR_INVALID_ARG, "null arguments");
+  if (a->dtype != MOE_DTYPE_BF16 && a->dtype != MOE_DTYPE_FP16)
+    return fail(MOE_ERR_INVALID_ARG, "dtype = %d: must be MOE_DTYPE_BF16 or MOE_DTYPE_FP16", a->dtype);
+  if (a->n < 0 || a->n_kv_heads < 0 || a->n_kv_heads > 65536)
+    return fail(MOE_ERR_INVALID_ARG, "n and n_kv_heads must be 0 or more (heads up to 65536)");
+  if (a->head_dim != 64 && a->head_dim != 128 && a->head_dim != 256)
+    return fail(MOE_ERR_UNSUPPORTED, "head_dim = %d: must be 64, 128 or 256", a->head_dim);
+  if (a->n == 0 || a->n_kv_heads == 0) return MOE_OK;
+  if (a->n_pages < 1 || a->page_size < 1)
+    return fail(MOE_ERR_INVALID_ARG, "n_pages and page_size must be 1 or more");
+  if (!a->slots || !aligned(a->slots, 8)) return fail(MOE_ERR_INVALID_ARG, "slots must be non-null and 8-byte aligned");
+  if (!a->k_cache || !a->v_cache || !a->k_out || !a->v_out || !aligned(a->k_cache, 16) || !aligned(a->v_cache, 16) ||
+      !aligned(a->k_out, 16) || !aligned(a->v_out, 16) || !a->scales.k_scale || !a->scales.v_scale)
+    return fail(MOE_ERR_INVALID_ARG, "the caches, scales and outputs must be non-null, caches and outputs 16-byte aligned");
+  if ((a->k_page_stride | a->k_row_stride | a->v_page_stride | a->v_row_stride) & 15)
+    return fail(MOE_ERR_INVALID_ARG, "every stride of the caches must be a multiple of 16 bytes");
+  if ((a->k_token_stride | a->k_head_stride | a->v_token_stride | a->v_head_stride) & 7)
+    return fail(MOE_ERR_INVALID_ARG, "every stride of the outputs must be a multiple of 8 elements (16 bytes)");
+  const int rc = check_device();
+  if (rc != MOE_OK) return rc;
+  const long long units = (long long)a->n * a->n_kv_heads * (a->head_dim / 16);
+  const long long blocks = (units + kReadThreads * kReadUnits - 1) / (kReadThreads * kReadUnits);
+  if (blocks > 0x7fffffffll) return fail(MOE_ERR_UNSUPPORTED, "%d rows: too many for one call", a->n);
+  return launch_pdl(read_e4m3_kernel, dim3((unsigned)blocks, 2), dim3(kReadThreads), 0, stream, 1, *a);
+}
+
+int moe_copy_scales(void* k_scales, void* v_scales, int n_layers, int64_t k_layer_stride, int64_t v_layer_stride,
+                    int64_t k_page_stride, int64_t v_page_stride, int64_t k_head_stride, int64_t v_head_stride,
+                    int n_pages, int page_size, int n_kv_heads, const int64_t* src, const int64_t* dst, int n,
+                    moe_stream_t stream) {
+  if (n < 0) return fail(MOE_ERR_INVALID_ARG, "n = %d < 0", n);
+  if (n > MOE_COPY_ROWS_MAX) return fail(MOE_ERR_UNSUPPORTED, "n = %d exceeds %d", n, MOE_COPY_ROWS_MAX);
+  if (!k_scales || !v_scales) return fail(MOE_ERR_INVALID_ARG, "the scales must be non-null");
+  if (n_layers < 1 || n_layers > 32767 || n_pages < 1 || page_size < 1 || n_kv_heads < 1 || n_kv_heads > 65536)
+    return fail(MOE_ERR_INVALID_ARG, "n_layers must be in 1..32767, n_kv_heads in 1..65536, n_pages and page_size 1 or "
+                                     "more");
+  if (n == 0) return MOE_OK;
+  if (!src || !dst || !aligned(src, 8) || !aligned(dst, 8))
+    return fail(MOE_ERR_INVALID_ARG, "src and dst must be non-null and 8-byte aligned");
+  const CopyScalesArgs a{{static_cast<uint8_t*>(k_scales), static_cast<uint8_t*>(v_scales)},
+                         {k_layer_stride, v_layer_stride},
+                         {k_page_stride, v_page_stride},
+                         {k_head_stride, v_head_stride},
+                         (int64_t)n_pages * page_size, page_size, n_kv_heads, n, src, dst};
+  const int rc = check_device();
+  if (rc != MOE_OK) return rc;
+  return launch_pdl(copy_scales_kernel, dim3((unsigned)((n_kv_heads + kScaleHeads - 1) / kScaleHeads), 2u * n_layers),
+                    dim3(kReadThreads), 0, stream, 1, a);
+}
+
+}  // extern "C"

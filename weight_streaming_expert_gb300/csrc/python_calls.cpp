@@ -79,11 +79,21 @@ bool cache(const Tensor& t, at::ScalarType type, int64_t n, int64_t dim, int64_t
   return t.dim() == 4 && t.scalar_type() == type && on(t, gpu) && t.size(2) == n && t.size(3) == dim &&
          t.stride(3) == 1 && t.stride(2) == dim;
 }
+// scales of a quantised cache: [pages, heads, page_size], each head's contiguous
+bool scales(const Tensor& t, const Tensor& cache, int64_t gpu) {
+  return t.dim() == 3 && t.scalar_type() == at::kByte && on(t, gpu) && t.size(0) == cache.size(0) &&
+         t.size(1) == cache.size(2) && t.size(2) == cache.size(1) && (t.size(2) < 2 || t.stride(2) == 1);
+}
 template <typename T>
 T* ptr(const Tensor& t) {
   return t.defined() ? static_cast<T*>(t.data_ptr()) : nullptr;
 }
 bool fits_int(int64_t v) { return v >= 0 && v <= 0x7fffffff; }
+
+moe_cache_scales_t scales_of(const Tensor& k, const Tensor& v) {
+  if (!k.defined()) return moe_cache_scales_t{};
+  return moe_cache_scales_t{k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), v.stride(0), v.stride(1)};
+}
 
 PyObject* qk_norm_rope(Args x) {
   const int64_t gpu = x.integer(), stream = x.integer(), dim = x.integer(), rotary = x.integer();
@@ -93,12 +103,16 @@ PyObject* qk_norm_rope(Args x) {
   const Tensor qw = x.tensor(true), kw = x.tensor(true), positions = x.tensor(), slots = x.tensor();
   const Tensor k_cache = x.tensor(), v_cache = x.tensor();
   Tensor out = x.tensor(true);
+  const Tensor k_scale = x.tensor(true), v_scale = x.tensor(true);
   if (x.bad || q.dim() != 3 || k.dim() != 3) return number(kDoesNotFit);
-  const auto type = q.scalar_type();
+  const bool quantised = k_scale.defined();
+  const auto type = q.scalar_type(), cached = quantised ? at::kFloat8_e4m3fn : type;
   const int64_t T = q.size(0), Hq = q.size(1), Hk = k.size(1);
   if (dtype_of(q) < 0 || !heads(q, type, T, Hq, dim, gpu) || !heads(k, type, T, Hk, dim, gpu) ||
-      !heads(v, type, T, Hk, dim, gpu) || !cache(k_cache, type, Hk, dim, gpu) || !cache(v_cache, type, Hk, dim, gpu) ||
-      !k_cache.sizes().equals(v_cache.sizes()) || !plain(positions, at::kInt, T, gpu) ||
+      !heads(v, type, T, Hk, dim, gpu) || !cache(k_cache, cached, Hk, dim, gpu) ||
+      !cache(v_cache, cached, Hk, dim, gpu) || !k_cache.sizes().equals(v_cache.sizes()) ||
+      quantised != v_scale.defined() ||
+      (quantised && (!scales(k_scale, k_cache, gpu) || !scales(v_scale, v_cache, gpu))) || !plain(positions, at::kInt, T, gpu) ||
       !plain(slots, at::kLong, T, gpu) || (qw.defined() && !plain(qw, type, dim, gpu)) ||
       (kw.defined() && !plain(kw, type, dim, gpu)) || (out.defined() && !heads(out, type, T, Hq, dim, gpu)) ||
       !fits_int(T) || !fits_int(Hq) || !fits_int(Hk) || !fits_int(k_cache.size(0)) || !fits_int(k_cache.size(1)))
@@ -111,7 +125,9 @@ PyObject* qk_norm_rope(Args x) {
                                   out.stride(0), out.stride(1), k_cache.data_ptr(), v_cache.data_ptr(),
                                   k_cache.stride(0), k_cache.stride(1), v_cache.stride(0), v_cache.stride(1),
                                   (int)k_cache.size(0), (int)k_cache.size(1)};
-  const int status = moe_qk_norm_rope(&a, reinterpret_cast<moe_stream_t>(stream));
+  const auto on_stream = reinterpret_cast<moe_stream_t>(stream);
+  const moe_cache_scales_t s = scales_of(k_scale, v_scale);
+  const int status = quantised ? moe_qk_norm_rope_e4m3(&a, &s, on_stream) : moe_qk_norm_rope(&a, on_stream);
   return status == MOE_OK ? THPVariable_Wrap(std::move(out)) : number(status);
 }
 
@@ -177,6 +193,50 @@ PyObject* copy(Args x) {
                             k.stride(1) * e, v.stride(1) * e, (int)k.size(1), k.size(2) * row * e, ptr<int32_t>(src),
                             ptr<int32_t>(dst), (int)n, s);
   return number(status);
+}
+
+PyObject* read_cache(Args x) {
+  const int64_t stream = x.integer();
+  const bool bf16 = x.truth();
+  const Tensor k = x.tensor(), v = x.tensor(), ks = x.tensor(), vs = x.tensor(), slots = x.tensor();
+  Tensor k_out = x.tensor(true), v_out = x.tensor(true);
+  if (x.bad || k.dim() != 4 || !k.is_cuda() || slots.dim() != 1) return number(kDoesNotFit);
+  const int64_t gpu = k.get_device(), n = slots.size(0), H = k.size(2), D = k.size(3);
+  const auto type = bf16 ? at::kBFloat16 : at::kHalf;
+  if (!cache(k, at::kFloat8_e4m3fn, H, D, gpu) || !cache(v, at::kFloat8_e4m3fn, H, D, gpu) ||
+      !k.sizes().equals(v.sizes()) || !scales(ks, k, gpu) || !scales(vs, v, gpu) || !plain(slots, at::kLong, n, gpu) ||
+      (k_out.defined() && !heads(k_out, type, n, H, D, gpu)) ||
+      (v_out.defined() && !heads(v_out, type, n, H, D, gpu)) || !fits_int(n) || !fits_int(H) || !fits_int(D) ||
+      !fits_int(k.size(0)) || !fits_int(k.size(1)))
+    return number(kDoesNotFit);
+  if (!k_out.defined()) k_out = at::empty({n, H, D}, k.options().dtype(type));
+  if (!v_out.defined()) v_out = at::empty({n, H, D}, k.options().dtype(type));
+  const moe_read_e4m3_args_t a{bf16 ? MOE_DTYPE_BF16 : MOE_DTYPE_FP16, (int)n, (int)H, (int)D, k.data_ptr(), v.data_ptr(),
+                               k.stride(0), k.stride(1), v.stride(0), v.stride(1), scales_of(ks, vs), (int)k.size(0),
+                               (int)k.size(1), ptr<int64_t>(slots), k_out.data_ptr(), v_out.data_ptr(), k_out.stride(0),
+                               k_out.stride(1), v_out.stride(0), v_out.stride(1)};
+  const int status = moe_read_e4m3(&a, reinterpret_cast<moe_stream_t>(stream));
+  if (status != MOE_OK) return number(status);
+  PyObject* o = THPVariable_Wrap(std::move(k_out));
+  PyObject* l = o ? THPVariable_Wrap(std::move(v_out)) : nullptr;
+  return l ? Py_BuildValue("(NN)", o, l) : (Py_XDECREF(o), nullptr);
+}
+
+// the scales of moved rows: pools [layers, pages, heads, page_size]
+PyObject* copy_scales(Args x) {
+  const int64_t stream = x.integer();
+  const Tensor k = x.tensor(), v = x.tensor(), src = x.tensor(), dst = x.tensor();
+  if (x.bad || k.dim() != 4 || !k.is_cuda() || src.dim() != 1) return number(kDoesNotFit);
+  const int64_t gpu = k.get_device(), n = src.size(0);
+  if (!k.sizes().equals(v.sizes()) || k.scalar_type() != at::kByte || v.scalar_type() != at::kByte || !on(v, gpu) ||
+      !plain(src, at::kLong, n, gpu) || !plain(dst, at::kLong, n, gpu) || !fits_int(n) || !fits_int(k.size(0)) ||
+      !fits_int(k.size(1)) || !fits_int(k.size(2)) || !fits_int(k.size(3)))
+    return number(kDoesNotFit);
+  for (const Tensor* t : {&k, &v})
+    if (t->size(3) > 1 && t->stride(3) != 1) return number(kDoesNotFit);
+  return number(moe_copy_scales(k.data_ptr(), v.data_ptr(), (int)k.size(0), k.stride(0), v.stride(0), k.stride(1),
+                                v.stride(1), k.stride(2), v.stride(2), (int)k.size(1), (int)k.size(3), (int)k.size(2),
+                                ptr<int64_t>(src), ptr<int64_t>(dst), (int)n, reinterpret_cast<moe_stream_t>(stream)));
 }
 
 PyObject* sample(Args x) {
@@ -257,6 +317,8 @@ PyCFunction entry() {
 PyMethodDef methods[] = {{"qk_norm_rope", entry<qk_norm_rope>(), METH_FASTCALL, nullptr},
                          {"attention", entry<attention>(), METH_FASTCALL, nullptr},
                          {"copy", entry<copy>(), METH_FASTCALL, nullptr},
+                         {"read_cache", entry<read_cache>(), METH_FASTCALL, nullptr},
+                         {"copy_scales", entry<copy_scales>(), METH_FASTCALL, nullptr},
                          {"sample", entry<sample>(), METH_FASTCALL, nullptr},
                          {"adjust_logits", entry<adjust_logits>(), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};

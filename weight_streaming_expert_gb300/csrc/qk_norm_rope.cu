@@ -24,10 +24,15 @@
 // + 8 heads of 128: 59 us, 5.6 TB/s; with weights and turns one after the other
 // and single products 73 us, 70 % of the issue slots.  6 tokens: 3.2 us, a
 // launch and two reads one after the other.
+//
+// Into a quantised cache the D/8 lanes of a head agree on its largest value by
+// shuffles and write a byte per value and one scale, 4 bytes a lane and half:
+// less to write for a few more instructions.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "attention.h"
+#include "e4m3.cuh"
 #include "host_util.cuh"
 
 namespace wse {
@@ -82,9 +87,11 @@ __device__ __forceinline__ f32x2 fma2(f32x2 x, f32x2 y, f32x2 z) {
   return v;
 }
 
-template <typename T, int D, bool kInterleaved>
+// kQuantised: the caches hold E4M3 codes, with the scales s.
+template <typename T, int D, bool kInterleaved, bool kQuantised>
 __global__ void __launch_bounds__(kRopeThreads, D == 256 ? 3 : 4) qk_norm_rope_kernel(
-    const __grid_constant__ moe_qk_norm_rope_args_t a, int warps_per_token) {
+    const __grid_constant__ moe_qk_norm_rope_args_t a, const __grid_constant__ moe_cache_scales_t s,
+    int warps_per_token) {
   constexpr int kLanes = D / 8;               // lanes of a head
   constexpr int kHeads = 32 / kLanes;         // heads of a group: what a warp does at a time
   __shared__ float2 turn[kRopeWarps][D / 2];  // (cos, sin) of the warp's token
@@ -173,16 +180,19 @@ __global__ void __launch_bounds__(kRopeThreads, D == 256 ? 3 : 4) qk_norm_rope_k
       }
     }
   };
-  // a group's values, normed and turned
-  auto finish = [&](uint2& v0, uint2& v1, bool norm) {
+  auto widen = [&](uint2 v0, uint2 v1, f32x2 (&x)[4]) {
     const T* e0 = reinterpret_cast<const T*>(&v0);
     const T* e1 = reinterpret_cast<const T*>(&v1);
-    f32x2 x[4], y[4];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       x[j] = pair_of(to_f32<T>(e0[2 * j]), to_f32<T>(e0[2 * j + 1]));
       x[2 + j] = pair_of(to_f32<T>(e1[2 * j]), to_f32<T>(e1[2 * j + 1]));
     }
+  };
+  // a group's values, normed and turned
+  auto turned = [&](uint2 v0, uint2 v1, bool norm, f32x2 (&y)[4]) {
+    f32x2 x[4];
+    widen(v0, v1, x);
     if (norm) {
       f32x2 sq2 = mul2(x[0], x[0]);
 #pragma unroll
@@ -208,6 +218,10 @@ __global__ void __launch_bounds__(kRopeThreads, D == 256 ? 3 : 4) qk_norm_rope_k
 #pragma unroll
       for (int j = 0; j < 4; ++j) y[j] = mul2(x[j], own[j]);
     }
+  };
+  auto finish = [&](uint2& v0, uint2& v1, bool norm) {
+    f32x2 y[4];
+    turned(v0, v1, norm, y);
     v0 = make_uint2(pack2<T>(both(y[0]).x, both(y[0]).y), pack2<T>(both(y[1]).x, both(y[1]).y));
     v1 = make_uint2(pack2<T>(both(y[2]).x, both(y[2]).y), pack2<T>(both(y[3]).x, both(y[3]).y));
   };
@@ -218,6 +232,28 @@ __global__ void __launch_bounds__(kRopeThreads, D == 256 ? 3 : 4) qk_norm_rope_k
   auto store = [&](T* p, uint2 v0, uint2 v1) {
     *reinterpret_cast<uint2*>(p) = v0;
     *reinterpret_cast<uint2*>(p + apart) = v1;
+  };
+
+  // a group of keys or values into the quantised cache, every lane of the warp
+  auto put_codes = [&](int kind, int head, bool mine, const f32x2 (&y)[4]) {
+    float largest = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) largest = fmaxf(largest, fmaxf(finite_size(both(y[j]).x), finite_size(both(y[j]).y)));
+#pragma unroll
+    for (int m = kLanes / 2; m > 0; m >>= 1) largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, m));
+    if (!mine) return;
+    const int e = scale_for(largest);
+    const float inv = power_of_two(-e);
+    uint8_t* codes = kind == 1 ? static_cast<uint8_t*>(a.k_cache) + page * a.k_page_stride + row * a.k_row_stride
+                               : static_cast<uint8_t*>(a.v_cache) + page * a.v_page_stride + row * a.v_row_stride;
+    codes += head * D;
+    *reinterpret_cast<uint32_t*>(codes + lo) = to_e4m3x4(both(y[0]).x, both(y[0]).y, both(y[1]).x, both(y[1]).y, inv);
+    *reinterpret_cast<uint32_t*>(codes + hi) = to_e4m3x4(both(y[2]).x, both(y[2]).y, both(y[3]).x, both(y[3]).y, inv);
+    if (part == 0) {
+      uint8_t* scale = kind == 1 ? static_cast<uint8_t*>(s.k_scale) + page * s.k_page_stride + head * s.k_head_stride
+                                 : static_cast<uint8_t*>(s.v_scale) + page * s.v_page_stride + head * s.v_head_stride;
+      scale[row] = (uint8_t)(e + kScaleBias);
+    }
   };
 
   const int g_first = warp % warps_per_token, whole = a.n_heads / kHeads;
@@ -264,6 +300,17 @@ __global__ void __launch_bounds__(kRopeThreads, D == 256 ? 3 : 4) qk_norm_rope_k
       const int g = g0 + i * warps_per_token;
       if (g >= groups) break;
       const int kind = kind_of(g), head = head_of(g, kind);
+      if (kQuantised && kind > 0) {
+        f32x2 y[4];
+        if (kind == 1) {
+          factors_of(1);
+          turned(x0[i], x1[i], a.k_weight != nullptr, y);
+        } else {
+          widen(x0[i], x1[i], y);
+        }
+        put_codes(kind, head, head < a.n_kv_heads && keep, y);
+        continue;
+      }
       if (kind < 2) {
         factors_of(kind);
         finish(x0[i], x1[i], (kind == 0 ? a.q_weight : a.k_weight) != nullptr);
@@ -273,13 +320,21 @@ __global__ void __launch_bounds__(kRopeThreads, D == 256 ? 3 : 4) qk_norm_rope_k
   }
 }
 
+using RopeKernel = void (*)(const moe_qk_norm_rope_args_t, const moe_cache_scales_t, int);
+
+template <typename T, int D>
+RopeKernel rope_kernel(bool interleaved, bool quantised) {
+  if (quantised) return interleaved ? qk_norm_rope_kernel<T, D, true, true> : qk_norm_rope_kernel<T, D, false, true>;
+  return interleaved ? qk_norm_rope_kernel<T, D, true, false> : qk_norm_rope_kernel<T, D, false, false>;
+}
+
+// s: the scales of a quantised cache, or nullptr.
 template <typename T>
-int launch_rope(const moe_qk_norm_rope_args_t& a, moe_stream_t stream) {
-  void (*kernel)(const moe_qk_norm_rope_args_t, int) = nullptr;
+int launch_rope(const moe_qk_norm_rope_args_t& a, const moe_cache_scales_t* s, moe_stream_t stream) {
   const bool il = a.interleaved != 0;
-  if (a.head_dim == 64) kernel = il ? qk_norm_rope_kernel<T, 64, true> : qk_norm_rope_kernel<T, 64, false>;
-  else if (a.head_dim == 128) kernel = il ? qk_norm_rope_kernel<T, 128, true> : qk_norm_rope_kernel<T, 128, false>;
-  else kernel = il ? qk_norm_rope_kernel<T, 256, true> : qk_norm_rope_kernel<T, 256, false>;
+  const RopeKernel kernel = a.head_dim == 64    ? rope_kernel<T, 64>(il, s)
+                            : a.head_dim == 128 ? rope_kernel<T, 128>(il, s)
+                                                : rope_kernel<T, 256>(il, s);
   // Several warps share a token as long as all CTAs are resident at once (4 per
   // SM): 1001 tokens of 16 + 4 heads of 64 take 4.4 us with 4 warps each, 5.3
   // with 8.  Beyond that a warp each, which works the angles out once: 16384
@@ -289,15 +344,10 @@ int launch_rope(const moe_qk_norm_rope_args_t& a, moe_stream_t stream) {
   while (warps > 1 && a.n_tokens * (long long)warps > resident) warps /= 2;
   const int tokens = kRopeWarps / warps;
   return launch_pdl(kernel, dim3((unsigned)((a.n_tokens + tokens - 1) / tokens)), dim3(kRopeThreads), 0, stream, 1, a,
-                    warps);
+                    s ? *s : moe_cache_scales_t{}, warps);
 }
 
-}  // namespace
-}  // namespace wse
-
-using namespace wse;
-
-extern "C" int moe_qk_norm_rope(const moe_qk_norm_rope_args_t* a, moe_stream_t stream) {
+int qk_norm_rope(const moe_qk_norm_rope_args_t* a, const moe_cache_scales_t* s, moe_stream_t stream) {
   if (!a) return fail(MOE_ERR_INVALID_ARG, "null arguments");
   if (a->dtype != MOE_DTYPE_BF16 && a->dtype != MOE_DTYPE_FP16)
     return fail(MOE_ERR_INVALID_ARG, "dtype = %d: must be MOE_DTYPE_BF16 or MOE_DTYPE_FP16", a->dtype);
@@ -323,9 +373,30 @@ extern "C" int moe_qk_norm_rope(const moe_qk_norm_rope_args_t* a, moe_stream_t s
        a->v_head_stride | a->q_out_token_stride | a->q_out_head_stride | a->k_page_stride | a->k_row_stride |
        a->v_page_stride | a->v_row_stride) & 7)
     return fail(MOE_ERR_INVALID_ARG, "every stride must be a multiple of 8 elements (16 bytes)");
+  if (s && a->n_kv_heads > 0) {
+    if (!s->k_scale || !s->v_scale) return fail(MOE_ERR_INVALID_ARG, "the scales must be non-null");
+    if ((a->k_page_stride | a->k_row_stride | a->v_page_stride | a->v_row_stride) & 15)
+      return fail(MOE_ERR_INVALID_ARG, "every stride of a quantised cache must be a multiple of 16 bytes");
+  }
   if (a->n_kv_heads > 0 && (a->n_pages < 1 || a->page_size < 1))
     return fail(MOE_ERR_INVALID_ARG, "n_pages and page_size must be 1 or more");
   const int rc = check_device();
   if (rc != MOE_OK) return rc;
-  return a->dtype == MOE_DTYPE_BF16 ? launch_rope<__nv_bfloat16>(*a, stream) : launch_rope<__half>(*a, stream);
+  return a->dtype == MOE_DTYPE_BF16 ? launch_rope<__nv_bfloat16>(*a, s, stream) : launch_rope<__half>(*a, s, stream);
 }
+
+}  // namespace
+}  // namespace wse
+
+using namespace wse;
+
+extern "C" {
+
+int moe_qk_norm_rope(const moe_qk_norm_rope_args_t* a, moe_stream_t stream) { return qk_norm_rope(a, nullptr, stream); }
+
+int moe_qk_norm_rope_e4m3(const moe_qk_norm_rope_args_t* a, const moe_cache_scales_t* s, moe_stream_t stream) {
+  if (!s) return fail(MOE_ERR_INVALID_ARG, "null scales");
+  return qk_norm_rope(a, s, stream);
+}
+
+}  // extern "C"

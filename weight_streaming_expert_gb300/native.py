@@ -75,6 +75,19 @@ class moe_qk_norm_rope_args_t(ctypes.Structure):
                 ("page_size", _i)]
 
 
+class moe_cache_scales_t(ctypes.Structure):
+    _fields_ = [("k_scale", _p), ("v_scale", _p), ("k_page_stride", _l), ("k_head_stride", _l), ("v_page_stride", _l),
+                ("v_head_stride", _l)]
+
+
+class moe_read_e4m3_args_t(ctypes.Structure):
+    _fields_ = [("dtype", _i), ("n", _i), ("n_kv_heads", _i), ("head_dim", _i), ("k_cache", _p), ("v_cache", _p),
+                ("k_page_stride", _l), ("k_row_stride", _l), ("v_page_stride", _l), ("v_row_stride", _l),
+                ("scales", moe_cache_scales_t), ("n_pages", _i), ("page_size", _i), ("slots", _p), ("k_out", _p),
+                ("v_out", _p), ("k_token_stride", _l), ("k_head_stride", _l), ("v_token_stride", _l),
+                ("v_head_stride", _l)]
+
+
 class moe_attn_args_t(ctypes.Structure):
     _fields_ = [("dtype", _i), ("batch", _i), ("n_tokens", _i), ("max_q_len", _i), ("scale", _f), ("q", _p),
                 ("q_token_stride", _l), ("q_head_stride", _l), ("k_cache", _p), ("v_cache", _p),
@@ -170,6 +183,13 @@ def lib(build_if_missing: bool = True):
         i64 = ctypes.c_int64
         L.moe_qk_norm_rope.argtypes = [ctypes.POINTER(moe_qk_norm_rope_args_t), vp]
         L.moe_qk_norm_rope.restype = ci
+        L.moe_qk_norm_rope_e4m3.argtypes = [ctypes.POINTER(moe_qk_norm_rope_args_t), ctypes.POINTER(moe_cache_scales_t),
+                                            vp]
+        L.moe_qk_norm_rope_e4m3.restype = ci
+        L.moe_read_e4m3.argtypes = [ctypes.POINTER(moe_read_e4m3_args_t), vp]
+        L.moe_read_e4m3.restype = ci
+        L.moe_copy_scales.argtypes = [vp, vp, ci, i64, i64, i64, i64, i64, i64, ci, ci, ci, vp, vp, ci, vp]
+        L.moe_copy_scales.restype = ci
         L.moe_attn_create.argtypes = [ci, ci, ci]
         L.moe_attn_create.restype = vp
         L.moe_attn_forward.argtypes = [vp, ctypes.POINTER(moe_attn_args_t), vp]
