@@ -165,6 +165,40 @@ typedef struct {
  */
 int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t stream);
 
+/*
+ * What a call may have besides.
+ *
+ * scales: a's caches are quantised (codes, strides in bytes, multiples of 16;
+ * scales 16-byte aligned with strides that are multiples of 16); q, out and
+ * dtype are as before.  Scores, statistics and sums are fp32; queries enter the
+ * products in fp16 around a power of two for each row (exact to 2^-37 of its
+ * largest value in bf16), and so do the probabilities times the values' scales.
+ * Chunks of more than 64 rows (max_q_len * n_heads / n_kv_heads) are unpacked
+ * to 16 bits in the workspace first, as moe_read_e4m3 does.
+ *
+ * prefix_len: the first prefix_len positions of every sequence are the same, in
+ * the same pages: those that the table's first row begins with (the other rows'
+ * first prefix_len / page_size entries are not read).  Whole pages, and all new
+ * tokens lie behind them (a sequence that is shorter is an error found on the
+ * device).  The prefix is read once for the whole batch instead of once for
+ * each sequence; the results are those of a call without, but for rounding.
+ * With scales at most 64 query heads may share a key/value head.
+ */
+typedef struct {
+  const moe_cache_scales_t* scales; /* host struct; NULL: a 16-bit cache */
+  int prefix_len;                   /* 0: none */
+  void* workspace;                  /* device, 16-byte aligned, free for other use once the call's work is done; */
+  size_t workspace_bytes;           /* moe_attn_workspace() of them (for chunks over codes that of one sequence
+                                    suffices: the sequences then take turns) */
+} moe_attn_opts_t;
+
+/* Bytes of workspace that moe_attn_forward_ex takes for such a call; 0: none. */
+size_t moe_attn_workspace(const moe_attn_t* h, const moe_attn_args_t* a, const moe_attn_opts_t* o);
+
+/* moe_attn_forward with options (NULL: none).  MOE_ERR_UNSUPPORTED also for a prefix whose tiles, with those of a batch
+ * of longest chunks, are more than 2e9. */
+int moe_attn_forward_ex(moe_attn_t* h, const moe_attn_args_t* a, const moe_attn_opts_t* o, moe_stream_t stream);
+
 /* Synchronises the handle's device, then returns and clears the sticky status: MOE_OK, MOE_ERR_INVALID_ARG (bad pages
  * or lengths) or MOE_ERR_DEVICE_TIMEOUT; moe_last_error() names what was found. */
 int moe_attn_get_status(moe_attn_t* h);

@@ -174,39 +174,49 @@ class PagedAttention:
         self._handle = h
 
     def forward(self, q, k_cache, v_cache, block_table, q_starts, kv_lens, max_q_len: int, scale: float | None = None,
-                tree_mask=None, out=None, return_lse: bool = False, stream=None):
+                tree_mask=None, out=None, return_lse: bool = False, stream=None, k_scale=None, v_scale=None,
+                prefix_len: int = 0):
         """q [T, Hq, D]; caches [pages, page_size, Hk, D]; block_table int32
         [B, pages of a row] (a view of a wider table, or one row expanded, is
         fine); q_starts int32 [B + 1]; kv_lens int32 [B] (the new tokens
         included); max_q_len: at least the longest chunk; scale: default
         D ** -0.5; tree_mask: int64 [T], bit j of a token's word set where it
         sees its chunk's token j, instead of the chain (chunks up to 64).
-        Returns out [T, Hq, D], with ``return_lse`` also fp32 [T, Hq]."""
+        Returns out [T, Hq, D], with ``return_lse`` also fp32 [T, Hq].
+
+        k_scale, v_scale (uint8 [pages, Hk, page_size]): the caches are
+        quantised, float8_e4m3fn codes as ``QKNormRope`` writes them.
+        prefix_len: every sequence begins with the same positions, as many, in
+        the same whole pages (forks: ``PagedKVCache.shared_prefix``) and before
+        all new tokens; they are then read once for the batch."""
         index = self._index
         if _elsewhere(index, stream):
             with _On(index, stream):
                 return self.forward(q, k_cache, v_cache, block_table, q_starts, kv_lens, max_q_len, scale, tree_mask,
-                                    out, return_lse)
+                                    out, return_lse, None, k_scale, v_scale, prefix_len)
         got = N.calls().attention(index, torch._C._cuda_getCurrentRawStream(index), self._handle, self.n_heads,
                                   self.n_kv_heads, self.head_dim, q, k_cache, v_cache, block_table, q_starts, kv_lens,
                                   max_q_len, self.head_dim ** -0.5 if scale is None else scale, tree_mask, out,
-                                  return_lse)
+                                  return_lse, k_scale, v_scale, prefix_len)
         if isinstance(got, int):
             if got < 0:
-                self._explain(q, k_cache, v_cache, block_table, q_starts, kv_lens, max_q_len, tree_mask, out)
+                self._explain(q, k_cache, v_cache, block_table, q_starts, kv_lens, max_q_len, tree_mask, out, k_scale,
+                              v_scale, prefix_len)
             N.check("moe_attn_forward", got)
         if out is None:
             return got
         return (out, got[1]) if return_lse else out
 
-    def _explain(self, q, k_cache, v_cache, block_table, q_starts, kv_lens, max_q_len, tree_mask, out):
+    def _explain(self, q, k_cache, v_cache, block_table, q_starts, kv_lens, max_q_len, tree_mask, out, k_scale, v_scale,
+                 prefix_len):
         _tensor("q", q)
         index, D, dt = self._index, self.head_dim, q.dtype
         if dt not in _DTYPES or q.dim() != 3 or q.shape[1] != self.n_heads:
             raise ValueError(f"q must be a bf16 or fp16 tensor [tokens, {self.n_heads}, {D}]")
         _heads("q", q, dt, index, D)
-        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-            _cache(name, t, dt, index, self.n_kv_heads, D)
+        _caches(k_cache, v_cache, k_scale, v_scale, dt, index, self.n_kv_heads, D)
+        if not isinstance(prefix_len, int) or not 0 <= prefix_len < 1 << 31:
+            raise ValueError("prefix_len must be an int of 0 or more")
         _tensor("block_table", block_table)
         if (block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.get_device() != index
                 or block_table.stride(1) != 1):

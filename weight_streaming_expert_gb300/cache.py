@@ -230,6 +230,17 @@ class PageTable:
         self._free = list(range(len(used), self.n_pages))
         return list(moves.items())
 
+    def shared_prefix(self, seqs) -> int:
+        """How many positions, in whole pages, all of the sequences begin with in
+        the same pages and have before their last."""
+        first = min((self._pages[s] for s in seqs), key=len, default=[])
+        n = 0
+        for i, page in enumerate(first):
+            if any(self._pages[s][i] != page or self._lens[s] <= (i + 1) * self.page_size for s in seqs):
+                break
+            n = (i + 1) * self.page_size
+        return n
+
     def slots(self, seq: int, positions):
         P, pages = self.page_size, self._pages[seq]
         return [pages[p // P] * P + p % P for p in positions]
@@ -326,6 +337,14 @@ class PagedKVCache:
         moves = self.table.compact()
         self._copy(moves, stream)
         return len(moves)
+
+    def shared_prefix(self, seqs, new: int = 1) -> int:
+        """The longest ``prefix_len`` of a ``PagedAttention`` call on the
+        sequences (forks) whose last `new` positions each are its new tokens: what
+        they begin with in the same whole pages."""
+        page = self.table.page_size
+        before = min((self.length(s) for s in seqs), default=0) - new
+        return max(0, min(self.table.shared_prefix(seqs), before // page * page))
 
     def block_table(self, seqs, stream=None):
         """(block table int32 [B, pages of the longest], kv_lens int32 [B]) of

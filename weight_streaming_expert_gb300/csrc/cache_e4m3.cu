@@ -1,8 +1,5 @@
 // cache_e4m3.cu -- reading rows of the quantised cache back, and moving its
 // scales (include/attention.h).
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include "attention.h"
 #include "e4m3.cuh"
 #include "host_util.cuh"
@@ -12,31 +9,6 @@ namespace {
 
 constexpr int kReadThreads = 256;
 constexpr int kReadUnits = 2;  // 16 codes each, that a thread has in flight
-
-// Sixteen codes times a power of two as 16-bit elements: exact in bf16; in fp16
-// rounded below 2^-14 and cut to its largest number.
-__device__ __forceinline__ void expand(uint4 codes, float scale, bool bf16, uint32_t (&o)[8]) {
-  const uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t half[2];
-    e4m3x4_to_f16x2(c[i], half[0], half[1]);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      float2 v = __half22float2(*reinterpret_cast<const __half2*>(&half[k]));
-      v.x *= scale;
-      v.y *= scale;
-      if (bf16) {
-        const __nv_bfloat162 r = __floats2bfloat162_rn(v.x, v.y);
-        o[2 * i + k] = *reinterpret_cast<const uint32_t*>(&r);
-      } else {
-        auto cut = [](float x) { return fabsf(x) > 65504.f ? copysignf(65504.f, x) : x; };  // a NaN stays
-        const __half2 r = __floats2half2_rn(cut(v.x), cut(v.y));
-        o[2 * i + k] = *reinterpret_cast<const uint32_t*>(&r);
-      }
-    }
-  }
-}
 
 // A thread takes 16 codes of a row; blockIdx.y: keys or values.  Bound by
 // memory: D + 1 bytes in and 2 D out for each row.
@@ -80,7 +52,7 @@ __global__ void __launch_bounds__(kReadThreads)
     const int t = (int)(u / per_token), in_token = (int)(u - (long long)t * per_token);
     const int head = in_token / per_head, part = in_token - head * per_head;
     uint32_t v[8];
-    expand(codes[i], power_of_two(exponent_of(byte[i])), a.dtype == MOE_DTYPE_BF16, v);
+    expand_e4m3(codes[i], power_of_two(exponent_of(byte[i])), a.dtype == MOE_DTYPE_BF16, v);
     uint4* to = reinterpret_cast<uint4*>(out + (t * token_stride + head * head_stride + part * 16) * 2);
     to[0] = make_uint4(v[0], v[1], v[2], v[3]);
     to[1] = make_uint4(v[4], v[5], v[6], v[7]);

@@ -6,6 +6,9 @@
 // is lost to the scale; code * 2^e is exact in bf16 and fp32.
 #pragma once
 
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
 #include <cstdint>
 
 #include "common.cuh"
@@ -45,6 +48,31 @@ __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d
       : "=r"(codes)
       : "f"(scaled(a)), "f"(scaled(b)), "f"(scaled(c)), "f"(scaled(d)));
   return codes;
+}
+
+// Sixteen codes times a power of two as 16-bit elements: exact in bf16; in fp16
+// rounded below 2^-14 and cut to its largest number.
+__device__ __forceinline__ void expand_e4m3(uint4 codes, float scale, bool bf16, uint32_t (&o)[8]) {
+  const uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t half[2];
+    e4m3x4_to_f16x2(c[i], half[0], half[1]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float2 v = __half22float2(*reinterpret_cast<const __half2*>(&half[k]));
+      v.x *= scale;
+      v.y *= scale;
+      if (bf16) {
+        const __nv_bfloat162 r = __floats2bfloat162_rn(v.x, v.y);
+        o[2 * i + k] = *reinterpret_cast<const uint32_t*>(&r);
+      } else {
+        auto cut = [](float x) { return fabsf(x) > 65504.f ? copysignf(65504.f, x) : x; };  // a NaN stays
+        const __half2 r = __floats2half2_rn(cut(v.x), cut(v.y));
+        o[2 * i + k] = *reinterpret_cast<const uint32_t*>(&r);
+      }
+    }
+  }
 }
 
 }  // namespace wse

@@ -92,7 +92,9 @@ bool fits_int(int64_t v) { return v >= 0 && v <= 0x7fffffff; }
 
 moe_cache_scales_t scales_of(const Tensor& k, const Tensor& v) {
   if (!k.defined()) return moe_cache_scales_t{};
-  return moe_cache_scales_t{k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), v.stride(0), v.stride(1)};
+  // the stride of a single page or head is any number
+  auto stride = [](const Tensor& t, int64_t d) { return t.size(d) > 1 ? t.stride(d) : 0; };
+  return moe_cache_scales_t{k.data_ptr(), v.data_ptr(), stride(k, 0), stride(k, 1), stride(v, 0), stride(v, 1)};
 }
 
 PyObject* qk_norm_rope(Args x) {
@@ -141,13 +143,18 @@ PyObject* attention(Args x) {
   const Tensor tree = x.tensor(true);
   Tensor out = x.tensor(true), lse;
   const bool want_lse = x.truth();
+  const Tensor k_scale = x.tensor(true), v_scale = x.tensor(true);
+  const int64_t prefix = x.integer();
   if (x.bad || q.dim() != 3 || table.dim() != 2) return number(kDoesNotFit);
-  const auto type = q.scalar_type();
+  const bool quantised = k_scale.defined();
+  const auto type = q.scalar_type(), cached = quantised ? at::kFloat8_e4m3fn : type;
   const int64_t T = q.size(0), B = table.size(0);
   // a row's distance and its pages are two things: rows may be shared, or part of a wider table
   const int64_t row_step = B > 1 && table.size(1) > 0 ? table.stride(0) : 0;
-  if (dtype_of(q) < 0 || !heads(q, type, T, Hq, dim, gpu) || !cache(k_cache, type, Hk, dim, gpu) ||
-      !cache(v_cache, type, Hk, dim, gpu) || !k_cache.sizes().equals(v_cache.sizes()) ||
+  if (dtype_of(q) < 0 || !heads(q, type, T, Hq, dim, gpu) || !cache(k_cache, cached, Hk, dim, gpu) ||
+      !cache(v_cache, cached, Hk, dim, gpu) || !k_cache.sizes().equals(v_cache.sizes()) ||
+      quantised != v_scale.defined() || !fits_int(prefix) ||
+      (quantised && (!scales(k_scale, k_cache, gpu) || !scales(v_scale, v_cache, gpu))) ||
       table.scalar_type() != at::kInt || !on(table, gpu) || table.stride(1) != 1 ||
       !plain(starts, at::kInt, B + 1, gpu) ||
       !plain(kv_lens, at::kInt, B, gpu) || (tree.defined() && !plain(tree, at::kLong, T, gpu)) ||
@@ -162,8 +169,22 @@ PyObject* attention(Args x) {
                           ptr<int32_t>(table), (int)row_step, ptr<int32_t>(starts), ptr<int32_t>(kv_lens),
                           ptr<int64_t>(tree), out.data_ptr(), out.stride(0), out.stride(1), ptr<float>(lse),
                           (int)table.size(1)};
-  const int status =
-      moe_attn_forward(reinterpret_cast<moe_attn_t*>(handle), &a, reinterpret_cast<moe_stream_t>(stream));
+  auto* const h = reinterpret_cast<moe_attn_t*>(handle);
+  const auto on_stream = reinterpret_cast<moe_stream_t>(stream);
+  int status;
+  if (quantised || prefix > 0) {
+    const moe_cache_scales_t s = scales_of(k_scale, v_scale);
+    moe_attn_opts_t o{quantised ? &s : nullptr, (int)prefix, nullptr, 0};
+    o.workspace_bytes = moe_attn_workspace(h, &a, &o);
+    Tensor workspace;  // goes back to the allocator at once, which keeps the stream's order
+    if (o.workspace_bytes > 0) {
+      workspace = at::empty({(int64_t)o.workspace_bytes}, q.options().dtype(at::kByte));
+      o.workspace = workspace.data_ptr();
+    }
+    status = moe_attn_forward_ex(h, &a, &o, on_stream);
+  } else {
+    status = moe_attn_forward(h, &a, on_stream);
+  }
   if (status != MOE_OK) return number(status);
   PyObject* o = THPVariable_Wrap(std::move(out));
   if (!want_lse || !o) return o;

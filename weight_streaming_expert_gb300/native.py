@@ -97,6 +97,11 @@ class moe_attn_args_t(ctypes.Structure):
                 ("lse", _p), ("table_pages", _i)]
 
 
+class moe_attn_opts_t(ctypes.Structure):
+    _fields_ = [("scales", ctypes.POINTER(moe_cache_scales_t)), ("prefix_len", _i), ("workspace", _p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
 class moe_adjust_logits_args_t(ctypes.Structure):
     _fields_ = [("logits", _p), ("row_stride", _l), ("out", _p), ("out_stride", _l), ("rows", _i), ("vocab", _i),
                 ("history", _p), ("n_history", _i), ("spans", _p), ("repetition", _p), ("presence", _p),
@@ -194,6 +199,10 @@ def lib(build_if_missing: bool = True):
         L.moe_attn_create.restype = vp
         L.moe_attn_forward.argtypes = [vp, ctypes.POINTER(moe_attn_args_t), vp]
         L.moe_attn_forward.restype = ci
+        L.moe_attn_forward_ex.argtypes = [vp, ctypes.POINTER(moe_attn_args_t), ctypes.POINTER(moe_attn_opts_t), vp]
+        L.moe_attn_forward_ex.restype = ci
+        L.moe_attn_workspace.argtypes = [vp, ctypes.POINTER(moe_attn_args_t), ctypes.POINTER(moe_attn_opts_t)]
+        L.moe_attn_workspace.restype = ctypes.c_size_t
         L.moe_attn_get_status.argtypes = [vp]
         L.moe_attn_get_status.restype = ci
         L.moe_attn_destroy.argtypes = [vp]
