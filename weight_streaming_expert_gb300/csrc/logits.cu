@@ -24,7 +24,7 @@ namespace {
 constexpr int kLogitThreads = 256;
 constexpr int kLogitLoads = 4;                              // float4 of a thread
 constexpr int kSlice = kLogitThreads * kLogitLoads * 4;     // tokens of a CTA
-constexpr uint32_t kPromptOnly = 0x80000000u;               // of a count word: it stands in the prompt
+constexpr int kTokens = 16;                                 // of the history that a thread has in flight
 
 struct Span {
   int begin, answer, end;
@@ -46,7 +46,9 @@ __device__ __forceinline__ Span span_of(const moe_adjust_logits_args_t& a, int r
 // kAligned: the output rows lie on the same remainder of 16 bytes.
 template <bool kInPlace, bool kAligned>
 __global__ void __launch_bounds__(kLogitThreads) adjust_logits_kernel(const __grid_constant__ moe_adjust_logits_args_t a) {
-  extern __shared__ uint4 table_words[];  // kSlice counts, then kSlice bias numbers (each only where given)
+  // kSlice counts of the answer's tokens and a byte for each that the prompt has,
+  // then kSlice bias numbers (each only where given)
+  extern __shared__ uint4 table_words[];
   const int tid = threadIdx.x, row = blockIdx.y;
   pdl_wait();
   pdl_launch_dependents();
@@ -56,29 +58,24 @@ __global__ void __launch_bounds__(kLogitThreads) adjust_logits_kernel(const __gr
   const int first = (int)blockIdx.x * kSlice - shift;  // token number 0 of the slice
   const bool counts = a.history != nullptr, biases = a.bias_ids != nullptr;
   uint32_t* count_of = reinterpret_cast<uint32_t*>(table_words);
-  int* bias_of = reinterpret_cast<int*>(count_of) + (counts ? kSlice : 0);
+  uint8_t* seen_in_prompt = reinterpret_cast<uint8_t*>(count_of + kSlice);
+  int* bias_of = reinterpret_cast<int*>(count_of) + (counts ? kSlice + kSlice / 4 : 0);
   const uint32_t* allowed = a.allowed ? a.allowed + row * a.allowed_stride : nullptr;
 
-  // the thread's four tokens of load i, their bits of the mask (those past the
-  // vocabulary's ends are 0 in `inside`)
+  // the thread's four tokens of load i; which of them the vocabulary holds, and
+  // which of those the mask allows
   auto token_of = [&](int i) { return first + (i * kLogitThreads + tid) * 4; };
   auto inside_of = [&](int v) {
+    if (v >= 0 && v + 3 < a.vocab) return 15u;
     uint32_t bits = 0;
-#pragma unroll
     for (int k = 0; k < 4; ++k) bits |= (unsigned)(v + k) < (unsigned)a.vocab ? 1u << k : 0u;
     return bits;
   };
   auto bits_of = [&](int v, uint32_t inside) {
     if (!allowed || !inside) return inside;
-    const int v0 = max(v, 0), v3 = min(v + 3, a.vocab - 1);
-    const uint64_t words = allowed[v0 >> 5] | (uint64_t)allowed[v3 >> 5] << 32;
-    uint32_t bits = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int at = (v + k & 31) + ((v + k) >> 5 == v0 >> 5 ? 0 : 32);
-      bits |= (uint32_t)(words >> at & 1) << k;
-    }
-    return bits & inside;
+    const int low = max(v, 0);
+    const uint32_t word = allowed[low >> 5], next = allowed[min(v + 3, a.vocab - 1) >> 5];
+    return __funnelshift_r(word, next, low & 31) << (low - v) & inside;
   };
   auto load4 = [&](int v, uint32_t wanted) {
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -104,22 +101,36 @@ __global__ void __launch_bounds__(kLogitThreads) adjust_logits_kernel(const __gr
 
   // ---- the tables
   if (counts || biases) {
-    const int words = ((counts ? kSlice : 0) + (biases ? kSlice : 0)) / 4;
+    // the history's first tokens are on their way while the tables are cleared
+    const Span span = counts ? span_of(a, row) : Span{0, 0, 0};
+    int token[kTokens];
+#pragma unroll
+    for (int k = 0; k < kTokens; ++k) {
+      const int i = span.begin + tid + k * kLogitThreads;
+      token[k] = i < span.end ? a.history[i] : -1;
+    }
+    const int words = ((counts ? kSlice + kSlice / 4 : 0) + (biases ? kSlice : 0)) / 4;
     for (int i = tid; i < words; i += kLogitThreads) table_words[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
     auto place_of = [&](int token) {  // in the slice, else past it
       return (unsigned)token < (unsigned)a.vocab ? (unsigned)(token - first) : ~0u;
     };
-    if (counts) {
-      const Span s = span_of(a, row);
-#pragma unroll 4
-      for (int i = s.begin + tid; i < s.end; i += kLogitThreads) {
-        const unsigned at = place_of(a.history[i]);
+    for (int at0 = span.begin + tid; at0 < span.end; at0 += kTokens * kLogitThreads) {
+      if (at0 != span.begin + tid) {
+#pragma unroll
+        for (int k = 0; k < kTokens; ++k) {
+          const int i = at0 + k * kLogitThreads;
+          token[k] = i < span.end ? a.history[i] : -1;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kTokens; ++k) {
+        const unsigned at = place_of(token[k]);
         if (at >= (unsigned)kSlice) continue;
-        if (i >= s.answer)
+        if (at0 + k * kLogitThreads >= span.answer)
           atomicAdd(count_of + at, 1u);
         else
-          atomicOr(count_of + at, kPromptOnly);
+          seen_in_prompt[at] = 1;  // by whichever thread
       }
     }
     if (biases) {
@@ -135,10 +146,10 @@ __global__ void __launch_bounds__(kLogitThreads) adjust_logits_kernel(const __gr
   // ---- the logits
   const float rep = a.repetition ? a.repetition[row] : 1.f, presence = a.presence ? a.presence[row] : 0.f;
   const float frequency = a.frequency ? a.frequency[row] : 0.f;
-  auto adjusted = [&](float v, uint32_t word, int bias) {
-    if (word) {
+  auto adjusted = [&](float v, uint32_t count, bool in_prompt, int bias) {
+    if (count || in_prompt) {
       if (a.repetition) v = v > 0.f ? __fdiv_rn(v, rep) : __fmul_rn(v, rep);
-      if (const uint32_t count = word & ~kPromptOnly) {
+      if (count) {
         if (a.frequency) v = __fsub_rn(v, __fmul_rn(frequency, (float)count));
         if (a.presence) v = __fsub_rn(v, presence);
       }
@@ -151,25 +162,34 @@ __global__ void __launch_bounds__(kLogitThreads) adjust_logits_kernel(const __gr
     const int v = token_of(i), at = v - first;
     const uint32_t inside = inside_of(v);
     if (!inside) continue;
-    uint4 word = make_uint4(0u, 0u, 0u, 0u);
+    uint4 count = make_uint4(0u, 0u, 0u, 0u);
+    uint32_t prompt = 0u;
     int4 bias = make_int4(0, 0, 0, 0);
-    if (counts) word = *reinterpret_cast<const uint4*>(count_of + at);
+    if (counts) {
+      count = *reinterpret_cast<const uint4*>(count_of + at);
+      prompt = *reinterpret_cast<const uint32_t*>(seen_in_prompt + at);
+    }
     if (biases) bias = *reinterpret_cast<const int4*>(bias_of + at);
-    const uint32_t* w = &word.x;
+    const uint32_t* c = &count.x;
     const int* b = &bias.x;
     uint32_t touched = 0;
+    if ((count.x | count.y | count.z | count.w | prompt) || (bias.x | bias.y | bias.z | bias.w)) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) touched |= w[k] || b[k] ? 1u << k : 0u;
+      for (int k = 0; k < 4; ++k) touched |= c[k] || (prompt >> 8 * k & 1) || b[k] ? 1u << k : 0u;
+    }
     if (kInPlace) {
       const uint32_t change = touched & allow[i];
       if (change) x[i] = load4(v, change);
     }
     float* p = &x[i].x;
+    if (touched) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (touched >> k & 1) p[k] = adjusted(p[k], w[k], b[k]);
-      if (!(allow[i] >> k & 1)) p[k] = -INFINITY;
+      for (int k = 0; k < 4; ++k)
+        if (touched >> k & 1) p[k] = adjusted(p[k], c[k], prompt >> 8 * k & 1, b[k]);
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (!(allow[i] >> k & 1)) p[k] = -INFINITY;
     if (kInPlace) {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
@@ -216,7 +236,7 @@ extern "C" int moe_adjust_logits(const moe_adjust_logits_args_t* a, moe_stream_t
   if (rc != MOE_OK) return rc;
   // up to three numbers before the first token, see `shift`
   const unsigned slices = (unsigned)((a->vocab + 3 + kSlice - 1) / kSlice);
-  const size_t smem = ((a->history ? 4u : 0u) + (a->bias_ids ? 4u : 0u)) * kSlice;
+  const size_t smem = ((a->history ? 5u : 0u) + (a->bias_ids ? 4u : 0u)) * kSlice;
   const bool same = ((reinterpret_cast<uintptr_t>(a->logits) ^ reinterpret_cast<uintptr_t>(a->out)) & 15) == 0 &&
                     (a->rows == 1 || ((a->row_stride ^ a->out_stride) & 3) == 0);
   return launch_pdl(in_place ? adjust_logits_kernel<true, true>

@@ -40,7 +40,6 @@ namespace wse {
 namespace {
 
 constexpr int kWarps = 8, kCodeThreads = (kWarps + 1) * 32;
-constexpr int kPiece = 16;  // positions of a warp's step
 
 template <int D>
 struct CodeLayout {
@@ -76,32 +75,26 @@ __device__ __forceinline__ uint32_t place_of(int r, int c) {
   return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ (r >> 1 & 3)) << 4);
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t at) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
-  return v;
+// 16 bytes to shared memory, both sides aligned to them, without waiting.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ uint2 lds64(uint32_t at) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t at) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
-  return v;
-}
-// dst, src and bytes multiples of 16.
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-               "r"(bytes), "r"(bar)
-               : "memory");
+// Arrives on `bar` once this thread's copies so far are in.
+__device__ __forceinline__ void arrive_with_copies(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 // An 8 x 8 block of 16-bit elements, a row's two in each lane, transposed.
 __device__ __forceinline__ uint32_t transposed(uint32_t v) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
   return d;
+}
+// D += A (16 x 16) B (16 x 8); unlike mma_f16 free to move among other work.
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // Codes that are NaN: the top bit of each such byte.
 __device__ __forceinline__ uint32_t nan_codes(uint32_t v) { return ((v & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
@@ -115,6 +108,21 @@ __device__ __forceinline__ bool row_sees(const P& p, const Item& it, int row, in
   return other < 0 || (other < 64 && ((unsigned long long)p.a.tree_mask[it.s.q0 + token] >> other & 1));
 }
 
+// Notes the columns from `column` on whose codes at `pos` are NaN (a bit of
+// `bad` for each byte) for those of the `rows` rows from `row0` that see them.
+template <typename P>
+__device__ __noinline__ void note_nan(const P& p, Item it, uint32_t* marks, volatile int* marked, uint32_t bad,
+                                      int row0, int rows, int pos, int column, int D) {
+  for (int row = row0; row < row0 + rows; ++row) {
+    if (!row_sees(p, it, row, pos)) continue;
+    for (int k = 0; k < 4; ++k) {
+      const int bit = row * D + column + k;
+      if (bad >> (8 * k + 7) & 1) atomicOr(marks + bit / 32, 1u << (bit & 31));
+    }
+    *marked = 1;
+  }
+}
+
 // kN: 8-row blocks of a warp; kG: groups of warps with rows of their own.  c:
 // scale * log2 e.
 template <int D, int kN, int kG, typename P>
@@ -125,6 +133,8 @@ __global__ void __launch_bounds__(kCodeThreads, 1)
   using L = CodeLayout<D>;
   constexpr int kStages = L::kStages;
   constexpr int kTogether = kWarps / kG;          // warps that share out the positions
+  constexpr int kB = kN == 1 ? 2 : 1;             // blocks of 16 positions of a warp's step
+  constexpr int kPiece = 16 * kB, kPieces = kTile / kPiece;
   constexpr int kSteps = D / 16;                  // MMAs of a score, and 16-column blocks of an output
   constexpr int kChunks = D / 64;                 // 16-byte columns of a key row in a lane
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -139,7 +149,7 @@ __global__ void __launch_bounds__(kCodeThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(full(s), 1);
+      mbar_init(full(s), 1 + 32);  // of the codes, and each copying lane's scales
       mbar_init(empty(s), kWarps);
     }
     fence_mbar_init();
@@ -161,46 +171,54 @@ __global__ void __launch_bounds__(kCodeThreads, 1)
   Item it{};
 
   if (warp == kWarps) {
-    // ---- copies: of a unit's pages, a lane each for the keys' codes, the values',
-    // and the scales of both
+    // ---- copies: of a unit's pages the codes with TMA, a lane each for keys and
+    // values, and the scales 16 bytes a lane (as small bulk copies they would be as
+    // many again for the copy engine)
     const int box_rows = min(a.page_size, kTile), per_unit = kTile / box_rows, page_log2 = 31 - __clz(a.page_size);
-    const int what = lane >> 3, box = lane & 7;
+    const int what = lane >> 3, place = lane & 7, step = what < 2 ? box_rows : 16;
     int filled = 0;
     while (walk.next(it)) {
+      // The table's entries come 32 at a time, an entry per lane, and a window
+      // ahead of their use: `even` and `odd` hold the windows of those numbers.
       const int32_t* row = p.table_row(it.b);
-      // this lane's table entry of a unit, a unit ahead of its use
-      auto entry = [&](int u) {
-        const int pos = u * kTile + box * box_rows;
-        return u < it.u1 && box < per_unit && pos < it.s.kv ? row[pos >> page_log2] : -1;
+      int even = 0, odd = 0, have = 0;
+      auto fetch = [&](int window) {
+        const int i = window * 32 + lane;
+        const int page = (long long)i * a.page_size < it.s.kv ? row[i] : -1;
+        if (window & 1)
+          odd = page;
+        else
+          even = page;
+        have = window;
       };
-      int next_page = entry(it.u0);
+      fetch((it.u0 * kTile >> page_log2) / 32);
+      fetch(have + 1);
       for (int u = it.u0; u < it.u1; ++u) {
-        const int page = next_page, pos = u * kTile + box * box_rows;
-        next_page = entry(u + 1);
-        const bool mine = box < per_unit && pos < it.s.kv;
+        const int pos = u * kTile + place * step, window = (u * kTile >> page_log2) / 32;
+        const int page = __shfl_sync(0xffffffffu, window & 1 ? odd : even, (pos >> page_log2) & 31);
+        const bool mine = pos < it.s.kv && (what >= 2 || place < per_unit);
         const bool there = (unsigned)page < (unsigned)a.n_pages;
         if (mine && !there) atomicOr(p.status, kAttnBadPage);
         const int stage = filled % kStages, round = filled / kStages;
         if (round > 0) wait(empty(stage), (round - 1) & 1);
         const unsigned boxes = __popc(__ballot_sync(0xffffffffu, mine && what < 2));
-        const unsigned bytes = __popc(__ballot_sync(0xffffffffu, mine && there && what >= 2));
-        if (lane == 0) mbar_arrive_expect_tx(full(stage), (boxes * D + bytes) * box_rows);
+        if (lane == 0) mbar_arrive_expect_tx(full(stage), boxes * D * box_rows);
         __syncwarp();
-        if (mine) {
-          const int in_page = pos & (a.page_size - 1);
-          if (what < 2) {  // a page that is not there lies outside the tensor and reads as zeros
-            tma_load_3d(sb + L::kRing + stage * L::kStage + what * L::kCodeTile + box * box_rows * D,
-                        what == 0 ? &k_map : &v_map, it.h * D, in_page, there ? page : a.n_pages, full(stage));
-          } else if (there) {
-            const char* from = what == 2 ? static_cast<const char*>(scales.k_scale) + page * scales.k_page_stride +
-                                               it.h * scales.k_head_stride
-                                         : static_cast<const char*>(scales.v_scale) + page * scales.v_page_stride +
-                                               it.h * scales.v_head_stride;
-            bulk_copy(sb + L::kScaleAt + stage * L::kScales + (what - 2) * kTile + box * box_rows, from + in_page,
-                     box_rows, full(stage));
-          }
+        if (mine && what < 2)  // a page that is not there lies outside the tensor and reads as zeros
+          tma_load_3d(sb + L::kRing + stage * L::kStage + what * L::kCodeTile + place * box_rows * D,
+                      what == 0 ? &k_map : &v_map, it.h * D, pos & (a.page_size - 1), there ? page : a.n_pages,
+                      full(stage));
+        if (mine && what >= 2 && there) {
+          const char* from = what == 2 ? static_cast<const char*>(scales.k_scale) + page * scales.k_page_stride +
+                                             it.h * scales.k_head_stride
+                                       : static_cast<const char*>(scales.v_scale) + page * scales.v_page_stride +
+                                             it.h * scales.v_head_stride;
+          copy16(sb + L::kScaleAt + stage * L::kScales + (what - 2) * kTile + place * 16,
+                 from + (pos & (a.page_size - 1)));
         }
+        arrive_with_copies(full(stage));
         ++filled;
+        if (((u + 1) * kTile >> page_log2) / 32 == have) fetch(have + 1);
       }
     }
     // no copy is in flight when the CTA ends, also after a wait has given up
@@ -277,63 +295,119 @@ __global__ void __launch_bounds__(kCodeThreads, 1)
       const int stage = taken % kStages;
       wait(full(stage), (taken / kStages) & 1);
       ++taken;
-      const uint32_t keys = sb + L::kRing + stage * L::kStage, values = keys + L::kCodeTile;
-      const uint32_t scale_at = sb + L::kScaleAt + stage * L::kScales;
+      const uint8_t* keys = smem + L::kRing + stage * L::kStage;
+      const uint8_t* values = keys + L::kCodeTile;
+      const uint8_t* scale_at = smem + L::kScaleAt + stage * L::kScales;
+      // this warp's steps of the unit; with more warps than steps units go to halves
+      // of the warps in turn
+      int piece = part;
+      if (kTogether > kPieces) piece = part / kPieces == ((u - it.u0) & 1) ? part % kPieces : kPieces;
 #pragma unroll 1
-      for (int piece = part; piece < kTile / kPiece; piece += kTogether) {
+      for (; piece < kPieces; piece += kTogether) {
         const int first = u * kTile + piece * kPiece;  // position
         if (first >= veil.hi) break;                    // none of these rows sees more
-        const int at = piece * kPiece + position_of<D>(g);
-        // ---- scores of positions at and at + 8
-        float s[kN][4];
+        // ---- scores of positions at(h) and at(h) + 8
+        auto at = [&](int h) { return piece * kPiece + 16 * h + position_of<D>(g); };
+        float s[kB][kN][4];
 #pragma unroll
-        for (int i = 0; i < kN; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+        for (int h = 0; h < kB; ++h) {
 #pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
-          const uint4 low = lds128(keys + place_of<D>(at, t + 4 * k)), high = lds128(keys + place_of<D>(at + 8, t + 4 * k));
-          const uint32_t lw[4] = {low.x, low.y, low.z, low.w}, hw[4] = {high.x, high.y, high.z, high.w};
+          for (int i = 0; i < kN; ++i) s[h][i][0] = s[h][i][1] = s[h][i][2] = s[h][i][3] = 0.f;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint32_t a0, a1, a2, a3;
-            e4m3x4_to_f16x2(lw[w], a0, a2);
-            e4m3x4_to_f16x2(hw[w], a1, a3);
+          for (int k = 0; k < kChunks; ++k) {
+            const uint4 low = *reinterpret_cast<const uint4*>(keys + place_of<D>(at(h), t + 4 * k));
+            const uint4 high = *reinterpret_cast<const uint4*>(keys + place_of<D>(at(h) + 8, t + 4 * k));
+            const uint32_t lw[4] = {low.x, low.y, low.z, low.w}, hw[4] = {high.x, high.y, high.z, high.w};
 #pragma unroll
-            for (int i = 0; i < kN; ++i) mma_f16(s[i], a0, a1, a2, a3, q[i][4 * k + w][0], q[i][4 * k + w][1]);
+            for (int w = 0; w < 4; ++w) {
+              uint32_t a0, a1, a2, a3;
+              e4m3x4_to_f16x2(lw[w], a0, a2);
+              e4m3x4_to_f16x2(hw[w], a1, a3);
+#pragma unroll
+              for (int i = 0; i < kN; ++i) mma(s[h][i], a0, a1, a2, a3, q[i][4 * k + w][0], q[i][4 * k + w][1]);
+            }
           }
         }
-        // the exponents of the two positions
-        const float ke[2] = {power_of_two(exponent_of(lds8(scale_at + at))),
-                             power_of_two(exponent_of(lds8(scale_at + at + 8)))};
-        const int f0 = exponent_of(lds8(scale_at + kTile + at)), f1 = exponent_of(lds8(scale_at + kTile + at + 8));
-        const float fe[2] = {(float)f0, (float)f1}, undo[2] = {power_of_two(-f0), power_of_two(-f1)};
-        bool grown = false;
-#pragma unroll
-        for (int i = 0; i < kN; ++i)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) s[i][k] = fmaf(s[i][k] * factor[i][k & 1], ke[k >> 1], fe[k >> 1]);
         const bool veiled = first + kPiece > veil.lo;
-        if (veiled) {
+        // the four positions that are this lane's columns of the probabilities, and of
+        // their values D / 8 bytes at its g
+        auto row_of = [&](int h, int r) {
+          return piece * kPiece + 16 * h + position_of<D>(2 * t + (r & 1)) + 8 * (r >> 1);
+        };
+        constexpr int kWords = D / 32;
+        uint32_t v[kB][4][kWords];
+#pragma unroll
+        for (int h = 0; h < kB; ++h)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            if (D == 128) {
+              const uint4 x =
+                  *reinterpret_cast<const uint4*>(values + place_of<D>(row_of(h, r), (g & 1) * 4 + (g >> 1)));
+              v[h][r][0] = x.x, v[h][r][1] = x.y, v[h][r][kWords - 2] = x.z, v[h][r][kWords - 1] = x.w;
+            } else {
+              const uint2 x =
+                  *reinterpret_cast<const uint2*>(values + place_of<D>(row_of(h, r), g >> 1) + (g & 1) * 8);
+              v[h][r][0] = x.x, v[h][r][1] = x.y;
+            }
+          }
+        float undo[kB][2];
+        float over = -INFINITY;  // by how much the largest exceeds its row's M
+#pragma unroll
+        for (int h = 0; h < kB; ++h) {
+          // the exponents of the two positions
+          const float ke[2] = {power_of_two(exponent_of(scale_at[at(h)])), power_of_two(exponent_of(scale_at[at(h) + 8]))};
+          const int f0 = exponent_of(scale_at[kTile + at(h)]), f1 = exponent_of(scale_at[kTile + at(h) + 8]);
+          const float fe[2] = {(float)f0, (float)f1};
+          undo[h][0] = power_of_two(-f0), undo[h][1] = power_of_two(-f1);
 #pragma unroll
           for (int i = 0; i < kN; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int pos = u * kTile + at + 8 * (k >> 1);
-              if (!row_sees(p, it, rows_at + 8 * i + 2 * t + (k & 1), pos)) s[i][k] = -INFINITY;
+            for (int k = 0; k < 4; ++k) s[h][i][k] = fmaf(s[h][i][k] * factor[i][k & 1], ke[k >> 1], fe[k >> 1]);
+        }
+        if (veiled) {
+          // a hidden position's probability is 0, but 0 * NaN is NaN: past the last
+          // position that any row sees values may be anything and become 0, before it
+          // NaN do and are noted for the rows that see them
+#pragma unroll
+          for (int h = 0; h < kB; ++h) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int pos = u * kTile + at(h) + 8 * (k >> 1);
+                if (!row_sees(p, it, rows_at + 8 * i + 2 * t + (k & 1), pos)) s[h][i][k] = -INFINITY;
+              }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int pos = u * kTile + row_of(h, r);
+#pragma unroll
+              for (int w = 0; w < kWords; ++w) {
+                if (pos >= veil.hi) v[h][r][w] = 0u;
+                const uint32_t bad = nan_codes(v[h][r][w]);
+                if (!bad) continue;
+                v[h][r][w] &= ~((bad >> 7) * 0xffu);
+                note_nan(p, it, marks, marked, bad, rows_at, 8 * kN, pos,
+                         (D == 128 ? 16 * ((g & 1) * 4 + (g >> 1)) : 8 * g) + 4 * w, D);
+              }
             }
+          }
         }
 #pragma unroll
-        for (int i = 0; i < kN; ++i)
+        for (int h = 0; h < kB; ++h)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) grown |= s[i][k] > M[i][k & 1] + kRescaleLog2;
-        if (__any_sync(0xffffffffu, grown)) {
+          for (int i = 0; i < kN; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) over = fmaxf(over, fmaxf(s[h][i][k], s[h][i][k + 2]) - M[i][k]);
+        if (__any_sync(0xffffffffu, over > kRescaleLog2)) {
 #pragma unroll
           for (int i = 0; i < kN; ++i)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              float top = fmaxf(s[i][k], s[i][k + 2]);
+              float top = M[i][k];
+#pragma unroll
+              for (int h = 0; h < kB; ++h) top = fmaxf(top, fmaxf(s[h][i][k], s[h][i][k + 2]));
 #pragma unroll
               for (int m = 4; m < 32; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-              top = fmaxf(top, M[i][k]);
               const float shrink = M[i][k] == -INFINITY ? 1.f : exp2_approx(M[i][k] - top);  // or nothing to shrink yet
               M[i][k] = top;
               l[i][k] *= shrink;
@@ -344,72 +418,35 @@ __global__ void __launch_bounds__(kCodeThreads, 1)
               }
             }
         }
-        uint32_t b[kN][2];
+        uint32_t b[kB][kN][2];
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          float x[4];
+        for (int h = 0; h < kB; ++h)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            x[k] = exp2_approx(s[i][k] - (M[i][k & 1] == -INFINITY ? 0.f : M[i][k & 1]));
-            l[i][k & 1] = fmaf(x[k], undo[k >> 1], l[i][k & 1]);
+          for (int i = 0; i < kN; ++i) {
+            float x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              x[k] = exp2_approx(s[h][i][k] - (M[i][k & 1] == -INFINITY ? 0.f : M[i][k & 1]));
+              l[i][k & 1] = fmaf(x[k], undo[h][k >> 1], l[i][k & 1]);
+            }
+            b[h][i][0] = transposed(pack<__half>(x[0], x[1]));
+            b[h][i][1] = transposed(pack<__half>(x[2], x[3]));
           }
-          b[i][0] = transposed(pack<__half>(x[0], x[1]));
-          b[i][1] = transposed(pack<__half>(x[2], x[3]));
-        }
-        // ---- values: of the four positions that are this lane's columns of b, D / 8
-        // bytes at its g
-        const int rows[4] = {piece * kPiece + position_of<D>(2 * t), piece * kPiece + position_of<D>(2 * t + 1),
-                             piece * kPiece + position_of<D>(2 * t) + 8, piece * kPiece + position_of<D>(2 * t + 1) + 8};
-        constexpr int kWords = D / 32;
-        uint32_t v[4][kWords];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if (D == 128) {
-            const uint4 x = lds128(values + place_of<D>(rows[r], (g & 1) * 4 + (g >> 1)));
-            v[r][0] = x.x, v[r][1] = x.y, v[r][kWords - 2] = x.z, v[r][kWords - 1] = x.w;
-          } else {
-            const uint2 x = lds64(values + place_of<D>(rows[r], g >> 1) + (g & 1) * 8);
-            v[r][0] = x.x, v[r][1] = x.y;
-          }
-        }
-        if (veiled) {
-          // a hidden position's probability is 0, but 0 * NaN is NaN: past the last
-          // position that any row sees values may be anything and become 0, before it
-          // NaN do and are noted for the rows that see them
+        for (int h = 0; h < kB; ++h)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int pos = u * kTile + rows[r];
+          for (int w = 0; w < kWords; ++w) {
 #pragma unroll
-            for (int w = 0; w < kWords; ++w) {
-              if (pos >= veil.hi) v[r][w] = 0u;
-              const uint32_t bad = nan_codes(v[r][w]);
-              if (!bad) continue;
-              v[r][w] &= ~((bad >> 7) * 0xffu);
-              const int column0 = D == 128 ? 16 * ((g & 1) * 4 + (g >> 1)) : 8 * g;
-              for (int row = rows_at; row < rows_at + 8 * kN; ++row) {
-                if (!row_sees(p, it, row, pos)) continue;
-                for (int k = 0; k < 4; ++k) {
-                  const int bit = row * D + column0 + 4 * w + k;
-                  if (bad >> (8 * k + 7) & 1) atomicOr(marks + bit / 32, 1u << (bit & 31));
-                }
-                *marked = 1;
-              }
+            for (int pair = 0; pair < 2; ++pair) {  // bytes 2 pair and 2 pair + 1 of the word: columns' block 2 w + pair
+              const uint32_t x = __byte_perm(v[h][0][w], v[h][1][w], pair == 0 ? 0x5140 : 0x7362);
+              const uint32_t y = __byte_perm(v[h][2][w], v[h][3][w], pair == 0 ? 0x5140 : 0x7362);
+              uint32_t a0, a1, a2, a3;
+              e4m3x4_to_f16x2(x, a0, a1);
+              e4m3x4_to_f16x2(y, a2, a3);
+#pragma unroll
+              for (int i = 0; i < kN; ++i) mma(o[i][2 * w + pair], a0, a1, a2, a3, b[h][i][0], b[h][i][1]);
             }
           }
-        }
-#pragma unroll
-        for (int w = 0; w < kWords; ++w) {
-#pragma unroll
-          for (int pair = 0; pair < 2; ++pair) {  // bytes 2 pair and 2 pair + 1 of the word: columns' block 2 w + pair
-            const uint32_t x = __byte_perm(v[0][w], v[1][w], pair == 0 ? 0x5140 : 0x7362);
-            const uint32_t y = __byte_perm(v[2][w], v[3][w], pair == 0 ? 0x5140 : 0x7362);
-            uint32_t a0, a1, a2, a3;
-            e4m3x4_to_f16x2(x, a0, a1);
-            e4m3x4_to_f16x2(y, a2, a3);
-#pragma unroll
-            for (int i = 0; i < kN; ++i) mma_f16(o[i][2 * w + pair], a0, a1, a2, a3, b[i][0], b[i][1]);
-          }
-        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty(stage));
