@@ -39,7 +39,7 @@
 namespace wse {
 namespace {
 
-constexpr int kWarps = 8, kCodeThreads = (kWarps + 1) * 32;
+constexpr int kWarps = 8, kCopyWarps = 4, kCodeThreads = (kWarps + kCopyWarps) * 32;
 
 template <int D>
 struct CodeLayout {
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kCodeThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(full(s), 1 + 32);  // of the codes, and each copying lane's scales
+      mbar_init(full(s), kCopyWarps * 5);  // of each its codes, and four lanes' scales
       mbar_init(empty(s), kWarps);
     }
     fence_mbar_init();
@@ -170,12 +170,20 @@ __global__ void __launch_bounds__(kCodeThreads, 1)
   Walk<1, P> walk(p, plan);
   Item it{};
 
-  if (warp == kWarps) {
-    // ---- copies: of a unit's pages the codes with TMA, a lane each for keys and
-    // values, and the scales 16 bytes a lane (as small bulk copies they would be as
-    // many again for the copy engine)
+  if (warp >= kWarps) {
+    // ---- copies, by four warps: keys and values, and the first and last pages of
+    // a unit.  The codes with TMA, a lane per page: the lanes' copies are issued one
+    // after the other, 90 clocks each, so one warp alone would need 1500 for a unit's
+    // 16 boxes of 16 rows, as long as memory does (pages of 16: 104 us, now 77).  The
+    // scales 16 bytes a lane.
+    const int values = (warp - kWarps) >> 1, half = (warp - kWarps) & 1;
     const int box_rows = min(a.page_size, kTile), per_unit = kTile / box_rows, page_log2 = 31 - __clz(a.page_size);
-    const int what = lane >> 3, place = lane & 7, step = what < 2 ? box_rows : 16;
+    const bool codes = lane < 4;
+    const int place = 4 * half + (lane & 3), step = codes ? box_rows : 16;
+    const CUtensorMap* const map = values ? &v_map : &k_map;
+    const char* const scale = static_cast<const char*>(values ? scales.v_scale : scales.k_scale);
+    const long long scale_page = values ? scales.v_page_stride : scales.k_page_stride;
+    const long long scale_head = values ? scales.v_head_stride : scales.k_head_stride;
     int filled = 0;
     while (walk.next(it)) {
       // The table's entries come 32 at a time, an entry per lane, and a window
@@ -196,27 +204,21 @@ __global__ void __launch_bounds__(kCodeThreads, 1)
       for (int u = it.u0; u < it.u1; ++u) {
         const int pos = u * kTile + place * step, window = (u * kTile >> page_log2) / 32;
         const int page = __shfl_sync(0xffffffffu, window & 1 ? odd : even, (pos >> page_log2) & 31);
-        const bool mine = pos < it.s.kv && (what >= 2 || place < per_unit);
+        const bool mine = lane < 8 && pos < it.s.kv && (!codes || place < per_unit);
         const bool there = (unsigned)page < (unsigned)a.n_pages;
         if (mine && !there) atomicOr(p.status, kAttnBadPage);
         const int stage = filled % kStages, round = filled / kStages;
         if (round > 0) wait(empty(stage), (round - 1) & 1);
-        const unsigned boxes = __popc(__ballot_sync(0xffffffffu, mine && what < 2));
+        const unsigned boxes = __popc(__ballot_sync(0xffffffffu, mine && codes));
         if (lane == 0) mbar_arrive_expect_tx(full(stage), boxes * D * box_rows);
         __syncwarp();
-        if (mine && what < 2)  // a page that is not there lies outside the tensor and reads as zeros
-          tma_load_3d(sb + L::kRing + stage * L::kStage + what * L::kCodeTile + place * box_rows * D,
-                      what == 0 ? &k_map : &v_map, it.h * D, pos & (a.page_size - 1), there ? page : a.n_pages,
-                      full(stage));
-        if (mine && what >= 2 && there) {
-          const char* from = what == 2 ? static_cast<const char*>(scales.k_scale) + page * scales.k_page_stride +
-                                             it.h * scales.k_head_stride
-                                       : static_cast<const char*>(scales.v_scale) + page * scales.v_page_stride +
-                                             it.h * scales.v_head_stride;
-          copy16(sb + L::kScaleAt + stage * L::kScales + (what - 2) * kTile + place * 16,
-                 from + (pos & (a.page_size - 1)));
-        }
-        arrive_with_copies(full(stage));
+        if (mine && !codes && there)
+          copy16(sb + L::kScaleAt + stage * L::kScales + values * kTile + place * 16,
+                 scale + page * scale_page + it.h * scale_head + (pos & (a.page_size - 1)));
+        if (lane >= 4 && lane < 8) arrive_with_copies(full(stage));
+        if (mine && codes)  // a page that is not there lies outside the tensor and reads as zeros
+          tma_load_3d(sb + L::kRing + stage * L::kStage + values * L::kCodeTile + place * box_rows * D, map, it.h * D,
+                      pos & (a.page_size - 1), there ? page : a.n_pages, full(stage));
         ++filled;
         if (((u + 1) * kTile >> page_log2) / 32 == have) fetch(have + 1);
       }
