@@ -20,8 +20,20 @@ struct Cut {
 constexpr double kMaxUnits = 2e9;          // of a call: they are counted in 32 bits
 constexpr int kMaxParts = 1024;            // CTAs, which is at least the shares of one tile
 
+// What an item costs besides its units, in units: its queries, the first scores
+// and the last sums, which nothing overlaps.  In the 16-bit kernel's pair form as
+// much as two units: ragged chunks of 900 to 1500 tokens over 1500 to 6000 take
+// 145 us with 0, 124 with 1, 119 with 2, 120 with 3.  In its split form, whose
+// copies run ahead, nothing to speak of (decode batch 130 us with 0 and 131 with
+// 1 or 2).
+template <int kTiles>
+constexpr int kItemCost = kTiles == 2 ? 2 : 0;
+
 struct AttnParams {
   static constexpr bool kShared = false;
+  static constexpr bool kAhead = false;  // a walk reads a sequence's lengths while it is at the one before
+  template <int kTiles>
+  static constexpr int kCost = kItemCost<kTiles>;
   moe_attn_args_t a;
   int n_kv_heads, group;
   int tokens;       // of a tile: 128 / group
@@ -47,6 +59,9 @@ struct AttnParams {
 // joins: where a share cut the tile in the parts, else in its place by token.
 struct SharedParams : AttnParams {
   static constexpr bool kShared = true;
+  static constexpr bool kAhead = true;
+  template <int kTiles>
+  static constexpr int kCost = 2;
   int prefix, prefix_pages;
   int prefix_items, own_items;  // items of each key/value head: of the prefix, and of a sequence
   float* whole_o;               // [prefix, own][n_tokens][heads][D]
@@ -127,10 +142,21 @@ struct Seq {
   int q0, n, kv, base;  // first new token, their count, positions, those before the chunk
   bool bad;
 };
-__device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
+// What memory says of a sequence.
+struct Lengths {
+  int q0, q1, kv;
+};
+__device__ __forceinline__ Lengths lengths_of(const AttnParams& p, int b) {
+  return {p.a.q_starts[b], p.a.q_starts[b + 1], p.a.kv_lens[b]};
+}
+__device__ __forceinline__ Lengths lengths_of(const SharedParams& p, int b) {
+  if (b == 0) return {0, p.a.q_starts[p.a.batch], 0};
+  return {p.a.q_starts[b - 1], p.a.q_starts[b], p.a.kv_lens[b - 1]};
+}
+__device__ __forceinline__ Seq seq_of(const AttnParams& p, int, const Lengths& n) {
   const moe_attn_args_t& a = p.a;
   Seq s;
-  const int q0 = a.q_starts[b], q1 = a.q_starts[b + 1], kv = a.kv_lens[b];
+  const int q0 = n.q0, q1 = n.q1, kv = n.kv;
   const long long room = min(1ll << 30, (long long)a.table_pages * a.page_size);
   s.q0 = max(0, min(q0, a.n_tokens));
   s.n = max(0, min(max(0, min(q1, a.n_tokens)) - s.q0, a.max_q_len));  // both in 0..n_tokens: no overflow
@@ -141,17 +167,17 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
   s.base = (int)max(-(1ll << 30), min(base, (1ll << 30) - 1));  // base + a token's number stays in 32 bits
   return s;
 }
-__device__ __forceinline__ Seq load_seq(const SharedParams& p, int b) {
+__device__ __forceinline__ Seq seq_of(const SharedParams& p, int b, const Lengths& n) {
   const moe_attn_args_t& a = p.a;
   Seq s;
   if (b == 0) {
     s.q0 = 0;
-    s.n = max(0, min(a.q_starts[a.batch], a.n_tokens));
+    s.n = max(0, min(n.q1, a.n_tokens));
     s.kv = s.base = p.prefix;
     s.bad = false;
     return s;
   }
-  const int q0 = a.q_starts[b - 1], q1 = a.q_starts[b], kv = a.kv_lens[b - 1];
+  const int q0 = n.q0, q1 = n.q1, kv = n.kv;
   const long long room = min(1ll << 30, (long long)(a.table_pages - p.prefix_pages) * a.page_size);
   s.q0 = max(0, min(q0, a.n_tokens));
   s.n = max(0, min(max(0, min(q1, a.n_tokens)) - s.q0, a.max_q_len));
@@ -161,6 +187,10 @@ __device__ __forceinline__ Seq load_seq(const SharedParams& p, int b) {
   s.bad = s.q0 != q0 || (long long)s.n != (long long)q1 - q0 || s.kv != own || base < 0;
   s.base = (int)max(-(1ll << 30), min(base, (1ll << 30) - 1));
   return s;
+}
+template <typename P>
+__device__ __forceinline__ Seq load_seq(const P& p, int b) {
+  return seq_of(p, b, lengths_of(p, b));
 }
 // 128-position tiles that item i of a sequence visits (at least one, which
 // writes the zeros of rows that see nothing).  kTiles: query tiles of an item.
@@ -177,14 +207,6 @@ template <typename X>
 __device__ __forceinline__ X uniform(X v) {
   return __shfl_sync(0xffffffffu, v, 0);
 }
-
-// What an item costs besides its units, in units: its queries, the first scores
-// and the last sums, which nothing overlaps.  In the pair form as much as two
-// units: ragged chunks of 900 to 1500 tokens over 1500 to 6000 take 145 us with
-// 0, 124 with 1, 119 with 2, 120 with 3.  In the split form, whose copies run
-// ahead, nothing to speak of (decode batch 130 us with 0 and 131 with 1 or 2).
-template <int kTiles>
-constexpr int kItemCost = kTiles == 2 ? 2 : 0;
 
 // A CTA's next piece of work.
 struct Item {
@@ -208,14 +230,26 @@ struct Walk {
   int b, h, tile, at, todo;
   Seq s;
   int loaded;
+  Lengths ahead;  // of the sequence after `loaded`
   __device__ Walk(const P& p_, const Plan& plan)
-      : p(p_), b(plan.b), h(plan.h), tile(plan.tile), at(plan.at), todo(plan.todo), s(plan.s), loaded(plan.b) {}
+      : p(p_), b(plan.b), h(plan.h), tile(plan.tile), at(plan.at), todo(plan.todo), s(plan.s), loaded(plan.b) {
+    if (P::kAhead) read_ahead();
+  }
+  __device__ void read_ahead() {
+    if (todo > 0 && loaded + 1 < p.sequences()) ahead = lengths_of(p, loaded + 1);
+  }
   __device__ bool next(Item& it) {
     if (todo <= 0) return false;
     for (;;) {
       if (loaded != b) {
-        s = load_seq(p, b);
-        loaded = b;
+        if (P::kAhead) {  // b is the next one: sequences are walked one by one
+          s = seq_of(p, b, ahead);
+          loaded = b;
+          read_ahead();
+        } else {
+          s = load_seq(p, b);
+          loaded = b;
+        }
       }
       if (tile * kTiles * p.tokens < s.n) break;
       tile = 0;
@@ -225,10 +259,10 @@ struct Walk {
     }
     it.b = b, it.h = h * p.spread + (int)blockIdx.x % p.spread, it.tile = tile, it.s = s;
     it.units = units_of<kTiles>(p, s, tile);
-    const int to = min(it.units + kItemCost<kTiles>, at + todo);
+    const int to = min(it.units + P::template kCost<kTiles>, at + todo);
     todo -= to - at;
-    it.u0 = max(0, at - kItemCost<kTiles>);
-    it.u1 = max(0, to - kItemCost<kTiles>);
+    it.u0 = max(0, at - P::template kCost<kTiles>);
+    it.u1 = max(0, to - P::template kCost<kTiles>);
     at = 0;
     ++tile;
     return it.u1 > 0;  // a share that ends before the item's first unit leaves it to the next
@@ -296,7 +330,7 @@ __device__ __forceinline__ Plan make_plan(const P& p, int per, long long lane_su
   plan.h = (unsigned)rest / (unsigned)own;
   rest -= plan.h * own;
   for (int tile = lane;; tile += 32) {  // 32 items at a time
-    const int u = tile * kTiles * p.tokens < plan.s.n ? units_of<kTiles>(p, plan.s, tile) + kItemCost<kTiles> : 0;
+    const int u = tile * kTiles * p.tokens < plan.s.n ? units_of<kTiles>(p, plan.s, tile) + P::template kCost<kTiles> : 0;
     const int to = scan_up(u);
     const unsigned past = __ballot_sync(0xffffffffu, to > rest);
     if (past) {
@@ -321,7 +355,7 @@ __device__ __forceinline__ Plan plan_of(const P& p, int* cost) {
     if (lane < p.sequences()) {
       const Seq s = load_seq(p, lane);
       if (s.bad && blockIdx.x == 0) atomicOr(p.status, kAttnBadLength);
-      for (int i = 0; i * kTiles * p.tokens < s.n; ++i) sum += units_of<kTiles>(p, s, i) + kItemCost<kTiles>;
+      for (int i = 0; i * kTiles * p.tokens < s.n; ++i) sum += units_of<kTiles>(p, s, i) + P::template kCost<kTiles>;
     }
     return make_plan<kTiles, false>(p, 1, sum, [&](int) { return sum; });
   }
@@ -330,7 +364,7 @@ __device__ __forceinline__ Plan plan_of(const P& p, int* cost) {
     if (s.bad && blockIdx.x == 0) atomicOr(p.status, kAttnBadLength);
     int sum = 0;
     for (int i = wide ? lane : 0; i * kTiles * p.tokens < s.n; i += wide ? 32 : 1)
-      sum += units_of<kTiles>(p, s, i) + kItemCost<kTiles>;
+      sum += units_of<kTiles>(p, s, i) + P::template kCost<kTiles>;
     if (wide) {
 #pragma unroll
       for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);

@@ -39,6 +39,20 @@
 namespace wse {
 namespace {
 
+// An item's start (the queries) and end (the warps' joining) take as long as some
+// units.
+constexpr int kCodeItemCost = 3;
+struct CodeParams : AttnParams {
+  static constexpr bool kAhead = true;
+  template <int kTiles>
+  static constexpr int kCost = kCodeItemCost;
+};
+struct SharedCodeParams : SharedParams {
+  static constexpr bool kAhead = true;
+  template <int kTiles>
+  static constexpr int kCost = kCodeItemCost;
+};
+
 constexpr int kWarps = 8, kCopyWarps = 4, kCodeThreads = (kWarps + kCopyWarps) * 32;
 
 template <int D>
@@ -649,13 +663,16 @@ __global__ void __launch_bounds__(kUnpackThreads) unpack_kernel(const __grid_con
 int code_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : kMaxCodeRows; }
 
 cudaError_t allow_quantised(int head_dim) {
-  const cudaError_t e = head_dim == 64 ? allow_rows<64, AttnParams>() : allow_rows<128, AttnParams>();
-  return e != cudaSuccess ? e : head_dim == 64 ? allow_rows<64, SharedParams>() : allow_rows<128, SharedParams>();
+  const cudaError_t e = head_dim == 64 ? allow_rows<64, CodeParams>() : allow_rows<128, CodeParams>();
+  return e != cudaSuccess   ? e
+         : head_dim == 64 ? allow_rows<64, SharedCodeParams>()
+                            : allow_rows<128, SharedCodeParams>();
 }
 
 int launch_quantised(const moe_attn& h, const AttnParams& p, const moe_cache_scales_t& s, const Maps& maps,
                      moe_stream_t stream) {
-  const int rc = h.head_dim == 64 ? launch_rows<64>(h, p, s, maps, stream) : launch_rows<128>(h, p, s, maps, stream);
+  const CodeParams c{p};
+  const int rc = h.head_dim == 64 ? launch_rows<64>(h, c, s, maps, stream) : launch_rows<128>(h, c, s, maps, stream);
   if (rc != MOE_OK) return rc;
   AttnParams joined = p;
   joined.a.scale = kUnitScale;
@@ -668,7 +685,8 @@ int launch_quantised(const moe_attn& h, const AttnParams& p, const moe_cache_sca
 
 int launch_quantised(const moe_attn& h, const SharedParams& p, const moe_cache_scales_t& s, const Maps& maps,
                      moe_stream_t stream) {
-  return h.head_dim == 64 ? launch_rows<64>(h, p, s, maps, stream) : launch_rows<128>(h, p, s, maps, stream);
+  const SharedCodeParams c{p};
+  return h.head_dim == 64 ? launch_rows<64>(h, c, s, maps, stream) : launch_rows<128>(h, c, s, maps, stream);
 }
 
 int launch_unpack(const moe_attn& h, const moe_attn_args_t& a, const moe_cache_scales_t& s, void* k_out, void* v_out,

@@ -20,76 +20,121 @@
 namespace wse {
 namespace {
 
-// Joins a token's results.  Block (i, y): item i of the sequences' own, 4 rows at
-// a time; the parts of a row, of the prefix and then of its own positions, are
-// read and added in that order by four threads for each column as in
-// join_kernel, so the same call gives the same bits every time.
-template <typename T, int D, int kTiles>
-__global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4)
-    shared_join_kernel(const __grid_constant__ SharedParams p) {
-  constexpr int kColumns = D / 4, kRows = kTiles * kTile;
-  __shared__ float factor[kJoinRows][2 * kMaxParts];
-  __shared__ float4 sums[kJoinGroups - 1][kJoinRows][kColumns];
-  __shared__ float2 total[kJoinRows];  // (1 / sum, log-sum)
-  const moe_attn_args_t& a = p.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int column = tid % kColumns, row = tid / kColumns % kJoinRows, group = tid / (kColumns * kJoinRows);
-  const int item = blockIdx.x % p.own_items, h = blockIdx.x / p.own_items % p.n_kv_heads;
-  const int b = blockIdx.x / p.own_items / p.n_kv_heads + 1;
-  // the lengths are no output of the kernel before, which starts this one only
-  // after it has waited for what came before itself
-  const Seq s = load_seq(p, b);
-  const int per = kTiles * p.tokens;
-  pdl_wait();
-  pdl_launch_dependents();
-  if (item * per >= s.n) return;
-  const Cut own = p.cuts[p.item_number(b, h, item)];
-  const float c = a.scale * 1.4426950408889634f;
+constexpr int kFewJoined = 8;  // parts of an item that a warp joins by itself
 
-  // row r of the item: its token in the sequence (s.n: none), and where its
-  // results lie
-  auto token_of = [&](int r) {
+// Where the results of the rows of one of a sequence's own items lie.
+template <int D, int kTiles>
+struct JoinItem {
+  static constexpr int kRows = kTiles * kTile;
+  const SharedParams& p;
+  int b, h, item;
+  Seq s;
+  Cut own;
+  __device__ JoinItem(const SharedParams& p_) : p(p_) {
+    item = blockIdx.x % p.own_items;
+    h = blockIdx.x / p.own_items % p.n_kv_heads;
+    b = blockIdx.x / p.own_items / p.n_kv_heads + 1;
+    // the lengths are no output of the kernel before, which starts this one only
+    // after it has waited for what came before itself
+    s = load_seq(p, b);
+  }
+  __device__ int per() const { return kTiles * p.tokens; }
+  // row r's token in the sequence; s.n: none
+  __device__ int token_of(int r) const {
     const int in_tile = r % kTile / p.group;
-    return in_tile < p.tokens ? item * per + r / kTile * p.tokens + in_tile : s.n;
-  };
+    return in_tile < p.tokens ? item * per() + r / kTile * p.tokens + in_tile : s.n;
+  }
   struct Row {
-    int token, head, first;  // first: parts of the prefix
+    int token, head, first;  // first: parts of the prefix, before the own ones
+    int row, before_row, parts;
     long long before, own;   // the whole results' places
-    int before_row, parts;
     Cut prefix;
   };
-  auto row_of = [&](int r) {
+  __device__ Row row_of(int r) const {
     Row x{};
     x.token = token_of(r);
     if (x.token >= s.n) return x;
-    const int t = s.q0 + x.token, place = t % per;
+    const int t = s.q0 + x.token, place = t % per();
+    x.row = r;
     x.head = h * p.group + r % kTile % p.group;
-    x.prefix = p.cuts[p.item_number(0, h, t / per)];
+    x.prefix = p.cuts[p.item_number(0, h, t / per())];
     x.before_row = place / p.tokens * kTile + place % p.tokens * p.group + r % kTile % p.group;
     x.before = p.whole_row(0, t, x.head);
     x.own = p.whole_row(b, t, x.head);
     x.first = x.prefix.parts;
     x.parts = x.first + own.parts;
     return x;
-  };
-  auto slot = [&](const Cut& cut, int i) { return 2ll * (cut.c + i * p.spread) + (i == 0 ? 1 : 0); };
-  auto ml_of = [&](const Row& x, int r, int i) {
+  }
+  __device__ long long slot(const Cut& cut, int i) const { return 2ll * (cut.c + i * p.spread) + (i == 0 ? 1 : 0); }
+  __device__ float2 ml_of(const Row& x, int i) const {
     if (i < x.first) return x.first == 1 ? p.whole_ml[x.before] : p.part_ml[slot(x.prefix, i) * kRows + x.before_row];
-    return own.parts == 1 ? p.whole_ml[x.own] : p.part_ml[slot(own, i - x.first) * kRows + r];
-  };
-  auto sums_of = [&](const Row& x, int r, int i) {
+    return own.parts == 1 ? p.whole_ml[x.own] : p.part_ml[slot(own, i - x.first) * kRows + x.row];
+  }
+  __device__ float4 sums_of(const Row& x, int i, int column) const {
     const float* at = i < x.first
                           ? (x.first == 1 ? p.whole_o + x.before * D
                                           : p.part_o + (slot(x.prefix, i) * kRows + x.before_row) * D)
                           : (own.parts == 1 ? p.whole_o + x.own * D
-                                            : p.part_o + (slot(own, i - x.first) * kRows + r) * D);
+                                            : p.part_o + (slot(own, i - x.first) * kRows + x.row) * D);
     return reinterpret_cast<const float4*>(at)[column];
-  };
+  }
+};
 
-  for (int r0 = blockIdx.y * kJoinRows; r0 < kRows; r0 += gridDim.y * kJoinRows) {
-    if (token_of(r0) >= s.n) continue;  // nor does a later row of the four have a token
-    const Row mine = row_of(r0 + row);
-    const bool valid = mine.token < s.n;
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+// (1 / sum, log-sum) of a row.
+__device__ __forceinline__ float2 total_of(float m, float l, float c) {
+  return make_float2(l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l),
+                     l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f);
+}
+__device__ __forceinline__ void add_scaled(float4& o, float4 v, float f) {
+  o.x = fmaf(v.x, f, o.x);
+  o.y = fmaf(v.y, f, o.y);
+  o.z = fmaf(v.z, f, o.z);
+  o.w = fmaf(v.w, f, o.w);
+}
+template <typename T>
+__device__ __forceinline__ void write_row(const SharedParams& p, long long t, int head, int column, float4 o, float2 total) {
+  const moe_attn_args_t& a = p.a;
+  *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + t * a.out_token_stride + head * a.out_head_stride + column * 4) =
+      make_uint2(pack<T>(o.x * total.x, o.y * total.x), pack<T>(o.z * total.x, o.w * total.x));
+  if (a.lse && column == 0) a.lse[t * (p.group * p.n_kv_heads) + head] = total.y;
+}
+
+// Joins a token's results.  Block (i, y): item i of the sequences' own, 4 rows at
+// a time; the parts of a row, of the prefix and then of its own positions, are
+// read and added in that order, so the same call gives the same bits every time.
+//
+// Where few tokens share the prefix it is cut into many parts (8 tokens of 20
+// heads: 30 for each), whose latency is what counts: four threads for each column
+// take a quarter of them each.
+template <typename T, int D, int kTiles>
+__global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4)
+    join_many_parts_kernel(const __grid_constant__ SharedParams p) {
+  constexpr int kColumns = D / 4;
+  __shared__ float factor[kJoinRows][2 * kMaxParts];
+  __shared__ float4 sums[kJoinGroups - 1][kJoinRows][kColumns];
+  __shared__ float2 total[kJoinRows];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int column = tid % kColumns, row = tid / kColumns % kJoinRows, group = tid / (kColumns * kJoinRows);
+  JoinItem<D, kTiles> it(p);
+  pdl_wait();
+  pdl_launch_dependents();
+  if (it.item * it.per() >= it.s.n) return;
+  it.own = p.cuts[p.item_number(it.b, it.h, it.item)];
+  const float c = p.a.scale * 1.4426950408889634f;
+  for (int r0 = blockIdx.y * kJoinRows; r0 < it.kRows; r0 += gridDim.y * kJoinRows) {
+    if (it.token_of(r0) >= it.s.n) continue;  // nor does a later row of the four have a token
+    const auto mine = it.row_of(r0 + row);
+    const bool valid = mine.token < it.s.n;
     // the first parts' sums are on their way while the factors are worked out
     constexpr int kAhead = 4;
     const int share = valid ? (mine.parts + kJoinGroups - 1) / kJoinGroups : 0;
@@ -97,62 +142,86 @@ __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4)
     float4 ahead[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
-      if (first + i < end) ahead[i] = sums_of(mine, r0 + row, first + i);
+      if (first + i < end) ahead[i] = it.sums_of(mine, first + i, column);
     if (warp < kJoinRows) {
-      const int r = r0 + warp;
-      const Row x = row_of(r);
-      if (x.token < s.n) {
+      const auto x = it.row_of(r0 + warp);
+      if (x.token < it.s.n) {
         float m = -INFINITY, l = 0.f;
-        for (int i = lane; i < x.parts; i += 32) m = fmaxf(m, ml_of(x, r, i).x);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        for (int i = lane; i < x.parts; i += 32) m = fmaxf(m, it.ml_of(x, i).x);
+        m = warp_max(m);
         for (int i = lane; i < x.parts; i += 32) {
-          const float2 ml = ml_of(x, r, i);
+          const float2 ml = it.ml_of(x, i);
           const float f = ml.x == -INFINITY ? 0.f : exp2_approx((ml.x - m) * c);
           factor[warp][i] = nothing_seen(ml) ? -1.f : f;
           l += ml.y * f;
         }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-        if (lane == 0)
-          total[warp] = make_float2(l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l),
-                                    l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f);
+        l = warp_sum(l);
+        if (lane == 0) total[warp] = total_of(m, l, c);
       }
     }
     __syncthreads();
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](int i, float4 v) {
       const float f = factor[row][i];
-      if (f < 0.f) return;
-      o.x = fmaf(v.x, f, o.x);
-      o.y = fmaf(v.y, f, o.y);
-      o.z = fmaf(v.z, f, o.z);
-      o.w = fmaf(v.w, f, o.w);
+      if (!(f < 0.f)) add_scaled(o, v, f);
     };
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
       if (first + i < end) add(first + i, ahead[i]);
 #pragma unroll 4
-    for (int i = first + kAhead; i < end; ++i) add(i, sums_of(mine, r0 + row, i));
+    for (int i = first + kAhead; i < end; ++i) add(i, it.sums_of(mine, i, column));
     if (group > 0) sums[group - 1][row][column] = o;
     __syncthreads();
     if (valid && group == 0) {
 #pragma unroll
-      for (int q = 0; q < kJoinGroups - 1; ++q) {
-        const float4 v = sums[q][row][column];
-        o.x += v.x;
-        o.y += v.y;
-        o.z += v.z;
-        o.w += v.w;
-      }
-      const float norm = total[row].x;
-      const long long t = s.q0 + mine.token;
-      *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + t * a.out_token_stride + mine.head * a.out_head_stride +
-                                column * 4) =
-          make_uint2(pack<T>(o.x * norm, o.y * norm), pack<T>(o.z * norm, o.w * norm));
-      if (a.lse && column == 0) a.lse[t * (p.group * p.n_kv_heads) + mine.head] = total[row].y;
+      for (int q = 0; q < kJoinGroups - 1; ++q) add_scaled(o, sums[q][row][column], 1.f);
+      write_row<T>(p, it.s.q0 + mine.token, mine.head, column, o, total[row]);
     }
     __syncthreads();  // before the next rows' factors are written
+  }
+}
+
+// The same for many tokens, whose results have few parts: a warp for each row,
+// and nothing shared (128 single tokens of 32 heads: 111 us with the kernel above).
+template <typename T, int D, int kTiles>
+__global__ void __launch_bounds__(32 * kJoinRows) join_few_parts_kernel(const __grid_constant__ SharedParams p) {
+  constexpr int kColumns = D / 4, kSide = 32 / kColumns;  // parts side by side
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, column = lane % kColumns, side = lane / kColumns;
+  JoinItem<D, kTiles> it(p);
+  pdl_wait();
+  pdl_launch_dependents();
+  if (it.item * it.per() >= it.s.n) return;
+  it.own = p.cuts[p.item_number(it.b, it.h, it.item)];
+  const float c = p.a.scale * 1.4426950408889634f;
+  for (int r = blockIdx.y * kJoinRows + warp; r < it.kRows; r += gridDim.y * kJoinRows) {
+    const auto x = it.row_of(r);
+    if (x.token >= it.s.n) continue;
+    float2 ml = lane < x.parts ? it.ml_of(x, lane) : make_float2(-INFINITY, 0.f);
+    float m = ml.x;
+    for (int i = lane + 32; i < x.parts; i += 32) m = fmaxf(m, it.ml_of(x, i).x);
+    m = warp_max(m);
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < x.parts; i0 += 32) {
+      if (i0 > 0) ml = i0 + lane < x.parts ? it.ml_of(x, i0 + lane) : make_float2(-INFINITY, 0.f);
+      const float f = ml.x == -INFINITY ? 0.f : exp2_approx((ml.x - m) * c);
+      l += ml.y * f;
+      const float used = nothing_seen(ml) ? -1.f : f;
+      const int n = min(32, x.parts - i0);
+#pragma unroll 4
+      for (int i = 0; i < n; i += kSide) {
+        const float g = __shfl_sync(0xffffffffu, used, (i + side) & 31);
+        if (i + side < n && !(g < 0.f)) add_scaled(o, it.sums_of(x, i0 + i + side, column), g);
+      }
+    }
+    if (kSide == 2) {
+      o.x += __shfl_xor_sync(0xffffffffu, o.x, 16);
+      o.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
+      o.z += __shfl_xor_sync(0xffffffffu, o.z, 16);
+      o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
+    }
+    l = warp_sum(l);
+    if (side == 0) write_row<T>(p, it.s.q0 + x.token, x.head, column, o, total_of(m, l, c));
   }
 }
 
@@ -181,13 +250,20 @@ int launch(const moe_attn& h, const SharedParams& p, const Maps& maps, moe_strea
                                                                 : launch<T, D, false>(h, p, maps, stream);
 }
 
-template <typename T, int D>
-int launch_join(const SharedParams& p, bool pair, moe_stream_t stream) {
+template <typename T, int D, int kTiles>
+int launch_join(const moe_attn& h, const SharedParams& p, moe_stream_t stream) {
   // as many blocks as the rows of an item have use for
-  const int rows = pair ? 2 * kTile : std::max(1, std::min(p.a.max_q_len, p.tokens)) * p.group;
+  const int rows = kTiles == 2 ? 2 * kTile : std::max(1, std::min(p.a.max_q_len, p.tokens)) * p.group;
   const dim3 grid((unsigned)(p.a.batch * p.n_kv_heads * p.own_items), (unsigned)((rows + kJoinRows - 1) / kJoinRows));
-  return launch_pdl(pair ? shared_join_kernel<T, D, 2> : shared_join_kernel<T, D, 1>, grid,
-                    dim3(kJoinRows * kJoinGroups * D / 4), 0, stream, 1, p);
+  // about as many parts has an item of the prefix if the CTAs do nothing else
+  const int parts = h.n_sms / p.spread / p.prefix_items;
+  return parts > kFewJoined ? launch_pdl(join_many_parts_kernel<T, D, kTiles>, grid, dim3(kJoinRows * kJoinGroups * D / 4),
+                                         0, stream, 1, p)
+                            : launch_pdl(join_few_parts_kernel<T, D, kTiles>, grid, dim3(32 * kJoinRows), 0, stream, 1, p);
+}
+template <typename T, int D>
+int launch_join(const moe_attn& h, const SharedParams& p, bool pair, moe_stream_t stream) {
+  return pair ? launch_join<T, D, 2>(h, p, stream) : launch_join<T, D, 1>(h, p, stream);
 }
 
 }  // namespace
@@ -195,7 +271,7 @@ int launch_join(const SharedParams& p, bool pair, moe_stream_t stream) {
 // Whether tiles go in pairs: own chunks of more than a tile do as without a
 // prefix, and where many tiles of tokens share the prefix each pair reads it once.
 bool shared_in_pairs(int n_tokens, int max_q_len, int tokens) {
-  return max_q_len > tokens || n_tokens >= 8 * tokens;
+  return max_q_len > tokens;
 }
 
 cudaError_t allow_shared(int head_dim) { return head_dim == 64 ? allow_all<64>() : allow_all<128>(); }
@@ -209,9 +285,9 @@ int launch_shared(const moe_attn& h, const SharedParams& p, const Maps& maps, mo
 
 int launch_shared_join(const moe_attn& h, const SharedParams& p, bool pair, moe_stream_t stream) {
   if (p.a.dtype == MOE_DTYPE_BF16)
-    return h.head_dim == 64 ? launch_join<__nv_bfloat16, 64>(p, pair, stream)
-                            : launch_join<__nv_bfloat16, 128>(p, pair, stream);
-  return h.head_dim == 64 ? launch_join<__half, 64>(p, pair, stream) : launch_join<__half, 128>(p, pair, stream);
+    return h.head_dim == 64 ? launch_join<__nv_bfloat16, 64>(h, p, pair, stream)
+                            : launch_join<__nv_bfloat16, 128>(h, p, pair, stream);
+  return h.head_dim == 64 ? launch_join<__half, 64>(h, p, pair, stream) : launch_join<__half, 128>(h, p, pair, stream);
 }
 
 }  // namespace wse
