@@ -55,6 +55,13 @@ struct SharedCodeParams : SharedParams {
 
 constexpr int kWarps = 8, kCopyWarps = 4, kCodeThreads = (kWarps + kCopyWarps) * 32;
 
+// Registers of a thread: the copying warps give most of theirs to the others,
+// which hold two blocks of positions at a time (16 rows: 110 us with one and 200
+// bytes spilled).  The shares add up to what the block is launched with, which
+// allow() makes sure of.
+constexpr int kLaunchRegisters = 168, kWorkRegisters = 224, kCopyRegisters = 56;
+static_assert(kWarps * kWorkRegisters + kCopyWarps * kCopyRegisters == (kWarps + kCopyWarps) * kLaunchRegisters);
+
 template <int D>
 struct CodeLayout {
   static constexpr uint32_t kCodeTile = kTile * D;            // codes of keys or values of a unit
@@ -147,7 +154,7 @@ __global__ void __launch_bounds__(kCodeThreads, 1)
   using L = CodeLayout<D>;
   constexpr int kStages = L::kStages;
   constexpr int kTogether = kWarps / kG;          // warps that share out the positions
-  constexpr int kB = kN == 1 ? 2 : 1;             // blocks of 16 positions of a warp's step
+  constexpr int kB = 2;                           // blocks of 16 positions of a warp's step
   constexpr int kPiece = 16 * kB, kPieces = kTile / kPiece;
   constexpr int kSteps = D / 16;                  // MMAs of a score, and 16-column blocks of an output
   constexpr int kChunks = D / 64;                 // 16-byte columns of a key row in a lane
@@ -185,6 +192,7 @@ __global__ void __launch_bounds__(kCodeThreads, 1)
   Item it{};
 
   if (warp >= kWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegisters));
     // ---- copies, by four warps: keys and values, and the first and last pages of
     // a unit.  The codes with TMA, a lane per page: the lanes' copies are issued one
     // after the other, 90 clocks each, so one warp alone would need 1500 for a unit's
@@ -246,6 +254,7 @@ __global__ void __launch_bounds__(kCodeThreads, 1)
   }
 
   // ---- scores, probabilities and sums
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWorkRegisters));
   const int g = lane >> 2, t = lane & 3;
   const int rows_at = warp / kTogether * (8 * kN), part = warp % kTogether;
   float* join = reinterpret_cast<float*>(smem + L::kJoinAt);
@@ -569,6 +578,11 @@ __global__ void __launch_bounds__(kCodeThreads, 1)
 
 template <int D, int kN, int kG, typename P>
 cudaError_t allow() {
+  // with fewer registers than the shares of its warps a block would wait for them for ever
+  cudaFuncAttributes f{};
+  const cudaError_t e = cudaFuncGetAttributes(&f, quantised_attention_kernel<D, kN, kG, P>);
+  if (e != cudaSuccess) return e;
+  if (f.numRegs != kLaunchRegisters) return cudaErrorInvalidKernelImage;
   return cudaFuncSetAttribute(quantised_attention_kernel<D, kN, kG, P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               (int)CodeLayout<D>::kSmem);
 }
