@@ -182,14 +182,15 @@ int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t strea
  * tokens lie behind them (a sequence that is shorter is an error found on the
  * device).  The prefix is read once for the whole batch instead of once for
  * each sequence; the results are those of a call without, but for rounding.
- * With scales at most 64 query heads may share a key/value head.
+ * Of a quantised cache's prefix, where it is read for more than 64 rows, and of
+ * such chunks' pages as above the 16-bit copies lie in the workspace.
  */
 typedef struct {
   const moe_cache_scales_t* scales; /* host struct; NULL: a 16-bit cache */
   int prefix_len;                   /* 0: none */
   void* workspace;                  /* device, 16-byte aligned, free for other use once the call's work is done; */
-  size_t workspace_bytes;           /* moe_attn_workspace() of them (for chunks over codes that of one sequence
-                                    suffices: the sequences then take turns) */
+  size_t workspace_bytes;           /* moe_attn_workspace() of them (for chunks over codes one sequence's pages
+                                    suffice: the sequences then take turns) */
 } moe_attn_opts_t;
 
 /* Bytes of workspace that moe_attn_forward_ex takes for such a call; 0: none. */

@@ -13,9 +13,10 @@ softmax probabilities pi_j, the scales 2^(e_j) and 2^(f_j) and the codes v_jd:
     largest one of at least 1 (per warp; the largest of a warp is at most that of
     all): a relative 2^-11, or the half step 2^-25 of that largest one;
   * the output is rounded once.
-Chunks of more than 64 rows go through 16 bits: their probabilities are rounded
-to the element type, which the tolerance of test_attention counts (fp16 holds
-these codes times their scales exactly)."""
+Chunks of more than 64 rows, and all rows over a shared prefix if they are more
+than 64 together, go through 16 bits: their probabilities are rounded to the
+element type, which the tolerance of test_attention counts (fp16 holds these
+codes times their scales exactly)."""
 import math
 
 import pytest
@@ -81,7 +82,8 @@ class CodeCase(Case):
 
     def check(self, out, lse, dtype, known_nan=None):
         h = torch.finfo(dtype).eps / 2
-        chunks = max(self.q_lens + [0]) * self.group > 64 and not getattr(self, "prefix", 0)
+        chunks = max(self.q_lens + [0]) * self.group > 64 or (getattr(self, "prefix", 0) and
+                                                              self.starts[-1] * self.group > 64)
         assert out.dtype == dtype
         for b, m in enumerate(self.q_lens):
             n, rows = max(0, self.kv_lens[b]), slice(self.starts[b], self.starts[b + 1])

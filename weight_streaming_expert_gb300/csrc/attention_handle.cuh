@@ -40,12 +40,11 @@ struct moe_attn {
 
 namespace wse {
 
-// shared_attention.cu: 16-bit caches, all tokens over a shared prefix
+// shared_attention.cu: 16-bit caches behind a shared prefix, in tiles of kTile rows or pairs of them
 cudaError_t allow_shared(int head_dim);
-int launch_shared(const moe_attn& h, const SharedParams& p, const Maps& maps, moe_stream_t stream);
-// ... and the joining of every token's two results, for tiles of kTile rows or pairs of them
-int launch_shared_join(const moe_attn& h, const SharedParams& p, bool pair, moe_stream_t stream);
-bool shared_in_pairs(int n_tokens, int max_q_len, int tokens);
+int launch_shared(const moe_attn& h, const SharedParams& p, bool pair, const Maps& maps, moe_stream_t stream);
+// ... and the joining of every token's two results
+int launch_shared_join(const moe_attn& h, const JoinParams& j, moe_stream_t stream);
 
 // quantised_attention.cu, whose scores and maxima are exponents in base 2: what
 // joins its results takes this scale
@@ -57,9 +56,16 @@ int launch_quantised(const moe_attn& h, const AttnParams& p, const moe_cache_sca
                      moe_stream_t stream);
 int launch_quantised(const moe_attn& h, const SharedParams& p, const moe_cache_scales_t& s, const Maps& maps,
                      moe_stream_t stream);
-// The pages of a->batch sequences in 16 bits, page i of sequence b as page b * table_pages + i of k_out and v_out, and
-// that table.
-int launch_unpack(const moe_attn& h, const moe_attn_args_t& a, const moe_cache_scales_t& s, void* k_out, void* v_out,
-                  int32_t* table, moe_stream_t stream);
+// Pages in 16 bits, for what reads them often.  Row b of the table, from its `skip`-th entry on, holds sequence b's
+// pages; page i of it becomes page first + b * pages + i of k and v, and entry skip + i of row b of `table`.
+struct Unpacked {
+  void* k;
+  void* v;
+  int32_t* table;
+  int table_stride, first;
+};
+// `len`: positions of each row, or kv_lens (-1) less those of the skipped pages
+int launch_unpack(const moe_attn& h, const moe_attn_args_t& a, const moe_cache_scales_t& s, const Unpacked& to, int batch,
+                  int skip, int pages, int len, moe_stream_t stream);
 
 }  // namespace wse

@@ -62,14 +62,18 @@ struct SharedParams : AttnParams {
   static constexpr bool kAhead = true;
   template <int kTiles>
   static constexpr int kCost = 2;
+  enum Lists { kBoth, kPrefixOnly, kOwnOnly };
+  Lists lists;                  // those that this launch works on
   int prefix, prefix_pages;
   int prefix_items, own_items;  // items of each key/value head: of the prefix, and of a sequence
   float* whole_o;               // [prefix, own][n_tokens][heads][D]
   float2* whole_ml;             // [prefix, own][n_tokens][heads]
   // `cuts` has an entry for every item: of the prefix by head and item, then of
   // the sequences by number, head and item; 1 part: not cut
-  __device__ __forceinline__ int sequences() const { return a.batch + 1; }
-  __device__ __forceinline__ int longest() const { return max(a.max_q_len, a.n_tokens); }
+  __device__ __forceinline__ int sequences() const { return lists == kPrefixOnly ? 1 : a.batch + 1; }
+  __device__ __forceinline__ int longest() const {
+    return lists == kOwnOnly ? a.max_q_len : max(a.max_q_len, a.n_tokens);
+  }
   __device__ __forceinline__ const int32_t* table_row(int b) const {
     return b == 0 ? a.block_table : a.block_table + (long long)(b - 1) * a.table_stride + prefix_pages;
   }
@@ -81,6 +85,18 @@ struct SharedParams : AttnParams {
   __device__ __forceinline__ long long whole_row(int b, int token, int head) const {
     return ((long long)(b == 0 ? 0 : a.n_tokens) + token) * (n_kv_heads * group) + head;
   }
+};
+
+// How the items of one list were cut into tiles, and what their results say.
+struct JoinSide {
+  int tokens, tiles;       // of a tile, of an item
+  const float* part_o;
+  const float2* part_ml;
+  float c;                 // a maximum times c is an exponent in base 2
+};
+struct JoinParams {
+  SharedParams p;
+  JoinSide before, own;    // of the prefix and of the sequences' own positions
 };
 
 namespace {
@@ -150,7 +166,7 @@ __device__ __forceinline__ Lengths lengths_of(const AttnParams& p, int b) {
   return {p.a.q_starts[b], p.a.q_starts[b + 1], p.a.kv_lens[b]};
 }
 __device__ __forceinline__ Lengths lengths_of(const SharedParams& p, int b) {
-  if (b == 0) return {0, p.a.q_starts[p.a.batch], 0};
+  if (b == 0) return {p.a.q_starts[0], p.a.q_starts[p.a.batch], 0};
   return {p.a.q_starts[b - 1], p.a.q_starts[b], p.a.kv_lens[b - 1]};
 }
 __device__ __forceinline__ Seq seq_of(const AttnParams& p, int, const Lengths& n) {
@@ -171,8 +187,8 @@ __device__ __forceinline__ Seq seq_of(const SharedParams& p, int b, const Length
   const moe_attn_args_t& a = p.a;
   Seq s;
   if (b == 0) {
-    s.q0 = 0;
-    s.n = max(0, min(n.q1, a.n_tokens));
+    s.q0 = max(0, min(n.q0, a.n_tokens));
+    s.n = p.lists == SharedParams::kOwnOnly ? 0 : max(0, min(n.q1, a.n_tokens) - s.q0);
     s.kv = s.base = p.prefix;
     s.bad = false;
     return s;

@@ -310,99 +310,185 @@ bool in_chunks(const moe_attn& h, const moe_attn_args_t& a) {
   return std::max(1ll, (long long)a.max_q_len) * (h.n_heads / h.n_kv_heads) > kMaxCodeRows;
 }
 constexpr size_t kUnpackBytes = size_t{1} << 30;  // sequences beyond that take turns
-// of a sequence in 16 bits, and its row of the table
-size_t sequence_bytes(const moe_attn& h, const moe_attn_args_t& a) {
-  const size_t pages = a.table_pages > 0 ? a.table_pages : a.table_stride;
-  return pages * ((size_t)a.page_size * h.n_kv_heads * h.head_dim * 4 + 16);
+// of a page in 16 bits, keys and values
+size_t page_bytes(const moe_attn& h, const moe_attn_args_t& a) {
+  return (size_t)a.page_size * h.n_kv_heads * h.head_dim * 4;
 }
-int forward_unpacked(moe_attn* h, const moe_attn_args_t& args, const moe_attn_opts_t& o, moe_stream_t stream) {
+// of a sequence's pages behind a prefix in 16 bits, and its row of the table
+size_t sequence_bytes(const moe_attn& h, const moe_attn_args_t& a, int prefix_pages) {
+  return (a.table_pages - prefix_pages) * page_bytes(h, a) + (size_t)a.table_pages * 16;
+}
+
+// Tiles of tokens from which the prefix's list runs by itself.
+constexpr int kApartTiles = 32;
+
+// How a call with options is worked on, and what it keeps in the workspace.
+struct Work {
+  bool unpack;                 // every page goes through 16 bits
+  // with a prefix:
+  bool apart;                  // its list runs by itself, over 16 bits, and the sequences' own after it
+  int tokens, tiles;           // of the prefix's tiles and items
+  int own_tokens, own_tiles;
+  int prefix_pages, prefix_items, own_items;
+  size_t ml_at, cuts_at, parts_at, part_ml_at, prefix_at, sequences_at;  // the last two: unpacked pages
+  size_t sequence, need, wanted;
+};
+Work work_of(const moe_attn& h, const moe_attn_args_t& a, const moe_attn_opts_t& o) {
+  const int group = h.n_heads / h.n_kv_heads, tile = kTile / group, longest = std::max(1, a.max_q_len);
+  Work w{};
+  w.unpack = o.scales && in_chunks(h, a);
+  w.prefix_pages = o.prefix_len / a.page_size;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t from = at;
+    at += (bytes + 15) / 16 * 16;
+    return from;
+  };
+  if (o.prefix_len > 0) {
+    if (o.scales && !w.unpack) {
+      // one tile of codes takes all tokens, or the prefix goes to the 16-bit kernel
+      w.apart = (long long)a.n_tokens * group > kMaxCodeRows;
+      w.own_tokens = code_rows((w.apart ? longest : a.n_tokens) * group) / group;
+      w.own_tiles = 1;
+    } else {
+      // many tiles of tokens: pairs of them over the prefix
+      w.own_tiles = longest > tile ? 2 : 1;
+      w.own_tokens = tile;
+      w.apart = w.own_tiles == 1 && a.n_tokens >= kApartTiles * tile;
+    }
+    w.tokens = w.apart ? tile : w.own_tokens;
+    w.tiles = w.apart ? (a.n_tokens > tile ? 2 : 1) : w.own_tiles;
+    const int per = w.tokens * w.tiles, own_per = w.own_tokens * w.own_tiles;
+    w.prefix_items = (a.n_tokens + per - 1) / per;
+    w.own_items = (int)(((long long)longest + own_per - 1) / own_per);
+    const size_t rows = 2 * (size_t)a.n_tokens * h.n_heads;
+    const size_t items = (size_t)h.n_kv_heads * (w.prefix_items + (size_t)a.batch * w.own_items);
+    take(rows * h.head_dim * sizeof(float));
+    w.ml_at = take(rows * sizeof(float2));
+    w.cuts_at = take(items * sizeof(Cut));
+    if (w.apart) {
+      const size_t parts = (size_t)h.n_sms * 2 * w.tiles * kTile;
+      w.parts_at = take(parts * h.head_dim * sizeof(float));
+      w.part_ml_at = take(parts * sizeof(float2));
+    }
+  }
+  if (w.unpack || (o.scales && w.apart)) w.prefix_at = take(w.prefix_pages * (page_bytes(h, a) + 16));
+  w.need = w.wanted = w.sequences_at = at;
+  if (w.unpack) {
+    w.sequence = sequence_bytes(h, a, w.prefix_pages);
+    w.need += w.sequence;
+    w.wanted += w.sequence * std::max<size_t>(1, std::min<size_t>(a.batch, kUnpackBytes / std::max<size_t>(w.sequence, 1)));
+  }
+  return w;
+}
+
+// The lists of a batch behind a prefix over 16-bit caches, or over codes the
+// sequences' own list at least (`first`: the prefix's pages in 16 bits then).
+int run_shared(moe_attn* h, const moe_attn_args_t& a, const moe_attn_opts_t& o, const Work& w, bool codes,
+               const moe_attn_args_t& first, moe_stream_t stream) {
+  char* at = static_cast<char*>(o.workspace);
+  SharedParams p{};
+  int rc = fill_params(*h, a, w.own_tokens, w.own_tiles, &p);
+  if (rc != MOE_OK) return rc;
+  p.fits = true;
+  p.by_item = false;
+  p.lists = w.apart ? SharedParams::kOwnOnly : SharedParams::kBoth;
+  p.prefix = o.prefix_len;
+  p.prefix_pages = w.prefix_pages;
+  p.prefix_items = w.prefix_items;
+  p.own_items = w.own_items;
+  p.whole_o = reinterpret_cast<float*>(at);
+  p.whole_ml = reinterpret_cast<float2*>(at + w.ml_at);
+  p.cuts = reinterpret_cast<Cut*>(at + w.cuts_at);
+  const float c = a.scale * 1.4426950408889634f;
+  JoinParams j{p, {}, {w.own_tokens, w.own_tiles, p.part_o, p.part_ml, codes ? 1.f : c}};
+  j.before = j.own;
+  Maps maps;
+  if (w.apart) {
+    SharedParams q = p;
+    q.a = first;
+    q.lists = SharedParams::kPrefixOnly;
+    q.tokens = w.tokens;
+    q.part_o = reinterpret_cast<float*>(at + w.parts_at);
+    q.part_ml = reinterpret_cast<float2*>(at + w.part_ml_at);
+    j.before = {w.tokens, w.tiles, q.part_o, q.part_ml, c};
+    rc = maps_16(h, first, w.tokens, &maps);
+    if (rc == MOE_OK) rc = launch_shared(*h, q, w.tiles == 2, maps, stream);
+    if (rc != MOE_OK) return rc;
+  }
+  rc = codes ? maps_codes(h, a, &maps) : maps_16(h, a, w.own_tokens, &maps);
+  if (rc == MOE_OK)
+    rc = codes ? launch_quantised(*h, p, *o.scales, maps, stream) : launch_shared(*h, p, w.own_tiles == 2, maps, stream);
+  return rc != MOE_OK ? rc : launch_shared_join(*h, j, stream);
+}
+
+// a's cache in 16-bit pages of the workspace, `pages` of them.
+moe_attn_args_t over_pages(const moe_attn& h, const moe_attn_args_t& a, const Unpacked& u, long long pages) {
+  const int64_t row = (int64_t)h.n_kv_heads * h.head_dim;
+  moe_attn_args_t r = a;
+  r.k_cache = u.k;
+  r.v_cache = u.v;
+  r.n_pages = (int)std::max(1ll, pages);
+  r.k_row_stride = r.v_row_stride = row;
+  r.k_page_stride = r.v_page_stride = a.page_size * row;
+  r.block_table = u.table;
+  r.table_stride = u.table_stride;
+  return r;
+}
+
+int forward_with(moe_attn* h, const moe_attn_args_t& args, const moe_attn_opts_t& o, moe_stream_t stream) {
   const moe_attn_args_t a = with_pages(args);
-  const int here = check_current(*h);
-  if (here != MOE_OK) return here;
-  const size_t one = sequence_bytes(*h, a), row = (size_t)h->n_kv_heads * h->head_dim;
+  const Work w = work_of(*h, a, o);
+  if (o.prefix_len > 0) {
+    const double units =
+        ((double)w.prefix_items * ((double)o.prefix_len / kTile + 1 + kItemCost<2>) +
+         (double)a.batch * w.own_items * item_cost(a, a.table_pages)) * h->n_kv_heads;
+    if (units > kMaxUnits) return too_much();
+  }
+  if (o.prefix_len == 0 && !w.unpack) return forward_codes(h, a, o, stream);
+  AttnParams limits;  // before anything is launched
+  const int tile = kTile / (h->n_heads / h->n_kv_heads);
+  int rc = w.unpack ? fill_params(*h, a, tile, a.max_q_len > tile ? 2 : 1, &limits) : MOE_OK;
+  if (rc == MOE_OK) rc = check_current(*h);
+  if (rc != MOE_OK) return rc;
+  char* at = static_cast<char*>(o.workspace);
+  if (!w.unpack) {
+    if (!o.scales || !w.apart) return run_shared(h, a, o, w, o.scales != nullptr, a, stream);
+    // the prefix in 16 bits
+    const size_t half = w.prefix_pages * page_bytes(*h, a) / 2;
+    const Unpacked u{at + w.prefix_at, at + w.prefix_at + half, reinterpret_cast<int32_t*>(at + w.prefix_at + 2 * half),
+                     w.prefix_pages, 0};
+    rc = launch_unpack(*h, a, *o.scales, u, 1, 0, w.prefix_pages, o.prefix_len, stream);
+    return rc != MOE_OK ? rc : run_shared(h, a, o, w, true, over_pages(*h, a, u, w.prefix_pages), stream);
+  }
   // rows without pages: nothing is unpacked, and one call does all
-  const int at_once = one == 0 ? a.batch : (int)std::min<size_t>(a.batch, o.workspace_bytes / one);
-  const long long pages = (long long)at_once * a.table_pages;
+  const int at_once =
+      w.sequence == 0 ? a.batch : (int)std::min<size_t>(a.batch, (o.workspace_bytes - w.sequences_at) / w.sequence);
+  const int own_pages = a.table_pages - w.prefix_pages;
+  const long long pages = w.prefix_pages + (long long)at_once * own_pages;
   if (pages > 0x7fffffffll) return too_much();
-  char* k = static_cast<char*>(o.workspace);
-  char* v = k + pages * a.page_size * row * 2;
-  int32_t* table = reinterpret_cast<int32_t*>(v + pages * a.page_size * row * 2);
+  const size_t half = pages * page_bytes(*h, a) / 2;
+  char* k = at + w.prefix_at;
+  const Unpacked u{k, k + half, reinterpret_cast<int32_t*>(k + 2 * half), a.table_pages, w.prefix_pages};
   for (int b = 0; b < a.batch; b += at_once) {
     moe_attn_args_t part = a;
     part.batch = std::min(at_once, a.batch - b);
     part.q_starts = a.q_starts + b;
     part.kv_lens = a.kv_lens + b;
     part.block_table = a.block_table + (long long)b * a.table_stride;
-    if (one > 0) {
-      const int rc = launch_unpack(*h, part, *o.scales, k, v, table, stream);
-      if (rc != MOE_OK) return rc;
-      part.k_cache = k;
-      part.v_cache = v;
-      part.n_pages = (int)pages;
-      part.k_row_stride = part.v_row_stride = row;
-      part.k_page_stride = part.v_page_stride = a.page_size * row;
-      part.block_table = table;
-      part.table_stride = a.table_pages;
+    if (b == 0 && o.prefix_len > 0) {
+      Unpacked prefix = u;
+      prefix.first = 0;
+      rc = launch_unpack(*h, a, *o.scales, prefix, 1, 0, w.prefix_pages, o.prefix_len, stream);
     }
-    const int rc = forward_16(h, part, stream);
+    if (rc == MOE_OK)
+      rc = launch_unpack(*h, part, *o.scales, u, part.batch, w.prefix_pages, own_pages, -1, stream);
+    if (rc != MOE_OK) return rc;
+    if (a.table_pages > 0) part = over_pages(*h, part, u, pages);
+    rc = o.prefix_len > 0 ? run_shared(h, part, o, w, false, part, stream) : forward_16(h, part, stream);
     if (rc != MOE_OK) return rc;
   }
   return MOE_OK;
-}
-
-// What a call with a prefix leaves in its workspace.
-struct SharedLayout {
-  int tokens, tiles, prefix_items, own_items;
-  size_t o_at, ml_at, cuts_at, bytes;
-};
-SharedLayout shared_layout(const moe_attn& h, const moe_attn_args_t& a, const moe_attn_opts_t& o) {
-  const int group = h.n_heads / h.n_kv_heads;
-  SharedLayout l{};
-  if (o.scales) {
-    l.tokens = code_rows((int)std::min<long long>(kMaxCodeRows, (long long)a.n_tokens * group)) / std::min(group, kMaxCodeRows);
-    l.tiles = 1;
-  } else {
-    l.tokens = kTile / group;
-    l.tiles = shared_in_pairs(a.n_tokens, a.max_q_len, l.tokens) ? 2 : 1;
-  }
-  const int per = l.tokens * l.tiles;
-  l.prefix_items = (a.n_tokens + per - 1) / per;
-  l.own_items = std::max(1, (int)(((long long)a.max_q_len + per - 1) / per));
-  const size_t rows = 2 * (size_t)a.n_tokens * h.n_heads;
-  const size_t items = (size_t)h.n_kv_heads * (l.prefix_items + (size_t)a.batch * l.own_items);
-  l.ml_at = rows * h.head_dim * sizeof(float);
-  l.cuts_at = l.ml_at + rows * sizeof(float2);
-  l.bytes = l.cuts_at + (items * sizeof(Cut) + 15) / 16 * 16;
-  return l;
-}
-int forward_shared(moe_attn* h, const moe_attn_args_t& args, const moe_attn_opts_t& o, moe_stream_t stream) {
-  const moe_attn_args_t a = with_pages(args);
-  const SharedLayout l = shared_layout(*h, a, o);
-  const double units = ((double)l.prefix_items * ((double)o.prefix_len / kTile + 1 + kItemCost<2>) +
-                        (double)a.batch * l.own_items * item_cost(a, a.table_pages)) * h->n_kv_heads;
-  if (units > kMaxUnits) return too_much();
-  SharedParams p{};
-  Maps maps;
-  int rc = fill_params(*h, a, l.tokens, l.tiles, &p);
-  if (rc == MOE_OK) rc = o.scales ? maps_codes(h, a, &maps) : maps_16(h, a, l.tokens, &maps);
-  if (rc != MOE_OK) return rc;
-  char* w = static_cast<char*>(o.workspace);
-  p.fits = true;
-  p.by_item = false;
-  p.prefix = o.prefix_len;
-  p.prefix_pages = o.prefix_len / a.page_size;
-  p.prefix_items = l.prefix_items;
-  p.own_items = l.own_items;
-  p.whole_o = reinterpret_cast<float*>(w);
-  p.whole_ml = reinterpret_cast<float2*>(w + l.ml_at);
-  p.cuts = reinterpret_cast<Cut*>(w + l.cuts_at);
-  if (o.scales) {
-    rc = launch_quantised(*h, p, *o.scales, maps, stream);
-    p.a.scale = kUnitScale;  // the codes' kernel leaves its maxima in powers of two
-  } else {
-    rc = launch_shared(*h, p, maps, stream);
-  }
-  return rc != MOE_OK ? rc : launch_shared_join(*h, p, l.tiles == 2, stream);
 }
 
 }  // namespace
@@ -461,11 +547,9 @@ int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t strea
 }
 
 size_t moe_attn_workspace(const moe_attn_t* h, const moe_attn_args_t* a, const moe_attn_opts_t* o) {
-  if (!h || !a || !o || a->batch <= 0 || a->n_tokens <= 0 || a->page_size <= 0) return 0;
-  if (o->prefix_len > 0) return shared_layout(*h, *a, *o).bytes;
-  if (!o->scales || !in_chunks(*h, *a)) return 0;
-  const size_t one = sequence_bytes(*h, *a);
-  return one * std::max<size_t>(1, std::min<size_t>(a->batch, kUnpackBytes / std::max<size_t>(one, 1)));
+  if (!h || !a || !o || a->batch <= 0 || a->n_tokens <= 0 || a->page_size <= 0 || o->prefix_len < 0) return 0;
+  const moe_attn_args_t all = with_pages(*a);
+  return o->prefix_len / a->page_size > all.table_pages ? 0 : work_of(*h, all, *o).wanted;
 }
 
 int moe_attn_forward_ex(moe_attn_t* h, const moe_attn_args_t* a, const moe_attn_opts_t* o, moe_stream_t stream) {
@@ -486,17 +570,10 @@ int moe_attn_forward_ex(moe_attn_t* h, const moe_attn_args_t* a, const moe_attn_
     if ((sc->k_page_stride | sc->k_head_stride | sc->v_page_stride | sc->v_head_stride) & 15)
       return fail(MOE_ERR_INVALID_ARG, "every stride of the scales must be a multiple of 16 bytes");
   }
-  const int group = h->n_heads / h->n_kv_heads;
-  if (sc && o->prefix_len > 0 && group > kMaxCodeRows)
-    return fail(MOE_ERR_UNSUPPORTED, "%d query heads share a key/value head: over a quantised cache with a prefix at most "
-                                     "%d can", group, kMaxCodeRows);
-  const size_t need = o->prefix_len > 0 ? shared_layout(*h, *a, *o).bytes
-                      : in_chunks(*h, *a) ? sequence_bytes(*h, *a)
-                                          : 0;
+  const size_t need = work_of(*h, with_pages(*a), *o).need;
   if (need > 0 && (!o->workspace || !aligned(o->workspace, 16) || o->workspace_bytes < need))
     return fail(MOE_ERR_INVALID_ARG, "the workspace must be 16-byte aligned and hold %zu bytes", need);
-  if (o->prefix_len > 0) return forward_shared(h, *a, *o, stream);
-  return in_chunks(*h, *a) ? forward_unpacked(h, *a, *o, stream) : forward_codes(h, *a, *o, stream);
+  return forward_with(h, *a, *o, stream);
 }
 
 int moe_attn_get_status(moe_attn_t* h) {

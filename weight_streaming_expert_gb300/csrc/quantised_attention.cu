@@ -57,8 +57,8 @@ constexpr int kWarps = 8, kCopyWarps = 4, kCodeThreads = (kWarps + kCopyWarps) *
 
 // Registers of a thread: the copying warps give most of theirs to the others,
 // which hold two blocks of positions at a time (16 rows: 110 us with one and 200
-// bytes spilled).  The shares add up to what the block is launched with, which
-// allow() makes sure of.
+// bytes spilled, 89 with two).  The shares add up to what the block is launched
+// with, which launch() makes sure of.
 constexpr int kLaunchRegisters = 168, kWorkRegisters = 224, kCopyRegisters = 56;
 static_assert(kWarps * kWorkRegisters + kCopyWarps * kCopyRegisters == (kWarps + kCopyWarps) * kLaunchRegisters);
 
@@ -578,11 +578,6 @@ __global__ void __launch_bounds__(kCodeThreads, 1)
 
 template <int D, int kN, int kG, typename P>
 cudaError_t allow() {
-  // with fewer registers than the shares of its warps a block would wait for them for ever
-  cudaFuncAttributes f{};
-  const cudaError_t e = cudaFuncGetAttributes(&f, quantised_attention_kernel<D, kN, kG, P>);
-  if (e != cudaSuccess) return e;
-  if (f.numRegs != kLaunchRegisters) return cudaErrorInvalidKernelImage;
   return cudaFuncSetAttribute(quantised_attention_kernel<D, kN, kG, P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               (int)CodeLayout<D>::kSmem);
 }
@@ -596,6 +591,13 @@ cudaError_t allow_rows() {
 
 template <int D, int kN, int kG, typename P>
 int launch(const moe_attn& h, const P& p, const moe_cache_scales_t& s, const Maps& maps, moe_stream_t stream) {
+  // with fewer registers than the shares of its warps a block would wait for them for ever
+  static const int registers = [] {
+    cudaFuncAttributes f{};
+    return cudaFuncGetAttributes(&f, quantised_attention_kernel<D, kN, kG, P>) == cudaSuccess ? f.numRegs : 0;
+  }();
+  if (registers != kLaunchRegisters)
+    return fail(MOE_ERR_CUDA, "the kernel has %d registers, not %d", registers, kLaunchRegisters);
   const float c = p.a.scale * 1.4426950408889634f;
   return launch_pdl(quantised_attention_kernel<D, kN, kG, P>, dim3(h.n_sms / p.spread * p.spread), dim3(kCodeThreads),
                     CodeLayout<D>::kSmem, stream, 1, p, s, c, maps.k, maps.v);
@@ -632,7 +634,8 @@ struct UnpackArgs {
   const int32_t* kv_lens;
   int32_t* table;
   int* status;
-  int table_stride, table_pages, page_size, n_pages, n_kv_heads, head_dim;
+  int table_stride, page_size, n_pages, n_kv_heads, head_dim;
+  int out_stride, first, skip, pages, len;  // Unpacked's, and launch_unpack's
   bool bf16;
 };
 
@@ -644,12 +647,12 @@ __global__ void __launch_bounds__(kUnpackThreads) unpack_kernel(const __grid_con
   const int i = blockIdx.x, b = blockIdx.y, z = blockIdx.z;
   pdl_wait();
   pdl_launch_dependents();
-  const long long to = (long long)b * a.table_pages + i;
+  const long long to = a.first + (long long)b * a.pages + i;
   const int tid = threadIdx.x;
-  if (z == 0 && tid == 0) a.table[to] = (int)to;
-  const long long len = a.kv_lens[b];
+  if (z == 0 && tid == 0) a.table[(long long)b * a.out_stride + a.skip + i] = (int)to;
+  const long long len = a.len >= 0 ? a.len : (long long)a.kv_lens[b] - (long long)a.skip * a.page_size;
   if ((long long)i * a.page_size >= len) return;
-  const int page = a.block_table[(long long)b * a.table_stride + i];
+  const int page = a.block_table[(long long)b * a.table_stride + a.skip + i];
   const bool there = (unsigned)page < (unsigned)a.n_pages;
   if (!there && tid == 0) atomicOr(a.status, kAttnBadPage);
   const int per_head = a.head_dim / 16, per_row = a.n_kv_heads * per_head, units = a.page_size * per_row;
@@ -703,19 +706,19 @@ int launch_quantised(const moe_attn& h, const SharedParams& p, const moe_cache_s
   return h.head_dim == 64 ? launch_rows<64>(h, c, s, maps, stream) : launch_rows<128>(h, c, s, maps, stream);
 }
 
-int launch_unpack(const moe_attn& h, const moe_attn_args_t& a, const moe_cache_scales_t& s, void* k_out, void* v_out,
-                  int32_t* table, moe_stream_t stream) {
+int launch_unpack(const moe_attn& h, const moe_attn_args_t& a, const moe_cache_scales_t& s, const Unpacked& to, int batch,
+                  int skip, int pages, int len, moe_stream_t stream) {
+  if (pages == 0) return MOE_OK;
   const UnpackArgs u{{static_cast<const uint8_t*>(a.k_cache), static_cast<const uint8_t*>(a.v_cache)},
                      {a.k_page_stride, a.v_page_stride},
                      {a.k_row_stride, a.v_row_stride},
                      {static_cast<const uint8_t*>(s.k_scale), static_cast<const uint8_t*>(s.v_scale)},
                      {s.k_page_stride, s.v_page_stride},
                      {s.k_head_stride, s.v_head_stride},
-                     {static_cast<uint16_t*>(k_out), static_cast<uint16_t*>(v_out)},
-                     a.block_table, a.kv_lens, table, h.status, a.table_stride, a.table_pages, a.page_size, a.n_pages,
-                     h.n_kv_heads, h.head_dim, a.dtype == MOE_DTYPE_BF16};
-  return launch_pdl(unpack_kernel, dim3((unsigned)a.table_pages, (unsigned)a.batch, 2), dim3(kUnpackThreads), 0, stream, 1,
-                    u);
+                     {static_cast<uint16_t*>(to.k), static_cast<uint16_t*>(to.v)},
+                     a.block_table, a.kv_lens, to.table, h.status, a.table_stride, a.page_size, a.n_pages, h.n_kv_heads,
+                     h.head_dim, to.table_stride, to.first, skip, pages, len, a.dtype == MOE_DTYPE_BF16};
+  return launch_pdl(unpack_kernel, dim3((unsigned)pages, (unsigned)batch, 2), dim3(kUnpackThreads), 0, stream, 1, u);
 }
 
 }  // namespace wse

@@ -23,26 +23,30 @@ namespace {
 constexpr int kFewJoined = 8;  // parts of an item that a warp joins by itself
 
 // Where the results of the rows of one of a sequence's own items lie.
-template <int D, int kTiles>
+template <int D>
 struct JoinItem {
-  static constexpr int kRows = kTiles * kTile;
+  const JoinParams& j;
   const SharedParams& p;
-  int b, h, item;
+  int b, h, item, first_token, tokens;  // the batch's first token, and how many there are from it
   Seq s;
   Cut own;
-  __device__ JoinItem(const SharedParams& p_) : p(p_) {
+  __device__ JoinItem(const JoinParams& j_) : j(j_), p(j_.p) {
     item = blockIdx.x % p.own_items;
     h = blockIdx.x / p.own_items % p.n_kv_heads;
     b = blockIdx.x / p.own_items / p.n_kv_heads + 1;
     // the lengths are no output of the kernel before, which starts this one only
     // after it has waited for what came before itself
     s = load_seq(p, b);
+    first_token = max(0, min(p.a.q_starts[0], p.a.n_tokens));
+    tokens = max(0, min(p.a.q_starts[p.a.batch], p.a.n_tokens) - first_token);
   }
-  __device__ int per() const { return kTiles * p.tokens; }
+  __device__ int rows() const { return j.own.tiles * kTile; }
+  __device__ bool empty() const { return item * j.own.tiles * j.own.tokens >= s.n; }
+  __device__ void load() { own = p.cuts[p.item_number(b, h, item)]; }
   // row r's token in the sequence; s.n: none
   __device__ int token_of(int r) const {
     const int in_tile = r % kTile / p.group;
-    return in_tile < p.tokens ? item * per() + r / kTile * p.tokens + in_tile : s.n;
+    return in_tile < j.own.tokens ? (item * j.own.tiles + r / kTile) * j.own.tokens + in_tile : s.n;
   }
   struct Row {
     int token, head, first;  // first: parts of the prefix, before the own ones
@@ -54,11 +58,13 @@ struct JoinItem {
     Row x{};
     x.token = token_of(r);
     if (x.token >= s.n) return x;
-    const int t = s.q0 + x.token, place = t % per();
+    const int in_group = r % kTile % p.group, t = s.q0 + x.token, from = t - first_token;
+    const int per = j.before.tiles * j.before.tokens, place = from % per;
     x.row = r;
-    x.head = h * p.group + r % kTile % p.group;
-    x.prefix = p.cuts[p.item_number(0, h, t / per())];
-    x.before_row = place / p.tokens * kTile + place % p.tokens * p.group + r % kTile % p.group;
+    x.head = h * p.group + in_group;
+    // starts that descend may name tokens that the prefix's list does not hold
+    x.prefix = (unsigned)from < (unsigned)tokens ? p.cuts[p.item_number(0, h, from / per)] : Cut{};
+    x.before_row = place / j.before.tokens * kTile + place % j.before.tokens * p.group + in_group;
     x.before = p.whole_row(0, t, x.head);
     x.own = p.whole_row(b, t, x.head);
     x.first = x.prefix.parts;
@@ -66,16 +72,22 @@ struct JoinItem {
     return x;
   }
   __device__ long long slot(const Cut& cut, int i) const { return 2ll * (cut.c + i * p.spread) + (i == 0 ? 1 : 0); }
+  __device__ long long place_of(const JoinSide& side, const Cut& cut, int i, int row) const {
+    return slot(cut, i) * (side.tiles * kTile) + row;
+  }
+  // part i's maximum as an exponent in base 2, and its sum
   __device__ float2 ml_of(const Row& x, int i) const {
-    if (i < x.first) return x.first == 1 ? p.whole_ml[x.before] : p.part_ml[slot(x.prefix, i) * kRows + x.before_row];
-    return own.parts == 1 ? p.whole_ml[x.own] : p.part_ml[slot(own, i - x.first) * kRows + x.row];
+    const bool before = i < x.first;
+    const float2 ml =
+        before ? (x.first == 1 ? p.whole_ml[x.before] : j.before.part_ml[place_of(j.before, x.prefix, i, x.before_row)])
+               : (own.parts == 1 ? p.whole_ml[x.own] : j.own.part_ml[place_of(j.own, own, i - x.first, x.row)]);
+    return make_float2(ml.x * (before ? j.before.c : j.own.c), ml.y);
   }
   __device__ float4 sums_of(const Row& x, int i, int column) const {
-    const float* at = i < x.first
-                          ? (x.first == 1 ? p.whole_o + x.before * D
-                                          : p.part_o + (slot(x.prefix, i) * kRows + x.before_row) * D)
-                          : (own.parts == 1 ? p.whole_o + x.own * D
-                                            : p.part_o + (slot(own, i - x.first) * kRows + x.row) * D);
+    const float* at =
+        i < x.first
+            ? (x.first == 1 ? p.whole_o + x.before * D : j.before.part_o + place_of(j.before, x.prefix, i, x.before_row) * D)
+            : (own.parts == 1 ? p.whole_o + x.own * D : j.own.part_o + place_of(j.own, own, i - x.first, x.row) * D);
     return reinterpret_cast<const float4*>(at)[column];
   }
 };
@@ -91,9 +103,9 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 // (1 / sum, log-sum) of a row.
-__device__ __forceinline__ float2 total_of(float m, float l, float c) {
+__device__ __forceinline__ float2 total_of(float m, float l) {
   return make_float2(l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l),
-                     l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f);
+                     l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f);
 }
 __device__ __forceinline__ void add_scaled(float4& o, float4 v, float f) {
   o.x = fmaf(v.x, f, o.x);
@@ -116,22 +128,21 @@ __device__ __forceinline__ void write_row(const SharedParams& p, long long t, in
 // Where few tokens share the prefix it is cut into many parts (8 tokens of 20
 // heads: 30 for each), whose latency is what counts: four threads for each column
 // take a quarter of them each.
-template <typename T, int D, int kTiles>
+template <typename T, int D>
 __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4)
-    join_many_parts_kernel(const __grid_constant__ SharedParams p) {
+    join_many_parts_kernel(const __grid_constant__ JoinParams j) {
   constexpr int kColumns = D / 4;
   __shared__ float factor[kJoinRows][2 * kMaxParts];
   __shared__ float4 sums[kJoinGroups - 1][kJoinRows][kColumns];
   __shared__ float2 total[kJoinRows];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int column = tid % kColumns, row = tid / kColumns % kJoinRows, group = tid / (kColumns * kJoinRows);
-  JoinItem<D, kTiles> it(p);
+  JoinItem<D> it(j);
   pdl_wait();
   pdl_launch_dependents();
-  if (it.item * it.per() >= it.s.n) return;
-  it.own = p.cuts[p.item_number(it.b, it.h, it.item)];
-  const float c = p.a.scale * 1.4426950408889634f;
-  for (int r0 = blockIdx.y * kJoinRows; r0 < it.kRows; r0 += gridDim.y * kJoinRows) {
+  if (it.empty()) return;
+  it.load();
+  for (int r0 = blockIdx.y * kJoinRows; r0 < it.rows(); r0 += gridDim.y * kJoinRows) {
     if (it.token_of(r0) >= it.s.n) continue;  // nor does a later row of the four have a token
     const auto mine = it.row_of(r0 + row);
     const bool valid = mine.token < it.s.n;
@@ -151,12 +162,12 @@ __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4)
         m = warp_max(m);
         for (int i = lane; i < x.parts; i += 32) {
           const float2 ml = it.ml_of(x, i);
-          const float f = ml.x == -INFINITY ? 0.f : exp2_approx((ml.x - m) * c);
+          const float f = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - m);
           factor[warp][i] = nothing_seen(ml) ? -1.f : f;
           l += ml.y * f;
         }
         l = warp_sum(l);
-        if (lane == 0) total[warp] = total_of(m, l, c);
+        if (lane == 0) total[warp] = total_of(m, l);
       }
     }
     __syncthreads();
@@ -175,7 +186,7 @@ __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4)
     if (valid && group == 0) {
 #pragma unroll
       for (int q = 0; q < kJoinGroups - 1; ++q) add_scaled(o, sums[q][row][column], 1.f);
-      write_row<T>(p, it.s.q0 + mine.token, mine.head, column, o, total[row]);
+      write_row<T>(j.p, it.s.q0 + mine.token, mine.head, column, o, total[row]);
     }
     __syncthreads();  // before the next rows' factors are written
   }
@@ -183,17 +194,16 @@ __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4)
 
 // The same for many tokens, whose results have few parts: a warp for each row,
 // and nothing shared (128 single tokens of 32 heads: 111 us with the kernel above).
-template <typename T, int D, int kTiles>
-__global__ void __launch_bounds__(32 * kJoinRows) join_few_parts_kernel(const __grid_constant__ SharedParams p) {
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kJoinRows) join_few_parts_kernel(const __grid_constant__ JoinParams j) {
   constexpr int kColumns = D / 4, kSide = 32 / kColumns;  // parts side by side
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, column = lane % kColumns, side = lane / kColumns;
-  JoinItem<D, kTiles> it(p);
+  JoinItem<D> it(j);
   pdl_wait();
   pdl_launch_dependents();
-  if (it.item * it.per() >= it.s.n) return;
-  it.own = p.cuts[p.item_number(it.b, it.h, it.item)];
-  const float c = p.a.scale * 1.4426950408889634f;
-  for (int r = blockIdx.y * kJoinRows + warp; r < it.kRows; r += gridDim.y * kJoinRows) {
+  if (it.empty()) return;
+  it.load();
+  for (int r = blockIdx.y * kJoinRows + warp; r < it.rows(); r += gridDim.y * kJoinRows) {
     const auto x = it.row_of(r);
     if (x.token >= it.s.n) continue;
     float2 ml = lane < x.parts ? it.ml_of(x, lane) : make_float2(-INFINITY, 0.f);
@@ -204,7 +214,7 @@ __global__ void __launch_bounds__(32 * kJoinRows) join_few_parts_kernel(const __
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i0 = 0; i0 < x.parts; i0 += 32) {
       if (i0 > 0) ml = i0 + lane < x.parts ? it.ml_of(x, i0 + lane) : make_float2(-INFINITY, 0.f);
-      const float f = ml.x == -INFINITY ? 0.f : exp2_approx((ml.x - m) * c);
+      const float f = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - m);
       l += ml.y * f;
       const float used = nothing_seen(ml) ? -1.f : f;
       const int n = min(32, x.parts - i0);
@@ -221,7 +231,7 @@ __global__ void __launch_bounds__(32 * kJoinRows) join_few_parts_kernel(const __
       o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
     }
     l = warp_sum(l);
-    if (side == 0) write_row<T>(p, it.s.q0 + x.token, x.head, column, o, total_of(m, l, c));
+    if (side == 0) write_row<T>(j.p, it.s.q0 + x.token, x.head, column, o, total_of(m, l));
   }
 }
 
@@ -245,49 +255,38 @@ int launch(const moe_attn& h, const SharedParams& p, const Maps& maps, moe_strea
                     dim3(L::kThreads), L::kSmem, stream, 1, p, maps.q, maps.k, maps.v);
 }
 template <typename T, int D>
-int launch(const moe_attn& h, const SharedParams& p, const Maps& maps, moe_stream_t stream) {
-  return shared_in_pairs(p.a.n_tokens, p.a.max_q_len, p.tokens) ? launch<T, D, true>(h, p, maps, stream)
-                                                                : launch<T, D, false>(h, p, maps, stream);
+int launch(const moe_attn& h, const SharedParams& p, bool pair, const Maps& maps, moe_stream_t stream) {
+  return pair ? launch<T, D, true>(h, p, maps, stream) : launch<T, D, false>(h, p, maps, stream);
 }
 
-template <typename T, int D, int kTiles>
-int launch_join(const moe_attn& h, const SharedParams& p, moe_stream_t stream) {
+template <typename T, int D>
+int launch_join(const moe_attn& h, const JoinParams& j, moe_stream_t stream) {
+  const SharedParams& p = j.p;
   // as many blocks as the rows of an item have use for
-  const int rows = kTiles == 2 ? 2 * kTile : std::max(1, std::min(p.a.max_q_len, p.tokens)) * p.group;
+  const int rows = j.own.tiles == 2 ? 2 * kTile : std::max(1, std::min(p.a.max_q_len, j.own.tokens)) * p.group;
   const dim3 grid((unsigned)(p.a.batch * p.n_kv_heads * p.own_items), (unsigned)((rows + kJoinRows - 1) / kJoinRows));
   // about as many parts has an item of the prefix if the CTAs do nothing else
   const int parts = h.n_sms / p.spread / p.prefix_items;
-  return parts > kFewJoined ? launch_pdl(join_many_parts_kernel<T, D, kTiles>, grid, dim3(kJoinRows * kJoinGroups * D / 4),
-                                         0, stream, 1, p)
-                            : launch_pdl(join_few_parts_kernel<T, D, kTiles>, grid, dim3(32 * kJoinRows), 0, stream, 1, p);
-}
-template <typename T, int D>
-int launch_join(const moe_attn& h, const SharedParams& p, bool pair, moe_stream_t stream) {
-  return pair ? launch_join<T, D, 2>(h, p, stream) : launch_join<T, D, 1>(h, p, stream);
+  return parts > kFewJoined ? launch_pdl(join_many_parts_kernel<T, D>, grid, dim3(kJoinRows * kJoinGroups * D / 4), 0,
+                                         stream, 1, j)
+                            : launch_pdl(join_few_parts_kernel<T, D>, grid, dim3(32 * kJoinRows), 0, stream, 1, j);
 }
 
 }  // namespace
 
-// Whether tiles go in pairs: own chunks of more than a tile do as without a
-// prefix, and where many tiles of tokens share the prefix each pair reads it once.
-bool shared_in_pairs(int n_tokens, int max_q_len, int tokens) {
-  return max_q_len > tokens;
-}
-
 cudaError_t allow_shared(int head_dim) { return head_dim == 64 ? allow_all<64>() : allow_all<128>(); }
 
-int launch_shared(const moe_attn& h, const SharedParams& p, const Maps& maps, moe_stream_t stream) {
+int launch_shared(const moe_attn& h, const SharedParams& p, bool pair, const Maps& maps, moe_stream_t stream) {
   if (p.a.dtype == MOE_DTYPE_BF16)
-    return h.head_dim == 64 ? launch<__nv_bfloat16, 64>(h, p, maps, stream)
-                            : launch<__nv_bfloat16, 128>(h, p, maps, stream);
-  return h.head_dim == 64 ? launch<__half, 64>(h, p, maps, stream) : launch<__half, 128>(h, p, maps, stream);
+    return h.head_dim == 64 ? launch<__nv_bfloat16, 64>(h, p, pair, maps, stream)
+                            : launch<__nv_bfloat16, 128>(h, p, pair, maps, stream);
+  return h.head_dim == 64 ? launch<__half, 64>(h, p, pair, maps, stream) : launch<__half, 128>(h, p, pair, maps, stream);
 }
 
-int launch_shared_join(const moe_attn& h, const SharedParams& p, bool pair, moe_stream_t stream) {
-  if (p.a.dtype == MOE_DTYPE_BF16)
-    return h.head_dim == 64 ? launch_join<__nv_bfloat16, 64>(h, p, pair, stream)
-                            : launch_join<__nv_bfloat16, 128>(h, p, pair, stream);
-  return h.head_dim == 64 ? launch_join<__half, 64>(h, p, pair, stream) : launch_join<__half, 128>(h, p, pair, stream);
+int launch_shared_join(const moe_attn& h, const JoinParams& j, moe_stream_t stream) {
+  if (j.p.a.dtype == MOE_DTYPE_BF16)
+    return h.head_dim == 64 ? launch_join<__nv_bfloat16, 64>(h, j, stream) : launch_join<__nv_bfloat16, 128>(h, j, stream);
+  return h.head_dim == 64 ? launch_join<__half, 64>(h, j, stream) : launch_join<__half, 128>(h, j, stream);
 }
 
 }  // namespace wse
