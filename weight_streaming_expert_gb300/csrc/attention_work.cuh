@@ -412,13 +412,14 @@ __device__ __forceinline__ void clear_cuts(const AttnParams& p) {
 template <int kThreads>
 __device__ __forceinline__ void clear_cuts(const SharedParams&) {}  // every item says it itself
 
-// By one thread at the end of each item that this share began (u0 = 0), `walk`
-// being past it: whether, and between which shares, it is cut.
-template <int kTiles, typename P>
-__device__ __forceinline__ void note_cut(const P& p, const Plan& plan, const Walk<kTiles, P>& walk, const Item& it) {
+// By one thread at the end of each item that this share began (u0 = 0), `todo`
+// being what the walk had left past it: whether, and between which shares, it is
+// cut.
+template <typename P>
+__device__ __forceinline__ void note_cut(const P& p, const Plan& plan, int todo, const Item& it) {
   const int n = it.u1 - it.u0;
   // which share holds its last unit
-  const int last = plan.start + (plan.todo - walk.todo) - n + it.units - 1;
+  const int last = plan.start + (plan.todo - todo) - n + it.units - 1;
   const int e = (unsigned)last / (unsigned)plan.share;
   if constexpr (P::kShared) {
     p.cuts[p.item_number(it.b, it.h, it.tile)] =

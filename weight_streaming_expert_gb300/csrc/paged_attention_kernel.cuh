@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(Layout<D, kPair>::kThreads, 1)
       }
       if (left_out[item % kItems] == item)
         add_not_finite<T, D, kPair>(p, it.b, it.h, it.tile, it.u0, it.u1, cut, slot, chain, r);
-      if (it.u0 == 0 && tid == 0) note_cut(p, plan, walk, it);
+      if (it.u0 == 0 && tid == 0) note_cut(p, plan, walk.todo, it);
       if (!kPair) named_sync(1, 256);  // both chains' sums are read before the next item's
     }
   } else {

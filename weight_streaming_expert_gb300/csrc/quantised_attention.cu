@@ -256,23 +256,19 @@ __global__ void __launch_bounds__(kCodeThreads, 1)
   // ---- scores, probabilities and sums
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWorkRegisters));
   const int g = lane >> 2, t = lane & 3;
-  const int rows_at = warp / kTogether * (8 * kN), part = warp % kTogether;
+  const int rows_at = warp / kTogether * (8 * kN), part = warp % kTogether;  // this warp's first row
   float* join = reinterpret_cast<float*>(smem + L::kJoinAt);
   float2* stats = reinterpret_cast<float2*>(smem + L::kStatsAt);
   int taken = 0;
-  while (walk.next(it)) {
-    const Veil veil = veil_of<1>(p, it.s, it.tile);
-    const int token0 = it.tile * p.tokens;
-    // this lane's columns of the queries of rows 8 i + g, as B; what their row's
-    // power of two leaves to the scores of rows 8 i + 2 t and + 1
-    uint32_t q[kN][kSteps][2];
-    float factor[kN][2];
+  // this lane's columns of the queries of rows 8 i + g, as B
+  uint32_t q[kN][kSteps][2];
+  auto load_queries = [&] {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int r = rows_at + 8 * i + g, in_tile = r / p.group;
-      const bool valid = in_tile < p.tokens && token0 + in_tile < it.s.n;
-      const uint16_t* from = static_cast<const uint16_t*>(a.q) + (long long)(it.s.q0 + token0 + in_tile) * a.q_token_stride +
-                             (long long)(it.h * p.group + r % p.group) * a.q_head_stride + 16 * t;
+      const int r = rows_at + 8 * i + g, in_tile = r / p.group, token = it.tile * p.tokens + in_tile;
+      const bool valid = in_tile < p.tokens && token < it.s.n;
+      const uint16_t* from = static_cast<const uint16_t*>(a.q) + (long long)(it.s.q0 + token) * a.q_token_stride +
+                             (long long)(it.h * p.group + r - in_tile * p.group) * a.q_head_stride + 16 * t;
 #pragma unroll
       for (int k = 0; k < kChunks; ++k) {
         uint4 v[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
@@ -283,6 +279,15 @@ __global__ void __launch_bounds__(kCodeThreads, 1)
         q[i][4 * k][0] = v[0].x, q[i][4 * k][1] = v[0].y, q[i][4 * k + 1][0] = v[0].z, q[i][4 * k + 1][1] = v[0].w;
         q[i][4 * k + 2][0] = v[1].x, q[i][4 * k + 2][1] = v[1].y, q[i][4 * k + 3][0] = v[1].z, q[i][4 * k + 3][1] = v[1].w;
       }
+    }
+  };
+  bool more = walk.next(it);
+  if (more) load_queries();
+  while (more) {
+    const Veil veil = veil_of<1>(p, it.s, it.tile);
+    float factor[kN][2];  // what their row's power of two leaves to the scores of rows 8 i + 2 t and + 1
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
       int e = 0;
       if (a.dtype == MOE_DTYPE_BF16) {
         float largest = 0.f;
@@ -477,57 +482,60 @@ __global__ void __launch_bounds__(kCodeThreads, 1)
       if (lane == 0) mbar_arrive(empty(stage));
     }
 
-    // ---- the end of the item: the warps that share its rows join their sums
+    // ---- the end of the item: the warps that share its rows join their sums,
+    // while the next item's queries are on their way
 #pragma unroll
     for (int i = 0; i < kN; ++i)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
 #pragma unroll
         for (int m = 4; m < 32; m <<= 1) l[i][k] += __shfl_xor_sync(0xffffffffu, l[i][k], m);
-        if (g == 0) stats[warp * 16 + 8 * i + 2 * t + k] = make_float2(M[i][k], l[i][k]);
+        if (g == 0) stats[warp * (8 * kN) + 8 * i + 2 * t + k] = make_float2(M[i][k], l[i][k]);
       }
-    named_sync(1, kWarps * 32);
-    const bool cut = it.u1 - it.u0 < it.units, raw = P::kShared || cut;
-    const int slot = 2 * blockIdx.x + (it.u0 == 0 ? 1 : 0);
-    const int lead = warp - part;  // the first of the warps together
-    const bool has_marks = *marked != 0;
+    const Item done = it;
+    const int todo = walk.todo;
+    bool has_marks = false;
+    const bool cut = done.u1 - done.u0 < done.units, raw = P::kShared || cut;
+    const int slot = 2 * blockIdx.x + (done.u0 == 0 ? 1 : 0);
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kTogether; ++w) top = fmaxf(top, stats[(lead + w) * 16 + 8 * i + 2 * t + k].x);
-        const float f = M[i][k] == -INFINITY ? 0.f : exp2_approx(M[i][k] - top);
-        // a row that saw nothing here has zeros, or NaN that has to show
-        const bool none = M[i][k] == -INFINITY && l[i][k] == 0.f;
         float* to = join + (warp * 8 + 2 * t + k) * (D + 4) + (D == 128 ? 16 * ((g & 1) * 4 + (g >> 1)) : 8 * g);
 #pragma unroll
-        for (int j = 0; j < kSteps; j += 2) {
-          float4 x = make_float4(o[i][j][k], o[i][j][k + 2], o[i][j + 1][k], o[i][j + 1][k + 2]);
-          if (none)
-            x = make_float4(0.f, 0.f, 0.f, 0.f);
-          else
-            x = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
-          *reinterpret_cast<float4*>(to + 2 * j) = x;
-        }
+        for (int j = 0; j < kSteps; j += 2)
+          *reinterpret_cast<float4*>(to + 2 * j) =
+              make_float4(o[i][j][k], o[i][j][k + 2], o[i][j + 1][k], o[i][j + 1][k + 2]);
+      }
+      if (kN == 1) {  // of 16 rows their registers would be too many
+        more = walk.next(it);
+        if (more) load_queries();
       }
       named_sync(1, kWarps * 32);
+      has_marks = *marked != 0;
       // a thread for four columns of a row of each group
+#pragma unroll 1
       for (int unit = tid; unit < kG * 8 * D / 4; unit += kWarps * 32) {
         const int column = unit % (D / 4) * 4, in_block = unit / (D / 4) % 8, group = unit / (D / 4) / 8;
-        const int r = group * 8 * kN + 8 * i + in_block, in_tile = r / p.group, token = token0 + in_tile;
-        if (in_tile >= p.tokens || token >= it.s.n) continue;
+        const int r = group * (8 * kN) + 8 * i + in_block, in_tile = r / p.group;
+        const int token = done.tile * p.tokens + in_tile;
+        if (in_tile >= p.tokens || token >= done.s.n) continue;
+        const int row = group * kTogether * (8 * kN) + 8 * i + in_block;  // of the first of its warps
         float m = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kTogether; ++w) m = fmaxf(m, stats[row + w * (8 * kN)].x);
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kTogether; ++w) m = fmaxf(m, stats[(group * kTogether + w) * 16 + 8 * i + in_block].x);
-#pragma unroll
         for (int w = 0; w < kTogether; ++w) {
-          const float2 ml = stats[(group * kTogether + w) * 16 + 8 * i + in_block];
-          sum += nothing_seen(ml) ? 0.f : ml.y * (ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - m));
+          const float2 ml = stats[row + w * (8 * kN)];
           const float4 v = *reinterpret_cast<const float4*>(join + ((group * kTogether + w) * 8 + in_block) * (D + 4) + column);
-          x.x += v.x, x.y += v.y, x.z += v.z, x.w += v.w;
+          if (nothing_seen(ml)) continue;
+          const float f = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - m);
+          sum = fmaf(ml.y, f, sum);
+          x.x = fmaf(v.x, f, x.x);
+          x.y = fmaf(v.y, f, x.y);
+          x.z = fmaf(v.z, f, x.z);
+          x.w = fmaf(v.w, f, x.w);
         }
         if (has_marks) {
           const uint32_t bits = marks[(r * D + column) / 32] >> (column & 31);
@@ -537,42 +545,45 @@ __global__ void __launch_bounds__(kCodeThreads, 1)
           if (bits & 4) x.z = nan;
           if (bits & 8) x.w = nan;
         }
-        const int head = it.h * p.group + r % p.group;
-        const long long t_row = it.s.q0 + token;
+        const int head = done.h * p.group + r - in_tile * p.group;
+        const long long t_row = done.s.q0 + token;
         if (raw) {
           float* to = p.part_o + ((long long)slot * kTile + r) * D;
-          float2* ml = p.part_ml + (long long)slot * kTile + r;
+          float2* to_ml = p.part_ml + (long long)slot * kTile + r;
           if constexpr (P::kShared) {
             if (!cut) {
-              const long long whole = p.whole_row(it.b, (int)t_row, head);
+              const long long whole = p.whole_row(done.b, (int)t_row, head);
               to = p.whole_o + whole * D;
-              ml = p.whole_ml + whole;
+              to_ml = p.whole_ml + whole;
             }
           }
           *reinterpret_cast<float4*>(to + column) = x;
-          if (column == 0) *ml = make_float2(m, sum);
+          if (column == 0) *to_ml = make_float2(m, sum);
         } else {
           const float norm = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-          uint2 v;
+          uint2 y;
           if (a.dtype == MOE_DTYPE_BF16)
-            v = make_uint2(pack<__nv_bfloat16>(x.x * norm, x.y * norm), pack<__nv_bfloat16>(x.z * norm, x.w * norm));
+            y = make_uint2(pack<__nv_bfloat16>(x.x * norm, x.y * norm), pack<__nv_bfloat16>(x.z * norm, x.w * norm));
           else
-            v = make_uint2(pack<__half>(x.x * norm, x.y * norm), pack<__half>(x.z * norm, x.w * norm));
+            y = make_uint2(pack<__half>(x.x * norm, x.y * norm), pack<__half>(x.z * norm, x.w * norm));
           *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + t_row * a.out_token_stride + head * a.out_head_stride +
-                                    column) = v;
+                                    column) = y;
           if (a.lse && column == 0)
-            a.lse[t_row * (p.group * p.n_kv_heads) + head] =
-                sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+            a.lse[t_row * (p.group * p.n_kv_heads) + head] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
         }
       }
-      named_sync(1, kWarps * 32);  // before the next block's sums, or the next item's statistics
+      named_sync(1, kWarps * 32);  // before the next block's sums, or the next item's
     }
+    if (done.u0 == 0 && tid == 0) note_cut(p, plan, todo, done);
     if (has_marks) {
       for (int k = tid; k < (int)L::kMarks / 4; k += kWarps * 32) marks[k] = 0u;
       if (tid == 0) *marked = 0;
       named_sync(1, kWarps * 32);
     }
-    if (it.u0 == 0 && tid == 0) note_cut(p, plan, walk, it);
+    if (kN > 1) {
+      more = walk.next(it);
+      if (more) load_queries();
+    }
   }
 }
 

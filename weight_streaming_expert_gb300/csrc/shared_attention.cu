@@ -20,7 +20,7 @@
 namespace wse {
 namespace {
 
-constexpr int kFewJoined = 8;  // parts of an item that a warp joins by itself
+constexpr int kFewJoined = 8;  // parts of an item that a warp joins by itself; more of them, too, of many rows
 
 // Where the results of the rows of one of a sequence's own items lie.
 template <int D>
@@ -267,9 +267,9 @@ int launch_join(const moe_attn& h, const JoinParams& j, moe_stream_t stream) {
   const dim3 grid((unsigned)(p.a.batch * p.n_kv_heads * p.own_items), (unsigned)((rows + kJoinRows - 1) / kJoinRows));
   // about as many parts has an item of the prefix if the CTAs do nothing else
   const int parts = h.n_sms / p.spread / p.prefix_items;
-  return parts > kFewJoined ? launch_pdl(join_many_parts_kernel<T, D>, grid, dim3(kJoinRows * kJoinGroups * D / 4), 0,
-                                         stream, 1, j)
-                            : launch_pdl(join_few_parts_kernel<T, D>, grid, dim3(32 * kJoinRows), 0, stream, 1, j);
+  return parts > kFewJoined && (long long)grid.x * grid.y <= 2 * h.n_sms
+             ? launch_pdl(join_many_parts_kernel<T, D>, grid, dim3(kJoinRows * kJoinGroups * D / 4), 0, stream, 1, j)
+             : launch_pdl(join_few_parts_kernel<T, D>, grid, dim3(32 * kJoinRows), 0, stream, 1, j);
 }
 
 }  // namespace
