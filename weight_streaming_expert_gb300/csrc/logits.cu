@@ -99,69 +99,65 @@ __global__ void __launch_bounds__(kLogitThreads) adjust_logits_kernel(const __gr
     for (int i = 0; i < kLogitLoads; ++i) x[i] = load4(token_of(i), allow[i]);
   }
 
+  // what is not given changes nothing as these numbers
+  const float rep = a.repetition ? a.repetition[row] : 1.f, presence = a.presence ? a.presence[row] : 0.f;
+  const float frequency = a.frequency ? a.frequency[row] : 0.f, inverse = __frcp_rn(rep);
+
   // ---- the tables
   if (counts || biases) {
     // the history's first tokens are on their way while the tables are cleared
     const Span span = counts ? span_of(a, row) : Span{0, 0, 0};
     int token[kTokens];
+    const int32_t* next = a.history + span.begin + tid;
+    int left = span.end - span.begin - tid;  // tokens from `next` on
+    auto read_tokens = [&] {
 #pragma unroll
-    for (int k = 0; k < kTokens; ++k) {
-      const int i = span.begin + tid + k * kLogitThreads;
-      token[k] = i < span.end ? a.history[i] : -1;
-    }
+      for (int k = 0; k < kTokens; ++k) token[k] = k * kLogitThreads < left ? next[k * kLogitThreads] : -1;
+    };
+    read_tokens();
     const int words = ((counts ? kSlice + kSlice / 4 : 0) + (biases ? kSlice : 0)) / 4;
     for (int i = tid; i < words; i += kLogitThreads) table_words[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
-    auto place_of = [&](int token) {  // in the slice, else past it
-      return (unsigned)token < (unsigned)a.vocab ? (unsigned)(token - first) : ~0u;
-    };
-    for (int at0 = span.begin + tid; at0 < span.end; at0 += kTokens * kLogitThreads) {
-      if (at0 != span.begin + tid) {
-#pragma unroll
-        for (int k = 0; k < kTokens; ++k) {
-          const int i = at0 + k * kLogitThreads;
-          token[k] = i < span.end ? a.history[i] : -1;
-        }
-      }
+    const int lowest = max(first, 0), skipped = lowest - first;  // the slice's first token, and its place
+    const unsigned here = (unsigned)max(0, min(first + kSlice, a.vocab) - lowest);  // a row's last slice may hold none
+    int answer = span.answer - span.begin - tid;  // tokens from `next` on that are the prompt's
+    while (left > 0) {
 #pragma unroll
       for (int k = 0; k < kTokens; ++k) {
-        const unsigned at = place_of(token[k]);
-        if (at >= (unsigned)kSlice) continue;
-        if (at0 + k * kLogitThreads >= span.answer)
-          atomicAdd(count_of + at, 1u);
+        const unsigned at = (unsigned)(token[k] - lowest);
+        if (at >= here) continue;
+        if (k * kLogitThreads >= answer)
+          atomicAdd(count_of + skipped + at, 1u);
         else
-          seen_in_prompt[at] = 1;  // by whichever thread
+          seen_in_prompt[skipped + at] = 1;  // by whichever thread
       }
+      next += kTokens * kLogitThreads;
+      left -= kTokens * kLogitThreads;
+      answer -= kTokens * kLogitThreads;
+      if (left > 0) read_tokens();
     }
     if (biases) {
       const int from = max(a.bias_starts[row], 0), to = min(a.bias_starts[row + 1], a.n_biases);
       for (int i = from + tid; i < to; i += kLogitThreads) {
-        const unsigned at = place_of(a.bias_ids[i]);
-        if (at < (unsigned)kSlice) atomicMax(bias_of + at, i - from + 1);
+        const unsigned at = (unsigned)(a.bias_ids[i] - lowest);
+        if (at < here) atomicMax(bias_of + skipped + at, i - from + 1);
       }
     }
     __syncthreads();
   }
 
   // ---- the logits
-  const float rep = a.repetition ? a.repetition[row] : 1.f, presence = a.presence ? a.presence[row] : 0.f;
-  const float frequency = a.frequency ? a.frequency[row] : 0.f;
-  auto adjusted = [&](float v, uint32_t count, bool in_prompt, int bias) {
-    if (count || in_prompt) {
-      if (a.repetition) v = v > 0.f ? __fdiv_rn(v, rep) : __fmul_rn(v, rep);
-      if (count) {
-        if (a.frequency) v = __fsub_rn(v, __fmul_rn(frequency, (float)count));
-        if (a.presence) v = __fsub_rn(v, presence);
-      }
-    }
-    if (bias) v = __fadd_rn(v, a.bias_values[max(a.bias_starts[row], 0) + bias - 1]);
-    return v;
+  // x / rep, by its reciprocal and what that leaves (a last bit off at most)
+  auto divided = [&](float v) {
+    const float q = __fmul_rn(v, inverse), rest = __fmaf_rn(-q, rep, v);
+    return fabsf(rest) < INFINITY ? __fmaf_rn(rest, inverse, q) : q;  // not of infinities
   };
 #pragma unroll
   for (int i = 0; i < kLogitLoads; ++i) {
     const int v = token_of(i), at = v - first;
     const uint32_t inside = inside_of(v);
     if (!inside) continue;
+    uint32_t touched = 0;
     uint4 count = make_uint4(0u, 0u, 0u, 0u);
     uint32_t prompt = 0u;
     int4 bias = make_int4(0, 0, 0, 0);
@@ -170,22 +166,31 @@ __global__ void __launch_bounds__(kLogitThreads) adjust_logits_kernel(const __gr
       prompt = *reinterpret_cast<const uint32_t*>(seen_in_prompt + at);
     }
     if (biases) bias = *reinterpret_cast<const int4*>(bias_of + at);
-    const uint32_t* c = &count.x;
-    const int* b = &bias.x;
-    uint32_t touched = 0;
-    if ((count.x | count.y | count.z | count.w | prompt) || (bias.x | bias.y | bias.z | bias.w)) {
+    const uint32_t c[4] = {count.x, count.y, count.z, count.w};
+    const int b[4] = {bias.x, bias.y, bias.z, bias.w};
+    const uint32_t any = count.x | count.y | count.z | count.w | prompt;
+    const int biased = bias.x | bias.y | bias.z | bias.w;
+    float p[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    if (kInPlace && (any || biased)) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) touched |= c[k] || (prompt >> 8 * k & 1) || b[k] ? 1u << k : 0u;
+      const float4 y = load4(v, touched & allow[i]);
+      p[0] = y.x, p[1] = y.y, p[2] = y.z, p[3] = y.w;
     }
-    if (kInPlace) {
-      const uint32_t change = touched & allow[i];
-      if (change) x[i] = load4(v, change);
+    if (any) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float y = p[k] > 0.f ? divided(p[k]) : __fmul_rn(p[k], rep);
+        p[k] = c[k] || (prompt >> 8 * k & 1) ? y : p[k];
+        const float less = __fsub_rn(__fsub_rn(p[k], __fmul_rn(frequency, (float)c[k])), presence);
+        p[k] = c[k] ? less : p[k];
+      }
     }
-    float* p = &x[i].x;
-    if (touched) {
+    if (biased) {
+      const float* values = a.bias_values + max(a.bias_starts[row], 0) - 1;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (touched >> k & 1) p[k] = adjusted(p[k], c[k], prompt >> 8 * k & 1, b[k]);
+        if (b[k]) p[k] = __fadd_rn(p[k], values[b[k]]);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -195,7 +200,7 @@ __global__ void __launch_bounds__(kLogitThreads) adjust_logits_kernel(const __gr
       for (int k = 0; k < 4; ++k)
         if ((inside >> k & 1) && ((touched >> k & 1) || !(allow[i] >> k & 1))) out[v + k] = p[k];
     } else if (kAligned && inside == 15u) {
-      *reinterpret_cast<float4*>(out + v) = x[i];
+      *reinterpret_cast<float4*>(out + v) = make_float4(p[0], p[1], p[2], p[3]);
     } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
