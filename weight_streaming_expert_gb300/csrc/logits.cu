@@ -24,7 +24,8 @@ namespace {
 constexpr int kLogitThreads = 256;
 constexpr int kLogitLoads = 4;                              // float4 of a thread
 constexpr int kSlice = kLogitThreads * kLogitLoads * 4;     // tokens of a CTA
-constexpr int kTokens = 16;                                 // of the history that a thread has in flight
+constexpr int kTokens = 12;                                 // of the history that a thread has in flight
+constexpr int kResident = 5;                                // CTAs of an SM (with 4: 31 us, with 6, which spill, 34)
 
 struct Span {
   int begin, answer, end;
@@ -45,7 +46,7 @@ __device__ __forceinline__ Span span_of(const moe_adjust_logits_args_t& a, int r
 // the row's address: token = number - shift.  kInPlace: out is logits.
 // kAligned: the output rows lie on the same remainder of 16 bytes.
 template <bool kInPlace, bool kAligned>
-__global__ void __launch_bounds__(kLogitThreads) adjust_logits_kernel(const __grid_constant__ moe_adjust_logits_args_t a) {
+__global__ void __launch_bounds__(kLogitThreads, kResident) adjust_logits_kernel(const __grid_constant__ moe_adjust_logits_args_t a) {
   // kSlice counts of the answer's tokens and a byte for each that the prompt has,
   // then kSlice bias numbers (each only where given)
   extern __shared__ uint4 table_words[];

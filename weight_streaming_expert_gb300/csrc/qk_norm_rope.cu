@@ -279,7 +279,16 @@ __global__ void __launch_bounds__(kRopeThreads, D == 256 ? 3 : 4) qk_norm_rope_k
       for (int i = lane; i < pairs; i += 32) {
         const unsigned long long at = (unsigned long long)(long long)a.positions[t] * a.turns[i];
         float sn, c;
-        sincospif((float)(int)(at >> 32) * 0x1p-31f, &sn, &c);  // in half turns, turns in [-1/2, 1/2)
+        if (kQuantised) {
+          // a key's codes are rounded from the fp32 values: those on the wrong side of a
+          // border become fewer with the angle's low bits, which turn by a little more
+          sincospif((float)(int)(at >> 40 << 8) * 0x1p-31f, &sn, &c);
+          const float rest = (float)(unsigned)(at >> 8) * 0x1p-55f * 3.14159265f, c0 = c;
+          c = fmaf(-sn, rest, c);
+          sn = fmaf(c0, rest, sn);
+        } else {
+          sincospif((float)(int)(at >> 32) * 0x1p-31f, &sn, &c);  // in half turns, turns in [-1/2, 1/2)
+        }
         turn[warp][i] = make_float2(c, sn);
       }
       __syncwarp();
