@@ -8,17 +8,17 @@ namespace wse {
 namespace {
 
 constexpr int kReadThreads = 256;
-constexpr int kReadUnits = 2;  // 16 codes each, that a thread has in flight
+constexpr int kReadTokens = 4;  // whose codes a lane has in flight
 
-// A thread takes 16 codes of a row; blockIdx.y: keys or values.  Bound by
-// memory: D + 1 bytes in and 2 D out for each row.
+// `lanes` of a warp take a token, 16 codes of it each at a time (so that its slot
+// is worked out once for them: with 16 codes of any row a thread the divisions
+// took longer than memory); blockIdx.y: keys or values.  Bound by memory: D + 1
+// bytes in and 2 D out for each row.
 __global__ void __launch_bounds__(kReadThreads)
-    read_e4m3_kernel(const __grid_constant__ moe_read_e4m3_args_t a) {
+    read_e4m3_kernel(const __grid_constant__ moe_read_e4m3_args_t a, int lanes) {
   const bool values = blockIdx.y != 0;
-  pdl_wait();
-  pdl_launch_dependents();
   const int per_head = a.head_dim / 16, per_token = a.n_kv_heads * per_head;
-  const long long units = (long long)a.n * per_token;
+  const int lane = threadIdx.x % lanes, tokens = kReadThreads / lanes;  // at a time
   const uint8_t* cache = static_cast<const uint8_t*>(values ? a.v_cache : a.k_cache);
   const uint8_t* scales = static_cast<const uint8_t*>(values ? a.scales.v_scale : a.scales.k_scale);
   const long long page_stride = values ? a.v_page_stride : a.k_page_stride;
@@ -28,34 +28,42 @@ __global__ void __launch_bounds__(kReadThreads)
   char* out = static_cast<char*>(values ? a.v_out : a.k_out);
   const long long token_stride = values ? a.v_token_stride : a.k_token_stride;
   const long long head_stride = values ? a.v_head_stride : a.k_head_stride;
-  const long long first = (long long)blockIdx.x * kReadThreads * kReadUnits + threadIdx.x;
-  uint4 codes[kReadUnits];
-  uint32_t byte[kReadUnits];
+  const long long first = (long long)blockIdx.x * (tokens * kReadTokens) + threadIdx.x / lanes;
+  pdl_wait();
+  pdl_launch_dependents();
+  const uint8_t* codes_at[kReadTokens];  // of the token's first head; nullptr: outside the cache
+  const uint8_t* scales_at[kReadTokens];
 #pragma unroll
-  for (int i = 0; i < kReadUnits; ++i) {
-    const long long u = first + i * kReadThreads;
-    codes[i] = make_uint4(0u, 0u, 0u, 0u);
-    byte[i] = kScaleBias;
-    if (u >= units) continue;
-    const int t = (int)(u / per_token), in_token = (int)(u - (long long)t * per_token);
-    const int head = in_token / per_head;
-    const long long slot = a.slots[t];
-    if (slot < 0 || slot >= (long long)a.n_pages * a.page_size) continue;
-    const long long page = slot / a.page_size, row = slot - page * a.page_size;
-    codes[i] = *reinterpret_cast<const uint4*>(cache + page * page_stride + row * row_stride + in_token * 16);
-    byte[i] = scales[page * scale_page + head * scale_head + row];
+  for (int i = 0; i < kReadTokens; ++i) {
+    const long long t = first + i * tokens, slot = t < a.n ? a.slots[t] : -1;
+    const bool there = slot >= 0 && slot < (long long)a.n_pages * a.page_size;
+    const long long page = slot >> 32 ? slot / a.page_size : (unsigned)slot / (unsigned)a.page_size;
+    const long long row = slot - page * a.page_size;
+    codes_at[i] = there ? cache + page * page_stride + row * row_stride : nullptr;
+    scales_at[i] = scales + page * scale_page + row;
   }
+  for (int u = lane; u < per_token; u += lanes) {
+    const int head = u / per_head, part = u - head * per_head;
+    uint4 codes[kReadTokens];
+    uint32_t byte[kReadTokens];
 #pragma unroll
-  for (int i = 0; i < kReadUnits; ++i) {
-    const long long u = first + i * kReadThreads;
-    if (u >= units) continue;
-    const int t = (int)(u / per_token), in_token = (int)(u - (long long)t * per_token);
-    const int head = in_token / per_head, part = in_token - head * per_head;
-    uint32_t v[8];
-    expand_e4m3(codes[i], power_of_two(exponent_of(byte[i])), a.dtype == MOE_DTYPE_BF16, v);
-    uint4* to = reinterpret_cast<uint4*>(out + (t * token_stride + head * head_stride + part * 16) * 2);
-    to[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    to[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    for (int i = 0; i < kReadTokens; ++i) {
+      codes[i] = make_uint4(0u, 0u, 0u, 0u);
+      byte[i] = kScaleBias;
+      if (!codes_at[i]) continue;
+      codes[i] = *reinterpret_cast<const uint4*>(codes_at[i] + u * 16);
+      byte[i] = scales_at[i][head * scale_head];
+    }
+#pragma unroll
+    for (int i = 0; i < kReadTokens; ++i) {
+      const long long t = first + i * tokens;
+      if (t >= a.n) continue;
+      uint32_t v[8];
+      expand_e4m3(codes[i], power_of_two(exponent_of(byte[i])), a.dtype == MOE_DTYPE_BF16, v);
+      uint4* to = reinterpret_cast<uint4*>(out + (t * token_stride + head * head_stride + part * 16) * 2);
+      to[0] = make_uint4(v[0], v[1], v[2], v[3]);
+      to[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
   }
 }
 
@@ -120,10 +128,11 @@ int moe_read_e4m3(const moe_read_e4m3_args_t* a, moe_stream_t stream) {
     return fail(MOE_ERR_INVALID_ARG, "every stride of the outputs must be a multiple of 8 elements (16 bytes)");
   const int rc = check_device();
   if (rc != MOE_OK) return rc;
-  const long long units = (long long)a->n * a->n_kv_heads * (a->head_dim / 16);
-  const long long blocks = (units + kReadThreads * kReadUnits - 1) / (kReadThreads * kReadUnits);
-  if (blocks > 0x7fffffffll) return fail(MOE_ERR_UNSUPPORTED, "%d rows: too many for one call", a->n);
-  return launch_pdl(read_e4m3_kernel, dim3((unsigned)blocks, 2), dim3(kReadThreads), 0, stream, 1, *a);
+  int lanes = 1;
+  while (lanes < 32 && lanes < a->n_kv_heads * (a->head_dim / 16)) lanes *= 2;
+  const long long tokens = (long long)kReadThreads / lanes * kReadTokens;  // of a CTA
+  return launch_pdl(read_e4m3_kernel, dim3((unsigned)((a->n + tokens - 1) / tokens), 2), dim3(kReadThreads), 0, stream, 1,
+                    *a, lanes);
 }
 
 int moe_copy_scales(void* k_scales, void* v_scales, int n_layers, int64_t k_layer_stride, int64_t v_layer_stride,
