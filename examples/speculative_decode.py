@@ -38,6 +38,7 @@ class Config:
     page: int = 16
     pages: int = 64
     max_len: int = 512
+    cache: torch.dtype = torch.bfloat16  # or float8_e4m3fn: quantised keys and values
 
 
 def rms(x, w, eps=1e-6):
@@ -67,11 +68,13 @@ class Model:
         self.head = LmHead(self.head_weight)
         self.rope = QKNormRope(c.head_dim, device=device)
         self.attention = PagedAttention(c.heads, c.kv_heads, c.head_dim, device=device)
-        self.cache = PagedKVCache(c.layers, c.pages, c.page, c.kv_heads, c.head_dim, c.max_len, device=device)
+        self.cache = PagedKVCache(c.layers, c.pages, c.page, c.kv_heads, c.head_dim, c.max_len, dtype=c.cache,
+                                  device=device)
 
-    def forward(self, seqs, tokens, positions=None, tree_mask=None):
+    def forward(self, seqs, tokens, positions=None, tree_mask=None, share=False):
         """`tokens[b]`: the new tokens of sequence seqs[b], which enter the
-        cache.  Returns the fp32 logits of all of them, one row per token."""
+        cache.  With `share` what forks have in common is read once for all of
+        them.  Returns the fp32 logits of all tokens, one row each."""
         c, cache = self.c, self.cache
         lens = [len(t) for t in tokens]
         starts = [0]
@@ -81,6 +84,7 @@ class Model:
             positions = [p for s, n in zip(seqs, lens) for p in range(cache.length(s), cache.length(s) + n)]
         slots = torch.cat([cache.extend(s, n) for s, n in zip(seqs, lens)])
         table, kv_lens = cache.block_table(seqs)
+        prefix = cache.shared_prefix(seqs, max(lens)) if share else 0
         i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=self.device)
         positions, starts = i32(positions), i32(starts)
         x = self.embed[torch.tensor([t for ts in tokens for t in ts], device=self.device)]
@@ -88,9 +92,9 @@ class Model:
         for layer, w in enumerate(self.weights):
             qkv = (rms(x, w["norm1"]) @ w["qkv"]).view(T, H + 2 * K, D)
             q = self.rope(qkv[:, :H], qkv[:, H:H + K], qkv[:, H + K:], w["q_norm"], w["k_norm"], positions, slots,
-                          cache.k[layer], cache.v[layer])
-            o = self.attention(q, cache.k[layer], cache.v[layer], table, starts, kv_lens, max(lens),
-                               tree_mask=tree_mask)
+                          **cache.layer(layer))
+            o = self.attention(q, block_table=table, q_starts=starts, kv_lens=kv_lens, max_q_len=max(lens),
+                               tree_mask=tree_mask, prefix_len=prefix, **cache.layer(layer))
             x = x + o.view(T, H * D) @ w["out"]
             y = rms(x, w["norm2"])
             x = x + torch.cat([self.moe[layer](part)[0] for part in y.split(MOE_MAX_TOKENS)])
