@@ -61,7 +61,7 @@ struct SharedParams : AttnParams {
   static constexpr bool kShared = true;
   static constexpr bool kAhead = true;
   template <int kTiles>
-  static constexpr int kCost = 2;
+  static constexpr int kCost = 3;
   enum Lists { kBoth, kPrefixOnly, kOwnOnly };
   Lists lists;                  // those that this launch works on
   int prefix, prefix_pages;
