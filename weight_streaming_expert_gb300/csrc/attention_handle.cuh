@@ -56,16 +56,17 @@ int launch_quantised(const moe_attn& h, const AttnParams& p, const moe_cache_sca
                      moe_stream_t stream);
 int launch_quantised(const moe_attn& h, const SharedParams& p, const moe_cache_scales_t& s, const Maps& maps,
                      moe_stream_t stream);
-// Pages in 16 bits, for what reads them often.  Row b of the table, from its `skip`-th entry on, holds sequence b's
-// pages; page i of it becomes page first + b * pages + i of k and v, and entry skip + i of row b of `table`.
+// Pages in 16 bits, for what reads them often: those of a prefix (of the table's first row) as pages 0 .. prefix_pages -
+// 1 of k and v, and behind them own_pages of each sequence.  `table` has a row of as many entries for each sequence, the
+// prefix's in the first one alone.
 struct Unpacked {
   void* k;
   void* v;
   int32_t* table;
-  int table_stride, first;
+  int table_stride, prefix_pages, own_pages;
 };
-// `len`: positions of each row, or kv_lens (-1) less those of the skipped pages
-int launch_unpack(const moe_attn& h, const moe_attn_args_t& a, const moe_cache_scales_t& s, const Unpacked& to, int batch,
-                  int skip, int pages, int len, moe_stream_t stream);
+// of the prefix, if `prefix`, and of `batch` sequences
+int launch_unpack(const moe_attn& h, const moe_attn_args_t& a, const moe_cache_scales_t& s, const Unpacked& to, bool prefix,
+                  int batch, moe_stream_t stream);
 
 }  // namespace wse

@@ -457,8 +457,8 @@ int forward_with(moe_attn* h, const moe_attn_args_t& args, const moe_attn_opts_t
     // the prefix in 16 bits
     const size_t half = w.prefix_pages * page_bytes(*h, a) / 2;
     const Unpacked u{at + w.prefix_at, at + w.prefix_at + half, reinterpret_cast<int32_t*>(at + w.prefix_at + 2 * half),
-                     w.prefix_pages, 0};
-    rc = launch_unpack(*h, a, *o.scales, u, 1, 0, w.prefix_pages, o.prefix_len, stream);
+                     w.prefix_pages, w.prefix_pages, 0};
+    rc = launch_unpack(*h, a, *o.scales, u, true, 0, stream);
     return rc != MOE_OK ? rc : run_shared(h, a, o, w, true, over_pages(*h, a, u, w.prefix_pages), stream);
   }
   // rows without pages: nothing is unpacked, and one call does all
@@ -469,20 +469,14 @@ int forward_with(moe_attn* h, const moe_attn_args_t& args, const moe_attn_opts_t
   if (pages > 0x7fffffffll) return too_much();
   const size_t half = pages * page_bytes(*h, a) / 2;
   char* k = at + w.prefix_at;
-  const Unpacked u{k, k + half, reinterpret_cast<int32_t*>(k + 2 * half), a.table_pages, w.prefix_pages};
+  const Unpacked u{k, k + half, reinterpret_cast<int32_t*>(k + 2 * half), a.table_pages, w.prefix_pages, own_pages};
   for (int b = 0; b < a.batch; b += at_once) {
     moe_attn_args_t part = a;
     part.batch = std::min(at_once, a.batch - b);
     part.q_starts = a.q_starts + b;
     part.kv_lens = a.kv_lens + b;
     part.block_table = a.block_table + (long long)b * a.table_stride;
-    if (b == 0 && o.prefix_len > 0) {
-      Unpacked prefix = u;
-      prefix.first = 0;
-      rc = launch_unpack(*h, a, *o.scales, prefix, 1, 0, w.prefix_pages, o.prefix_len, stream);
-    }
-    if (rc == MOE_OK)
-      rc = launch_unpack(*h, part, *o.scales, u, part.batch, w.prefix_pages, own_pages, -1, stream);
+    rc = launch_unpack(*h, part, *o.scales, u, b == 0 && o.prefix_len > 0, part.batch, stream);
     if (rc != MOE_OK) return rc;
     if (a.table_pages > 0) part = over_pages(*h, part, u, pages);
     rc = o.prefix_len > 0 ? run_shared(h, part, o, w, false, part, stream) : forward_16(h, part, stream);

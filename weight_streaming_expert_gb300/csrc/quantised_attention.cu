@@ -646,24 +646,25 @@ struct UnpackArgs {
   int32_t* table;
   int* status;
   int table_stride, page_size, n_pages, n_kv_heads, head_dim;
-  int out_stride, first, skip, pages, len;  // Unpacked's, and launch_unpack's
-  bool bf16;
+  int out_stride, prefix_pages, own_pages;
+  bool prefix, bf16;
 };
 
 constexpr int kUnpackThreads = 256;
 
-// CTA (i, b, z): page i of sequence b, keys or values; it has nothing to do past
-// the sequence's end.  Bound by memory.
+// CTA (x, z): a page of the prefix, then of the sequences one after the other,
+// keys or values; it has nothing to do past a sequence's end.  Bound by memory.
 __global__ void __launch_bounds__(kUnpackThreads) unpack_kernel(const __grid_constant__ UnpackArgs a) {
-  const int i = blockIdx.x, b = blockIdx.y, z = blockIdx.z;
+  const int from_prefix = a.prefix ? a.prefix_pages : 0, z = blockIdx.y, tid = threadIdx.x;
+  const bool prefix = (int)blockIdx.x < from_prefix;
+  const int at = (int)blockIdx.x - (prefix ? 0 : from_prefix), b = prefix ? 0 : at / a.own_pages;
+  const int i = prefix ? at : at - b * a.own_pages, skip = prefix ? 0 : a.prefix_pages;
   pdl_wait();
   pdl_launch_dependents();
-  const long long to = a.first + (long long)b * a.pages + i;
-  const int tid = threadIdx.x;
-  if (z == 0 && tid == 0) a.table[(long long)b * a.out_stride + a.skip + i] = (int)to;
-  const long long len = a.len >= 0 ? a.len : (long long)a.kv_lens[b] - (long long)a.skip * a.page_size;
-  if ((long long)i * a.page_size >= len) return;
-  const int page = a.block_table[(long long)b * a.table_stride + a.skip + i];
+  const long long to = prefix ? at : (long long)a.prefix_pages + at;
+  if (z == 0 && tid == 0) a.table[(long long)b * a.out_stride + skip + i] = (int)to;
+  if (!prefix && ((long long)skip + i) * a.page_size >= a.kv_lens[b]) return;
+  const int page = a.block_table[(long long)b * a.table_stride + skip + i];
   const bool there = (unsigned)page < (unsigned)a.n_pages;
   if (!there && tid == 0) atomicOr(a.status, kAttnBadPage);
   const int per_head = a.head_dim / 16, per_row = a.n_kv_heads * per_head, units = a.page_size * per_row;
@@ -717,8 +718,9 @@ int launch_quantised(const moe_attn& h, const SharedParams& p, const moe_cache_s
   return h.head_dim == 64 ? launch_rows<64>(h, c, s, maps, stream) : launch_rows<128>(h, c, s, maps, stream);
 }
 
-int launch_unpack(const moe_attn& h, const moe_attn_args_t& a, const moe_cache_scales_t& s, const Unpacked& to, int batch,
-                  int skip, int pages, int len, moe_stream_t stream) {
+int launch_unpack(const moe_attn& h, const moe_attn_args_t& a, const moe_cache_scales_t& s, const Unpacked& to, bool prefix,
+                  int batch, moe_stream_t stream) {
+  const long long pages = (prefix ? to.prefix_pages : 0) + (long long)batch * to.own_pages;
   if (pages == 0) return MOE_OK;
   const UnpackArgs u{{static_cast<const uint8_t*>(a.k_cache), static_cast<const uint8_t*>(a.v_cache)},
                      {a.k_page_stride, a.v_page_stride},
@@ -728,8 +730,8 @@ int launch_unpack(const moe_attn& h, const moe_attn_args_t& a, const moe_cache_s
                      {s.k_head_stride, s.v_head_stride},
                      {static_cast<uint16_t*>(to.k), static_cast<uint16_t*>(to.v)},
                      a.block_table, a.kv_lens, to.table, h.status, a.table_stride, a.page_size, a.n_pages, h.n_kv_heads,
-                     h.head_dim, to.table_stride, to.first, skip, pages, len, a.dtype == MOE_DTYPE_BF16};
-  return launch_pdl(unpack_kernel, dim3((unsigned)pages, (unsigned)batch, 2), dim3(kUnpackThreads), 0, stream, 1, u);
+                     h.head_dim, to.table_stride, to.prefix_pages, to.own_pages, prefix, a.dtype == MOE_DTYPE_BF16};
+  return launch_pdl(unpack_kernel, dim3((unsigned)pages, 2), dim3(kUnpackThreads), 0, stream, 1, u);
 }
 
 }  // namespace wse
