@@ -81,7 +81,8 @@ typedef struct {
 /*
  * The same with a quantised cache: a's caches hold codes (strides in bytes).
  * Keys are quantised from their fp32 values after norm and rotation, not
- * rounded to 16 bits in between.
+ * rounded to 16 bits in between.  No slot may be in slots twice: its codes and
+ * its scale would be of different tokens.
  */
 int moe_qk_norm_rope_e4m3(const moe_qk_norm_rope_args_t* a, const moe_cache_scales_t* s, moe_stream_t stream);
 

@@ -228,6 +228,19 @@ def test_long_histories_and_large_vocabularies():
 
 
 @pytest.mark.gpu
+def test_rows_beyond_32_bit_offsets():
+    from weight_streaming_expert_gb300 import adjust_logits
+    c = mixed(3, 700, seed=10)
+    x = c.inputs()
+    far = torch.empty(2 * ((1 << 30) + 700) + 700, device=DEV)  # rows 2^32 bytes apart and more
+    view = far.as_strided((3, 700), ((1 << 30) + 700, 1))
+    view.copy_(x["logits"])
+    c.check(adjust_logits(**{**x, "logits": view}))
+    adjust_logits(**{**x, "logits": view, "out": view})
+    c.check(view)
+
+
+@pytest.mark.gpu
 def test_captured_and_on_another_stream():
     from weight_streaming_expert_gb300 import adjust_logits
     c = mixed(6, 3001, seed=8)

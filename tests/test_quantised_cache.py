@@ -288,6 +288,48 @@ def test_scales_move_with_their_rows(Hk, page):
 
 
 @pytest.mark.gpu
+def test_pages_whose_scales_do_not_fit_are_refused_before_any_moves():
+    from weight_streaming_expert_gb300 import copy_pages
+    pools = {n: torch.zeros(1, 4, 8, 1, 64, dtype=torch.uint8, device=DEV) for n in ("k_pool", "v_pool")}
+    pools["k_pool"][:, 0] = 7
+    scale = torch.zeros(1, 4, 1, 8, dtype=torch.uint8, device=DEV)
+    i = torch.arange(2, dtype=torch.int32, device=DEV)
+    with pytest.raises(ValueError, match="16 bytes"):
+        copy_pages(**pools, src=i[:1], dst=i[1:], k_scale=scale, v_scale=scale.clone())
+    assert (pools["k_pool"][:, 1] == 0).all()
+
+
+@pytest.mark.gpu
+def test_codes_beyond_32_bit_offsets():
+    """Rows past 2^32 bytes of the pool, written, read back and attended to."""
+    from weight_streaming_expert_gb300 import PagedAttention, read_cache
+    page, Hk, D = 256, 8, 128
+    pages = (1 << 32) // (page * Hk * D) + 9
+    cache = {n + "_cache": torch.empty(pages, page, Hk, D, dtype=torch.uint8, device=DEV).view(E4M3) for n in "kv"}
+    cache.update({n + "_scale": torch.empty(pages, Hk, page, dtype=torch.uint8, device=DEV) for n in "kv"})
+    x = torch.randn(300, 3 * Hk, D, generator=torch.Generator().manual_seed(1)).bfloat16()
+    table = torch.tensor([[pages - 1, pages - 3]], dtype=torch.int32)
+    at = torch.arange(300)
+    slots = table[0].long()[at // page] * page + at % page
+    q = write(x, Hk, Hk, D, cache, slots)
+    k, v = read_cache(**cache, slots=slots.to(DEV))
+    for got, y in ((k, x[:, Hk:2 * Hk]), (v, x[:, 2 * Hk:])):
+        codes, e = quantised(y.float())
+        assert torch.equal(got.cpu().float(), torch.ldexp(codes.view(E4M3).float(), e[..., None]))
+    attn = PagedAttention(Hk, Hk, D, device=DEV)
+    i32 = lambda *t: torch.tensor(t, dtype=torch.int32, device=DEV)
+    for m in (1, 90):  # over the codes, and through 16 bits
+        out = attn(q[300 - m:], block_table=table.to(DEV), q_starts=i32(0, m), kv_lens=i32(300), max_q_len=m, **cache)
+        s = torch.einsum("mhd,nhd->hmn", q[300 - m:].double(), k.double()) * D ** -0.5
+        s.masked_fill_(torch.arange(300, device=DEV)[None, None] > (300 - m + torch.arange(m, device=DEV))[None, :, None], -math.inf)
+        want = torch.einsum("hmn,nhd->mhd", s.softmax(-1), v.double())
+        # two roundings to bf16, relative to values of at most the largest
+        assert (out.double() - want).abs().max() <= 2.0 ** -7 * v.abs().max()
+    assert attn.status() == 0
+    attn.close()
+
+
+@pytest.mark.gpu
 def test_refusals():
     from weight_streaming_expert_gb300 import QKNormRope, copy_pages, copy_rows, read_cache
     cache = empty_cache(3, 16, 2, 64)

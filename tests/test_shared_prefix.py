@@ -123,6 +123,13 @@ def test_batches_of_single_tokens(codes, batch):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("codes", [False, True])
+def test_the_largest_batch(codes):
+    rng = random.Random(9)
+    run(Shared([1] * 4096, [rng.randint(1, 20) for _ in range(4096)], 32, 1, 1, 64, 16, seed=9, codes=codes))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("codes", [False, True])
 @pytest.mark.parametrize("m", [1, 7, 16, 31, 33, 64, 65, 100, 260])
 def test_chunks(codes, m):
     run(Shared([m, m // 2, 0, 1], [m, m + 5, 40, 1], 320, 4, 2, 128, 32, seed=m, codes=codes))

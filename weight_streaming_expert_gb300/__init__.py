@@ -21,5 +21,6 @@ __all__ = list(_HOMES)
 
 def __getattr__(name):
     if name in _HOMES:
-        return getattr(importlib.import_module("." + _HOMES[name], __name__), name)
+        value = globals()[name] = getattr(importlib.import_module("." + _HOMES[name], __name__), name)  # asked for once
+        return value
     raise AttributeError(name)

@@ -121,7 +121,8 @@ class QKNormRope:
         slot writes nothing), caches [pages, page_size, Hk, D].  Returns q_out
         (a new contiguous tensor, or the given one; it may be q).  With k_scale
         and v_scale (uint8 [pages, Hk, page_size]) the caches are quantised:
-        float8_e4m3fn codes, a power of two for each row of a head."""
+        float8_e4m3fn codes, a power of two for each row of a head; no slot may
+        be in slots twice then."""
         index = self._index
         if index < 0:
             raise ValueError("the operator was made on the CPU: its calls need a GPU")

@@ -56,8 +56,9 @@ def copy_pages(k_pool, v_pool, src, dst, stream=None, k_scale=None, v_scale=None
     quantised = k_scale is not None or v_scale is not None
     if quantised:
         _scale_pools(k_pool, v_pool, k_scale, v_scale)
-        if any(t.stride(2) != t.shape[3] for t in (k_scale, v_scale)):
-            raise ValueError("the scales' pages must be contiguous")
+        for t in (k_scale, v_scale):  # before anything has moved
+            if t.stride(2) != t.shape[3] or any(n % 16 for n in (t.shape[2] * t.shape[3], t.stride(0), t.stride(1))):
+                raise ValueError("the scales' pages must be contiguous, of whole 16 bytes and as many apart")
     _copy("moe_copy_pages", False, k_pool, v_pool, src, dst, stream)
     if quantised:
         _copy("moe_copy_pages", False, k_scale.unsqueeze(2), v_scale.unsqueeze(2), src, dst, stream)
