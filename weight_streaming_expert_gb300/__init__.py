@@ -5,17 +5,17 @@ combine) runs in hand-written sm_103a CUDA kernels behind the C ABI in
 ``include/moe.h``; ``MoELayer`` is its Python face.  ``LmHead`` is the bf16
 vocabulary projection of the same decode step (``include/lm_head.h``).  The step's
 attention half stands in ``include/attention.h`` (``QKNormRope``,
-``PagedAttention``, ``PagedKVCache``), penalties and masks on the logits and the
-draw of the next tokens in ``include/sampling.h`` (``adjust_logits``, ``sample``).  Importing the package loads nothing; the
-CUDA library is loaded (and must exist) on first use.
+``PagedAttention``, ``PagedKVCache``, ``read_cache``), penalties and masks on
+the logits and the draw of the next tokens in ``include/sampling.h``
+(``adjust_logits``, ``sample``).  Importing the package loads nothing; the CUDA
+library is loaded (and must exist) on first use.
 """
 import importlib
 
 _HOMES = {"MoELayer": "layer", "LmHead": "layer", "tp_slice": "layer", "combine_partials": "layer",
           "QKNormRope": "attention", "PagedAttention": "attention", "PagedKVCache": "cache", "PageTable": "cache",
           "copy_pages": "cache", "copy_rows": "cache", "read_cache": "cache",
-          "sample": "sampling",
-          "adjust_logits": "sampling"}
+          "adjust_logits": "sampling", "sample": "sampling"}
 __all__ = list(_HOMES)
 
 

@@ -60,6 +60,8 @@ struct AttnParams {
 struct SharedParams : AttnParams {
   static constexpr bool kShared = true;
   static constexpr bool kAhead = true;
+  // 128 tokens behind 16,384 take 78 us with 2, 75 with 4, 79 with 6; 8 tokens
+  // behind 8,192 17.4 with 2, 18.1 with 4
   template <int kTiles>
   static constexpr int kCost = 3;
   enum Lists { kBoth, kPrefixOnly, kOwnOnly };

@@ -15,6 +15,11 @@
 //
 // In place nothing is asked for ahead: only tokens that change are read, and
 // those that the mask forbids only written.
+//
+// 64 rows of 157,184 with histories up to 8,000, masks and biases: 28 us, 3 TB/s
+// (nothing to adjust: 14 us).  A CTA's life is three latencies, of the row's span,
+// of its tokens and logits, and of the table, and the CTAs come in three waves;
+// half the issue slots are taken.  6 rows with a history of 4,000: 6.4 us.
 #include "host_util.cuh"
 #include "sampling.h"
 

@@ -319,7 +319,8 @@ size_t sequence_bytes(const moe_attn& h, const moe_attn_args_t& a, int prefix_pa
   return (a.table_pages - prefix_pages) * page_bytes(h, a) + (size_t)a.table_pages * 16;
 }
 
-// Tiles of tokens from which the prefix's list runs by itself.
+// Tiles of tokens from which the prefix's list runs by itself (16 tiles behind
+// 16,384 positions: 136 us in one list, 152 apart; 32 tiles 209 and 182).
 constexpr int kApartTiles = 32;
 
 // How a call with options is worked on, and what it keeps in the workspace.

@@ -31,6 +31,11 @@
 // unit's codes for itself, as O of more rows does not fit a warp's registers.
 // Each warp has its own M, sums and O, which are joined at an item's end through
 // shared memory, in the order of the warps.
+//
+// One GB300 (copy 6693 GB/s), 32 single tokens of 32/4 heads of 128 over 2,000 to
+// 32,768 positions: 73 us, 5.7 TB/s, of which 10 us are the call's start and end
+// (a tile of 8 rows; 16 rows 92 us, 32 rows 131, 64 rows 175: the conversions'
+// instructions and their latency).  6 tokens over 8,192: 15.8 us.
 #include <algorithm>
 
 #include "attention_handle.cuh"
@@ -40,7 +45,8 @@ namespace wse {
 namespace {
 
 // An item's start (the queries) and end (the warps' joining) take as long as some
-// units.
+// units: 32 sequences of 2,000 to 32,768 positions 79 us with 0, 76 with 2, 73
+// with 4; 128 short ones behind a prefix 250 with 2, 266 with 4.
 constexpr int kCodeItemCost = 3;
 struct CodeParams : AttnParams {
   static constexpr bool kAhead = true;

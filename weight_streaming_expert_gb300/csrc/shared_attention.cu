@@ -10,8 +10,14 @@
 // One list and one launch for both: prefix and own tiles fill the SMs together,
 // and a share's cut may fall anywhere.  A tile that no share cuts leaves its sums
 // in fp32 by token, 4 D bytes a row written and read back once, which is little
-// beside the prefix (128 single tokens of 32 heads over 16,384 positions: 4.2 of
-// 380 MB) and keeps the output's rounding the only one.
+// beside the positions (128 single tokens of 32/4 heads of 128 behind 16,384: 8 of
+// 215 MB) and keeps the output's rounding the only one.
+//
+// What bounds it: of few tokens the latencies of a short call and of joining the
+// prefix's many parts (8 tokens of 20/4 heads behind 8,192 positions: 18 us); of
+// large batches the products over the prefix and the short own items, 3 to 4 us
+// each that nothing overlaps (128 tokens behind 16,384 with up to 2,000 of their
+// own: 77 us, where each sequence read the prefix for itself 13 times the bytes).
 #include <algorithm>
 
 #include "attention_handle.cuh"
@@ -193,7 +199,7 @@ __global__ void __launch_bounds__(kJoinRows * kJoinGroups * D / 4)
 }
 
 // The same for many tokens, whose results have few parts: a warp for each row,
-// and nothing shared (128 single tokens of 32 heads: 111 us with the kernel above).
+// and nothing shared (128 single tokens behind 16,384: 81 us, with the kernel above 111).
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kJoinRows) join_few_parts_kernel(const __grid_constant__ JoinParams j) {
   constexpr int kColumns = D / 4, kSide = 32 / kColumns;  // parts side by side
