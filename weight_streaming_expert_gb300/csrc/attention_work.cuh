@@ -313,9 +313,9 @@ __device__ __forceinline__ Veil veil_of(const P& p, const Seq& s, int item) {
 
 // Where this CTA's share begins, found by each warp for itself: lane l has the
 // sequences l * per, .., whose costs (one head's units) cost(b) gives and sum
-// to `lane_sum`.
-template <int kTiles, bool kChecked, typename P, typename Cost>
-__device__ __forceinline__ Plan make_plan(const P& p, int per, long long lane_sum, Cost cost) {
+// to `lane_sum`; seq_at(b): sequence b, the same in every lane.
+template <int kTiles, bool kChecked, typename P, typename Cost, typename SeqAt>
+__device__ __forceinline__ Plan make_plan(const P& p, int per, long long lane_sum, Cost cost, SeqAt seq_at) {
   const int lane = threadIdx.x & 31;
   const int heads = p.n_kv_heads / p.spread, shares = gridDim.x / p.spread;
   if (kChecked && !p.fits) {
@@ -344,7 +344,7 @@ __device__ __forceinline__ Plan make_plan(const P& p, int per, long long lane_su
   plan.b = __shfl_sync(0xffffffffu, b, src);
   int rest = plan.start - __shfl_sync(0xffffffffu, at, src);
   own = __shfl_sync(0xffffffffu, own, src);
-  plan.s = load_seq(p, plan.b);
+  plan.s = seq_at(plan.b);
   plan.h = (unsigned)rest / (unsigned)own;
   rest -= plan.h * own;
   for (int tile = lane;; tile += 32) {  // 32 items at a time
@@ -370,12 +370,17 @@ __device__ __forceinline__ Plan plan_of(const P& p, int* cost) {
   const bool wide = p.longest() > 4 * kTiles * p.tokens;  // sequences of many items: a warp each
   if (p.sequences() <= 32 && !wide && p.fits) {
     int sum = 0;
+    Seq s{};
     if (lane < p.sequences()) {
-      const Seq s = load_seq(p, lane);
+      s = load_seq(p, lane);
       if (s.bad && blockIdx.x == 0) atomicOr(p.status, kAttnBadLength);
       for (int i = 0; i * kTiles * p.tokens < s.n; ++i) sum += units_of<kTiles>(p, s, i) + P::template kCost<kTiles>;
     }
-    return make_plan<kTiles, false>(p, 1, sum, [&](int) { return sum; });
+    return make_plan<kTiles, false>(p, 1, sum, [&](int) { return sum; }, [&](int b) {
+      if (kTiles == 2) return load_seq(p, b);  // chunks: 4 us slower with the shuffles, ragged ones of 121
+      auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, b); };
+      return Seq{of(s.q0), of(s.n), of(s.kv), of(s.base), false};
+    });
   }
   for (int b = wide ? warp : tid; b < p.sequences(); b += wide ? kThreads / 32 : kThreads) {
     const Seq s = load_seq(p, b);
@@ -393,7 +398,8 @@ __device__ __forceinline__ Plan plan_of(const P& p, int* cost) {
   const int per = (p.sequences() + 31) / 32;
   long long sum = 0;
   for (int b = lane * per; b < min(p.sequences(), (lane + 1) * per); ++b) sum += cost[b];
-  const Plan plan = make_plan<kTiles, true>(p, per, sum, [&](int b) { return cost[b]; });
+  const Plan plan = make_plan<kTiles, true>(p, per, sum, [&](int b) { return cost[b]; },
+                                           [&](int b) { return load_seq(p, b); });
   fence_proxy_async_smem();  // the costs' place becomes the ring
   __syncthreads();
   return plan;
