@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kCodeThreads, 1)
     // ---- copies, by four warps: keys and values, and the first and last pages of
     // a unit.  The codes with TMA, a lane per page: the lanes' copies are issued one
     // after the other, 90 clocks each, so one warp alone would need 1500 for a unit's
-    // 16 boxes of 16 rows, as long as memory does (pages of 16: 104 us, now 77).  The
+    // 16 boxes of 16 rows, as long as memory does (pages of 16: 104 us, with four 79).  The
     // scales 16 bytes a lane.
     const int values = (warp - kWarps) >> 1, half = (warp - kWarps) & 1;
     const int box_rows = min(a.page_size, kTile), per_unit = kTile / box_rows, page_log2 = 31 - __clz(a.page_size);
