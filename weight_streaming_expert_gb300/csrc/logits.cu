@@ -19,7 +19,7 @@
 // 64 rows of 157,184 with histories up to 8,000, masks and biases: 28 us, 3 TB/s
 // (nothing to adjust: 14 us).  A CTA's life is three latencies, of the row's span,
 // of its tokens and logits, and of the table, and the CTAs come in three waves;
-// half the issue slots are taken.  6 rows with a history of 4,000: 6.4 us.
+// half the issue slots are taken.  6 rows with a history of 4,000: 6.0 us.
 #include "host_util.cuh"
 #include "sampling.h"
 
@@ -29,7 +29,7 @@ namespace {
 constexpr int kLogitThreads = 256;
 constexpr int kLogitLoads = 4;                              // float4 of a thread
 constexpr int kSlice = kLogitThreads * kLogitLoads * 4;     // tokens of a CTA
-constexpr int kTokens = 12;                                 // of the history that a thread has in flight
+constexpr int kTokens = 8;                                 // of the history that a thread has in flight
 constexpr int kResident = 5;                                // CTAs of an SM (with 4: 31 us, with 6, which spill, 34)
 
 struct Span {
