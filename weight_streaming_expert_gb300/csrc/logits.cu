@@ -29,8 +29,8 @@ namespace {
 constexpr int kLogitThreads = 256;
 constexpr int kLogitLoads = 4;                              // float4 of a thread
 constexpr int kSlice = kLogitThreads * kLogitLoads * 4;     // tokens of a CTA
-constexpr int kTokens = 8;                                 // of the history that a thread has in flight
-constexpr int kResident = 5;                                // CTAs of an SM (with 4: 31 us, with 6, which spill, 34)
+constexpr int kTokens = 8;                                  // of the history that a thread has in flight
+constexpr int kResident = 5;                                // CTAs of an SM (64 rows: with 4 31 us, with 5 or 6 28)
 
 struct Span {
   int begin, answer, end;
