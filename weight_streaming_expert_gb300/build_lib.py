@@ -51,7 +51,7 @@ def _headers():
 
 
 def _library_inputs():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + _headers()
+    return _sources() + [p for end in ("*.cuh", "*.h") for p in glob.glob(os.path.join(CSRC, end))] + _headers()
 
 
 def _inputs():

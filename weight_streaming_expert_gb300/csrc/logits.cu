@@ -21,6 +21,7 @@
 // of its tokens and logits, and of the table, and the CTAs come in three waves;
 // half the issue slots are taken.  6 rows with a history of 4,000: 6.0 us.
 #include "host_util.cuh"
+#include "list_parts.h"
 #include "sampling.h"
 
 namespace wse {
@@ -32,18 +33,10 @@ constexpr int kSlice = kLogitThreads * kLogitLoads * 4;     // tokens of a CTA
 constexpr int kTokens = 8;                                  // of the history that a thread has in flight
 constexpr int kResident = 5;                                // CTAs of an SM (64 rows: with 4 31 us, with 5 or 6 28)
 
-struct Span {
-  int begin, answer, end;
-};
-
 // (begin, answer, end) of a row, cut to the history.
 __device__ __forceinline__ Span span_of(const moe_adjust_logits_args_t& a, int row) {
   const int32_t* s = a.spans + 3ll * row;
-  Span r;
-  r.begin = max(s[0], 0);
-  r.end = min(s[2], a.n_history);
-  r.answer = max(s[1], r.begin);
-  return r;
+  return cut_span(s[0], s[1], s[2], a.n_history);
 }
 
 // The slice's tokens are numbered from the 16-byte boundary at or before the
