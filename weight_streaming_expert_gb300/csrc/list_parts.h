@@ -27,4 +27,15 @@ WSE_BOTH Span cut_span(int begin, int answer, int end, int n) {
   return s;
 }
 
+// A row's entries from..to-1 of a list: 0 <= from <= to <= n.
+struct Part {
+  int from, to;
+};
+WSE_BOTH Part cut_part(int from, int to, int n) {
+  Part p;
+  p.from = cut_to(from, 0, n);
+  p.to = cut_to(to, p.from, n);
+  return p;
+}
+
 }  // namespace wse

@@ -38,6 +38,10 @@ __device__ __forceinline__ Span span_of(const moe_adjust_logits_args_t& a, int r
   const int32_t* s = a.spans + 3ll * row;
   return cut_span(s[0], s[1], s[2], a.n_history);
 }
+// The row's entries of the list of biases, cut to it.
+__device__ __forceinline__ Part part_of(const moe_adjust_logits_args_t& a, int row) {
+  return cut_part(a.bias_starts[row], a.bias_starts[row + 1], a.n_biases);
+}
 
 // The slice's tokens are numbered from the 16-byte boundary at or before the
 // row's first logit, so that a thread's four lie in one aligned load whatever
@@ -136,10 +140,11 @@ __global__ void __launch_bounds__(kLogitThreads, kResident) adjust_logits_kernel
       if (left > 0) read_tokens();
     }
     if (biases) {
-      const int from = max(a.bias_starts[row], 0), to = min(a.bias_starts[row + 1], a.n_biases);
-      for (int i = from + tid; i < to; i += kLogitThreads) {
-        const unsigned at = (unsigned)(a.bias_ids[i] - lowest);
-        if (at < here) atomicMax(bias_of + skipped + at, i - from + 1);
+      const Part part = part_of(a, row);
+      const unsigned entries = (unsigned)(part.to - part.from);  // up to INT_MAX: the step past them stays in 32 bits
+      for (unsigned i = tid; i < entries; i += kLogitThreads) {
+        const unsigned at = (unsigned)(a.bias_ids[part.from + i] - lowest);
+        if (at < here) atomicMax(bias_of + skipped + at, (int)i + 1);
       }
     }
     __syncthreads();
@@ -186,7 +191,7 @@ __global__ void __launch_bounds__(kLogitThreads, kResident) adjust_logits_kernel
       }
     }
     if (biased) {
-      const float* values = a.bias_values + max(a.bias_starts[row], 0) - 1;
+      const float* values = a.bias_values + part_of(a, row).from - 1;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (b[k]) p[k] = __fadd_rn(p[k], values[b[k]]);
