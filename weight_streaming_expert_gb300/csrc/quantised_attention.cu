@@ -102,9 +102,10 @@ __device__ __forceinline__ uint32_t place_of(int r, int c) {
   return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ (r >> 1 & 3)) << 4);
 }
 
-// 16 bytes to shared memory, both sides aligned to them, without waiting.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 16 bytes to shared memory, both sides aligned to them, without waiting; zeros
+// without a look at `src` where it is not there.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 // Arrives on `bar` once this thread's copies so far are in.
 __device__ __forceinline__ void arrive_with_copies(uint32_t bar) {
@@ -240,9 +241,11 @@ __global__ void __launch_bounds__(kCodeThreads, 1)
         const unsigned boxes = __popc(__ballot_sync(0xffffffffu, mine && codes));
         if (lane == 0) mbar_arrive_expect_tx(full(stage), boxes * D * box_rows);
         __syncwarp();
-        if (mine && !codes && there)
+        // a page that is not there: codes of zero with the least scale, so that they
+        // weigh as zeros do and do not push M up with a scale that lay there before
+        if (mine && !codes)
           copy16(sb + L::kScaleAt + stage * L::kScales + values * kTile + place * 16,
-                 scale + page * scale_page + it.h * scale_head + (pos & (a.page_size - 1)));
+                 scale + (there ? page * scale_page + it.h * scale_head + (pos & (a.page_size - 1)) : 0), there);
         if (lane >= 4 && lane < 8) arrive_with_copies(full(stage));
         if (mine && codes)  // a page that is not there lies outside the tensor and reads as zeros
           tma_load_3d(sb + L::kRing + stage * L::kStage + values * L::kCodeTile + place * box_rows * D, map, it.h * D,
