@@ -179,8 +179,8 @@ int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t strea
  *
  * prefix_len: the first prefix_len positions of every sequence are the same, in
  * the same pages: those that the table's first row begins with (the other rows'
- * first prefix_len / page_size entries are not read).  Whole pages, and all new
- * tokens lie behind them (a sequence that is shorter is an error found on the
+ * first prefix_len / page_size entries are not read).  Whole pages, up to 2^30
+ * positions, and all new tokens lie behind them (a sequence that is shorter is an error found on the
  * device).  The prefix is read once for the whole batch instead of once for
  * each sequence; the results are those of a call without, but for rounding.
  * Of a quantised cache's prefix, where it is read for more than 64 rows, and of

@@ -223,6 +223,8 @@ int check_current(const moe_attn& h) {
   return MOE_OK;
 }
 
+constexpr int kMaxPrefix = 1 << 30;  // positions: a token's number added to them stays in 32 bits
+
 int too_much() { return fail(MOE_ERR_UNSUPPORTED, "too much work for one call: split the tokens"); }
 
 // Units of a key/value head's longest possible item, with what it costs besides.
@@ -542,7 +544,9 @@ int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t strea
 }
 
 size_t moe_attn_workspace(const moe_attn_t* h, const moe_attn_args_t* a, const moe_attn_opts_t* o) {
-  if (!h || !a || !o || a->batch <= 0 || a->n_tokens <= 0 || a->page_size <= 0 || o->prefix_len < 0) return 0;
+  if (!h || !a || !o || a->batch <= 0 || a->n_tokens <= 0 || a->page_size <= 0 || o->prefix_len < 0 ||
+      o->prefix_len > kMaxPrefix)
+    return 0;
   const moe_attn_args_t all = with_pages(*a);
   return o->prefix_len / a->page_size > all.table_pages ? 0 : work_of(*h, all, *o).wanted;
 }
@@ -555,6 +559,8 @@ int moe_attn_forward_ex(moe_attn_t* h, const moe_attn_args_t* a, const moe_attn_
   const moe_cache_scales_t* sc = o->scales;
   if (o->prefix_len < 0 || o->prefix_len % a->page_size)
     return fail(MOE_ERR_INVALID_ARG, "prefix_len = %d: must be whole pages of %d", o->prefix_len, a->page_size);
+  if (o->prefix_len > kMaxPrefix)
+    return fail(MOE_ERR_UNSUPPORTED, "prefix_len = %d exceeds %d", o->prefix_len, kMaxPrefix);
   const int table_pages = a->table_pages > 0 ? a->table_pages : a->table_stride;
   if (a->batch > 0 && o->prefix_len / a->page_size > table_pages)
     return fail(MOE_ERR_INVALID_ARG, "prefix_len = %d: a row of the table holds %d pages", o->prefix_len, table_pages);
