@@ -29,3 +29,21 @@ def test_prefixes_beyond_2_30_positions(codes):
     for prefix in ((1 << 30) + 256, (1 << 31) - 256):
         status, text = forward((4, 2, 64), prefix, s, **wide)
         assert status == N.MOE_ERR_UNSUPPORTED and "prefix_len" in text, (prefix, text)
+
+
+def test_limits_count_what_the_lists_do():
+    """Items cost three units besides their own, over codes and behind a prefix:
+    many short ones are more work than two units each would say."""
+    from weight_streaming_expert_gb300 import native as N
+    s = N.moe_cache_scales_t(4096, 4096, 1 << 20, 16, 1 << 20, 16)
+    heads = (65536, 65536, 64)
+    # (32000 / 8 + 4000) items of each head at 1/8 + 1 + 3 units: 2.16e9; at 1/8 + 1 + 2 1.64e9
+    status, text = forward(heads, 0, s, batch=4000, n_tokens=32000, max_q_len=1, table_stride=1)
+    assert status == N.MOE_ERR_UNSUPPORTED and "too much work" in text, text
+    # 4000 * 2 own items at 2/8 + 1 + 3 and 16 over the prefix: 2.23e9 and 1.71e9
+    status, text = forward(heads, 16, batch=4000, n_tokens=4000, max_q_len=300, table_stride=2)
+    assert status == N.MOE_ERR_UNSUPPORTED and "too much work" in text, text
+    # what stays under the limit gets as far as the device
+    for prefix, codes in ((0, s), (16, None)):
+        status, text = forward(heads, prefix, codes, batch=2000, n_tokens=2000, max_q_len=1, table_stride=2)
+        assert status != N.MOE_ERR_UNSUPPORTED, text

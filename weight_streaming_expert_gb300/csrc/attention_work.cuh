@@ -28,6 +28,13 @@ constexpr int kMaxParts = 1024;            // CTAs, which is at least the shares
 // 1 or 2).
 template <int kTiles>
 constexpr int kItemCost = kTiles == 2 ? 2 : 0;
+// ... in the lists of a batch behind a prefix: 128 tokens behind 16,384 take 78 us
+// with 2, 75 with 4, 79 with 6; 8 tokens behind 8,192 17.4 with 2, 18.1 with 4
+constexpr int kSharedItemCost = 3;
+// ... over codes, whose items end with the warps' joining: 32 sequences of 2,000 to
+// 32,768 positions 79 us with 0, 76 with 2, 73 with 4; 128 short ones behind a
+// prefix 250 with 2, 266 with 4
+constexpr int kCodeItemCost = 3;
 
 struct AttnParams {
   static constexpr bool kShared = false;
@@ -60,10 +67,8 @@ struct AttnParams {
 struct SharedParams : AttnParams {
   static constexpr bool kShared = true;
   static constexpr bool kAhead = true;
-  // 128 tokens behind 16,384 take 78 us with 2, 75 with 4, 79 with 6; 8 tokens
-  // behind 8,192 17.4 with 2, 18.1 with 4
   template <int kTiles>
-  static constexpr int kCost = 3;
+  static constexpr int kCost = kSharedItemCost;
   enum Lists { kBoth, kPrefixOnly, kOwnOnly };
   Lists lists;                  // those that this launch works on
   int prefix, prefix_pages;

@@ -227,14 +227,15 @@ constexpr int kMaxPrefix = 1 << 30;  // positions: a token's number added to the
 
 int too_much() { return fail(MOE_ERR_UNSUPPORTED, "too much work for one call: split the tokens"); }
 
-// Units of a key/value head's longest possible item, with what it costs besides.
-double item_cost(const moe_attn_args_t& a, int pages) {
-  return std::min(1073741824., (double)pages * a.page_size) / kTile + 1 + kItemCost<2>;
+// Units of a key/value head's longest possible item, with the `besides` that its
+// list counts for each.
+double item_cost(const moe_attn_args_t& a, int pages, int besides) {
+  return std::min(1073741824., (double)pages * a.page_size) / kTile + 1 + besides;
 }
 
 // A call's parameters for tiles of `tokens` tokens, items of `tiles`.
-int fill_params(const moe_attn& h, const moe_attn_args_t& a, int tokens, int tiles, AttnParams* p) {
-  const double item_tokens = (double)tiles * tokens, cost = item_cost(a, a.table_pages);
+int fill_params(const moe_attn& h, const moe_attn_args_t& a, int tokens, int tiles, int besides, AttnParams* p) {
+  const double item_tokens = (double)tiles * tokens, cost = item_cost(a, a.table_pages, besides);
   if ((a.n_tokens / item_tokens + a.batch) * h.n_kv_heads * cost > kMaxUnits) return too_much();
   const int rc = check_current(h);
   if (rc != MOE_OK) return rc;
@@ -285,7 +286,7 @@ int forward_16(moe_attn* h, const moe_attn_args_t& args, moe_stream_t stream) {
   const int tokens = kTile / (h->n_heads / h->n_kv_heads);
   AttnParams p;
   Maps maps;
-  int rc = fill_params(*h, a, tokens, a.max_q_len > tokens ? 2 : 1, &p);
+  int rc = fill_params(*h, a, tokens, a.max_q_len > tokens ? 2 : 1, kItemCost<2>, &p);
   if (rc == MOE_OK) rc = maps_16(h, a, tokens, &maps);
   if (rc != MOE_OK) return rc;
   if (a.dtype == MOE_DTYPE_BF16)
@@ -300,7 +301,7 @@ int forward_codes(moe_attn* h, const moe_attn_args_t& args, const moe_attn_opts_
   const int group = h->n_heads / h->n_kv_heads, tokens = code_rows(std::max(1, a.max_q_len) * group) / group;
   AttnParams p;
   Maps maps;
-  int rc = fill_params(*h, a, tokens, 1, &p);
+  int rc = fill_params(*h, a, tokens, 1, kCodeItemCost, &p);
   if (rc == MOE_OK) rc = maps_codes(h, a, &maps);
   return rc != MOE_OK ? rc : launch_quantised(*h, p, *o.scales, maps, stream);
 }
@@ -391,7 +392,7 @@ int run_shared(moe_attn* h, const moe_attn_args_t& a, const moe_attn_opts_t& o, 
                const moe_attn_args_t& first, moe_stream_t stream) {
   char* at = static_cast<char*>(o.workspace);
   SharedParams p{};
-  int rc = fill_params(*h, a, w.own_tokens, w.own_tiles, &p);
+  int rc = fill_params(*h, a, w.own_tokens, w.own_tiles, kSharedItemCost, &p);
   if (rc != MOE_OK) return rc;
   p.fits = true;
   p.by_item = false;
@@ -444,14 +445,16 @@ int forward_with(moe_attn* h, const moe_attn_args_t& args, const moe_attn_opts_t
   const Work w = work_of(*h, a, o);
   if (o.prefix_len > 0) {
     const double units =
-        ((double)w.prefix_items * ((double)o.prefix_len / kTile + 1 + kItemCost<2>) +
-         (double)a.batch * w.own_items * item_cost(a, a.table_pages)) * h->n_kv_heads;
+        ((double)w.prefix_items * ((double)o.prefix_len / kTile + 1 + kSharedItemCost) +
+         (double)a.batch * w.own_items * item_cost(a, a.table_pages, kSharedItemCost)) * h->n_kv_heads;
     if (units > kMaxUnits) return too_much();
   }
   if (o.prefix_len == 0 && !w.unpack) return forward_codes(h, a, o, stream);
   AttnParams limits;  // before anything is launched
   const int tile = kTile / (h->n_heads / h->n_kv_heads);
-  int rc = w.unpack ? fill_params(*h, a, tile, a.max_q_len > tile ? 2 : 1, &limits) : MOE_OK;
+  int rc = w.unpack ? fill_params(*h, a, tile, a.max_q_len > tile ? 2 : 1,
+                                  o.prefix_len > 0 ? kSharedItemCost : kItemCost<2>, &limits)
+                    : MOE_OK;
   if (rc == MOE_OK) rc = check_current(*h);
   if (rc != MOE_OK) return rc;
   char* at = static_cast<char*>(o.workspace);

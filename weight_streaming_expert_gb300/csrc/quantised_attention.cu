@@ -44,15 +44,12 @@
 namespace wse {
 namespace {
 
-// An item's start (the queries) and end (the warps' joining) take as long as some
-// units: 32 sequences of 2,000 to 32,768 positions 79 us with 0, 76 with 2, 73
-// with 4; 128 short ones behind a prefix 250 with 2, 266 with 4.
-constexpr int kCodeItemCost = 3;
 struct CodeParams : AttnParams {
   static constexpr bool kAhead = true;
   template <int kTiles>
   static constexpr int kCost = kCodeItemCost;
 };
+static_assert(kCodeItemCost <= kSharedItemCost, "the host's limit of a batch behind a prefix counts the latter");
 struct SharedCodeParams : SharedParams {
   static constexpr bool kAhead = true;
   template <int kTiles>
