@@ -47,3 +47,42 @@ def test_limits_count_what_the_lists_do():
     for prefix, codes in ((0, s), (16, None)):
         status, text = forward(heads, prefix, codes, batch=2000, n_tokens=2000, max_q_len=1, table_stride=2)
         assert status != N.MOE_ERR_UNSUPPORTED, text
+
+
+@pytest.mark.parametrize("codes", [False, True])
+def test_a_longest_chunk_above_all_tokens_is_all_tokens(codes):
+    """max_q_len is a bound, and no chunk is longer than the call's tokens: a
+    loose one takes no more work or room."""
+    from weight_streaming_expert_gb300 import native as N
+    L = N.lib()
+    s = N.moe_cache_scales_t(4096, 4096, 512, 256, 512, 256) if codes else None
+    heads = (8, 2, 64)
+    fake = ctypes.create_string_buffer(struct.pack("5i", *heads, 152, 1 << 20), 4096)
+    for prefix in (16, 0):
+        o = N.moe_attn_opts_t(ctypes.pointer(s) if s else None, prefix, 4096, ROOM)
+        room = []
+        for longest in (5, 6, 1 << 20, (1 << 31) - 1):
+            k = dict(batch=4000, n_tokens=5, max_q_len=longest, table_stride=1 << 10)
+            room.append(L.moe_attn_workspace(fake, ctypes.byref(args(**k)), ctypes.byref(o)))
+            if s or prefix:
+                status, text = forward(heads, prefix, s, **k)
+                assert "too much work" not in text and "workspace" not in text, (prefix, longest, text)
+        assert room == room[:1] * 4, (prefix, room)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("codes", [False, True])
+def test_a_loose_longest_chunk_has_the_same_results(codes):
+    import torch
+
+    from tests.test_shared_prefix import Shared
+    from weight_streaming_expert_gb300 import PagedAttention
+    case = Shared([1, 2, 0, 1], [20, 300, 7, 1], 96, 8, 2, 64, 16, seed=3, codes=codes)
+    attn = PagedAttention(8, 2, 64, device="cuda:0")
+    x = case.inputs()
+    want, want_lse = attn(**{**x, "max_q_len": 4}, return_lse=True)
+    case.check(want, want_lse, torch.bfloat16)
+    for longest in (1000, 1 << 20, (1 << 31) - 1):
+        out, lse = attn(**{**x, "max_q_len": longest}, return_lse=True)
+        assert attn.status() == 0 and torch.equal(out, want) and torch.equal(lse, want_lse)
+    attn.close()

@@ -281,6 +281,14 @@ moe_attn_args_t with_pages(const moe_attn_args_t& a) {
   return r;
 }
 
+// What a call with options works on: its longest chunk goes into its tiles, lists
+// and workspace, and none is longer than all tokens.
+moe_attn_args_t with_bounds(const moe_attn_args_t& a) {
+  moe_attn_args_t r = with_pages(a);
+  r.max_q_len = std::min(a.max_q_len, a.n_tokens);
+  return r;
+}
+
 int forward_16(moe_attn* h, const moe_attn_args_t& args, moe_stream_t stream) {
   const moe_attn_args_t a = with_pages(args);
   const int tokens = kTile / (h->n_heads / h->n_kv_heads);
@@ -296,8 +304,7 @@ int forward_16(moe_attn* h, const moe_attn_args_t& args, moe_stream_t stream) {
                            : launch_attn<__half, 128>(h, p, maps, stream);
 }
 
-int forward_codes(moe_attn* h, const moe_attn_args_t& args, const moe_attn_opts_t& o, moe_stream_t stream) {
-  const moe_attn_args_t a = with_pages(args);
+int forward_codes(moe_attn* h, const moe_attn_args_t& a, const moe_attn_opts_t& o, moe_stream_t stream) {
   const int group = h->n_heads / h->n_kv_heads, tokens = code_rows(std::max(1, a.max_q_len) * group) / group;
   AttnParams p;
   Maps maps;
@@ -440,8 +447,7 @@ moe_attn_args_t over_pages(const moe_attn& h, const moe_attn_args_t& a, const Un
   return r;
 }
 
-int forward_with(moe_attn* h, const moe_attn_args_t& args, const moe_attn_opts_t& o, moe_stream_t stream) {
-  const moe_attn_args_t a = with_pages(args);
+int forward_with(moe_attn* h, const moe_attn_args_t& a, const moe_attn_opts_t& o, moe_stream_t stream) {
   const Work w = work_of(*h, a, o);
   if (o.prefix_len > 0) {
     const double units =
@@ -550,7 +556,7 @@ size_t moe_attn_workspace(const moe_attn_t* h, const moe_attn_args_t* a, const m
   if (!h || !a || !o || a->batch <= 0 || a->n_tokens <= 0 || a->page_size <= 0 || o->prefix_len < 0 ||
       o->prefix_len > kMaxPrefix)
     return 0;
-  const moe_attn_args_t all = with_pages(*a);
+  const moe_attn_args_t all = with_bounds(*a);
   return o->prefix_len / a->page_size > all.table_pages ? 0 : work_of(*h, all, *o).wanted;
 }
 
@@ -574,10 +580,11 @@ int moe_attn_forward_ex(moe_attn_t* h, const moe_attn_args_t* a, const moe_attn_
     if ((sc->k_page_stride | sc->k_head_stride | sc->v_page_stride | sc->v_head_stride) & 15)
       return fail(MOE_ERR_INVALID_ARG, "every stride of the scales must be a multiple of 16 bytes");
   }
-  const size_t need = work_of(*h, with_pages(*a), *o).need;
+  const moe_attn_args_t all = with_bounds(*a);
+  const size_t need = work_of(*h, all, *o).need;
   if (need > 0 && (!o->workspace || !aligned(o->workspace, 16) || o->workspace_bytes < need))
     return fail(MOE_ERR_INVALID_ARG, "the workspace must be 16-byte aligned and hold %zu bytes", need);
-  return forward_with(h, *a, *o, stream);
+  return forward_with(h, all, *o, stream);
 }
 
 int moe_attn_get_status(moe_attn_t* h) {
