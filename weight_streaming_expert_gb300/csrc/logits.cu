@@ -104,7 +104,11 @@ __global__ void __launch_bounds__(kLogitThreads, kResident) adjust_logits_kernel
 
   // what is not given changes nothing as these numbers
   const float rep = a.repetition ? a.repetition[row] : 1.f, presence = a.presence ? a.presence[row] : 0.f;
-  const float frequency = a.frequency ? a.frequency[row] : 0.f, inverse = __frcp_rn(rep);
+  const float frequency = a.frequency ? a.frequency[row] : 0.f;
+  // what it is divided by, and the power of two that this leaves: of a repetition
+  // whose reciprocal would be subnormal or infinite
+  const float scale = fabsf(rep) < 0x1p-100f ? 0x1p60f : fabsf(rep) > 0x1p100f ? 0x1p-60f : 1.f;
+  const float by = rep * scale, inverse = __frcp_rn(by);
 
   // ---- the tables
   if (counts || biases) {
@@ -151,10 +155,12 @@ __global__ void __launch_bounds__(kLogitThreads, kResident) adjust_logits_kernel
   }
 
   // ---- the logits
-  // x / rep, by its reciprocal and what that leaves (a last bit off at most)
+  // v / rep by the reciprocal and a correction from what the product leaves
+  // (Markstein's division): a last bit off at most, or the last two of a v below
+  // 2^-125, whose remainder loses bits
   auto divided = [&](float v) {
-    const float q = __fmul_rn(v, inverse), rest = __fmaf_rn(-q, rep, v);
-    return fabsf(rest) < INFINITY ? __fmaf_rn(rest, inverse, q) : q;  // not of infinities
+    const float q = __fmul_rn(v, inverse), rest = __fmaf_rn(-q, by, v);
+    return __fmul_rn(fabsf(rest) < INFINITY ? __fmaf_rn(rest, inverse, q) : q, scale);  // not of infinities
   };
 #pragma unroll
   for (int i = 0; i < kLogitLoads; ++i) {
