@@ -57,8 +57,9 @@ def copy_pages(k_pool, v_pool, src, dst, stream=None, k_scale=None, v_scale=None
     if quantised:
         _scale_pools(k_pool, v_pool, k_scale, v_scale)
         for t in (k_scale, v_scale):  # before anything has moved
-            if t.stride(2) != t.shape[3] or any(n % 16 for n in (t.shape[2] * t.shape[3], t.stride(0), t.stride(1))):
-                raise ValueError("the scales' pages must be contiguous, of whole 16 bytes and as many apart")
+            numbers = (t.shape[2] * t.shape[3], t.stride(0), t.stride(1), t.data_ptr())
+            if t.stride(2) != t.shape[3] or any(n % 16 for n in numbers):
+                raise ValueError("the scales' pages must be contiguous, of whole 16 bytes, as many apart and aligned to them")
     _copy("moe_copy_pages", False, k_pool, v_pool, src, dst, stream)
     if quantised:
         _copy("moe_copy_pages", False, k_scale.unsqueeze(2), v_scale.unsqueeze(2), src, dst, stream)
