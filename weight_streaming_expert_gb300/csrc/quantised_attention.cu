@@ -657,21 +657,16 @@ struct UnpackArgs {
 };
 
 constexpr int kUnpackThreads = 256;
+// Most CTAs of a call, in waves of them: 32 chunks of 9 tokens of 32/4 heads over
+// 2,000 to 32,768 positions in a table of that width take 460 us with 2, 415 with 4,
+// 409 with 8, and with one for each page of it 436; over up to 2,000 in a table of
+// 18,000 63, 64, 69 and 116.
+constexpr int kUnpackWaves = 4;
 
-// CTA (x, z): a page of the prefix, then of the sequences one after the other,
-// keys or values; it has nothing to do past a sequence's end.  Bound by memory.
-__global__ void __launch_bounds__(kUnpackThreads) unpack_kernel(const __grid_constant__ UnpackArgs a) {
-  const int from_prefix = a.prefix ? a.prefix_pages : 0, z = blockIdx.y, tid = threadIdx.x;
-  const bool prefix = (int)blockIdx.x < from_prefix;
-  const int at = (int)blockIdx.x - (prefix ? 0 : from_prefix), b = prefix ? 0 : at / a.own_pages;
-  const int i = prefix ? at : at - b * a.own_pages, skip = prefix ? 0 : a.prefix_pages;
-  pdl_wait();
-  pdl_launch_dependents();
-  const long long to = prefix ? at : (long long)a.prefix_pages + at;
-  if (z == 0 && tid == 0) a.table[(long long)b * a.out_stride + skip + i] = (int)to;
-  if (!prefix && ((long long)skip + i) * a.page_size >= a.kv_lens[b]) return;
-  const int page = a.block_table[(long long)b * a.table_stride + skip + i];
+// Page `page` of the cache in 16 bits as page `to`, by a CTA.
+__device__ __forceinline__ void unpack_page(const UnpackArgs& a, int z, int page, long long to) {
   const bool there = (unsigned)page < (unsigned)a.n_pages;
+  const int tid = threadIdx.x;
   if (!there && tid == 0) atomicOr(a.status, kAttnBadPage);
   const int per_head = a.head_dim / 16, per_row = a.n_kv_heads * per_head, units = a.page_size * per_row;
   const uint8_t* from = a.cache[z] + (there ? page : 0) * a.page_stride[z];
@@ -690,6 +685,25 @@ __global__ void __launch_bounds__(kUnpackThreads) unpack_kernel(const __grid_con
     uint4* dst = reinterpret_cast<uint4*>(out + (long long)u * 16);
     dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
     dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+// CTA (x, z): a page of the prefix, then `ctas` for each sequence, which take its
+// pages in turn, as many as the length found here says; z: keys or values.
+__global__ void __launch_bounds__(kUnpackThreads) unpack_kernel(const __grid_constant__ UnpackArgs a, int ctas) {
+  const int from_prefix = a.prefix ? a.prefix_pages : 0, x = (int)blockIdx.x, z = blockIdx.y;
+  const bool prefix = x < from_prefix;
+  const int b = prefix ? 0 : (x - from_prefix) / ctas, skip = prefix ? 0 : a.prefix_pages;
+  int i = prefix ? x : x - from_prefix - b * ctas;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int32_t* row = a.block_table + (long long)b * a.table_stride + skip;
+  // of the sequence's own pages those that begin before its end
+  const int pages = prefix ? a.prefix_pages : a.own_pages, len = prefix ? 0x7fffffff : a.kv_lens[b];
+  for (; i < pages && (prefix || ((long long)skip + i) * a.page_size < len); i += prefix ? pages : ctas) {
+    const long long to = prefix ? i : (long long)a.prefix_pages + (long long)b * a.own_pages + i;
+    if (z == 0 && threadIdx.x == 0) a.table[(long long)b * a.out_stride + skip + i] = (int)to;
+    unpack_page(a, z, row[i], to);
   }
 }
 
@@ -726,8 +740,12 @@ int launch_quantised(const moe_attn& h, const SharedParams& p, const moe_cache_s
 
 int launch_unpack(const moe_attn& h, const moe_attn_args_t& a, const moe_cache_scales_t& s, const Unpacked& to, bool prefix,
                   int batch, moe_stream_t stream) {
-  const long long pages = (prefix ? to.prefix_pages : 0) + (long long)batch * to.own_pages;
-  if (pages == 0) return MOE_OK;
+  // a CTA for each page that the table has room for, unless they are too many: the
+  // table may be much wider than its sequences are long
+  const int most = kUnpackWaves * h.n_sms * (2048 / kUnpackThreads) / 2;
+  const int ctas = std::min(to.own_pages, std::max(1, most / std::max(1, batch)));
+  const long long grid = (prefix ? to.prefix_pages : 0) + (long long)batch * ctas;
+  if (grid == 0) return MOE_OK;
   const UnpackArgs u{{static_cast<const uint8_t*>(a.k_cache), static_cast<const uint8_t*>(a.v_cache)},
                      {a.k_page_stride, a.v_page_stride},
                      {a.k_row_stride, a.v_row_stride},
@@ -737,7 +755,7 @@ int launch_unpack(const moe_attn& h, const moe_attn_args_t& a, const moe_cache_s
                      {static_cast<uint16_t*>(to.k), static_cast<uint16_t*>(to.v)},
                      a.block_table, a.kv_lens, to.table, h.status, a.table_stride, a.page_size, a.n_pages, h.n_kv_heads,
                      h.head_dim, to.table_stride, to.prefix_pages, to.own_pages, prefix, a.dtype == MOE_DTYPE_BF16};
-  return launch_pdl(unpack_kernel, dim3((unsigned)pages, 2), dim3(kUnpackThreads), 0, stream, 1, u);
+  return launch_pdl(unpack_kernel, dim3((unsigned)grid, 2), dim3(kUnpackThreads), 0, stream, 1, u, std::max(1, ctas));
 }
 
 }  // namespace wse
