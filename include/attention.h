@@ -180,21 +180,27 @@ int moe_attn_forward(moe_attn_t* h, const moe_attn_args_t* a, moe_stream_t strea
  * prefix_len: the first prefix_len positions of every sequence are the same, in
  * the same pages: those that the table's first row begins with (the other rows'
  * first prefix_len / page_size entries are not read).  Whole pages, up to 2^30
- * positions, and all new tokens lie behind them (a sequence that is shorter is an error found on the
- * device).  The prefix is read once for the whole batch instead of once for
- * each sequence; the results are those of a call without, but for rounding.
- * Of a quantised cache's prefix, where it is read for more than 64 rows, and of
- * such chunks' pages as above the 16-bit copies lie in the workspace.
+ * positions, and all new tokens lie behind them (a sequence that is shorter is
+ * an error found on the device).  The prefix is read once for the whole batch
+ * instead of once for each sequence; the results are those of a call without,
+ * but for rounding.  Of a quantised cache's prefix, where it is read for more
+ * than 64 rows, and of such chunks' pages as above the 16-bit copies lie in the
+ * workspace.
+ *
+ * The workspace for chunks over codes goes by what a row of the table could hold
+ * (table_pages), since only the device knows the lengths: up to a gigabyte of
+ * sequences, or one that takes more.  With less than all of them the sequences
+ * take turns, so a table (or a view of it) no wider than the longest sequence
+ * is faster and smaller.
  */
 typedef struct {
   const moe_cache_scales_t* scales; /* host struct; NULL: a 16-bit cache */
   int prefix_len;                   /* 0: none */
   void* workspace;                  /* device, 16-byte aligned, free for other use once the call's work is done; */
-  size_t workspace_bytes;           /* moe_attn_workspace() of them (for chunks over codes one sequence's pages
-                                    suffice: the sequences then take turns) */
+  size_t workspace_bytes;           /* moe_attn_workspace() of them; for chunks over codes one sequence's pages suffice */
 } moe_attn_opts_t;
 
-/* Bytes of workspace that moe_attn_forward_ex takes for such a call; 0: none. */
+/* Bytes of workspace that moe_attn_forward_ex takes for such a call; 0: none, or a call that it refuses. */
 size_t moe_attn_workspace(const moe_attn_t* h, const moe_attn_args_t* a, const moe_attn_opts_t* o);
 
 /* moe_attn_forward with options (NULL: none).  MOE_ERR_UNSUPPORTED also for a prefix whose tiles, with those of a batch

@@ -58,7 +58,8 @@ int moe_sample(const float* logits, int64_t row_stride, int rows, int vocab, con
  *   x + bias         of the last entry for v in the row's part of the list;
  *   -inf             where v's bit of the row's mask is 0 (whatever x was),
  * each step in fp32 and rounded (the division to within its last bit, of logits
- * below 2^-125 its last two).  What is not given is left out; a NaN without a mask's 0 stays one.  The same inputs give the same bits every time.
+ * below 2^-125 its last two).  What is not given is left out; a NaN without a
+ * mask's 0 stays one.  The same inputs give the same bits every time.
  * Asynchronous on `stream`, allocates nothing, can be captured into a graph.
  */
 typedef struct {

@@ -180,16 +180,21 @@ class PagedAttention:
         """q [T, Hq, D]; caches [pages, page_size, Hk, D]; block_table int32
         [B, pages of a row] (a view of a wider table, or one row expanded, is
         fine); q_starts int32 [B + 1]; kv_lens int32 [B] (the new tokens
-        included); max_q_len: at least the longest chunk; scale: default
+        included); max_q_len: at least the longest chunk, and the nearer to it
+        the better a call is laid out; scale: default
         D ** -0.5; tree_mask: int64 [T], bit j of a token's word set where it
         sees its chunk's token j, instead of the chain (chunks up to 64).
         Returns out [T, Hq, D], with ``return_lse`` also fp32 [T, Hq].
 
         k_scale, v_scale (uint8 [pages, Hk, page_size]): the caches are
-        quantised, float8_e4m3fn codes as ``QKNormRope`` writes them.
+        quantised, float8_e4m3fn codes as ``QKNormRope`` writes them.  Chunks of
+        more than 64 rows (tokens times heads that share one of the cache) are
+        unpacked first, in a workspace that goes by the table's width: give a
+        view as narrow as the longest sequence.
         prefix_len: every sequence begins with the same positions, as many, in
-        the same whole pages (forks: ``PagedKVCache.shared_prefix``) and before
-        all new tokens; they are then read once for the batch."""
+        the same whole pages (forks: ``PagedKVCache.shared_prefix``, which says
+        from where it pays) and before all new tokens; they are then read once
+        for the batch."""
         index = self._index
         if _elsewhere(index, stream):
             with _On(index, stream):

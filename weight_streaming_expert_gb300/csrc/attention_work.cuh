@@ -28,12 +28,14 @@ constexpr int kMaxParts = 1024;            // CTAs, which is at least the shares
 // 1 or 2).
 template <int kTiles>
 constexpr int kItemCost = kTiles == 2 ? 2 : 0;
-// ... in the lists of a batch behind a prefix: 128 tokens behind 16,384 take 78 us
-// with 2, 75 with 4, 79 with 6; 8 tokens behind 8,192 17.4 with 2, 18.1 with 4
+// ... in the lists of a batch behind a prefix: 128 tokens behind 16,384 take 78.6 us
+// with 2, 77.5 with 3, 76.1 with 4, 64 of them 44.9, 45.8 and 45.8; 8 behind 8,192
+// 17.9 to 18.0 with each
 constexpr int kSharedItemCost = 3;
 // ... over codes, whose items end with the warps' joining: 32 sequences of 2,000 to
-// 32,768 positions 79 us with 0, 76 with 2, 73 with 4; 128 short ones behind a
-// prefix 250 with 2, 266 with 4
+// 32,768 positions 73.5 us with 2, 73.2 with 3, 73.1 with 4 (79 with 0), a chain of
+// 6 over 8,192 15.9, 15.6 and 15.8; behind a prefix 128 tokens 112, 109 and 108, 8
+// tokens 20.1, 20.3 and 21.2
 constexpr int kCodeItemCost = 3;
 
 struct AttnParams {

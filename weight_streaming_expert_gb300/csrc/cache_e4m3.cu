@@ -11,10 +11,11 @@ constexpr int kReadThreads = 256;
 
 // `lanes` of a warp take a token, 16 codes of it each at a time (so that its slot
 // is worked out once for them: with 16 codes of any row a thread the divisions
-// took longer than memory); blockIdx.y: keys or values.  Bound by memory: D + 1
-// bytes in and 2 D out for each row.  16384 tokens of 4 heads of 128: 11.2 us,
-// 4.5 TB/s, with four tokens a lane in flight and fewer threads 12.9; 6 tokens
-// 1.7 us.
+// took longer than memory); blockIdx.y: keys or values.  D + 1 bytes in and 2 D
+// out for each row, but bound by the latency of its waves (slot, then codes and
+// scale, then the stores) and by issue: 16384 tokens of 4 heads of 128 11.2 us
+// (memory needs 7.5), 73 % of the issue slots, DRAM 14 %; with four tokens a lane
+// in flight and fewer threads 12.9.  6 tokens 1.7 us, a launch.
 __global__ void __launch_bounds__(kReadThreads, 8)
     read_e4m3_kernel(const __grid_constant__ moe_read_e4m3_args_t a, int lanes) {
   const bool values = blockIdx.y != 0;

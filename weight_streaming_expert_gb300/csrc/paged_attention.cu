@@ -315,7 +315,9 @@ int forward_codes(moe_attn* h, const moe_attn_args_t& a, const moe_attn_opts_t& 
 
 // Chunks of more rows than a tile over codes has: where a position's codes would
 // be converted for every tile, they are converted once for all of them, into
-// pages of 16 bits that the 16-bit kernel reads.
+// pages of 16 bits that the 16-bit kernel reads.  Up to there a tile is faster: 64
+// rows of 32 sequences of 2,000 to 32,768 positions 175 us, unpacked 368, 32 rows
+// 131 and 423; of one over 8,192 17.1 and 20.8.
 bool in_chunks(const moe_attn& h, const moe_attn_args_t& a) {
   return std::max(1ll, (long long)a.max_q_len) * (h.n_heads / h.n_kv_heads) > kMaxCodeRows;
 }

@@ -11,7 +11,7 @@
 // has grown by more than 8, so a p_j is at most 2^8 and the largest about 1:
 // what fp16 rounds away of the others is 2^-11 of each, or 2^-25 of the largest.
 //
-// Reading the cache is the bound, at 22 bytes a clock and SM, so a code may cost
+// Reading the cache is the bound of few rows, at 22 bytes a clock and SM, so a code may cost
 // few instructions and little shared memory traffic: a warp takes 16 positions
 // from where the copies put them straight into the registers that the warp-wide
 // MMA wants (m16n8k16, fp16), converted two at a time, and never writes them back.
@@ -34,8 +34,9 @@
 //
 // One GB300 (copy 6693 GB/s), 32 single tokens of 32/4 heads of 128 over 2,000 to
 // 32,768 positions: 73 us, 5.7 TB/s, of which 10 us are the call's start and end
-// (a tile of 8 rows; 16 rows 92 us, 32 rows 131, 64 rows 175: the conversions'
-// instructions and their latency).  6 tokens over 8,192: 15.8 us.
+// (a tile of 8 rows; 16 rows 91 us, 32 rows 131, 64 rows 175: the conversions'
+// instructions and their latency, where 16-bit caches take 124 to 137 at any of
+// these rows).  6 tokens over 8,192: 15.5 us.
 #include <algorithm>
 
 #include "attention_handle.cuh"
@@ -60,7 +61,7 @@ constexpr int kWarps = 8, kCopyWarps = 4, kCodeThreads = (kWarps + kCopyWarps) *
 
 // Registers of a thread: the copying warps give most of theirs to the others,
 // which hold two blocks of positions at a time (16 rows: 110 us with one and 200
-// bytes spilled, 89 with two).  The shares add up to what the block is launched
+// bytes spilled, 89 with two when that was built, 91 now).  The shares add up to what the block is launched
 // with, which launch() makes sure of.
 constexpr int kLaunchRegisters = 168, kWorkRegisters = 224, kCopyRegisters = 56;
 static_assert(kWarps * kWorkRegisters + kCopyWarps * kCopyRegisters == (kWarps + kCopyWarps) * kLaunchRegisters);
@@ -689,7 +690,10 @@ __device__ __forceinline__ void unpack_page(const UnpackArgs& a, int z, int page
 }
 
 // CTA (x, z): a page of the prefix, then `ctas` for each sequence, which take its
-// pages in turn, as many as the length found here says; z: keys or values.
+// pages in turn, as many as the length found here says; z: keys or values.  Of a
+// prompt's hundreds of pages it is the latency of length, entry and codes (6 MB:
+// 11 us under a profiler, DRAM 9 %), of the decode batch's 0.4 GB memory (about 260
+// us, 4.7 TB/s read and written).
 __global__ void __launch_bounds__(kUnpackThreads) unpack_kernel(const __grid_constant__ UnpackArgs a, int ctas) {
   const int from_prefix = a.prefix ? a.prefix_pages : 0, x = (int)blockIdx.x, z = blockIdx.y;
   const bool prefix = x < from_prefix;

@@ -26,7 +26,11 @@
 namespace wse {
 namespace {
 
-constexpr int kFewJoined = 8;  // parts of an item that a warp joins by itself; more of them, too, of many rows
+// Parts of an item that a warp joins by itself (4, 8 or 16: no call measured tells
+// them apart); more of them, too, where the rows are many: beyond this many waves of
+// joining CTAs (24 tokens of 20/4 heads behind 8,192: 25.1 us with 2, 26.8 with 1;
+// 64 of 32/4 behind 16,384: 45.7 with 1 or 2, 57 with 8).
+constexpr int kFewJoined = 8, kJoinWaves = 2;
 
 // Where the results of the rows of one of a sequence's own items lie.
 template <int D>
@@ -273,7 +277,7 @@ int launch_join(const moe_attn& h, const JoinParams& j, moe_stream_t stream) {
   const dim3 grid((unsigned)(p.a.batch * p.n_kv_heads * p.own_items), (unsigned)((rows + kJoinRows - 1) / kJoinRows));
   // about as many parts has an item of the prefix if the CTAs do nothing else
   const int parts = h.n_sms / p.spread / p.prefix_items;
-  return parts > kFewJoined && (long long)grid.x * grid.y <= 2 * h.n_sms
+  return parts > kFewJoined && (long long)grid.x * grid.y <= kJoinWaves * h.n_sms
              ? launch_pdl(join_many_parts_kernel<T, D>, grid, dim3(kJoinRows * kJoinGroups * D / 4), 0, stream, 1, j)
              : launch_pdl(join_few_parts_kernel<T, D>, grid, dim3(32 * kJoinRows), 0, stream, 1, j);
 }
